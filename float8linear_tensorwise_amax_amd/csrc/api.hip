@@ -18,6 +18,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "check.h"
 #include "device_common.h"
 #include "internal.h"
 
@@ -30,8 +31,6 @@ static __device__ __align__(256) uint8_t scratch[kStaticScratchBytes];
 namespace f8lin {
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 22;        // per matrix dimension (32-bit tile offsets)
-constexpr int64_t kMaxElems = (int64_t)1 << 40;      // per tensor
 constexpr int kUpdateBatch = 16;
 
 struct StateBatch {
@@ -59,35 +58,7 @@ __global__ void delayed_update_kernel(StateBatch batch, int32_t *status) {
   st.amax[0] = 0.0f;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// A data pointer may be NULL only when its tensor is empty.
-bool missing(const void *p, int64_t elems) { return p == nullptr && elems > 0; }
-
 bool bad_dim(int64_t d) { return d < 0 || d > kMaxDim || (d % 16) != 0; }
-
-struct Range {
-  const void *p;
-  int64_t bytes;
-};
-
-bool overlaps(const Range &a, const Range &b) {
-  if (a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, a1 = a0 + (uintptr_t)a.bytes;
-  const uintptr_t b0 = (uintptr_t)b.p, b1 = b0 + (uintptr_t)b.bytes;
-  return a0 < b1 && b0 < a1;
-}
-
-// Every output range must be disjoint from every other range.
-bool any_overlap(const Range *outs, int nout, const Range *ins, int nin) {
-  for (int i = 0; i < nout; ++i) {
-    for (int j = i + 1; j < nout; ++j)
-      if (overlaps(outs[i], outs[j])) return true;
-    for (int j = 0; j < nin; ++j)
-      if (overlaps(outs[i], ins[j])) return true;
-  }
-  return false;
-}
 
 int check_fmt(int f) { return (f == F8LIN_E4M3 || f == F8LIN_E5M2) ? F8LIN_OK : F8LIN_EINVAL; }
 int check_algo(int a) { return (a == F8LIN_AMAX_ATOMIC || a == F8LIN_AMAX_TWOPASS) ? F8LIN_OK : F8LIN_EINVAL; }
@@ -104,20 +75,10 @@ int check_ws(const void *ws, size_t ws_bytes) {
   return F8LIN_OK;
 }
 
-int status_of(hipError_t e) { return e == hipSuccess ? F8LIN_OK : F8LIN_EHIP; }
-
-bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
-
 // Records an optional timing event on the call's stream.
 int record(void *ev, hipStream_t s) {
   return ev ? status_of(hipEventRecord((hipEvent_t)ev, s)) : F8LIN_OK;
 }
-
-#define F8_TRY(expr)                 \
-  do {                               \
-    const int st_ = (expr);          \
-    if (st_ != F8LIN_OK) return st_; \
-  } while (0)
 
 // Validation shared by f8lin_cast_transpose and the orchestrated casts.
 int validate_cast(const uint16_t *x, int64_t rows, int64_t cols, int fmt, int mode, const f8lin_state *st,

@@ -1,0 +1,229 @@
+// Global norm of a list of tensors, and scaling them to a largest norm: the
+// step between the layers' backward passes and the optimiser.
+//   n = sqrt(sum g^2), sum |g| or max |g| over every element of every tensor;
+//   c = min(1, max_norm / (n + 1e-6)) in binary32;  out = c * g, rounded once.
+// A NaN anywhere makes n and c NaN; an Inf makes n Inf and c 0 (so that Inf
+// elements become NaN and the others 0).
+//
+// HBM-bound: the norm reads every element once, the scaling reads it again
+// and writes it.  Sums are taken in binary64: the square of a 16-bit float is
+// exact in it, cannot overflow or vanish, and the order of a fixed grid is
+// the same on every run (no atomics).
+// Tables of up to kGradBatch tensors go to the kernel as an argument, so a
+// call copies nothing to the device; the tensors are cut into pieces of
+// kPiece elements, dealt to the workgroups round robin.  Longer lists take one
+// launch per table, each adding to the partial results of the one before.
+// The scaling kernel's workgroups reduce the partial results themselves.
+#include <algorithm>
+
+#include "mx_common.h"
+
+namespace f8lin {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPiece = 16384;
+constexpr int kNormGrid = kGradPartials;
+
+struct GradTable {
+  const void *g[kGradBatch];
+  void *out[kGradBatch];
+  int64_t n[kGradBatch];
+  int first[kGradBatch];  // first piece of each tensor
+  uint8_t in_dtype[kGradBatch], out_dtype[kGradBatch];
+  int count, pieces;
+};
+
+// Tensor of piece p: the last one whose first piece is at or before p.
+__device__ __forceinline__ int tensor_of(const GradTable &t, int p) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= p) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int P>
+__device__ __forceinline__ void fold(double &s, float v) {
+  if constexpr (P == F8LIN_NORM_2) s = fma((double)v, (double)v, s);
+  if constexpr (P == F8LIN_NORM_1) s += (double)fabsf(v);
+  if constexpr (P == F8LIN_NORM_INF) s = (v != v) ? (double)v : fmax(s, (double)fabsf(v));  // (a NaN in s: below)
+}
+template <int P>
+__device__ __forceinline__ double join(double a, double b) {
+  if constexpr (P != F8LIN_NORM_INF) return a + b;
+  return (a != a) ? a : (b != b) ? b : fmax(a, b);
+}
+
+template <int P>
+__device__ __forceinline__ double block_join(double s) {
+  __shared__ double red[kThreads / 64];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) s = join<P>(s, __shfl_xor(s, off, 64));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  return join<P>(join<P>(red[0], red[1]), join<P>(red[2], red[3]));
+}
+
+template <int P, int DT>
+__device__ __forceinline__ double piece_norm(const void *g, int64_t begin, int64_t n) {
+  typedef typename MxElem<DT>::type elem;
+  const elem *x = reinterpret_cast<const elem *>(g) + begin;
+  const int len = (int)min((int64_t)kPiece, n - begin);
+  double s = 0.0;
+  bool nan = false;
+  for (int i = 8 * (int)threadIdx.x; i < len; i += 8 * kThreads) {
+    float v[8];
+    load8<DT>(x + i, len - i, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (P == F8LIN_NORM_INF) nan = nan || v[k] != v[k];
+      fold<P>(s, v[k]);
+    }
+  }
+  return nan ? __builtin_nan("") : s;
+}
+
+template <int P>
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const GradTable tab, double *partials, int add) {
+  double s = 0.0;
+  for (int p = blockIdx.x; p < tab.pieces; p += gridDim.x) {
+    const int t = tensor_of(tab, p);
+    const int64_t begin = (int64_t)(p - tab.first[t]) * kPiece;
+    double v;
+    if (tab.in_dtype[t] == F8LIN_BF16) v = piece_norm<P, F8LIN_BF16>(tab.g[t], begin, tab.n[t]);
+    else if (tab.in_dtype[t] == F8LIN_FP16) v = piece_norm<P, F8LIN_FP16>(tab.g[t], begin, tab.n[t]);
+    else v = piece_norm<P, F8LIN_FP32>(tab.g[t], begin, tab.n[t]);
+    s = join<P>(s, v);
+  }
+  s = block_join<P>(s);
+  if (threadIdx.x == 0) partials[blockIdx.x] = add ? join<P>(partials[blockIdx.x], s) : s;
+}
+
+template <int P>
+__device__ __forceinline__ float norm_of(const double *partials) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < kNormGrid; i += kThreads) s = join<P>(s, partials[i]);
+  s = block_join<P>(s);
+  return (float)(P == F8LIN_NORM_2 ? sqrt(s) : s);
+}
+
+template <int P>
+__global__ __launch_bounds__(kThreads) void grad_norm_final_kernel(const double *partials, float *norm) {
+  const float n = norm_of<P>(partials);
+  if (threadIdx.x == 0) norm[0] = n;
+}
+
+template <int DI>
+__device__ __forceinline__ void piece_scale(const void *g, void *out, int out_dtype, int64_t begin, int64_t n, float c) {
+  typedef typename MxElem<DI>::type elem;
+  const elem *x = reinterpret_cast<const elem *>(g) + begin;
+  const int len = (int)min((int64_t)kPiece, n - begin);
+  for (int i = 8 * (int)threadIdx.x; i < len; i += 8 * kThreads) {
+    float v[8];
+    load8<DI>(x + i, len - i, v);
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = f32_to_elem(v[k] * c, out_dtype);
+    if (out_dtype == F8LIN_FP32) {
+      uint32_t *dst = reinterpret_cast<uint32_t *>(out) + begin + i;
+      if (i + 8 <= len) {
+        reinterpret_cast<u32x4_u *>(dst)[0] = u32x4{o[0], o[1], o[2], o[3]};
+        reinterpret_cast<u32x4_u *>(dst)[1] = u32x4{o[4], o[5], o[6], o[7]};
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k < len) dst[k] = o[k];
+      }
+    } else {
+      uint16_t *dst = reinterpret_cast<uint16_t *>(out) + begin + i;
+      if (i + 8 <= len) {
+        *reinterpret_cast<u32x4_u *>(dst) =
+            u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k < len) dst[k] = (uint16_t)o[k];
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable tab, const float *norm, float max_norm) {
+  float c = max_norm / (norm[0] + 1e-6f);
+  c = c > 1.0f ? 1.0f : c;  // (a NaN stays one)
+  for (int p = blockIdx.x; p < tab.pieces; p += gridDim.x) {
+    const int t = tensor_of(tab, p);
+    // a factor of one leaves a tensor scaled in place as it is
+    if (c == 1.0f && tab.g[t] == tab.out[t]) continue;
+    const int64_t begin = (int64_t)(p - tab.first[t]) * kPiece;
+    if (tab.in_dtype[t] == F8LIN_BF16)
+      piece_scale<F8LIN_BF16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+    else if (tab.in_dtype[t] == F8LIN_FP16)
+      piece_scale<F8LIN_FP16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+    else
+      piece_scale<F8LIN_FP32>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+  }
+}
+
+// Fills the table with the next tensors of the list (empty ones left out);
+// returns the index after the last one taken.
+int fill(GradTable &tab, const f8lin_grad *list, int at, int count, bool outs) {
+  int64_t pieces = 0;
+  tab.count = 0;
+  for (; at < count && tab.count < kGradBatch; ++at) {
+    const f8lin_grad &g = list[at];
+    if (g.n == 0) continue;
+    const int64_t np = (g.n + kPiece - 1) / kPiece;
+    if (pieces + np > 0x7FFFFFFF) break;  // (one tensor of 2^40 elements has 2^26 pieces)
+    tab.g[tab.count] = g.g;
+    tab.out[tab.count] = outs ? g.out : nullptr;
+    tab.n[tab.count] = g.n;
+    tab.first[tab.count] = (int)pieces;
+    tab.in_dtype[tab.count] = (uint8_t)g.dtype;
+    tab.out_dtype[tab.count] = (uint8_t)g.out_dtype;
+    ++tab.count;
+    pieces += np;
+  }
+  tab.pieces = (int)pieces;
+  return at;
+}
+
+template <int P>
+void launch_norm(const f8lin_grad *list, int count, double *partials, float *norm, hipStream_t stream) {
+  int at = 0;
+  bool add = false;
+  do {
+    GradTable tab = {};
+    at = fill(tab, list, at, count, false);
+    grad_norm_kernel<P><<<kNormGrid, kThreads, 0, stream>>>(tab, partials, add ? 1 : 0);
+    add = true;
+  } while (at < count);
+  grad_norm_final_kernel<P><<<1, kThreads, 0, stream>>>(partials, norm);
+}
+
+}  // namespace
+
+hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, double *partials, float *norm,
+                            hipStream_t stream) {
+  if (norm_type == F8LIN_NORM_2) launch_norm<F8LIN_NORM_2>(list, count, partials, norm, stream);
+  else if (norm_type == F8LIN_NORM_1) launch_norm<F8LIN_NORM_1>(list, count, partials, norm, stream);
+  else launch_norm<F8LIN_NORM_INF>(list, count, partials, norm, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const f8lin_grad *list, int count, const float *norm, float max_norm, hipStream_t stream) {
+  for (int at = 0; at < count;) {
+    GradTable tab = {};
+    at = fill(tab, list, at, count, true);
+    if (tab.count == 0) continue;
+    const unsigned grid = (unsigned)std::min(tab.pieces, 4096);
+    grad_scale_kernel<<<grid, kThreads, 0, stream>>>(tab, norm, max_norm);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace f8lin

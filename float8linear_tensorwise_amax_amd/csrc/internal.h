@@ -119,4 +119,61 @@ size_t split_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 hipError_t launch_delayed_update(const f8lin_state *states, int n, hipStream_t stream);
 
+// ---- MXFP4 (microscaled 4-bit) operators
+// Up to kMxMaxQuant tensors of one dtype per launch; the launch writes q
+// (blocks along the rows) for all of them or for none (q.codes null), and so
+// for qt (blocks along the columns, transposed).
+constexpr int kMxMaxQuant = 2;
+struct MxQuant {
+  const void *x;
+  int dtype;
+  int64_t rows, cols, ldx;
+  f8lin_mxfp4 q, qt;
+  // if set (needs qt): fp32 column sums over each 128-row tile,
+  // colsum[tile_row * cols + col], for the bias gradient
+  float *colsum;
+};
+hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_t stream);
+constexpr int kMxTile = 128;
+hipError_t launch_mx_dequantize(const f8lin_mxfp4 &q, int64_t rows, int64_t cols, int dtype, void *out,
+                                hipStream_t stream);
+hipError_t launch_mx_dbias(const float *colsum, int64_t tiles, int64_t n, void *db, int dtype, hipStream_t stream);
+
+constexpr int kMxMaxGemms = 2;
+struct MxGemm {
+  f8lin_mxfp4 a, b;
+  void *c;
+  const void *bias;  // (N), added in fp32, or null
+  int64_t M, N, K;
+  int c_dtype, bias_dtype;
+};
+hipError_t launch_mx_gemms(const MxGemm *d, int count, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+// Y = X4 . W4^T with X quantised inside the product's kernel (few rows).
+struct MxLinear {
+  const void *x;
+  int x_dtype;
+  int64_t ldx;
+  f8lin_mxfp4 w;
+  void *y;
+  int y_dtype;
+  const void *bias;
+  int bias_dtype;
+  int64_t M, N, K;
+  int rule;
+};
+bool mx_linear_fused(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream);
+
+// Row stride (bytes) of the codes of an MXFP4 tensor with n columns.
+inline int64_t mx_ld(int64_t n) { return (n + 31) / 32 * 16; }
+
+// ---- Gradient norm and clipping
+constexpr int kGradBatch = 96;       // tensors per launch: their table is a kernel argument
+constexpr int kGradPartials = 1024;  // workgroups of the norm, one binary64 partial result each
+hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, double *partials, float *norm,
+                            hipStream_t stream);
+hipError_t launch_grad_scale(const f8lin_grad *list, int count, const float *norm, float max_norm, hipStream_t stream);
+
 }  // namespace f8lin

@@ -6,9 +6,11 @@ checks dtypes / devices / contiguity, passes raw pointers and the current HIP
 stream, and raises F8linError on a non-zero status.  Importing it fails
 loudly if the library is not built -- there is no fallback.
 """
+import array
 import ctypes
+import math
 import os
-from typing import Optional, Sequence
+from typing import List, Optional, Sequence
 
 import torch
 
@@ -445,3 +447,321 @@ class LinearBuffers:
 
     def states(self):
         return [self.sx, self.sw, self.sdy]
+
+
+# ------------------------------------------------------------------- MXFP4
+
+MX_FLOOR = 0
+MX_CEIL = 1
+_RULE = {"floor": MX_FLOOR, "ceil": MX_CEIL, MX_FLOOR: MX_FLOOR, MX_CEIL: MX_CEIL}
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+MXFP4_BLOCK = 32
+
+
+class MxStruct(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("ld", _i64), ("scale_ld", _i64)]
+
+
+class MxGemmDesc(ctypes.Structure):
+    _fields_ = [("a", MxStruct), ("b", MxStruct), ("c", _vp), ("bias", _vp), ("M", _i64), ("N", _i64), ("K", _i64),
+                ("c_dtype", _int), ("bias_dtype", _int)]
+
+
+class MxFwdArgs(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("x", _vp), ("w", _vp), ("ldx", _i64), ("y", _vp),
+                ("bias", _vp), ("x_dtype", _int), ("w_dtype", _int), ("y_dtype", _int), ("bias_dtype", _int),
+                ("x4", MxStruct), ("x4t", MxStruct), ("w4", MxStruct), ("w4t", MxStruct), ("rule", _int),
+                ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
+
+
+class MxBwdArgs(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("dy", _vp), ("lddy", _i64), ("dx", _vp), ("dw", _vp),
+                ("dbias", _vp), ("dy_dtype", _int), ("dx_dtype", _int), ("dw_dtype", _int), ("dbias_dtype", _int),
+                ("x4t", MxStruct), ("w4t", MxStruct), ("dy4", MxStruct), ("dy4t", MxStruct), ("rule", _int),
+                ("dbias_ws", _vp), ("dbias_ws_bytes", ctypes.c_size_t), ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("g", _vp), ("out", _vp), ("n", _i64), ("dtype", _int), ("out_dtype", _int)]
+
+
+_mxp = ctypes.POINTER(MxStruct)
+_lib.f8lin_mxfp4_ld.argtypes = [_i64]
+_lib.f8lin_mxfp4_ld.restype = _i64
+_lib.f8lin_mxfp4_scale_ld.argtypes = [_i64]
+_lib.f8lin_mxfp4_scale_ld.restype = _i64
+_lib.f8lin_mxfp4_quantize.argtypes = [_vp, _int, _i64, _i64, _i64, _mxp, _mxp, _int, _vp]
+_lib.f8lin_mxfp4_dequantize.argtypes = [_mxp, _i64, _i64, _int, _vp, _vp]
+_lib.f8lin_mxfp4_gemm.argtypes = [ctypes.POINTER(MxGemmDesc), _int, _vp, ctypes.c_size_t, _vp]
+_lib.f8lin_mxfp4_gemm_workspace_bytes.argtypes = [_i64, _i64, _i64]
+_lib.f8lin_mxfp4_gemm_workspace_bytes.restype = ctypes.c_size_t
+_lib.f8lin_mxfp4_forward.argtypes = [ctypes.POINTER(MxFwdArgs), _vp]
+_lib.f8lin_mxfp4_backward.argtypes = [ctypes.POINTER(MxBwdArgs), _vp]
+_lib.f8lin_mxfp4_dbias_workspace_bytes.argtypes = [_i64, _i64]
+_lib.f8lin_mxfp4_dbias_workspace_bytes.restype = ctypes.c_size_t
+_lib.f8lin_grad_workspace_bytes.argtypes = []
+_lib.f8lin_grad_workspace_bytes.restype = ctypes.c_size_t
+_lib.f8lin_grad_norm.argtypes = [_vp, _int, _int, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.f8lin_grad_clip.argtypes = [_vp, _int, _int, ctypes.c_float, _vp, _int, _vp, ctypes.c_size_t, _vp]
+for _name in ("f8lin_mxfp4_quantize", "f8lin_mxfp4_dequantize", "f8lin_mxfp4_gemm", "f8lin_mxfp4_forward",
+              "f8lin_mxfp4_backward", "f8lin_grad_norm", "f8lin_grad_clip"):
+    getattr(_lib, _name).restype = _int
+
+
+def _call(fn, device: torch.device, stream, *args):
+    """Calls fn(*args, stream) with `device` current: the stream is the given one, or the device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(fn(*args, raw))
+    else:
+        _check(fn(*args, raw))
+
+
+def _dense(t: torch.Tensor, what: str, device: torch.device = None) -> int:
+    """Pointer of a contiguous bf16 / fp16 / fp32 GPU tensor (on `device`, if given)."""
+    if not t.is_cuda:
+        raise ValueError("f8lin: tensors must be on the GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"f8lin: {what} is on {t.device}, expected {device}")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"f8lin: {what} must be bfloat16, float16 or float32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"f8lin: {what} must be contiguous")
+    return t.data_ptr()
+
+
+def _dense_ld(t: torch.Tensor, what: str, device: torch.device = None):
+    """(pointer, row stride in elements) of a 2-D bf16 / fp16 / fp32 tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("f8lin: tensors must be on the GPU")
+    if device is not None and t.device != device:
+        raise ValueError(f"f8lin: {what} is on {t.device}, expected {device}")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"f8lin: {what} must be bfloat16, float16 or float32, got {t.dtype}")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if t.numel() and ((cols > 1 and t.stride(1) != 1) or ld < cols):
+        raise ValueError(f"f8lin: {what}'s rows must be contiguous and must not overlap")
+    return t.data_ptr(), max(ld, cols)
+
+
+class MXFP4Tensor:
+    """A (rows, cols) tensor of 4-bit codes with one 8-bit scale per 32
+    consecutive elements of a row (f8lin_mxfp4).
+
+    codes  (rows, >= 16 * ceil(cols / 32)) uint8: two e2m1 codes a byte, the even element in its low half; the
+           codes past cols in the last block are zero
+    scales (rows, >= ceil(cols / 32) rounded up to 16) uint8: e8m0, 2^(byte - 127), 255 for NaN
+    Both with contiguous rows 16 bytes aligned.  A row's codes and scales are views into what you pass."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "_c")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        nb = -(-cols // MXFP4_BLOCK)
+        for name, t, need in (("codes", codes, 16 * nb), ("scales", scales, -(-nb // 16) * 16)):
+            if t.dtype != torch.uint8 or t.dim() != 2:
+                raise TypeError(f"MXFP4Tensor: {name} must be a 2-D uint8 tensor")
+            if not t.is_cuda or t.device != codes.device:
+                raise ValueError("MXFP4Tensor: codes and scales must be on one GPU")
+            if rows and cols and (t.shape[0] != rows or t.shape[1] < need or t.stride(1) != 1):
+                raise ValueError(f"MXFP4Tensor: {name} of a ({rows}, {cols}) tensor must be ({rows}, >= {need}) with "
+                                 "contiguous rows")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        if rows and cols:
+            one = rows == 1  # (a single row has no stride to speak of)
+            self._c = MxStruct(codes.data_ptr(), scales.data_ptr(), codes.shape[1] // 16 * 16 if one else codes.stride(0),
+                               scales.shape[1] // 16 * 16 if one else scales.stride(0))
+        else:
+            self._c = MxStruct(None, None, 0, 0)
+
+    device = property(lambda self: self.codes.device)
+
+    def dequantize(self, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+        """The values this tensor stands for, rounded to `dtype`."""
+        out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
+        mxfp4_dequantize(self, out, stream)
+        return out
+
+
+_NO_MX = MxStruct(None, None, 0, 0)
+
+
+def _mx(t: Optional[MXFP4Tensor], rows: int, cols: int, what: str, device=None) -> MxStruct:
+    if t is None:
+        return _NO_MX
+    if (t.rows, t.cols) != (rows, cols):
+        raise ValueError(f"f8lin: {what} must be a ({rows}, {cols}) MXFP4 tensor, got ({t.rows}, {t.cols})")
+    if device is not None and t.codes.device != device:
+        raise ValueError(f"f8lin: {what} is on {t.codes.device}, expected {device}")
+    return t._c
+
+
+def new_mxfp4(rows: int, cols: int, device="cuda") -> MXFP4Tensor:
+    """An uninitialised MXFP4 tensor with the library's strides."""
+    ld, sld = _lib.f8lin_mxfp4_ld(cols), _lib.f8lin_mxfp4_scale_ld(cols)
+    buf = torch.empty(rows * (ld + sld), dtype=torch.uint8, device=device)
+    return MXFP4Tensor(buf[:rows * ld].view(rows, ld), buf[rows * ld:].view(rows, sld), rows, cols)
+
+
+def mxfp4_quantize(x: torch.Tensor, q: Optional[MXFP4Tensor], qt: Optional[MXFP4Tensor] = None, rule="floor",
+                   stream=None):
+    """x (rows, cols) -> q (rows, cols), blocks along the rows, and / or qt (cols, rows), the transposed tensor with
+    blocks along x's columns.  rule: "floor" (exponent of the largest magnitude) or "ceil" (nothing saturates)."""
+    if x.dim() != 2:
+        raise ValueError("mxfp4_quantize takes a 2-D tensor")
+    rows, cols = x.shape
+    p, ld = _dense_ld(x, "x")
+    a, b = _mx(q, rows, cols, "q", x.device), _mx(qt, cols, rows, "qt", x.device)
+    _call(_lib.f8lin_mxfp4_quantize, x.device, stream, p, _DTYPE[x.dtype], rows, cols, ld, ctypes.byref(a),
+          ctypes.byref(b), _RULE[rule])
+
+
+def mxfp4_dequantize(q: MXFP4Tensor, out: torch.Tensor, stream=None):
+    """out (rows, cols) = the values q stands for."""
+    if tuple(out.shape) != (q.rows, q.cols):
+        raise ValueError("mxfp4_dequantize: shape mismatch")
+    p = _dense(out, "out", q.device)
+    _call(_lib.f8lin_mxfp4_dequantize, out.device, stream, ctypes.byref(q._c), q.rows, q.cols, _DTYPE[out.dtype], p)
+
+
+def mxfp4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.f8lin_mxfp4_gemm_workspace_bytes(M, N, K))
+
+
+def mxfp4_gemm(items, ws: Optional[torch.Tensor] = None, stream=None):
+    """One or two products c (M, N) = a (M, K) . b (N, K)^T (+ bias) in one call; items: (a, b, c) or (a, b, c, bias)
+    tuples, a and b MXFP4Tensors.  ws: optional uint8 scratch (the sum of mxfp4_gemm_workspace_bytes)."""
+    arr = (MxGemmDesc * max(1, len(items)))()
+    dev = None
+    for i, item in enumerate(items):
+        a, b, c = item[:3]
+        bias = item[3] if len(item) > 3 else None
+        M, K, N = a.rows, a.cols, b.rows
+        dev = c.device if dev is None else dev
+        if b.cols != K or tuple(c.shape) != (M, N) or (bias is not None and tuple(bias.shape) != (N,)):
+            raise ValueError("mxfp4_gemm: shape mismatch")
+        arr[i] = MxGemmDesc(_mx(a, M, K, "a", dev), _mx(b, N, K, "b", dev), _dense(c, "c", dev),
+                            None if bias is None else _dense(bias, "bias", dev), M, N, K, _DTYPE[c.dtype],
+                            0 if bias is None else _DTYPE[bias.dtype])
+    if dev is None:
+        raise ValueError("mxfp4_gemm: no products given")
+    _call(_lib.f8lin_mxfp4_gemm, dev, stream, arr, len(items), _ptr(ws), _nbytes(ws))
+
+
+def mxfp4_forward(x, w, y, x4: Optional[MXFP4Tensor], w4: MXFP4Tensor, x4t=None, w4t=None, bias=None, rule="floor",
+                  ws: Optional[torch.Tensor] = None, stream=None):
+    """y (M, N) = x4 . w4^T (+ bias).  w (N, K): quantised into w4 (and w4t); None: w4 already holds the weight.
+    x4 is scratch unless x4t is asked for; ws: optional scratch of mxfp4_gemm_workspace_bytes(M, N, K)."""
+    M, K = x.shape
+    N = w4.rows
+    dev = x.device
+    if tuple(y.shape) != (M, N) or (w is not None and tuple(w.shape) != (N, K)) or \
+            (bias is not None and tuple(bias.shape) != (N,)):
+        raise ValueError("mxfp4_forward: shape mismatch")
+    px, ldx = _dense_ld(x, "x")
+    a = MxFwdArgs(M, N, K, px, None if w is None else _dense(w, "w", dev), ldx, _dense(y, "y", dev),
+                  None if bias is None else _dense(bias, "bias", dev), _DTYPE[x.dtype],
+                  0 if w is None else _DTYPE[w.dtype], _DTYPE[y.dtype], 0 if bias is None else _DTYPE[bias.dtype],
+                  _mx(x4, M, K, "x4", dev), _mx(x4t, K, M, "x4t", dev), _mx(w4, N, K, "w4", dev),
+                  _mx(w4t, K, N, "w4t", dev), _RULE[rule], _ptr(ws), _nbytes(ws))
+    _call(_lib.f8lin_mxfp4_forward, dev, stream, ctypes.byref(a))
+
+
+def mxfp4_dbias_workspace_bytes(M: int, N: int) -> int:
+    return int(_lib.f8lin_mxfp4_dbias_workspace_bytes(M, N))
+
+
+def mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, dbias=None, dbias_ws=None, rule="floor",
+                   ws: Optional[torch.Tensor] = None, stream=None):
+    """dx (M, K), dw (N, K) and dbias (N) -- each may be None -- of the layer whose forward left x4t (K, M) and
+    w4t (K, N).  dy4 (M, N; for dx) and dy4t (N, M; for dw or dbias) receive dY's two layouts; dbias_ws: float32
+    scratch of mxfp4_dbias_workspace_bytes(M, N)."""
+    M, N = dy.shape
+    K = (dx if dx is not None else dw).shape[1] if dx is not None or dw is not None else 0
+    dev = dy.device
+    if (dx is not None and tuple(dx.shape) != (M, K)) or (dw is not None and tuple(dw.shape) != (N, K)) or \
+            (dbias is not None and tuple(dbias.shape) != (N,)):
+        raise ValueError("mxfp4_backward: shape mismatch")
+    p, ld = _dense_ld(dy, "dy")
+    opt = lambda t, what: None if t is None else _dense(t, what, dev)  # noqa: E731
+    dt = lambda t: 0 if t is None else _DTYPE[t.dtype]  # noqa: E731
+    a = MxBwdArgs(M, N, K, p, ld, opt(dx, "dx"), opt(dw, "dw"), opt(dbias, "dbias"), _DTYPE[dy.dtype], dt(dx), dt(dw),
+                  dt(dbias), _mx(x4t if dw is not None else None, K, M, "x4t", dev),
+                  _mx(w4t if dx is not None else None, K, N, "w4t", dev), _mx(dy4, M, N, "dy4", dev),
+                  _mx(dy4t, N, M, "dy4t", dev), _RULE[rule], _ptr(dbias_ws, torch.float32), _nbytes(dbias_ws),
+                  _ptr(ws), _nbytes(ws))
+    _call(_lib.f8lin_mxfp4_backward, dev, stream, ctypes.byref(a))
+
+
+# --------------------------------------------------- gradient norm and clipping
+
+_NORM = {2.0: 0, 1.0: 1, math.inf: 2}
+
+
+def grad_workspace_bytes() -> int:
+    return int(_lib.f8lin_grad_workspace_bytes())
+
+
+def new_grad_workspace(device="cuda") -> torch.Tensor:
+    """Scratch for grad_norm / grad_clip (uninitialised; one for each call that may overlap another in time)."""
+    return torch.empty(grad_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def _is_dense(t: torch.Tensor) -> bool:
+    """Whether t covers numel() consecutive elements of memory exactly once, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def _norm_type(norm_type) -> int:
+    code = _NORM.get(float(norm_type))
+    if code is None:
+        raise ValueError(f"f8lin: norm_type must be 2, 1 or inf, got {norm_type!r}")
+    return code
+
+
+def _grad_table(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]], device: torch.device):
+    """The list as the C ABI takes it: four 64-bit words a tensor (g, out, n, dtype | out_dtype << 32)."""
+    words: List[int] = []
+    outs = grads if outs is None else outs
+    if len(outs) != len(grads):
+        raise ValueError("f8lin: as many outputs as gradients")
+    for g, o in zip(grads, outs):
+        dt, odt = _DTYPE.get(g.dtype), _DTYPE.get(o.dtype)
+        if dt is None or odt is None:
+            raise TypeError("f8lin: gradients must be bfloat16, float16 or float32")
+        if g.device != device or o.device != device:
+            raise ValueError(f"f8lin: gradients must all be on {device}")
+        if g.layout is not torch.strided or not _is_dense(g) or \
+                (o is not g and (o.shape != g.shape or (g.numel() > 0 and o.stride() != g.stride()))):
+            raise ValueError("f8lin: gradients must be dense, and an output laid out as its gradient")
+        words += (g.data_ptr(), o.data_ptr(), g.numel(), dt | odt << 32)
+    return array.array("q", words)
+
+
+def grad_norm(grads: Sequence[torch.Tensor], out: torch.Tensor, ws: torch.Tensor, norm_type: float = 2.0, stream=None):
+    """out[0] (float32) = the norm of all gradients' elements as one vector; norm_type 2, 1 or inf."""
+    code = _norm_type(norm_type)
+    tab = _grad_table(grads, None, out.device)
+    _call(_lib.f8lin_grad_norm, out.device, stream, tab.buffer_info()[0], len(grads), code,
+          _ptr(out, torch.float32), _ptr(ws), _nbytes(ws))
+
+
+def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor, ws: Optional[torch.Tensor],
+              norm_type: float = 2.0, outs: Optional[Sequence[torch.Tensor]] = None, norm_given: bool = False,
+              stream=None):
+    """norm[0] (float32) = the norm as grad_norm gives it (norm_given: it is read instead), then every gradient times
+    min(1, max_norm / (norm + 1e-6)), in place or into outs (laid out alike; any of the three types)."""
+    code = _norm_type(norm_type)
+    tab = _grad_table(grads, outs, norm.device)
+    _call(_lib.f8lin_grad_clip, norm.device, stream, tab.buffer_info()[0], len(grads), code, float(max_norm),
+          _ptr(norm, torch.float32), 1 if norm_given else 0, _ptr(ws), _nbytes(ws))

@@ -23,6 +23,14 @@ registered buffers, so model.state_dict() / load_state_dict() save and
 restore it and model.to() moves it; which delayed roles have taken their
 first step is saved as the module's extra state.
 
+MXFP4.  mxfp4_linear / MXFP4Linear / convert_to_mxfp4_training are the same
+layer with 4-bit operands (one 8-bit scale per 32 values along each product's
+contraction, so no scaling state); any feature and token counts, in bf16,
+fp16 or fp32.  freeze_mxfp4 keeps only the 4-bit weights, for serving.
+
+Gradient clipping.  clip_grad_norm_ (in place), clip_grads (into new tensors)
+and get_grad_norm work on a list of gradients after backward.
+
 Delayed scaling, per role:
   * the scale comes from the largest amax of the previous steps (the
     history), and the cast folds this step's amax into the state;
@@ -37,10 +45,11 @@ Delayed scaling, per role:
     none for dy), and only those roles count as initialised.
 """
 from dataclasses import dataclass, field
-from typing import Dict, Optional
+from typing import Dict, Iterable, List, Optional, Tuple, Union
 
 import torch
 import torch.nn as nn
+from torch.autograd.function import once_differentiable
 
 from . import f8lin
 
@@ -325,3 +334,226 @@ def sync_float8_amax_and_scale_history(module: nn.Module, check: bool = False) -
         if bad:
             raise RuntimeError(f"sync_float8_amax_and_scale_history: {len(bad)} corrupt delayed-scaling "
                                f"state(s) (invalid count/pos), left unchanged: state indices {bad}")
+
+
+# ------------------------------------------------------------------- MXFP4
+
+def _workspace(n: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t as a 2-D tensor with contiguous rows (a copy only where its strides need one)."""
+    t = t.reshape(-1, t.shape[-1])
+    if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+        t = t.contiguous()
+    return t
+
+
+class _MXFP4LinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, rule):
+        M, K = x.shape
+        N = weight.shape[0]
+        dev = x.device
+        w = weight.contiguous()
+        y = torch.empty((M, N), dtype=x.dtype, device=dev)
+        x4, w4 = f8lin.new_mxfp4(M, K, dev), f8lin.new_mxfp4(N, K, dev)
+        # the transposed copies only for the gradients that will be asked for
+        x4t = f8lin.new_mxfp4(K, M, dev) if ctx.needs_input_grad[1] else None
+        w4t = f8lin.new_mxfp4(K, N, dev) if ctx.needs_input_grad[0] else None
+        ws = _workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), dev)
+        f8lin.mxfp4_forward(x, w, y, x4, w4, x4t, w4t, None if bias is None else bias.contiguous(), rule, ws)
+        saved = [t for q in (x4t, w4t) if q is not None for t in (q.codes, q.scales)]
+        ctx.save_for_backward(*saved)
+        ctx.args = (M, N, K, rule, x.dtype, weight.dtype, None if bias is None else bias.dtype)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        M, N, K, rule, x_dtype, w_dtype, b_dtype = ctx.args
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        dev = dy.device
+        saved = list(ctx.saved_tensors)
+        x4t = f8lin.MXFP4Tensor(saved.pop(0), saved.pop(0), K, M) if need_w else None
+        w4t = f8lin.MXFP4Tensor(saved.pop(0), saved.pop(0), K, N) if need_x else None
+        dy = _rows(dy)
+        dx = torch.empty((M, K), dtype=x_dtype, device=dev) if need_x else None
+        dw = torch.empty((N, K), dtype=w_dtype, device=dev) if need_w else None
+        db = db_ws = None
+        if need_b:
+            db = torch.empty((N,), dtype=b_dtype, device=dev)
+            db_ws = torch.empty(max(1, f8lin.mxfp4_dbias_workspace_bytes(M, N) // 4), dtype=torch.float32, device=dev)
+        dy4 = f8lin.new_mxfp4(M, N, dev) if need_x else None
+        dy4t = f8lin.new_mxfp4(N, M, dev) if need_w or need_b else None
+        ws = _workspace((f8lin.mxfp4_gemm_workspace_bytes(M, K, N) if need_x else 0)
+                        + (f8lin.mxfp4_gemm_workspace_bytes(N, K, M) if need_w else 0), dev)
+        f8lin.mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, db, db_ws, rule, ws)
+        return dx, dw, db, None
+
+
+def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor], bias: Optional[torch.Tensor] = None,
+                 rule: str = "floor") -> torch.Tensor:
+    """y = x . weight^T (+ bias) with both operands of the product in MXFP4; y has x's dtype.
+
+    weight a (out, in) tensor: it is quantised by the call, and the call is differentiable in x, weight and bias
+    (the two backward products run in MXFP4 too, on operands quantised along their own contractions).
+    weight an f8lin.MXFP4Tensor of (out, in): for serving; x must not need a gradient."""
+    if not x.is_cuda:
+        raise RuntimeError("mxfp4_linear runs on the GPU only (libf8lin has no CPU path)")
+    packed = isinstance(weight, f8lin.MXFP4Tensor)
+    N, K = (weight.rows, weight.cols) if packed else weight.shape
+    if x.dim() < 1 or x.shape[-1] != K:
+        raise ValueError(f"expected last dimension {K}, got {tuple(x.shape)}")
+    lead = x.shape[:-1]
+    # (an empty last dimension leaves reshape nothing to infer the rows from)
+    x2 = _rows(x) if x.numel() else x.reshape(lead.numel(), K)
+    if not packed:
+        return _MXFP4LinearFn.apply(x2, weight, bias, rule).reshape(*lead, N)
+    if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):
+        raise RuntimeError("mxfp4_linear: a quantised weight has no backward; call it under torch.no_grad()")
+    M = x2.shape[0]
+    y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    f8lin.mxfp4_forward(x2, None, y, f8lin.new_mxfp4(M, K, x.device), weight,
+                        bias=None if bias is None else bias.contiguous(), rule=rule,
+                        ws=_workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), x.device))
+    return y.reshape(*lead, N)
+
+
+class MXFP4Linear(nn.Module):
+    """nn.Linear whose products run in MXFP4 (mxfp4_linear).  freeze() replaces the weight by its 4-bit form, kept in
+    the buffers weight_codes and weight_scales, after which the layer only serves."""
+
+    def __init__(self, in_features: int, out_features: int, rule: str = "floor", weight: Optional[torch.Tensor] = None,
+                 device=None, dtype=torch.bfloat16, bias=False):
+        super().__init__()
+        if rule not in ("floor", "ceil"):
+            raise ValueError(f"rule must be 'floor' or 'ceil', got {rule!r}")
+        self.in_features, self.out_features, self.rule = in_features, out_features, rule
+        if weight is None:
+            weight = torch.empty((out_features, in_features), device=device, dtype=dtype)
+            nn.init.kaiming_uniform_(weight, a=5 ** 0.5)
+        if tuple(weight.shape) != (out_features, in_features):
+            raise ValueError("weight must have shape (out_features, in_features)")
+        self.weight = weight if isinstance(weight, nn.Parameter) else nn.Parameter(weight)
+        if isinstance(bias, torch.Tensor):
+            if tuple(bias.shape) != (out_features,):
+                raise ValueError("bias must have shape (out_features,)")
+            self.bias = bias if isinstance(bias, nn.Parameter) else nn.Parameter(bias)
+        elif bias:
+            self.bias = nn.Parameter(torch.zeros(out_features, device=self.weight.device, dtype=self.weight.dtype))
+        else:
+            self.register_parameter("bias", None)
+        self.register_buffer("weight_codes", None)
+        self.register_buffer("weight_scales", None)
+
+    @property
+    def frozen(self) -> bool:
+        return self.weight_codes is not None
+
+    @torch.no_grad()
+    def freeze(self) -> "MXFP4Linear":
+        """Quantises the weight once and drops its full form."""
+        if not self.frozen:
+            q = f8lin.new_mxfp4(self.out_features, self.in_features, self.weight.device)
+            f8lin.mxfp4_quantize(self.weight.detach().contiguous(), q, None, self.rule)
+            self.weight_codes, self.weight_scales = q.codes.contiguous(), q.scales.contiguous()
+            self.weight = None
+        return self
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if not self.frozen:
+            return mxfp4_linear(x, self.weight, self.bias, self.rule)
+        q = f8lin.MXFP4Tensor(self.weight_codes, self.weight_scales, self.out_features, self.in_features)
+        with torch.no_grad():
+            return mxfp4_linear(x, q, self.bias, self.rule)
+
+    def extra_repr(self):
+        return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "
+                f"rule={self.rule}, frozen={self.frozen}")
+
+
+def convert_to_mxfp4_training(module: nn.Module, rule: str = "floor", module_filter_fn=None) -> nn.Module:
+    """Replaces every nn.Linear (that module_filter_fn(fqn, module) accepts, if given) by an MXFP4Linear sharing its
+    weight and bias Parameters.  Returns the module."""
+    if type(module) is nn.Linear:
+        raise ValueError("convert the parent module, not a bare nn.Linear")
+    for fqn, child in list(module.named_modules()):
+        if type(child) is nn.Linear and (module_filter_fn is None or module_filter_fn(fqn, child)):
+            parent, _, name = fqn.rpartition(".")
+            setattr(module.get_submodule(parent), name,
+                    MXFP4Linear(child.in_features, child.out_features, rule, weight=child.weight,
+                                bias=child.bias if child.bias is not None else False))
+    return module
+
+
+def freeze_mxfp4(module: nn.Module) -> nn.Module:
+    """freeze() on every MXFP4Linear of the module: 4-bit weights only, for serving.  Returns the module."""
+    for m in module.modules():
+        if isinstance(m, MXFP4Linear):
+            m.freeze()
+    return module
+
+
+# --------------------------------------------------- gradient norm and clipping
+
+def _dense_copy(g: torch.Tensor) -> torch.Tensor:
+    return g if f8lin._is_dense(g) else g.contiguous()
+
+
+def _gradients(parameters: Union[torch.Tensor, Iterable[torch.Tensor]]) -> List[torch.Tensor]:
+    params = [parameters] if isinstance(parameters, torch.Tensor) else parameters
+    return [p.grad for p in params if p.grad is not None]
+
+
+def get_grad_norm(grads: Iterable[torch.Tensor], norm_type: float = 2.0) -> torch.Tensor:
+    """The norm (2, 1 or inf) of all the gradients' elements as one vector: a float32 scalar on their GPU."""
+    grads = [_dense_copy(g) for g in grads]
+    if not grads:
+        return torch.zeros((), dtype=torch.float32)
+    dev = grads[0].device
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    f8lin.grad_norm(grads, norm, f8lin.new_grad_workspace(dev), norm_type)
+    return norm[0]
+
+
+def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0,
+               out_dtype: Optional[torch.dtype] = None) -> Tuple[torch.Tensor, List[torch.Tensor]]:
+    """(norm, clipped): the gradients times min(1, max_norm / (norm + 1e-6)) in new tensors (of out_dtype, e.g.
+    float32 for a full-precision optimiser behind 16-bit gradients; default their own)."""
+    grads = [_dense_copy(g) for g in grads]
+    if not grads:
+        return torch.zeros((), dtype=torch.float32), []
+    dev = grads[0].device
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    outs = [torch.empty_like(g, dtype=out_dtype) for g in grads]
+    f8lin.grad_clip(grads, max_norm, norm, f8lin.new_grad_workspace(dev), norm_type, outs)
+    return norm[0], outs
+
+
+@torch.no_grad()
+def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float, norm_type: float = 2.0,
+                    error_if_nonfinite: bool = False) -> torch.Tensor:
+    """Scales the parameters' gradients in place so that the norm of all of them together is at most max_norm;
+    returns the norm they had.  A NaN norm makes every gradient NaN; error_if_nonfinite=True reads the norm back
+    instead (a host synchronisation) and raises before anything is scaled."""
+    grads = _gradients(parameters)
+    if not grads:
+        return torch.zeros((), dtype=torch.float32)
+    flat = [_dense_copy(g) for g in grads]
+    dev = flat[0].device
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    ws = f8lin.new_grad_workspace(dev)
+    if error_if_nonfinite:
+        f8lin.grad_norm(flat, norm, ws, norm_type)
+        if not torch.isfinite(norm).item():
+            raise RuntimeError(f"the norm of order {norm_type} of the gradients is not finite, so they cannot be "
+                               "clipped")
+        f8lin.grad_clip(flat, max_norm, norm, None, norm_type, norm_given=True)
+    else:
+        f8lin.grad_clip(flat, max_norm, norm, ws, norm_type)
+    for g, f in zip(grads, flat):
+        if f is not g:
+            g.copy_(f)
+    return norm[0]

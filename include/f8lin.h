@@ -372,6 +372,154 @@ int f8lin_backward_noalloc(const f8lin_bwd_args *args, void *stream);
  * state), EALIGN. */
 int f8lin_delayed_update(const f8lin_state *states, int n_states, int32_t *status, void *stream);
 
+/* ===================================================================== MXFP4
+ * Microscaled 4-bit floating point (the OCP microscaling format MXFP4): 32
+ * consecutive values along a product's contraction form a block of 32 e2m1
+ * codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) that share one e8m0 scale
+ * byte e, standing for 2^(e - 127) (255: NaN).  The matrix cores apply the
+ * scales themselves, at twice the fp8 rate.
+ *    m    = max |x| of the block
+ *    FLOOR: e - 127 = floor(log2 m) - 2
+ *    CEIL : e - 127 = the smallest integer with m <= 6 * 2^(e - 127)
+ *           (both clamped to e >= 0; m = 0 gives e = 0)
+ *    code = RNE_sat(x * 2^(127 - e)): ties to the even mantissa, magnitudes
+ *           above 6 become 6 (FLOOR rule only), the sign of zero is kept
+ *    A block that holds an Inf or a NaN gets e = 255 and zero codes: all 32
+ *    of its values read back as NaN, and so does every product it enters.
+ * Unlike the fp8 entry points, every size may be odd and data may be bf16,
+ * fp16 or fp32 with a row stride. */
+typedef enum { F8LIN_BF16 = 0, F8LIN_FP16 = 1, F8LIN_FP32 = 2 } f8lin_dtype;
+typedef enum { F8LIN_MX_FLOOR = 0, F8LIN_MX_CEIL = 1 } f8lin_mx_rule;
+
+/* A (rows, cols) MXFP4 tensor with blocks along its rows (device pointers,
+ * caller-owned, both 16-byte aligned).  Row r's codes start at codes + r * ld:
+ * 16 bytes per block, the even element of a byte in its low half; the codes
+ * of the last block past cols are zero.  Its scale bytes start at
+ * scales + r * scale_ld; bytes past the last block may hold anything.
+ * ld and scale_ld: multiples of 16, at least 16 * ceil(cols / 32) and
+ * ceil(cols / 32) rounded up to 16; at most 2^22. */
+typedef struct {
+  uint8_t *codes, *scales;
+  int64_t ld, scale_ld;
+} f8lin_mxfp4;
+
+/* The strides this library lays new tensors out with (bytes; 0 for cols < 0). */
+int64_t f8lin_mxfp4_ld(int64_t cols);
+int64_t f8lin_mxfp4_scale_ld(int64_t cols);
+
+/* x (rows, cols) -> q (rows, cols) with blocks along the rows, and / or qt
+ * (cols, rows), the transposed tensor with blocks along x's columns, in one
+ * pass over x.  A layout whose codes pointer is NULL is not written (one of
+ * the two must be; both may be NULL only if x is empty).  dtype:
+ * f8lin_dtype; ldx: x's row stride in elements (0: cols); x needs its
+ * element's alignment only.  Errors: EINVAL (null pointers, bad enum, outputs
+ * overlapping), ESHAPE (a dimension negative or above 2^22, more than 2^40
+ * elements, a stride too small or not a multiple of 16), EALIGN. */
+int f8lin_mxfp4_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx, const f8lin_mxfp4 *q,
+                         const f8lin_mxfp4 *qt, int rule, void *stream);
+
+/* The values q stands for: out (rows, cols) contiguous, of dtype `dtype`,
+ * rounded to nearest even where that type cannot hold them. */
+int f8lin_mxfp4_dequantize(const f8lin_mxfp4 *q, int64_t rows, int64_t cols, int dtype, void *out, void *stream);
+
+/* C (M, N) = A (M, K) . B (N, K)^T (+ bias (N), added in fp32 to every row):
+ * MXFP4 operands with blocks along K, exact products, fp32 accumulation, one
+ * rounding to c_dtype.  bias may be NULL.  K = 0 gives C = bias (or 0).
+ * count (1 .. F8LIN_MXFP4_MAX_BATCH) products in one call.
+ * ws: optional scratch (NULL = none) of f8lin_mxfp4_gemm_workspace_bytes
+ * bytes per product, 16-byte aligned, no initialisation, with which a product
+ * of few output tiles and a long contraction is split along K; its partial
+ * sums meet in a fixed order (the same bits on every run). */
+#define F8LIN_MXFP4_MAX_BATCH 2
+typedef struct {
+  f8lin_mxfp4 a, b;
+  void *c;
+  const void *bias;
+  int64_t M, N, K;
+  int c_dtype, bias_dtype;
+} f8lin_mxfp4_gemm_desc;
+int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *ws, size_t ws_bytes, void *stream);
+size_t f8lin_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Forward of a linear layer with 4-bit operands: Y = X4 . W4^T (+ bias).
+ * w != NULL (training): X and W are quantised, x4 / w4 for this product and,
+ * where their codes are not NULL, x4t / w4t for the backward.
+ * w == NULL (serving, or a weight quantised before): w4 already holds W and
+ * w4t is not touched.  With few rows and no x4t the quantisation of X then
+ * happens inside the product's kernel and x4 is left unwritten: x4 is scratch
+ * unless x4t is asked for.
+ * Errors as above; nothing is launched on error. */
+typedef struct {
+  int64_t M, N, K;
+  const void *x, *w; /* (M, K) with row stride ldx; (N, K) contiguous, or NULL */
+  int64_t ldx;       /* elements; 0: K */
+  void *y;           /* (M, N) */
+  const void *bias;  /* (N) or NULL */
+  int x_dtype, w_dtype, y_dtype, bias_dtype;
+  f8lin_mxfp4 x4, x4t, w4, w4t; /* (M, K), (K, M), (N, K), (K, N) */
+  int rule;
+  void *ws; /* optional: f8lin_mxfp4_gemm_workspace_bytes(M, N, K) */
+  size_t ws_bytes;
+} f8lin_mxfp4_fwd_args;
+int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *args, void *stream);
+
+/* Its backward: dY (M, N) is quantised along N (dy4) and along M (dy4t), then
+ *   dX (M, K) = dY4 . W4t^T  (contraction over N)
+ *   dW (N, K) = dY4t . X4t^T (contraction over M)
+ *   dbias (N) = column sums of dY (not quantised; fp32 in a fixed order)
+ * dx, dw and dbias may each be NULL (not computed; dx without dw needs no
+ * x4t / dy4t, dw without dx no w4t / dy4).  dbias needs dbias_ws of
+ * f8lin_mxfp4_dbias_workspace_bytes(M, N) bytes. */
+typedef struct {
+  int64_t M, N, K;
+  const void *dy;
+  int64_t lddy; /* elements; 0: N */
+  void *dx, *dw, *dbias;
+  int dy_dtype, dx_dtype, dw_dtype, dbias_dtype;
+  f8lin_mxfp4 x4t, w4t, dy4, dy4t; /* (K, M), (K, N), (M, N), (N, M) */
+  int rule;
+  float *dbias_ws;
+  size_t dbias_ws_bytes;
+  void *ws; /* optional: f8lin_mxfp4_gemm_workspace_bytes(M, K, N) + ...(N, K, M) */
+  size_t ws_bytes;
+} f8lin_mxfp4_bwd_args;
+int f8lin_mxfp4_backward(const f8lin_mxfp4_bwd_args *args, void *stream);
+size_t f8lin_mxfp4_dbias_workspace_bytes(int64_t M, int64_t N);
+
+/* ============================================== gradient norm and clipping
+ * The norm of all elements of a list of tensors as if they were one vector:
+ *   NORM_2: sqrt(sum g^2)   NORM_1: sum |g|   NORM_INF: max |g|
+ * summed in binary64 in a fixed order (the same bits on every run), rounded
+ * once to fp32.  A NaN element gives a NaN norm; an empty list gives 0. */
+typedef enum { F8LIN_NORM_2 = 0, F8LIN_NORM_1 = 1, F8LIN_NORM_INF = 2 } f8lin_norm;
+typedef struct {
+  const void *g; /* n contiguous elements, aligned to their element */
+  void *out;     /* f8lin_grad_clip: n elements (may be g itself, if the dtypes agree); f8lin_grad_norm: unused */
+  int64_t n;
+  int dtype, out_dtype; /* f8lin_dtype */
+} f8lin_grad;
+
+/* norm_out[0] = the norm.  list is a host array of count >= 0 entries, read
+ * before the call returns.  ws: f8lin_grad_workspace_bytes() bytes, 16-byte
+ * aligned, no initialisation needed; calls that overlap in time need one
+ * each.  Errors: EINVAL (null pointers, bad enum, count < 0, norm_out or an
+ * output overlapping anything else), ESHAPE (n negative or above 2^40),
+ * EALIGN, EWORKSPACE, EHIP (a launch failed, or no host memory for the
+ * overlap check). */
+int f8lin_grad_norm(const f8lin_grad *list, int count, int norm_type, float *norm_out, void *ws, size_t ws_bytes,
+                    void *stream);
+size_t f8lin_grad_workspace_bytes(void);
+
+/* The norm as above (norm_given nonzero: norm[0] already holds it, e.g. one
+ * summed over the shards of a distributed model, and is only read; ws may be
+ * NULL), then for every tensor
+ *   out = c * g,  c = min(1, max_norm / (norm + 1e-6))
+ * in fp32, rounded once to out_dtype.  c is NaN with a NaN norm and 0 with an
+ * infinite one (so Inf elements become NaN, the others 0).  max_norm >= 0.
+ * A tensor may not be listed twice. */
+int f8lin_grad_clip(const f8lin_grad *list, int count, int norm_type, float max_norm, float *norm, int norm_given,
+                    void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,270 @@
+"""Host-side validation of the MXFP4 and gradient-clipping entry points (every call here is refused, or has nothing
+to launch), the module swap, and the plain oracle's own pins."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+import torch.nn as nn
+
+from float8linear_tensorwise_amax_amd import f8lin
+from float8linear_tensorwise_amax_amd import module as m
+from oracle import mxfp4 as mx
+
+OK, EINVAL, ESHAPE, EALIGN, EWORKSPACE = 0, 1, 2, 3, 4
+MB = 1 << 20
+A = 0x100000000  # fake, never-dereferenced addresses, 16 MiB apart below
+SL = 16 * MB
+BF16, FP16, FP32 = 0, 1, 2
+lib = f8lin._lib
+Mx, Fwd, Bwd, Desc, Grad = f8lin.MxStruct, f8lin.MxFwdArgs, f8lin.MxBwdArgs, f8lin.MxGemmDesc, f8lin.Grad
+
+
+def mxs(i, rows, cols):
+    """A well-formed MXFP4 tensor at slot i."""
+    return Mx(A + i * SL, A + i * SL + 8 * MB, lib.f8lin_mxfp4_ld(cols), lib.f8lin_mxfp4_scale_ld(cols))
+
+
+def moved(q, **kw):
+    c = Mx(q.codes, q.scales, q.ld, q.scale_ld)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def test_strides():
+    for n, ld, sld in ((0, 0, 0), (1, 16, 16), (32, 16, 16), (33, 32, 16), (512, 256, 16), (513, 272, 32),
+                       (4096, 2048, 128), (1600, 800, 64), (-1, 0, 0)):
+        assert (lib.f8lin_mxfp4_ld(n), lib.f8lin_mxfp4_scale_ld(n)) == (ld, sld), n
+    # rows of whole 32 KiB are set apart
+    assert lib.f8lin_mxfp4_ld(65536) >= 32768 and lib.f8lin_mxfp4_ld(65536) % 16 == 0
+
+
+def test_quantize_rejections():
+    f = lib.f8lin_mxfp4_quantize
+    q, qt = mxs(1, 40, 100), mxs(2, 100, 40)
+    r = ctypes.byref
+
+    def call(x=A, dt=BF16, rows=40, cols=100, ld=0, q=q, qt=qt, rule=0):
+        return f(x, dt, rows, cols, ld, None if q is None else r(q), None if qt is None else r(qt), rule, None)
+
+    assert call(dt=3) == EINVAL and call(dt=-1) == EINVAL and call(rule=2) == EINVAL
+    assert call(rows=-1) == ESHAPE and call(cols=(1 << 22) + 1) == ESHAPE
+    assert call(rows=1 << 21, cols=1 << 21) == ESHAPE                      # more than 2^40 elements
+    assert call(ld=99) == ESHAPE                                            # rows that overlap
+    assert call(x=None) == EINVAL and call(x=A + 1) == EALIGN and call(x=A + 2, dt=FP32) == EALIGN
+    assert call(q=None, qt=None) == EINVAL
+    assert call(q=moved(q, codes=q.codes + 8)) == EALIGN
+    assert call(q=moved(q, scales=None)) == EINVAL
+    assert call(q=moved(q, ld=q.ld - 16)) == ESHAPE and call(q=moved(q, ld=q.ld + 8)) == ESHAPE
+    assert call(qt=moved(qt, scale_ld=0)) == ESHAPE and call(qt=moved(qt, scale_ld=24)) == ESHAPE
+    assert call(q=moved(q, codes=A + 1024)) == EINVAL                       # inside x
+    assert call(qt=moved(qt, codes=q.codes + 64)) == EINVAL                 # the two layouts overlap
+    assert call(qt=moved(qt, scales=q.scales)) == EINVAL
+    assert call(ld=1 << 20, q=moved(q, codes=A + SL)) == EINVAL             # x's stride reaches q
+    assert call(rows=0) == OK and call(cols=0, x=None, q=None, qt=None) == OK
+
+
+def test_dequantize_rejections():
+    f = lib.f8lin_mxfp4_dequantize
+    q = mxs(1, 40, 100)
+    assert f(None, 40, 100, BF16, A, None) == EINVAL
+    assert f(ctypes.byref(q), 40, 100, 5, A, None) == EINVAL
+    assert f(ctypes.byref(q), 40, 1 << 23, BF16, A, None) == ESHAPE
+    assert f(ctypes.byref(q), 40, 100, FP32, A + 2, None) == EALIGN
+    assert f(ctypes.byref(q), 40, 100, FP32, q.codes - 64, None) == EINVAL
+    assert f(ctypes.byref(q), 0, 100, FP32, None, None) == OK
+
+
+def test_gemm_rejections():
+    f = lib.f8lin_mxfp4_gemm
+
+    def desc(**kw):
+        d = Desc(mxs(1, 40, 100), mxs(2, 50, 100), A, None, 40, 50, 100, BF16, BF16)
+        for k, v in kw.items():
+            setattr(d, k, v)
+        return d
+
+    def call(*ds, ws=None, n=0, count=None):
+        return f((Desc * max(1, len(ds)))(*ds), len(ds) if count is None else count, ws, n, None)
+
+    assert f(None, 1, None, 0, None) == EINVAL
+    assert call(count=0) == EINVAL and call(desc(), desc(), desc()) == EINVAL
+    assert call(desc(M=-1)) == ESHAPE and call(desc(K=1 << 23)) == ESHAPE
+    assert call(desc(c=None)) == EINVAL and call(desc(c=A + 1)) == EALIGN and call(desc(c_dtype=7)) == EINVAL
+    assert call(desc(bias=A + 4 * SL, bias_dtype=9)) == EINVAL and call(desc(bias=A + 4 * SL + 1)) == EALIGN
+    assert call(desc(bias=A + 64)) == EINVAL                                # the bias inside C
+    assert call(desc(a=moved(mxs(1, 40, 100), ld=48))) == ESHAPE
+    assert call(desc(b=moved(mxs(2, 50, 100), codes=None))) == EINVAL
+    assert call(desc(c=A + SL)) == EINVAL                                   # C is A's codes
+    assert call(desc(), desc(a=mxs(3, 40, 100))) == EINVAL                  # both write one C
+    assert call(desc(), desc(c=A + 2 * SL)) == EINVAL                       # the second's C is the first's B
+    assert call(desc(), ws=A + 5 * SL + 8, n=64) == EALIGN
+    assert call(desc(), ws=A + 2 * SL, n=64) == EINVAL                      # scratch over B
+    assert call(desc(M=0), desc(N=0)) == OK
+    g = lib.f8lin_mxfp4_gemm_workspace_bytes
+    assert g(-1, 5, 5) == 0 and g(1 << 23, 1, 1) == 0
+
+
+def fwd(**kw):
+    a = Fwd(40, 50, 100, A, None, 0, A + SL, None, BF16, BF16, BF16, BF16, mxs(2, 40, 100), mxs(3, 100, 40),
+            mxs(4, 50, 100), mxs(5, 100, 50), 0, None, 0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_forward_rejections():
+    f = lib.f8lin_mxfp4_forward
+    none = Mx(None, None, 0, 0)
+
+    def call(**kw):
+        return f(ctypes.byref(fwd(**kw)), None)
+
+    W = A + 6 * SL
+    assert f(None, None) == EINVAL
+    assert call(rule=3) == EINVAL and call(N=-2) == ESHAPE and call(ldx=99) == ESHAPE
+    assert call(x=None) == EINVAL and call(x=A + 1) == EALIGN and call(y=A + SL + 1) == EALIGN
+    assert call(x_dtype=4) == EINVAL and call(y_dtype=-1) == EINVAL
+    assert call(w=W, w_dtype=8) == EINVAL and call(w=W + 1) == EALIGN
+    assert call(x4=none) == EINVAL and call(w4=none) == EINVAL              # x4 is needed when x4t is asked for
+    assert call(x4t=moved(mxs(3, 100, 40), ld=0)) == ESHAPE
+    assert call(w=W, w4t=moved(mxs(5, 100, 50), scale_ld=8)) == ESHAPE
+    assert call(y=A) == EINVAL and call(bias=A + SL) == EINVAL
+    assert call(w=W, w4=mxs(2, 50, 100)) == EINVAL                          # w4 and x4 are both written
+    assert call(w=A + 4 * SL) == EINVAL                                     # w inside w4
+    assert call(ws=A + 7 * SL + 4, ws_bytes=32) == EALIGN and call(ws=A, ws_bytes=32) == EINVAL
+    assert call(M=0) == OK
+
+
+def bwd(**kw):
+    a = Bwd(40, 50, 100, A, 0, A + SL, A + 2 * SL, None, BF16, BF16, BF16, BF16, mxs(3, 100, 40), mxs(4, 100, 50),
+            mxs(5, 40, 50), mxs(6, 50, 40), 0, None, 0, None, 0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_backward_rejections():
+    f = lib.f8lin_mxfp4_backward
+    none = Mx(None, None, 0, 0)
+
+    def call(**kw):
+        return f(ctypes.byref(bwd(**kw)), None)
+
+    DB, WS = A + 7 * SL, A + 8 * SL
+    need = lib.f8lin_mxfp4_dbias_workspace_bytes(40, 50)
+    assert need == 50 * 4 and lib.f8lin_mxfp4_dbias_workspace_bytes(129, 7) == 56
+    assert lib.f8lin_mxfp4_dbias_workspace_bytes(-1, 7) == 0
+    assert f(None, None) == EINVAL
+    assert call(rule=-1) == EINVAL and call(K=-1) == ESHAPE and call(lddy=49) == ESHAPE
+    assert call(dy=None) == EINVAL and call(dy=A + 1) == EALIGN and call(dw=A + 2 * SL + 1) == EALIGN
+    assert call(dx_dtype=3) == EINVAL and call(dy_dtype=3) == EINVAL
+    for name in ("x4t", "w4t", "dy4", "dy4t"):
+        assert call(**{name: none}) == EINVAL
+    assert call(dx=None, x4t=none) == EINVAL and call(dw=None, w4t=none) == EINVAL
+    assert call(dbias=DB) == EWORKSPACE and call(dbias=DB, dbias_ws=WS, dbias_ws_bytes=need - 1) == EWORKSPACE
+    assert call(dbias=DB, dbias_ws=WS + 4, dbias_ws_bytes=need) == EALIGN
+    assert call(dbias=A, dbias_ws=WS, dbias_ws_bytes=need) == EINVAL
+    assert call(dx=A + 2 * SL + 64) == EINVAL                               # dX inside dW
+    assert call(dw=A + 3 * SL) == EINVAL                                    # dW over x4t
+    assert call(dy4=mxs(6, 40, 50)) == EINVAL
+    assert call(ws=A + SL, ws_bytes=16) == EINVAL
+    assert call(dx=None, dw=None) == OK                                     # nothing asked for
+
+
+def test_grad_rejections():
+    norm_f, clip_f = lib.f8lin_grad_norm, lib.f8lin_grad_clip
+    WSB = lib.f8lin_grad_workspace_bytes()
+    NORM, WS = A + 5 * SL, A + 6 * SL
+
+    def table(*entries):
+        arr = (Grad * max(1, len(entries)))(*[Grad(*e) for e in entries])
+        return arr, ctypes.cast(arr, ctypes.c_void_p)
+
+    def norm(*entries, count=None, p=0, out=NORM, ws=WS, n=WSB):
+        arr, t = table(*entries)
+        return norm_f(t, len(entries) if count is None else count, p, out, ws, n, None)
+
+    def clip(*entries, p=0, mx_=1.0, out=NORM, given=0, ws=WS, n=WSB):
+        arr, t = table(*entries)
+        return clip_f(t, len(entries), p, mx_, out, given, ws, n, None)
+
+    ok, two = (A, A, 100, FP32, FP32), (A + SL, A + SL, 100, BF16, BF16)
+    assert norm(ok, p=3) == EINVAL and norm(ok, out=None) == EINVAL and norm(ok, out=NORM + 2) == EALIGN
+    assert norm_f(None, 1, 0, NORM, WS, WSB, None) == EINVAL and norm(ok, count=-1) == EINVAL
+    assert norm((A, None, -1, FP32, FP32)) == ESHAPE and norm((A, None, (1 << 40) + 1, FP32, FP32)) == ESHAPE
+    assert norm((None, None, 4, FP32, FP32)) == EINVAL and norm((A + 2, None, 4, FP32, FP32)) == EALIGN
+    assert norm((A, None, 4, 3, FP32)) == EINVAL
+    assert norm(ok, ws=None) == EWORKSPACE and norm(ok, n=WSB - 1) == EWORKSPACE and norm(ok, ws=WS + 8) == EWORKSPACE
+    assert norm(ok, out=A + 40) == EINVAL and norm(ok, ws=A - 16) == EINVAL and norm(ok, out=WS + 64) == EINVAL
+    assert clip(ok, two, mx_=-1.0) == EINVAL and clip(ok, two, mx_=math.nan) == EINVAL
+    assert clip(ok, ok) == EINVAL                                           # one tensor twice
+    assert clip(ok, (A + 396, A + 396, 4, FP32, FP32)) == EINVAL            # overlapping by one element
+    assert clip((A, A, 100, FP32, BF16)) == EINVAL                          # in place, to another type
+    assert clip((A, A + 200, 100, FP32, FP32)) == EINVAL                    # an output inside its input
+    assert clip(ok, (A + SL, A, 100, BF16, FP32)) == EINVAL                 # an output over another input
+    assert clip((A, A + SL, 100, FP32, FP32), (A + 2 * SL, A + SL, 100, FP32, FP32)) == EINVAL
+    assert clip((A, A + SL + 1, 100, FP32, BF16)) == EALIGN and clip((A, None, 100, FP32, BF16)) == EINVAL
+    assert clip(ok, out=A, given=1, ws=None) == EINVAL                      # the given norm inside a gradient
+    assert clip(ok, ws=None) == EWORKSPACE
+
+
+def test_convert_and_module_checks():
+    model = nn.Sequential(nn.Linear(7, 13), nn.ReLU(), nn.Sequential(nn.Linear(13, 5, bias=False)), nn.Linear(5, 2))
+    w, b = model[0].weight, model[0].bias
+    assert m.convert_to_mxfp4_training(model, "ceil", lambda fqn, mod: fqn != "3") is model
+    assert isinstance(model[0], m.MXFP4Linear) and model[0].weight is w and model[0].bias is b
+    assert isinstance(model[2][0], m.MXFP4Linear) and model[2][0].bias is None and model[2][0].rule == "ceil"
+    assert type(model[3]) is nn.Linear and "rule=ceil" in repr(model)
+    assert set(model.state_dict()) == {"0.weight", "0.bias", "2.0.weight", "3.weight", "3.bias"}
+    with pytest.raises(ValueError):
+        m.convert_to_mxfp4_training(nn.Linear(4, 4))
+    with pytest.raises(ValueError):
+        m.MXFP4Linear(4, 4, rule="even")
+    with pytest.raises(ValueError):
+        m.MXFP4Linear(4, 4, weight=torch.zeros(4, 5))
+    with pytest.raises(ValueError):
+        m.MXFP4Linear(4, 4, bias=torch.zeros(5))
+    with pytest.raises(RuntimeError):
+        model[0](torch.zeros(2, 7))                     # no CPU path
+    with pytest.raises(ValueError):
+        f8lin.MXFP4Tensor(torch.zeros((4, 16), dtype=torch.uint8), torch.zeros((4, 16), dtype=torch.uint8), 4, 32)
+    with pytest.raises(ValueError):
+        f8lin._norm_type(3)
+
+
+def test_dense_layouts():
+    t = torch.zeros((4, 6, 8))
+    for d in (t, t.permute(2, 0, 1), t.transpose(0, 2), t[1:2], t[:, :, 0:0], t[0, 0, 0], t[2], t.permute(1, 2, 0)[:, None]):
+        assert f8lin._is_dense(d)
+    for d in (t[:, :, ::2], t[:, 1:], t[::2], t[:1].expand(4, 6, 8), torch.zeros(1).expand(3)):
+        assert not f8lin._is_dense(d)
+
+
+def test_oracle_pins():
+    """Values worked out by hand from the format's definition."""
+    x = np.zeros((1, 32))
+    x[0, :16] = [6, 5, 5.0001, 4.9999, 3.5, 3.4999, 2.5, 2.5001, 1.75, 1.7499, 1.25, 1.2501, 0.75, 0.7499, 0.25, 0.2501]
+    codes, scales = mx.quantize(x)
+    assert scales[0, 0] == 127  # floor(log2 6) - 2 = 0
+    assert mx.values(codes, scales, 16)[0].tolist() == [6, 4, 6, 4, 4, 3, 2, 3, 2, 1.5, 1, 1.5, 1, 0.5, 0, 0.5]
+    x[0, 0] = 7.5  # still 2^0 by the floor rule (saturates at 6); 2^1 by the ceil rule
+    assert mx.rounded(x)[0, 0] == 6 and mx.quantize(x, "ceil")[1][0, 0] == 128 and mx.rounded(x, "ceil")[0, 0] == 8
+    x[0, 0] = 6.0001
+    assert mx.quantize(x, "ceil")[1][0, 0] == 128 and mx.quantize(x)[1][0, 0] == 127
+    x[0, 0] = -np.inf
+    assert mx.quantize(x)[1][0, 0] == 255 and not mx.quantize(x)[0].any() and np.isnan(mx.rounded(x)).all()
+    z = np.full((1, 33), -0.0)
+    c, s = mx.quantize(z)
+    assert s.tolist() == [[0, 0]] and c[0, :33].tolist() == [8] * 33 and not c[0, 33:].any()
+    assert mx.quantize(np.full((1, 1), 2.0 ** -149))[1][0, 0] == 0
+    assert np.array_equal(mx.unpack(mx.pack(codes)), codes)
+    assert mx.norm([np.array([3.0]), np.array([[4.0]])], 2.0) == 5.0 and mx.norm([], math.inf) == 0.0
+    assert mx.norm([np.array([-3.0, 1.0])], 1.0) == 4.0 and mx.norm([np.array([-3.0, 1.0])], math.inf) == 3.0
+    # the same rounding as torch's own bf16 for a grid of the same spacing: round half to even
+    v = np.arange(0, 2.01, 0.125)
+    t = np.zeros((1, 32))
+    t[0, :17], t[0, 31] = v, 4.0
+    assert np.array_equal(mx.rounded(t)[0, :17], np.round(v * 2) / 2)
