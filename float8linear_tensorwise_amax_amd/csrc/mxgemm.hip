@@ -36,12 +36,18 @@ struct MxProblem {
   int64_t lda, lsa, ldb, lsb;
   int M, N, nb;      // nb: MX blocks of K
   int c_dtype, bias_dtype;
-  int tiles_m, tiles_n, splits, group;
+  int tiles, splits, group, group_log;  // output tiles, K ranges, tile-rows per group (a power of two)
+  // divisors: tiles, tiles per group, tile-rows of the last group
+  int group_tiles, last_rows, last_group;
+  uint32_t inv_tiles, inv_group_tiles, inv_last_rows;
+  int nkb, pairs;    // K blocks of 128 bytes, and pairs of them
 };
 struct MxBatch {
   MxProblem p[kMxMaxGemms];
   int count;
 };
+typedef __attribute__((address_space(4))) MxBatch MxBatchArg;
+typedef __attribute__((address_space(4))) MxProblem MxProblemArg;
 
 __device__ __forceinline__ v8i frag8(const u32x4 &a) {
   return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
@@ -69,15 +75,12 @@ constexpr int kOutOfRange = (int)0x80000000u;
 
 constexpr int waitcnt(int vm, int lgkm) { return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lgkm << 8); }
 
-// (tile-row, tile-column) of a local tile index: groups of G tile-rows, each
-// walked column by column, so that the tiles an XCD runs at once form a
-// compact patch whose operand slices its L2 shares.
-__device__ __forceinline__ void mx_tile_coords(int local, int G, int tiles_m, int tiles_n, int &tm, int &tn) {
-  const int gsize = G * tiles_n;
-  const int grp = local / gsize, in = local % gsize;
-  const int gm = min(G, tiles_m - grp * G);
-  tm = grp * G + in % gm;
-  tn = in / gm;
+// n / d for 0 <= n < 2^31 with inv = min(2^32 - 1, floor(2^32 / d)) from the
+// host: the estimate is at most one too small.  (A tile's coordinates are
+// worked out between two tiles, where nothing hides a division.)
+__device__ __forceinline__ int div_by(int n, int d, uint32_t inv) {
+  const int q = (int)(((uint64_t)(uint32_t)n * inv) >> 32);
+  return n - q * d >= d ? q + 1 : q;
 }
 
 // One output tile (of one K range) of one problem.
@@ -87,14 +90,17 @@ struct Item {
   int nb;        // MX blocks from kb0 to the end of the range
 };
 
-template <int BM, int BN, int MINB>
-__global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch batch) {
+template <int BM, int BN, int MINB, int DT, bool SPLIT>
+__global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch) {
+  // The problems are read where the launch put them, through the scalar
+  // cache (an argument indexed at run time would be copied to scratch).
+  const MxBatchArg &batch = *(const MxBatchArg *)__builtin_amdgcn_kernarg_segment_ptr();
   constexpr int MI = BM / 32, NJ = BN / 32;  // 16 x 16 blocks of a wave tile
   constexpr int NM = MI * NJ, NR = MI + NJ;  // MFMAs, and fragment reads, per step of 128 elements
   constexpr int NC = MI + NJ;                // 1 KB copies per wave and K block
   constexpr int OPA = BM * kBlockBytes, STB = OPA + BN * kBlockBytes;
   constexpr int SCA = BM * 16, SCB = SCA + BN * 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STB + 2 * SCB];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STB + 3 * SCB];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -106,7 +112,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
   const int xcd = (int)blockIdx.x % kXcds;
   const int nwg = (int)gridDim.x, wx = nwg / kXcds + (xcd < nwg % kXcds ? 1 : 0);
   auto share = [&](int i, int &st, int &ln) {
-    const int T = i < batch.count ? batch.p[i].tiles_m * batch.p[i].tiles_n * batch.p[i].splits : 0;
+    const int T = i < batch.count ? batch.p[i].tiles * batch.p[i].splits : 0;
     const int per = T / kXcds, rem = T % kXcds;
     st = xcd * per + min(xcd, rem);
     ln = per + (xcd < rem ? 1 : 0);
@@ -120,17 +126,26 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
     Item w;
     w.pi = it < ln0 ? 0 : 1;
     const int t = it < ln0 ? st0 + it : st1 + it - ln0;
-    const MxProblem &P = batch.p[w.pi];
-    const int per = P.tiles_m * P.tiles_n;
-    w.range = t / per;
-    int tm, tn;
-    mx_tile_coords(t - w.range * per, P.group, P.tiles_m, P.tiles_n, tm, tn);
-    w.m0 = tm * BM;
-    w.n0 = tn * BN;
+    const MxProblemArg &P = batch.p[w.pi];
     // K ranges hold whole pairs of K blocks (16 bytes of scales)
-    const int nkb = (P.nb + kBlocksPerK - 1) / kBlocksPerK, np = (nkb + 1) / 2;
-    w.kb0 = w.range * np / P.splits * 2;
-    const int end = min((w.range + 1) * np / P.splits * 2, nkb);
+    w.range = 0;
+    w.kb0 = 0;
+    int end = P.nkb, local = t;
+    if constexpr (SPLIT) {
+      w.range = div_by(t, P.tiles, P.inv_tiles);
+      local = t - w.range * P.tiles;
+      w.kb0 = w.range * P.pairs / P.splits * 2;
+      end = min((w.range + 1) * P.pairs / P.splits * 2, P.nkb);
+    }
+    // groups of `group` tile-rows, each walked column by column, so that the
+    // tiles an XCD runs at once form a compact patch whose operand slices its
+    // L2 shares
+    const int grp = div_by(local, P.group_tiles, P.inv_group_tiles), in = local - grp * P.group_tiles;
+    const bool tail = grp == P.last_group;
+    const int rows = tail ? P.last_rows : P.group;
+    const int tn = tail ? div_by(in, P.last_rows, P.inv_last_rows) : in >> P.group_log;
+    w.m0 = (grp * P.group + in - tn * rows) * BM;
+    w.n0 = tn * BN;
     w.nkb = end - w.kb0;
     w.nb = min(end * kBlocksPerK, P.nb) - w.kb0 * kBlocksPerK;
     return w;
@@ -155,7 +170,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   int va[2], vb[2], vsa, vsb, step_a, step_b, step_sa, step_sb;
   auto set_copy_item = [&](bool live) {
-    const MxProblem &P = batch.p[ci.pi];
+    const MxProblemArg &P = batch.p[ci.pi];
     const int rows_a = min(BM, P.M - ci.m0), rows_b = min(BN, P.N - ci.n0);
     ra = __builtin_amdgcn_make_buffer_rsrc((void *)(P.a + ci.m0 * P.lda + ci.kb0 * kBlockBytes), (short)0,
                                            rows_a * (int)P.lda - ci.kb0 * kBlockBytes, 0x00020000);
@@ -198,20 +213,31 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
     }
     __builtin_amdgcn_raw_ptr_buffer_load_lds(b ? rb : ra, (lds_void *)dst, 16, v, c_kb * kBlockBytes, 0, 0);
   };
-  // the scales of the cursor's block and the one after: 64 rows per copy
+  // The scales of the cursor's block and the one after, 64 rows per copy, into
+  // the ring; at a pair's second block the same copies read nothing and land
+  // in a spare slot, so that the loop holds no branch.
   auto copy_scales = [&]() {
-    uint8_t *dst = smem + 2 * STB + (c_pair & 1) * SCB;
-    const int so = (ci.kb0 + c_kb) * kBlocksPerK;
+    const bool even = !(c_kb & 1);
+    uint8_t *dst = smem + 2 * STB + (even ? (c_pair & 1) * SCB : 2 * SCB);
+    const int so = (ci.kb0 + c_kb) * kBlocksPerK, odd = even ? 0 : kOutOfRange;
 #pragma unroll
     for (int s0 = 0; s0 < (BM + BN) / 64; s0 += 4) {
-      const int s = s0 + wave;
-      if (s < BM / 64)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(dst + s * 1024), 16, vsa + s * step_sa, so, 0, 0);
-      else if (s < (BM + BN) / 64)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(dst + s * 1024), 16, vsb + (s - BM / 64) * step_sb,
-                                                 so, 0, 0);
+      if constexpr ((BM / 64) % 4 == 0 && (BN / 64) % 4 == 0) {
+        const int s = s0 + wave;
+        if (s0 < BM / 64)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(dst + s * 1024), 16, (vsa + s * step_sa) | odd, so,
+                                                   0, 0);
+        else
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(dst + s * 1024), 16,
+                                                   (vsb + (s - BM / 64) * step_sb) | odd, so, 0, 0);
+      } else {
+        static_assert(BM + BN == 256, "one copy per wave");
+        const bool b = wave >= BM / 64;
+        const int v = b ? vsb + (wave - BM / 64) * step_sb : vsa + wave * step_sa;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b ? rsb : rsa, (lds_void *)(dst + wave * 1024), 16, v | odd, so, 0, 0);
+      }
     }
-    ++c_pair;
+    c_pair += even ? 1 : 0;
   };
   auto advance = [&]() {
     if (++c_kb >= ci.nkb) {
@@ -233,7 +259,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
   }
   const int sbase_a = 2 * STB + (wm + r) * 16 + 2 * g, sbase_b = 2 * STB + SCA + (wn + r) * 16 + 2 * g;
   u32x4 fa[2][MI], fb[2][NJ];
-  int sa[MI], sb[NJ], sa_n[MI], sb_n[NJ];
+  int sa_n[MI], sb_n[NJ];
   auto read = [&](int stage, int set, int k) {  // B's fragments first: the first MFMAs need them all
     const int b = k == 0 || k > NJ ? 0 : 1, f = k == 0 ? 0 : (b ? k - 1 : k - NJ);
     const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + stage * STB + base[b][set] + f * 2048);
@@ -247,12 +273,6 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
     else sb_n[f] = v;
   };
   v4f acc[MI][NJ];
-  auto clear = [&]() {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  };
 
   // scale bytes past the range's MX blocks may be anything (NaN among them): zero
   auto mask_scales = [&](int left) {
@@ -266,58 +286,46 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
     }
   };
 
-  // ---- Output of a finished tile; returns whether exactly NST stores were issued by every wave
-  constexpr int NST16 = NM / 2, NST32 = NM;
-  auto store_tile = [&](const Item &w) -> int {
-    const MxProblem &P = batch.p[w.pi];
+  // ---- Output of a finished tile.  A tile that lies inside C issues exactly
+  // NST stores per wave, which the next tile's first wait allows for; one on
+  // the edge waits for its stores here.
+  constexpr int NST = DT == F8LIN_FP32 ? NM : NM / 2;
+  auto store_tile = [&](const Item &w, auto INSIDE) __attribute__((always_inline)) {
+    constexpr bool inside = decltype(INSIDE)::value;
+    const MxProblemArg &P = batch.p[w.pi];
     const int M = P.M, N = P.N;
-    const bool partial = P.splits > 1;
-    const int dt = partial ? F8LIN_FP32 : P.c_dtype;
-    const bool inside = w.m0 + BM <= M && w.n0 + BN <= N;
-    const int row0 = w.m0 + wm + r;
-    if (P.bias && !partial) {
+    const int row0 = w.m0 + wm + r, col0 = w.n0 + wn;
+    // One row pointer, moved on from row block to row block (opaque to the
+    // compiler, which would otherwise hold an address for every store).
+    constexpr int ES = DT == F8LIN_FP32 ? 4 : 2;
+    const int lane_col = DT == F8LIN_FP32 ? 4 * g : 16 * (g & 1) + 8 * (g >> 1);
+    const int left = N - col0 - lane_col;  // columns from this lane's first one to the edge
+    int64_t at = (int64_t)(uintptr_t)P.c + (((SPLIT ? (int64_t)w.range * M : 0) + row0) * N + col0 + lane_col) * ES;
+    const int64_t step = (int64_t)16 * N * ES;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int col = w.n0 + wn + 16 * j + 4 * g + v;
-          const float b = col < N ? load_elem(P.bias, col, P.bias_dtype) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < MI; ++i) acc[i][j][v] += b;
-        }
-    }
-    if (dt == F8LIN_FP32) {
-      float *c = reinterpret_cast<float *>(P.c) + (partial ? (int64_t)w.range * M * N : 0);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int row = row0 + 16 * i;
-        float *cr = c + (int64_t)row * N + w.n0 + wn + 4 * g;
+    for (int i = 0; i < MI; ++i) {
+      const bool row_ok = inside || row0 + 16 * i < M;
+      if constexpr (DT == F8LIN_FP32) {
+        float *dst = reinterpret_cast<float *>((uintptr_t)at);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const int left = N - (w.n0 + wn + 4 * g + 16 * j);
-          if (inside || (row < M && left >= 4)) {
-            *reinterpret_cast<u32x4_u *>(cr + 16 * j) = __builtin_bit_cast(u32x4, acc[i][j]);
-          } else if (row < M) {
+          if (inside || (row_ok && left >= 16 * j + 4)) {
+            *reinterpret_cast<u32x4_u *>(dst + 16 * j) = __builtin_bit_cast(u32x4, acc[i][j]);
+          } else if (row_ok) {
 #pragma unroll
             for (int v = 0; v < 3; ++v)
-              if (v < left) cr[16 * j + v] = acc[i][j][v];
+              if (left > 16 * j + v) dst[16 * j + v] = acc[i][j][v];
           }
         }
-      }
-      return inside ? 2 : 0;
-    }
-    uint16_t *c = reinterpret_cast<uint16_t *>(P.c);
-    auto put = [&](auto BF) {
-      auto pack = [&](float x, float y) -> uint32_t {
-        if constexpr (decltype(BF)::value)
-          return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{x, y}, bf16x2_t));
-        else
-          return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x) |
-                 (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)y) << 16;
-      };
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int row = row0 + 16 * i;
+      } else {
+        auto pack = [&](float x, float y) -> uint32_t {
+          if constexpr (DT == F8LIN_BF16)
+            return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{x, y}, bf16x2_t));
+          else
+            return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x) |
+                   (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)y) << 16;
+        };
+        uint16_t *dst = reinterpret_cast<uint16_t *>((uintptr_t)at);
 #pragma unroll
         for (int j = 0; j < NJ; j += 2) {
           // lane group g: columns 8 (g / 2) .. + 7 of block j + g % 2
@@ -326,21 +334,20 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
           const auto hi = __builtin_amdgcn_permlane16_swap(pack(acc[i][j][2], acc[i][j][3]),
                                                            pack(acc[i][j + 1][2], acc[i][j + 1][3]), false, false);
           const u32x4 o = {lo[0], hi[0], lo[1], hi[1]};
-          const int col = w.n0 + wn + 16 * (j + (g & 1)) + 8 * (g >> 1);
-          uint16_t *dst = c + (int64_t)row * N + col;
-          if (inside || (row < M && col + 8 <= N)) {
-            *reinterpret_cast<u32x4_u *>(dst) = o;
-          } else if (row < M) {
+          if (inside || (row_ok && left >= 16 * j + 8)) {
+            *reinterpret_cast<u32x4_u *>(dst + 16 * j) = o;
+          } else if (row_ok) {
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              if (col + v < N) dst[v] = (uint16_t)(o[v >> 1] >> (16 * (v & 1)));
+            for (int v = 0; v < 7; ++v)
+              if (left > 16 * j + v) dst[16 * j + v] = (uint16_t)(o[v >> 1] >> (16 * (v & 1)));
           }
         }
       }
-    };
-    if (dt == F8LIN_BF16) put(std::true_type());
-    else put(std::false_type());
-    return inside ? 1 : 0;
+      at += step;
+      asm volatile("" : "+v"(at));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (!inside) __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
   };
 
   // ---- Prologue: blocks 0 and 1 of the stream
@@ -350,25 +357,18 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
 #pragma unroll
   for (int q = 0; q < NC; ++q) copy(0, q);
   advance();
-  if (!(c_kb & 1)) copy_scales();
+  copy_scales();
 #pragma unroll
   for (int q = 0; q < NC; ++q) copy(1, q);
-  advance();
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
   __builtin_amdgcn_s_barrier();
   Item cur = decode(it);
   it += wx;
-  Item nxt = it < total ? decode(it) : cur;
-  int kb = 0, stage = 0, r_pair = 0, stored = 0;
+  int stage = 0, r_pair = 0;
 #pragma unroll
   for (int k = 0; k < NR; ++k) read(0, 0, k);
 #pragma unroll
   for (int k = 0; k < NR; ++k) read_scale(0, k);
-  mask_scales(cur.nb);
-#pragma unroll
-  for (int i = 0; i < MI; ++i) sa[i] = sa_n[i];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) sb[j] = sb_n[j];
 
   // Slots of a block's 2 NM MFMAs: step-1 fragments are read over the first
   // half of step 0; the barrier follows at slot TB; copies go out from there,
@@ -378,10 +378,19 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
   constexpr int CG = NM >= 64 ? 2 : 1;
   constexpr int RG = NM / 2 / NR;  // MFMAs per fragment read
   static_assert(RG >= 1 && TB + NC * CG < 2 * NM, "schedule");
-  for (;;) {
-   clear();
-   for (kb = 0; kb < cur.nkb; ++kb) {
-    const bool last = kb + 1 == cur.nkb;
+  auto block = [&](int kb) __attribute__((always_inline)) {
+    // (everything that branches comes first: the compiler moves MFMAs across
+    // branches, away from the reads and copies they are to run next to)
+    advance();
+    mask_scales(cur.nb - kb * kBlocksPerK);
+    int sa[MI], sb[NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i] = sa_n[i];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) sb[j] = sb_n[j];
+    int after = kb + 1;
+    asm volatile("" : "+s"(after));  // (opaque: no copy of the loop for the last block)
+    const int nkb_next = after == cur.nkb ? 0 : after;
     int q = 0;
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
@@ -390,20 +399,26 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
                                                                    sb[j], 0, sa[i]);
       if (t % RG == 0 && t / RG < NR) read(stage, 1, t / RG);
       if (t == TB) {
-        // this wave has read the whole stage and has its copies of the next
-        // block (a tile stored in between: its stores may still be under way)
-        if (stored == 0) __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
-        else if (stored == 1) __builtin_amdgcn_s_waitcnt(waitcnt(NST16, 0));
-        else __builtin_amdgcn_s_waitcnt(waitcnt(NST32 > 63 ? 63 : NST32, 0));
-        stored = 0;
+        // This wave has read the whole stage and has its copies of the next
+        // block.  In a tile's first block only the last tile's stores came
+        // after those copies, so they may still be under way.  (The branch is
+        // out of the compiler's sight: it would move MFMAs across one.)
+        asm volatile(
+            "s_waitcnt vmcnt(%1) lgkmcnt(0)\n\t"
+            "s_cmp_eq_u32 %0, 0\n\t"
+            "s_cbranch_scc1 .Lfirst%=\n\t"
+            "s_waitcnt vmcnt(0)\n"
+            ".Lfirst%=:"
+            :
+            : "s"(kb), "n"(NST > 63 ? 63 : NST)
+            : "scc", "memory");
         __builtin_amdgcn_s_barrier();
-        if (!(c_kb & 1)) copy_scales();
+        copy_scales();
       }
       if (t > TB && (t - TB - 1) % CG == 0 && q < NC) copy(stage, q++);
       __builtin_amdgcn_sched_barrier(0);
     }
-    const int nkb_next = last ? 0 : kb + 1;
-    if (!(nkb_next & 1)) ++r_pair;
+    r_pair += nkb_next & 1 ? 0 : 1;
     const int soff = (r_pair & 1) * SCB + (nkb_next & 1) * 8;
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
@@ -417,19 +432,34 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch 
       if ((NM + t - TB - 1) % CG == 0 && q < NC) copy(stage, q++);
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance();
-    mask_scales(last ? nxt.nb : cur.nb - (kb + 1) * kBlocksPerK);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = sa_n[i];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) sb[j] = sb_n[j];
     stage ^= 1;
-   }
-   stored = __builtin_amdgcn_readfirstlane(store_tile(cur));
-   if (it >= total) break;
-   cur = nxt;
-   it += wx;
-   if (it < total) nxt = decode(it);
+  };
+  for (;;) {
+    // the sums start from the bias
+    {
+      const MxProblemArg &P = batch.p[cur.pi];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        v4f init = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (!SPLIT && P.bias) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int col = cur.n0 + wn + 16 * j + 4 * g + v;
+            init[v] = col < P.N ? load_elem(P.bias, col, P.bias_dtype) : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[i][j] = init;
+      }
+    }
+    for (int kb = 0; kb < cur.nkb; ++kb) block(kb);
+    if (cur.m0 + BM <= batch.p[cur.pi].M && cur.n0 + BN <= batch.p[cur.pi].N)
+      store_tile(cur, std::true_type());
+    else
+      store_tile(cur, std::false_type());
+    if (it >= total) break;
+    cur = decode(it);
+    it += wx;
   }
   // (the cursor's last copies fetch nothing but still write zeros into LDS)
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
@@ -453,6 +483,49 @@ __global__ __launch_bounds__(256) void mx_fill_kernel(void *c, int c_dtype, int6
     store_elem(c, i, bias ? load_elem(bias, i % N, bias_dtype) : 0.0f, c_dtype);
 }
 
+void set_tiles(MxProblem &p, int bm, int bn, int group_log, int splits) {
+  const int tm = (p.M + bm - 1) / bm, tn = (p.N + bn - 1) / bn;
+  auto inv = [](int d) { return (uint32_t)std::min<uint64_t>(0xFFFFFFFFull, (1ull << 32) / (uint64_t)d); };
+  p.tiles = tm * tn;
+  p.splits = splits;
+  p.group_log = group_log;
+  p.group = 1 << group_log;
+  p.group_tiles = p.group * tn;
+  p.last_rows = tm % p.group ? tm % p.group : p.group;
+  p.last_group = (tm - 1) >> group_log;
+  p.inv_tiles = inv(p.tiles);
+  p.inv_group_tiles = inv(p.group_tiles);
+  p.inv_last_rows = inv(p.last_rows);
+  p.nkb = (p.nb + kBlocksPerK - 1) / kBlocksPerK;
+  p.pairs = (p.nkb + 1) / 2;
+}
+
+template <int BM, int BN, int MINB, bool SPLIT>
+void launch_tiled(const MxBatch &b, int dt, unsigned grid, hipStream_t stream) {
+  if (SPLIT || dt == F8LIN_FP32)
+    mx_gemm_tiled_kernel<BM, BN, MINB, F8LIN_FP32, SPLIT><<<grid, 256, 0, stream>>>(b);
+  else if (dt == F8LIN_BF16)
+    mx_gemm_tiled_kernel<BM, BN, MINB, F8LIN_BF16, false><<<grid, 256, 0, stream>>>(b);
+  else
+    mx_gemm_tiled_kernel<BM, BN, MINB, F8LIN_FP16, false><<<grid, 256, 0, stream>>>(b);
+}
+
+// One launch for problems of one output type.
+void launch_batch(MxBatch &b, int dt, hipStream_t stream) {
+  int64_t big = 0;
+  for (int i = 0; i < b.count; ++i) big += ((b.p[i].M + 255) / 256) * (int64_t)((b.p[i].N + 255) / 256);
+  const bool use_big = big >= kCUs;
+  int64_t tiles = 0;
+  for (int i = 0; i < b.count; ++i) {
+    set_tiles(b.p[i], use_big ? 256 : 128, use_big ? 256 : 128, use_big ? 2 : 3, 1);
+    tiles += b.p[i].tiles;
+  }
+  if (use_big)
+    launch_tiled<256, 256, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
+  else
+    launch_tiled<128, 128, 2, false>(b, dt, (unsigned)std::min<int64_t>(tiles, 2 * kCUs), stream);
+}
+
 }  // namespace
 
 size_t mx_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
@@ -460,8 +533,7 @@ bool mx_linear_fused(int64_t, int64_t, int64_t) { return false; }
 hipError_t launch_mx_linear(const MxLinear &, hipStream_t) { return hipErrorInvalidValue; }
 
 hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream_t stream) {
-  MxBatch b = {};
-  int64_t big = 0;
+  MxBatch b[3] = {};  // by output type
   for (int i = 0; i < count; ++i) {
     if (d[i].M == 0 || d[i].N == 0) continue;
     if (d[i].K == 0) {
@@ -470,26 +542,26 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream
           d[i].c, d[i].c_dtype, mn, (int)d[i].N, d[i].bias, d[i].bias_dtype);
       continue;
     }
-    MxProblem &p = b.p[b.count++];
-    p = MxProblem{d[i].a.codes, d[i].a.scales, d[i].b.codes, d[i].b.scales, d[i].c,     d[i].bias,
-                  d[i].a.ld,    d[i].a.scale_ld, d[i].b.ld,  d[i].b.scale_ld, (int)d[i].M, (int)d[i].N,
-                  (int)((d[i].K + kMxBlock - 1) / kMxBlock), d[i].c_dtype, d[i].bias_dtype, 0, 0, 1, 4};
-    big += ((d[i].M + 255) / 256) * ((d[i].N + 255) / 256);
+    MxBatch &list = b[d[i].c_dtype];
+    MxProblem &p = list.p[list.count++];
+    p.a = d[i].a.codes;
+    p.as = d[i].a.scales;
+    p.b = d[i].b.codes;
+    p.bs = d[i].b.scales;
+    p.c = d[i].c;
+    p.bias = d[i].bias;
+    p.lda = d[i].a.ld;
+    p.lsa = d[i].a.scale_ld;
+    p.ldb = d[i].b.ld;
+    p.lsb = d[i].b.scale_ld;
+    p.M = (int)d[i].M;
+    p.N = (int)d[i].N;
+    p.nb = (int)((d[i].K + kMxBlock - 1) / kMxBlock);
+    p.c_dtype = d[i].c_dtype;
+    p.bias_dtype = d[i].bias_dtype;
   }
-  if (b.count == 0) return hipGetLastError();
-  const bool use_big = big >= kCUs;
-  const int bm = use_big ? 256 : 128;
-  int64_t tiles = 0;
-  for (int i = 0; i < b.count; ++i) {
-    MxProblem &p = b.p[i];
-    p.tiles_m = (p.M + bm - 1) / bm;
-    p.tiles_n = (p.N + bm - 1) / bm;
-    tiles += (int64_t)p.tiles_m * p.tiles_n;
-  }
-  if (use_big)
-    mx_gemm_tiled_kernel<256, 256, 1><<<(unsigned)std::min<int64_t>(tiles, kCUs), 256, 0, stream>>>(b);
-  else
-    mx_gemm_tiled_kernel<128, 128, 2><<<(unsigned)std::min<int64_t>(tiles, 2 * kCUs), 256, 0, stream>>>(b);
+  for (int dt = 0; dt < 3; ++dt)
+    if (b[dt].count > 0) launch_batch(b[dt], dt, stream);
   return hipGetLastError();
 }
 
