@@ -26,11 +26,6 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
-  return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
-}
-
 struct QuantJob {
   const void *x;
   int64_t rows, cols, ldx;

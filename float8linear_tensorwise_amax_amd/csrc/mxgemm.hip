@@ -90,7 +90,7 @@ struct Item {
   int nb;        // MX blocks from kb0 to the end of the range
 };
 
-template <int BM, int BN, int MINB, int DT, bool SPLIT>
+template <int BM, int BN, int NS, int MINB, int DT, bool SPLIT>
 __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch) {
   // The problems are read where the launch put them, through the scalar
   // cache (an argument indexed at run time would be copied to scratch).
@@ -100,7 +100,14 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   constexpr int NC = MI + NJ;                // 1 KB copies per wave and K block
   constexpr int OPA = BM * kBlockBytes, STB = OPA + BN * kBlockBytes;
   constexpr int SCA = BM * 16, SCB = SCA + BN * 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STB + 3 * SCB];
+  // pairs of K blocks whose scales are held: those of the NS - 1 blocks yet to
+  // be read and of the one being copied, each of which may be a tile's only one
+  constexpr int RING = NS <= 2 ? 2 : (NS <= 4 ? 4 : 8);
+  static_assert(RING >= NS, "scale ring");
+  constexpr int NSC = (BM + BN + 255) / 256;  // scale copies per wave and K block
+  constexpr int NCP = NC + NSC;
+  static_assert((NS - 1) * NCP <= 63, "vmcnt");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STB + (RING + 1) * SCB];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -218,24 +225,21 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   // in a spare slot, so that the loop holds no branch.
   auto copy_scales = [&]() {
     const bool even = !(c_kb & 1);
-    uint8_t *dst = smem + 2 * STB + (even ? (c_pair & 1) * SCB : 2 * SCB);
+    uint8_t *dst = smem + NS * STB + (even ? (c_pair & (RING - 1)) * SCB : RING * SCB);
     const int so = (ci.kb0 + c_kb) * kBlocksPerK, odd = even ? 0 : kOutOfRange;
-#pragma unroll
-    for (int s0 = 0; s0 < (BM + BN) / 64; s0 += 4) {
-      if constexpr ((BM / 64) % 4 == 0 && (BN / 64) % 4 == 0) {
-        const int s = s0 + wave;
-        if (s0 < BM / 64)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(dst + s * 1024), 16, (vsa + s * step_sa) | odd, so,
-                                                   0, 0);
-        else
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(dst + s * 1024), 16,
-                                                   (vsb + (s - BM / 64) * step_sb) | odd, so, 0, 0);
-      } else {
-        static_assert(BM + BN == 256, "one copy per wave");
-        const bool b = wave >= BM / 64;
-        const int v = b ? vsb + (wave - BM / 64) * step_sb : vsa + wave * step_sa;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(b ? rsb : rsa, (lds_void *)(dst + wave * 1024), 16, v | odd, so, 0, 0);
-      }
+    if constexpr (BM == 256 && BN == 256) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(dst + wave * 1024), 16, (vsa + wave * step_sa) | odd, so,
+                                               0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(dst + SCA + wave * 1024), 16,
+                                               (vsb + wave * step_sb) | odd, so, 0, 0);
+    } else {
+      static_assert(BM + BN <= 256, "at most one copy per wave");
+      // (a wave without rows of its own copies nothing into the spare slot, so
+      // that every wave has issued as many copies)
+      const bool b = wave >= BM / 64, none = wave >= (BM + BN) / 64;
+      const int v = none ? kOutOfRange : b ? vsb + (wave - BM / 64) * step_sb : vsa + wave * step_sa;
+      uint8_t *const to = none ? smem + NS * STB + RING * SCB : dst + wave * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b ? rsb : rsa, (lds_void *)to, 16, v | odd, so, 0, 0);
     }
     c_pair += even ? 1 : 0;
   };
@@ -257,7 +261,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
     base[0][s] = (wm + r) * kBlockBytes + place;
     base[1][s] = OPA + (wn + r) * kBlockBytes + place;
   }
-  const int sbase_a = 2 * STB + (wm + r) * 16 + 2 * g, sbase_b = 2 * STB + SCA + (wn + r) * 16 + 2 * g;
+  const int sbase_a = NS * STB + (wm + r) * 16 + 2 * g, sbase_b = NS * STB + SCA + (wn + r) * 16 + 2 * g;
   u32x4 fa[2][MI], fb[2][NJ];
   int sa_n[MI], sb_n[NJ];
   auto read = [&](int stage, int set, int k) {  // B's fragments first: the first MFMAs need them all
@@ -350,17 +354,18 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
     if constexpr (!inside) __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
   };
 
-  // ---- Prologue: blocks 0 and 1 of the stream
+  // ---- Prologue: the first NS blocks of the stream
   set_copy_item(true);
   mask_copies();
-  copy_scales();
+#pragma unroll 1
+  for (int st = 0;;) {
+    copy_scales();
 #pragma unroll
-  for (int q = 0; q < NC; ++q) copy(0, q);
-  advance();
-  copy_scales();
-#pragma unroll
-  for (int q = 0; q < NC; ++q) copy(1, q);
-  __builtin_amdgcn_s_waitcnt(waitcnt(0, 15));
+    for (int q = 0; q < NC; ++q) copy(st, q);
+    if (++st == NS) break;
+    advance();
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt((NS - 1) * NCP, 15));
   __builtin_amdgcn_s_barrier();
   Item cur = decode(it);
   it += wx;
@@ -374,10 +379,10 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   // half of step 0; the barrier follows at slot TB; copies go out from there,
   // one every CG MFMAs; step 1 reads the next block's step-0 fragments and
   // scales.
-  constexpr int TB = NM * 5 / 8;
-  constexpr int CG = NM >= 64 ? 2 : 1;
-  constexpr int RG = NM / 2 / NR;  // MFMAs per fragment read
-  static_assert(RG >= 1 && TB + NC * CG < 2 * NM, "schedule");
+  constexpr int CG = NM >= 64 ? 5 : 1;
+  constexpr int RG = NM / 2 / NR > 0 ? NM / 2 / NR : 1;  // MFMAs per fragment read
+  constexpr int TB = NM * 9 / 16 > (NR - 1) * RG ? NM * 9 / 16 : (NR - 1) * RG;
+  static_assert(TB < NM && TB + NC * CG < 2 * NM, "schedule");
   auto block = [&](int kb) __attribute__((always_inline)) {
     // (everything that branches comes first: the compiler moves MFMAs across
     // branches, away from the reads and copies they are to run next to)
@@ -400,10 +405,12 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
       if (t % RG == 0 && t / RG < NR) read(stage, 1, t / RG);
       if (t == TB) {
         // This wave has read the whole stage and has its copies of the next
-        // block.  In a tile's first block only the last tile's stores came
-        // after those copies, so they may still be under way.  (The branch is
-        // out of the compiler's sight: it would move MFMAs across one.)
-        asm volatile(
+        // block.  With two stages, in a tile's first block only the last
+        // tile's stores came after those copies, so they may still be under
+        // way.  (The branch is out of the compiler's sight: it would move
+        // MFMAs across one.)
+        if constexpr (NS > 2) __builtin_amdgcn_s_waitcnt(waitcnt((NS - 2) * NCP, 0));
+        else asm volatile(
             "s_waitcnt vmcnt(%1) lgkmcnt(0)\n\t"
             "s_cmp_eq_u32 %0, 0\n\t"
             "s_cbranch_scc1 .Lfirst%=\n\t"
@@ -419,20 +426,21 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
       __builtin_amdgcn_sched_barrier(0);
     }
     r_pair += nkb_next & 1 ? 0 : 1;
-    const int soff = (r_pair & 1) * SCB + (nkb_next & 1) * 8;
+    const int soff = (r_pair & (RING - 1)) * SCB + (nkb_next & 1) * 8;
+    const int next = stage + 1 == NS ? 0 : stage + 1;
 #pragma unroll
     for (int t = 0; t < NM; ++t) {
       const int i = t / NJ, j = t % NJ;
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[1][j]), frag8(fa[1][i]), acc[i][j], 4, 4, 1,
                                                                    sb[j], 1, sa[i]);
       if (t % RG == 0 && t / RG < NR) {
-        read(stage ^ 1, 0, t / RG);
+        read(next, 0, t / RG);
         read_scale(soff, t / RG);
       }
       if ((NM + t - TB - 1) % CG == 0 && q < NC) copy(stage, q++);
       __builtin_amdgcn_sched_barrier(0);
     }
-    stage ^= 1;
+    stage = next;
   };
   for (;;) {
     // the sums start from the bias
@@ -463,6 +471,161 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   }
   // (the cursor's last copies fetch nothing but still write zeros into LDS)
   __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
+}
+
+// ---- Few rows (M <= 64): bound by reading B once.  A workgroup of NW waves
+// owns 16 rows of B (16 output columns), so N / 16 workgroups stream B; the
+// waves split K in 128-byte blocks (wave w takes blocks w, w + NW, ...), load
+// operands straight into registers, U blocks in flight, and their partial
+// sums meet in LDS.  FUSED (X not yet quantised, M <= 16): every workgroup
+// quantises X into LDS itself while its first loads of B are under way.
+struct MxSkinny {
+  const uint8_t *a, *as, *b, *bs;
+  const void *x;
+  void *c;
+  const void *bias;
+  int64_t lda, lsa, ldb, lsb, ldx;
+  int M, N, K, nb, nkb;
+  int c_dtype, bias_dtype;
+};
+constexpr int kSkinnyMaxM = 64;
+
+
+// LDS strides of the quantised X: rows 16 bytes apart from a multiple of 128
+// (bank conflicts), scales after all codes.
+__host__ __device__ constexpr int fused_row(int nkb) { return nkb * kBlockBytes + 16; }
+__host__ __device__ constexpr int fused_scale_row(int nkb) { return nkb * kBlocksPerK; }
+__host__ __device__ constexpr int fused_bytes(int M, int nkb) { return M * (fused_row(nkb) + fused_scale_row(nkb)); }
+
+#ifndef XU
+#define XU 4
+#define XFM 2
+#define XNW8 512
+#endif
+constexpr int kFusedMaxM = XFM;
+template <int MT, int NW, bool FUSED, int XDT, int RULE>
+__global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
+  constexpr int U = MT == 1 ? XU : (MT == 2 ? 4 : 2);
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16;
+  const int rows_b = min(16, P.N - n0);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.b + n0 * P.ldb), (short)0,
+                                                                      rows_b * (int)P.ldb, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.bs + n0 * P.lsb), (short)0,
+                                                                       rows_b * (int)P.lsb, 0x00020000);
+  __amdgpu_buffer_rsrc_t ra, rsa;
+  if constexpr (!FUSED) {
+    ra = __builtin_amdgcn_make_buffer_rsrc((void *)P.a, (short)0, P.M * (int)P.lda, 0x00020000);
+    rsa = __builtin_amdgcn_make_buffer_rsrc((void *)P.as, (short)0, P.M * (int)P.lsa, 0x00020000);
+  }
+  // chunks g and 4 + g of block kb of a row (four lanes read 64 bytes in a
+  // row) and the block's eight scale bytes; chunks past K lie outside the
+  // buffer
+  auto load = [&](__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rss, int ld, int ls, int row, int kb, u32x4(&f)[2],
+                  u32x2 &sc) {
+    const int c = kb * kBlocksPerK + g;
+    const int o = row * ld + c * 16;
+    f[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, c < P.nb ? o : kOutOfRange, 0, 0));
+    f[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, c + 4 < P.nb ? o + 64 : kOutOfRange, 0, 0));
+    sc = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                       rss, kb < P.nkb ? row * ls + kb * kBlocksPerK : kOutOfRange, 0, 0));
+  };
+  // this lane's two scale bytes, in bytes 0 and 1; zero past K
+  const uint32_t pick = 0x0C0C0400u + 0x0101u * g;
+  auto scale = [&](const u32x2 &sc, int kb) {
+    const int left = P.nb - kb * kBlocksPerK - g;
+    uint32_t sel = pick;
+    if (left <= 4) sel = left <= 0 ? 0x0C0C0C0Cu : (sel & 0xFFu) | 0x0C0C0C00u;
+    return (int)__builtin_amdgcn_perm(sc.y, sc.x, sel);
+  };
+  v4f acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 fb[U][2], fa[FUSED ? 1 : U][MT][2];
+  u32x2 sb[U], sa[FUSED ? 1 : U][MT];
+  auto load_all = [&](int kb0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      load(rb, rsb, (int)P.ldb, (int)P.lsb, r, kb0 + NW * u, fb[u], sb[u]);
+      if constexpr (!FUSED) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) load(ra, rsa, (int)P.lda, (int)P.lsa, 16 * m + r, kb0 + NW * u, fa[u][m], sa[u][m]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all U blocks in flight before the first use
+  };
+  int kb0 = wave;
+  load_all(kb0);
+  const int xrow = fused_row(P.nkb), xsrow = fused_scale_row(P.nkb);
+  uint8_t *const xs = dyn + P.M * xrow;
+  if constexpr (FUSED) {
+    typedef typename MxElem<XDT>::type elem;
+    for (int m = 0; m < P.M; ++m) {
+      const elem *x = reinterpret_cast<const elem *>(P.x) + m * P.ldx;
+      for (int i = threadIdx.x; i < P.nkb * kBlocksPerK * 4; i += 64 * NW) {  // eight values each, a block per quad
+        float v[8];
+        load8<XDT>(x + 8 * i, P.K - 8 * i, v);
+        uint32_t mag = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mag = max(mag, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+        const int e = mx_scale_byte<RULE>(quad_max(mag));
+        *reinterpret_cast<uint32_t *>(dyn + m * xrow + 4 * i) = e == kMxNan ? 0u : mx_cvt8(v, mx_scale_f32(e));
+        if ((i & 3) == 0) xs[m * xsrow + (i >> 2)] = (uint8_t)e;
+      }
+    }
+    __syncthreads();
+  }
+  for (;;) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + NW * u;
+      const int sbu = scale(sb[u], kb);
+      if constexpr (FUSED) {
+        fa[0][0][0] = fa[0][0][1] = u32x4{0, 0, 0, 0};
+        sa[0][0] = u32x2{0, 0};
+        if (r < P.M && kb < P.nkb) {
+          const u32x4 *src = reinterpret_cast<const u32x4 *>(dyn + r * xrow + kb * kBlockBytes + 16 * g);
+          fa[0][0][0] = src[0];
+          fa[0][0][1] = src[4];
+          sa[0][0] = *reinterpret_cast<const u32x2 *>(xs + r * xsrow + kb * kBlocksPerK);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int ua = FUSED ? 0 : u;
+        const int sau = scale(sa[ua][m], kb);
+        acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[u][0]), frag8(fa[ua][m][0]), acc[m], 4, 4, 0,
+                                                                  sbu, 0, sau);
+        acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[u][1]), frag8(fa[ua][m][1]), acc[m], 4, 4, 1,
+                                                                  sbu, 1, sau);
+      }
+    }
+    kb0 += NW * U;
+    if (kb0 >= P.nkb) break;
+    load_all(kb0);
+  }
+  __syncthreads();  // (the quantised X is read by all: the partial sums take its place)
+  v4f *red = reinterpret_cast<v4f *>(dyn);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) red[(wave * MT + m) * 64 + lane] = acc[m];
+  __syncthreads();
+  if (wave < MT) {
+    const int m = wave;
+    v4f t = red[m * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) t += red[(w * MT + m) * 64 + lane];
+    const int row = 16 * m + r, col = n0 + 4 * g;
+    if (row < P.M) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (col + v < P.N) {
+          const float b = P.bias ? load_elem(P.bias, col + v, P.bias_dtype) : 0.0f;
+          store_elem(P.c, (int64_t)row * P.N + col + v, t[v] + b, P.c_dtype);
+        }
+    }
+  }
 }
 
 // C = sum over ranges of the fp32 partial products, in range order (+ bias), rounded.
@@ -500,40 +663,100 @@ void set_tiles(MxProblem &p, int bm, int bn, int group_log, int splits) {
   p.pairs = (p.nkb + 1) / 2;
 }
 
-template <int BM, int BN, int MINB, bool SPLIT>
+template <int BM, int BN, int NS, int MINB, bool SPLIT>
 void launch_tiled(const MxBatch &b, int dt, unsigned grid, hipStream_t stream) {
   if (SPLIT || dt == F8LIN_FP32)
-    mx_gemm_tiled_kernel<BM, BN, MINB, F8LIN_FP32, SPLIT><<<grid, 256, 0, stream>>>(b);
+    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP32, SPLIT><<<grid, 256, 0, stream>>>(b);
   else if (dt == F8LIN_BF16)
-    mx_gemm_tiled_kernel<BM, BN, MINB, F8LIN_BF16, false><<<grid, 256, 0, stream>>>(b);
+    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_BF16, false><<<grid, 256, 0, stream>>>(b);
   else
-    mx_gemm_tiled_kernel<BM, BN, MINB, F8LIN_FP16, false><<<grid, 256, 0, stream>>>(b);
+    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP16, false><<<grid, 256, 0, stream>>>(b);
+}
+
+template <int MT, bool FUSED, int XDT, int RULE>
+void launch_skinny_nw(const MxSkinny &k, hipStream_t stream) {
+  const unsigned grid = (unsigned)((k.N + 15) / 16);
+  const size_t x = FUSED ? fused_bytes(k.M, k.nkb) : 0;
+  // eight waves where there are few workgroups
+  if (grid <= XNW8)
+    mx_skinny_kernel<MT, 8, FUSED, XDT, RULE><<<grid, 512, std::max<size_t>(x, 8 * MT * 1024), stream>>>(k);
+  else
+    mx_skinny_kernel<MT, 4, FUSED, XDT, RULE><<<grid, 256, std::max<size_t>(x, 4 * MT * 1024), stream>>>(k);
+}
+
+void launch_skinny(const MxProblem &p, hipStream_t stream) {
+  MxSkinny k = {};
+  k.a = p.a, k.as = p.as, k.b = p.b, k.bs = p.bs, k.c = p.c, k.bias = p.bias;
+  k.lda = p.lda, k.lsa = p.lsa, k.ldb = p.ldb, k.lsb = p.lsb;
+  k.M = p.M, k.N = p.N, k.nb = p.nb, k.nkb = (p.nb + kBlocksPerK - 1) / kBlocksPerK;
+  k.c_dtype = p.c_dtype, k.bias_dtype = p.bias_dtype;
+  switch ((p.M + 15) / 16) {
+    case 1: launch_skinny_nw<1, false, 0, 0>(k, stream); break;
+    case 2: launch_skinny_nw<2, false, 0, 0>(k, stream); break;
+    case 3: launch_skinny_nw<3, false, 0, 0>(k, stream); break;
+    default: launch_skinny_nw<4, false, 0, 0>(k, stream); break;
+  }
 }
 
 // One launch for problems of one output type.
 void launch_batch(MxBatch &b, int dt, hipStream_t stream) {
-  int64_t big = 0;
-  for (int i = 0; i < b.count; ++i) big += ((b.p[i].M + 255) / 256) * (int64_t)((b.p[i].N + 255) / 256);
-  const bool use_big = big >= kCUs;
+  int64_t big = 0, mid = 0;
+  for (int i = 0; i < b.count; ++i) {
+    big += ((b.p[i].M + 255) / 256) * (int64_t)((b.p[i].N + 255) / 256);
+    mid += ((b.p[i].M + 127) / 128) * (int64_t)((b.p[i].N + 127) / 128);
+  }
+  const int force = getenv("XCFG") ? atoi(getenv("XCFG")) : -1;
+  const int cfg = force >= 0 ? force : big >= kCUs ? 0 : mid > kCUs ? 1 : mid > kCUs / 2 ? 2 : 3;
+  const int bm = cfg == 0 ? 256 : cfg < 3 ? 128 : 64;
   int64_t tiles = 0;
   for (int i = 0; i < b.count; ++i) {
-    set_tiles(b.p[i], use_big ? 256 : 128, use_big ? 256 : 128, use_big ? 2 : 3, 1);
+    set_tiles(b.p[i], bm, bm, cfg == 0 ? 2 : 3, 1);
     tiles += b.p[i].tiles;
   }
-  if (use_big)
-    launch_tiled<256, 256, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
+  if (cfg == 0)
+    launch_tiled<256, 256, 2, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
+  else if (cfg == 1)
+    launch_tiled<128, 128, 2, 2, false>(b, dt, (unsigned)std::min<int64_t>(tiles, 2 * kCUs), stream);
+  else if (cfg == 2)
+    launch_tiled<128, 128, 4, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
   else
-    launch_tiled<128, 128, 2, false>(b, dt, (unsigned)std::min<int64_t>(tiles, 2 * kCUs), stream);
+    launch_tiled<64, 64, 8, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
 }
 
 }  // namespace
 
 size_t mx_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-bool mx_linear_fused(int64_t, int64_t, int64_t) { return false; }
-hipError_t launch_mx_linear(const MxLinear &, hipStream_t) { return hipErrorInvalidValue; }
+// Few enough rows, and few enough bytes for every workgroup to quantise them
+// itself (at most 35 KB of LDS).
+bool mx_linear_fused(int64_t M, int64_t N, int64_t K) {
+  const int64_t nkb = (K + 8 * kBlocksPerK * 4 - 1) / (8 * kBlocksPerK * 4);
+  return M > 0 && N > 0 && K > 0 && M <= kFusedMaxM && M * nkb <= 256;
+}
+
+hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream) {
+  MxSkinny k = {};
+  k.x = l.x, k.ldx = l.ldx, k.b = l.w.codes, k.bs = l.w.scales, k.ldb = l.w.ld, k.lsb = l.w.scale_ld;
+  k.c = l.y, k.c_dtype = l.y_dtype, k.bias = l.bias, k.bias_dtype = l.bias_dtype;
+  k.M = (int)l.M, k.N = (int)l.N, k.K = (int)l.K;
+  k.nb = (int)((l.K + kMxBlock - 1) / kMxBlock), k.nkb = (k.nb + kBlocksPerK - 1) / kBlocksPerK;
+#define F8_MX_L(DT)                                              \
+  if (l.rule == F8LIN_MX_CEIL)                                   \
+    launch_skinny_nw<1, true, DT, F8LIN_MX_CEIL>(k, stream);     \
+  else                                                           \
+    launch_skinny_nw<1, true, DT, F8LIN_MX_FLOOR>(k, stream)
+  if (l.x_dtype == F8LIN_BF16) {
+    F8_MX_L(F8LIN_BF16);
+  } else if (l.x_dtype == F8LIN_FP16) {
+    F8_MX_L(F8LIN_FP16);
+  } else {
+    F8_MX_L(F8LIN_FP32);
+  }
+#undef F8_MX_L
+  return hipGetLastError();
+}
 
 hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream_t stream) {
-  MxBatch b[3] = {};  // by output type
+  MxBatch b[3] = {};  // by output type (a problem of few rows has a launch of its own)
   for (int i = 0; i < count; ++i) {
     if (d[i].M == 0 || d[i].N == 0) continue;
     if (d[i].K == 0) {
@@ -543,7 +766,7 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream
       continue;
     }
     MxBatch &list = b[d[i].c_dtype];
-    MxProblem &p = list.p[list.count++];
+    MxProblem &p = list.p[list.count];
     p.a = d[i].a.codes;
     p.as = d[i].a.scales;
     p.b = d[i].b.codes;
@@ -559,6 +782,10 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream
     p.nb = (int)((d[i].K + kMxBlock - 1) / kMxBlock);
     p.c_dtype = d[i].c_dtype;
     p.bias_dtype = d[i].bias_dtype;
+    if (p.M <= kSkinnyMaxM)
+      launch_skinny(p, stream);
+    else
+      ++list.count;
   }
   for (int dt = 0; dt < 3; ++dt)
     if (b[dt].count > 0) launch_batch(b[dt], dt, stream);
