@@ -193,6 +193,8 @@ int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *p, void *stream) {
   return status_of(launch_mx_gemms(&g, 1, a.ws, a.ws ? a.ws_bytes : 0, s));
 }
 
+int f8lin_mxfp4_forward_fused(int64_t M, int64_t N, int64_t K) { return mx_linear_fused(M, N, K) ? 1 : 0; }
+
 size_t f8lin_mxfp4_dbias_workspace_bytes(int64_t M, int64_t N) {
   if (M < 0 || N < 0) return 0;
   return (size_t)dbias_tiles(M) * (size_t)N * sizeof(float);

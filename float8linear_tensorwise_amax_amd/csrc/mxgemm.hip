@@ -756,9 +756,11 @@ hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream) {
 }
 
 hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream_t stream) {
+  bool any = false;
   MxBatch b[3] = {};  // by output type (a problem of few rows has a launch of its own)
   for (int i = 0; i < count; ++i) {
     if (d[i].M == 0 || d[i].N == 0) continue;
+    any = true;
     if (d[i].K == 0) {
       const int64_t mn = d[i].M * d[i].N;
       mx_fill_kernel<<<(unsigned)std::min<int64_t>((mn + 255) / 256, 8192), 256, 0, stream>>>(
@@ -789,7 +791,7 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream
   }
   for (int dt = 0; dt < 3; ++dt)
     if (b[dt].count > 0) launch_batch(b[dt], dt, stream);
-  return hipGetLastError();
+  return any ? hipGetLastError() : hipSuccess;
 }
 
 }  // namespace f8lin

@@ -10,6 +10,7 @@ import array
 import ctypes
 import math
 import os
+import struct
 from typing import List, Optional, Sequence
 
 import torch
@@ -485,18 +486,19 @@ class Grad(ctypes.Structure):
     _fields_ = [("g", _vp), ("out", _vp), ("n", _i64), ("dtype", _int), ("out_dtype", _int)]
 
 
-_mxp = ctypes.POINTER(MxStruct)
 _lib.f8lin_mxfp4_ld.argtypes = [_i64]
 _lib.f8lin_mxfp4_ld.restype = _i64
 _lib.f8lin_mxfp4_scale_ld.argtypes = [_i64]
 _lib.f8lin_mxfp4_scale_ld.restype = _i64
-_lib.f8lin_mxfp4_quantize.argtypes = [_vp, _int, _i64, _i64, _i64, _mxp, _mxp, _int, _vp]
-_lib.f8lin_mxfp4_dequantize.argtypes = [_mxp, _i64, _i64, _int, _vp, _vp]
-_lib.f8lin_mxfp4_gemm.argtypes = [ctypes.POINTER(MxGemmDesc), _int, _vp, ctypes.c_size_t, _vp]
+_lib.f8lin_mxfp4_quantize.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _vp]
+_lib.f8lin_mxfp4_dequantize.argtypes = [_vp, _i64, _i64, _int, _vp, _vp]
+_lib.f8lin_mxfp4_gemm.argtypes = [_vp, _int, _vp, ctypes.c_size_t, _vp]
 _lib.f8lin_mxfp4_gemm_workspace_bytes.argtypes = [_i64, _i64, _i64]
 _lib.f8lin_mxfp4_gemm_workspace_bytes.restype = ctypes.c_size_t
-_lib.f8lin_mxfp4_forward.argtypes = [ctypes.POINTER(MxFwdArgs), _vp]
-_lib.f8lin_mxfp4_backward.argtypes = [ctypes.POINTER(MxBwdArgs), _vp]
+_lib.f8lin_mxfp4_forward.argtypes = [_vp, _vp]
+_lib.f8lin_mxfp4_forward_fused.argtypes = [_i64, _i64, _i64]
+_lib.f8lin_mxfp4_forward_fused.restype = _int
+_lib.f8lin_mxfp4_backward.argtypes = [_vp, _vp]
 _lib.f8lin_mxfp4_dbias_workspace_bytes.argtypes = [_i64, _i64]
 _lib.f8lin_mxfp4_dbias_workspace_bytes.restype = ctypes.c_size_t
 _lib.f8lin_grad_workspace_bytes.argtypes = []
@@ -506,6 +508,14 @@ _lib.f8lin_grad_clip.argtypes = [_vp, _int, _int, ctypes.c_float, _vp, _int, _vp
 for _name in ("f8lin_mxfp4_quantize", "f8lin_mxfp4_dequantize", "f8lin_mxfp4_gemm", "f8lin_mxfp4_forward",
               "f8lin_mxfp4_backward", "f8lin_grad_norm", "f8lin_grad_clip"):
     getattr(_lib, _name).restype = _int
+
+
+# The argument structures as bytes: packing one costs a fraction of filling a ctypes.Structure field by field.
+_MX = struct.Struct("@4q")
+_MX_FWD = struct.Struct("@8q4i16qi4x2q")
+_MX_BWD = struct.Struct("@8q4i16qi4x4q")
+for _fmt, _cls in ((_MX, MxStruct), (_MX_FWD, MxFwdArgs), (_MX_BWD, MxBwdArgs)):
+    assert _fmt.size == ctypes.sizeof(_cls)
 
 
 def _call(fn, device: torch.device, stream, *args):
@@ -535,6 +545,8 @@ def _dense(t: torch.Tensor, what: str, device: torch.device = None) -> int:
 
 def _dense_ld(t: torch.Tensor, what: str, device: torch.device = None):
     """(pointer, row stride in elements) of a 2-D bf16 / fp16 / fp32 tensor whose rows are contiguous."""
+    if t.is_contiguous():
+        return _dense(t, what, device), t.shape[1]
     if not t.is_cuda:
         raise ValueError("f8lin: tensors must be on the GPU")
     if device is not None and t.device != device:
@@ -557,53 +569,82 @@ class MXFP4Tensor:
     scales (rows, >= ceil(cols / 32) rounded up to 16) uint8: e8m0, 2^(byte - 127), 255 for NaN
     Both with contiguous rows 16 bytes aligned.  A row's codes and scales are views into what you pass."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "_c")
+    __slots__ = ("_codes", "_scales", "rows", "cols", "device", "buffer", "_c")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         nb = -(-cols // MXFP4_BLOCK)
-        for name, t, need in (("codes", codes, 16 * nb), ("scales", scales, -(-nb // 16) * 16)):
-            if t.dtype != torch.uint8 or t.dim() != 2:
-                raise TypeError(f"MXFP4Tensor: {name} must be a 2-D uint8 tensor")
-            if not t.is_cuda or t.device != codes.device:
-                raise ValueError("MXFP4Tensor: codes and scales must be on one GPU")
-            if rows and cols and (t.shape[0] != rows or t.shape[1] < need or t.stride(1) != 1):
-                raise ValueError(f"MXFP4Tensor: {name} of a ({rows}, {cols}) tensor must be ({rows}, >= {need}) with "
-                                 "contiguous rows")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2 or scales.dim() != 2:
+            raise TypeError("MXFP4Tensor: codes and scales must be 2-D uint8 tensors")
+        if not codes.is_cuda or scales.device != codes.device:
+            raise ValueError("MXFP4Tensor: codes and scales must be on one GPU")
+        self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
+        self.device, self.buffer = codes.device, None
         if rows and cols:
-            one = rows == 1  # (a single row has no stride to speak of)
-            self._c = MxStruct(codes.data_ptr(), scales.data_ptr(), codes.shape[1] // 16 * 16 if one else codes.stride(0),
-                               scales.shape[1] // 16 * 16 if one else scales.stride(0))
+            (cr, cw), (sr, sw) = codes.shape, scales.shape
+            sn = -(-nb // 16) * 16
+            if cr != rows or sr != rows or cw < 16 * nb or sw < sn or codes.stride(1) != 1 or scales.stride(1) != 1:
+                raise ValueError(f"MXFP4Tensor: a ({rows}, {cols}) tensor has codes ({rows}, >= {16 * nb}) and scales "
+                                 f"({rows}, >= {sn}) with contiguous rows")
+            # (a single row has no stride to speak of)
+            self._c = (codes.data_ptr(), scales.data_ptr(), codes.stride(0) if rows > 1 else 16 * nb,
+                       scales.stride(0) if rows > 1 else sn)
         else:
-            self._c = MxStruct(None, None, 0, 0)
+            self._c = _NO_MX
 
-    device = property(lambda self: self.codes.device)
+    @classmethod
+    def _of(cls, buffer: torch.Tensor, rows: int, cols: int, ld: int, scale_ld: int) -> "MXFP4Tensor":
+        """The tensor laid out in one flat buffer: all codes, then all scales."""
+        t = cls.__new__(cls)
+        t._codes = t._scales = None
+        t.rows, t.cols, t.device, t.buffer = rows, cols, buffer.device, buffer
+        p = buffer.data_ptr()
+        t._c = (p, p + rows * ld, ld, scale_ld)
+        return t
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n, ld = self.rows, self._c[2]
+            self._codes = self.buffer[:n * ld].view(n, ld)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            n, ld, sld = self.rows, self._c[2], self._c[3]
+            self._scales = self.buffer[n * ld:n * (ld + sld)].view(n, sld)
+        return self._scales
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
         """The values this tensor stands for, rounded to `dtype`."""
-        out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
+        out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.device)
         mxfp4_dequantize(self, out, stream)
         return out
 
 
-_NO_MX = MxStruct(None, None, 0, 0)
+_NO_MX = (0, 0, 0, 0)
 
 
-def _mx(t: Optional[MXFP4Tensor], rows: int, cols: int, what: str, device=None) -> MxStruct:
+def _mx(t: Optional[MXFP4Tensor], rows: int, cols: int, what: str, device=None):
+    """(codes, scales, ld, scale_ld) as f8lin_mxfp4 has them."""
     if t is None:
         return _NO_MX
-    if (t.rows, t.cols) != (rows, cols):
+    if t.rows != rows or t.cols != cols:
         raise ValueError(f"f8lin: {what} must be a ({rows}, {cols}) MXFP4 tensor, got ({t.rows}, {t.cols})")
-    if device is not None and t.codes.device != device:
-        raise ValueError(f"f8lin: {what} is on {t.codes.device}, expected {device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"f8lin: {what} is on {t.device}, expected {device}")
     return t._c
 
 
 def new_mxfp4(rows: int, cols: int, device="cuda") -> MXFP4Tensor:
     """An uninitialised MXFP4 tensor with the library's strides."""
     ld, sld = _lib.f8lin_mxfp4_ld(cols), _lib.f8lin_mxfp4_scale_ld(cols)
-    buf = torch.empty(rows * (ld + sld), dtype=torch.uint8, device=device)
-    return MXFP4Tensor(buf[:rows * ld].view(rows, ld), buf[rows * ld:].view(rows, sld), rows, cols)
+    return MXFP4Tensor._of(torch.empty(rows * (ld + sld), dtype=torch.uint8, device=device), rows, cols, ld, sld)
+
+
+def mxfp4_of(buffer: torch.Tensor, rows: int, cols: int) -> MXFP4Tensor:
+    """The (rows, cols) tensor that new_mxfp4 laid out in `buffer` (its .buffer)."""
+    return MXFP4Tensor._of(buffer, rows, cols, _lib.f8lin_mxfp4_ld(cols), _lib.f8lin_mxfp4_scale_ld(cols))
 
 
 def mxfp4_quantize(x: torch.Tensor, q: Optional[MXFP4Tensor], qt: Optional[MXFP4Tensor] = None, rule="floor",
@@ -614,9 +655,9 @@ def mxfp4_quantize(x: torch.Tensor, q: Optional[MXFP4Tensor], qt: Optional[MXFP4
         raise ValueError("mxfp4_quantize takes a 2-D tensor")
     rows, cols = x.shape
     p, ld = _dense_ld(x, "x")
-    a, b = _mx(q, rows, cols, "q", x.device), _mx(qt, cols, rows, "qt", x.device)
-    _call(_lib.f8lin_mxfp4_quantize, x.device, stream, p, _DTYPE[x.dtype], rows, cols, ld, ctypes.byref(a),
-          ctypes.byref(b), _RULE[rule])
+    dev = x.device
+    _call(_lib.f8lin_mxfp4_quantize, dev, stream, p, _DTYPE[x.dtype], rows, cols, ld,
+          _MX.pack(*_mx(q, rows, cols, "q", dev)), _MX.pack(*_mx(qt, cols, rows, "qt", dev)), _RULE[rule])
 
 
 def mxfp4_dequantize(q: MXFP4Tensor, out: torch.Tensor, stream=None):
@@ -624,7 +665,7 @@ def mxfp4_dequantize(q: MXFP4Tensor, out: torch.Tensor, stream=None):
     if tuple(out.shape) != (q.rows, q.cols):
         raise ValueError("mxfp4_dequantize: shape mismatch")
     p = _dense(out, "out", q.device)
-    _call(_lib.f8lin_mxfp4_dequantize, out.device, stream, ctypes.byref(q._c), q.rows, q.cols, _DTYPE[out.dtype], p)
+    _call(_lib.f8lin_mxfp4_dequantize, out.device, stream, _MX.pack(*q._c), q.rows, q.cols, _DTYPE[out.dtype], p)
 
 
 def mxfp4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -643,12 +684,17 @@ def mxfp4_gemm(items, ws: Optional[torch.Tensor] = None, stream=None):
         dev = c.device if dev is None else dev
         if b.cols != K or tuple(c.shape) != (M, N) or (bias is not None and tuple(bias.shape) != (N,)):
             raise ValueError("mxfp4_gemm: shape mismatch")
-        arr[i] = MxGemmDesc(_mx(a, M, K, "a", dev), _mx(b, N, K, "b", dev), _dense(c, "c", dev),
+        arr[i] = MxGemmDesc(MxStruct(*_mx(a, M, K, "a", dev)), MxStruct(*_mx(b, N, K, "b", dev)), _dense(c, "c", dev),
                             None if bias is None else _dense(bias, "bias", dev), M, N, K, _DTYPE[c.dtype],
                             0 if bias is None else _DTYPE[bias.dtype])
     if dev is None:
         raise ValueError("mxfp4_gemm: no products given")
     _call(_lib.f8lin_mxfp4_gemm, dev, stream, arr, len(items), _ptr(ws), _nbytes(ws))
+
+
+def mxfp4_forward_fused(M: int, N: int, K: int) -> bool:
+    """Whether mxfp4_forward with a quantised weight and no x4t quantises X inside the product (x4 may be None)."""
+    return bool(_lib.f8lin_mxfp4_forward_fused(M, N, K))
 
 
 def mxfp4_forward(x, w, y, x4: Optional[MXFP4Tensor], w4: MXFP4Tensor, x4t=None, w4t=None, bias=None, rule="floor",
@@ -662,12 +708,12 @@ def mxfp4_forward(x, w, y, x4: Optional[MXFP4Tensor], w4: MXFP4Tensor, x4t=None,
             (bias is not None and tuple(bias.shape) != (N,)):
         raise ValueError("mxfp4_forward: shape mismatch")
     px, ldx = _dense_ld(x, "x")
-    a = MxFwdArgs(M, N, K, px, None if w is None else _dense(w, "w", dev), ldx, _dense(y, "y", dev),
-                  None if bias is None else _dense(bias, "bias", dev), _DTYPE[x.dtype],
-                  0 if w is None else _DTYPE[w.dtype], _DTYPE[y.dtype], 0 if bias is None else _DTYPE[bias.dtype],
-                  _mx(x4, M, K, "x4", dev), _mx(x4t, K, M, "x4t", dev), _mx(w4, N, K, "w4", dev),
-                  _mx(w4t, K, N, "w4t", dev), _RULE[rule], _ptr(ws), _nbytes(ws))
-    _call(_lib.f8lin_mxfp4_forward, dev, stream, ctypes.byref(a))
+    a = _MX_FWD.pack(M, N, K, px, 0 if w is None else _dense(w, "w", dev), ldx, _dense(y, "y", dev),
+                     0 if bias is None else _dense(bias, "bias", dev), _DTYPE[x.dtype],
+                     0 if w is None else _DTYPE[w.dtype], _DTYPE[y.dtype], 0 if bias is None else _DTYPE[bias.dtype],
+                     *_mx(x4, M, K, "x4", dev), *_mx(x4t, K, M, "x4t", dev), *_mx(w4, N, K, "w4", dev),
+                     *_mx(w4t, K, N, "w4t", dev), _RULE[rule], _ptr(ws) or 0, _nbytes(ws))
+    _call(_lib.f8lin_mxfp4_forward, dev, stream, a)
 
 
 def mxfp4_dbias_workspace_bytes(M: int, N: int) -> int:
@@ -686,14 +732,14 @@ def mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, dbias=None, dbias_ws=None, r
             (dbias is not None and tuple(dbias.shape) != (N,)):
         raise ValueError("mxfp4_backward: shape mismatch")
     p, ld = _dense_ld(dy, "dy")
-    opt = lambda t, what: None if t is None else _dense(t, what, dev)  # noqa: E731
+    opt = lambda t, what: 0 if t is None else _dense(t, what, dev)  # noqa: E731
     dt = lambda t: 0 if t is None else _DTYPE[t.dtype]  # noqa: E731
-    a = MxBwdArgs(M, N, K, p, ld, opt(dx, "dx"), opt(dw, "dw"), opt(dbias, "dbias"), _DTYPE[dy.dtype], dt(dx), dt(dw),
-                  dt(dbias), _mx(x4t if dw is not None else None, K, M, "x4t", dev),
-                  _mx(w4t if dx is not None else None, K, N, "w4t", dev), _mx(dy4, M, N, "dy4", dev),
-                  _mx(dy4t, N, M, "dy4t", dev), _RULE[rule], _ptr(dbias_ws, torch.float32), _nbytes(dbias_ws),
-                  _ptr(ws), _nbytes(ws))
-    _call(_lib.f8lin_mxfp4_backward, dev, stream, ctypes.byref(a))
+    a = _MX_BWD.pack(M, N, K, p, ld, opt(dx, "dx"), opt(dw, "dw"), opt(dbias, "dbias"), _DTYPE[dy.dtype], dt(dx), dt(dw),
+                     dt(dbias), *_mx(x4t if dw is not None else None, K, M, "x4t", dev),
+                     *_mx(w4t if dx is not None else None, K, N, "w4t", dev), *_mx(dy4, M, N, "dy4", dev),
+                     *_mx(dy4t, N, M, "dy4t", dev), _RULE[rule], _ptr(dbias_ws, torch.float32) or 0, _nbytes(dbias_ws),
+                     _ptr(ws) or 0, _nbytes(ws))
+    _call(_lib.f8lin_mxfp4_backward, dev, stream, a)
 
 
 # --------------------------------------------------- gradient norm and clipping

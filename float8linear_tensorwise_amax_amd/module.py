@@ -344,6 +344,8 @@ def _workspace(n: int, device) -> Optional[torch.Tensor]:
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """t as a 2-D tensor with contiguous rows (a copy only where its strides need one)."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t
     t = t.reshape(-1, t.shape[-1])
     if t.numel() and ((t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
         t = t.contiguous()
@@ -364,8 +366,7 @@ class _MXFP4LinearFn(torch.autograd.Function):
         w4t = f8lin.new_mxfp4(K, N, dev) if ctx.needs_input_grad[0] else None
         ws = _workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), dev)
         f8lin.mxfp4_forward(x, w, y, x4, w4, x4t, w4t, None if bias is None else bias.contiguous(), rule, ws)
-        saved = [t for q in (x4t, w4t) if q is not None for t in (q.codes, q.scales)]
-        ctx.save_for_backward(*saved)
+        ctx.save_for_backward(*(q.buffer for q in (x4t, w4t) if q is not None))
         ctx.args = (M, N, K, rule, x.dtype, weight.dtype, None if bias is None else bias.dtype)
         return y
 
@@ -376,8 +377,8 @@ class _MXFP4LinearFn(torch.autograd.Function):
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         dev = dy.device
         saved = list(ctx.saved_tensors)
-        x4t = f8lin.MXFP4Tensor(saved.pop(0), saved.pop(0), K, M) if need_w else None
-        w4t = f8lin.MXFP4Tensor(saved.pop(0), saved.pop(0), K, N) if need_x else None
+        x4t = f8lin.mxfp4_of(saved.pop(0), K, M) if need_w else None
+        w4t = f8lin.mxfp4_of(saved.pop(0), K, N) if need_x else None
         dy = _rows(dy)
         dx = torch.empty((M, K), dtype=x_dtype, device=dev) if need_x else None
         dw = torch.empty((N, K), dtype=w_dtype, device=dev) if need_w else None
@@ -415,10 +416,11 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
         raise RuntimeError("mxfp4_linear: a quantised weight has no backward; call it under torch.no_grad()")
     M = x2.shape[0]
     y = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    f8lin.mxfp4_forward(x2, None, y, f8lin.new_mxfp4(M, K, x.device), weight,
+    fused = f8lin.mxfp4_forward_fused(M, N, K)  # X is quantised inside the product: no buffers
+    f8lin.mxfp4_forward(x2, None, y, None if fused else f8lin.new_mxfp4(M, K, x.device), weight,
                         bias=None if bias is None else bias.contiguous(), rule=rule,
-                        ws=_workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), x.device))
-    return y.reshape(*lead, N)
+                        ws=None if fused else _workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), x.device))
+    return y if x.dim() == 2 else y.reshape(*lead, N)
 
 
 class MXFP4Linear(nn.Module):

@@ -445,9 +445,9 @@ size_t f8lin_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * w != NULL (training): X and W are quantised, x4 / w4 for this product and,
  * where their codes are not NULL, x4t / w4t for the backward.
  * w == NULL (serving, or a weight quantised before): w4 already holds W and
- * w4t is not touched.  With few rows and no x4t the quantisation of X then
- * happens inside the product's kernel and x4 is left unwritten: x4 is scratch
- * unless x4t is asked for.
+ * w4t is not touched.  Where f8lin_mxfp4_forward_fused(M, N, K) is nonzero
+ * (few rows) and no x4t is asked for, X is then quantised inside the product's
+ * kernel and x4 is not used: its pointers may be NULL.
  * Errors as above; nothing is launched on error. */
 typedef struct {
   int64_t M, N, K;
@@ -462,6 +462,7 @@ typedef struct {
   size_t ws_bytes;
 } f8lin_mxfp4_fwd_args;
 int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *args, void *stream);
+int f8lin_mxfp4_forward_fused(int64_t M, int64_t N, int64_t K);
 
 /* Its backward: dY (M, N) is quantised along N (dy4) and along M (dy4t), then
  *   dX (M, K) = dY4 . W4t^T  (contraction over N)
