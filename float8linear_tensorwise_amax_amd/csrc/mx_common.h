@@ -98,23 +98,105 @@ __device__ __forceinline__ uint32_t f32_to_elem(float v, int dt) {
 }
 __host__ __device__ __forceinline__ int elem_bytes(int dt) { return dt == F8LIN_FP32 ? 4 : 2; }
 
-// Eight values of type DT at p (any element address) as binary32; `n` of them
-// exist (the rest read as +0).
+// Eight consecutive elements as they lie in memory: the 16-bit types in
+// pairs, as the conversion instructions take them.
 template <int DT>
-__device__ __forceinline__ void load8(const typename MxElem<DT>::type *p, int n, float (&v)[8]) {
+struct Raw8 {
+  u32x4 w[DT == F8LIN_FP32 ? 2 : 1];
+};
+
+// Eight elements of type DT at p (any element address); `n` of them exist
+// (the rest read as +0).
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const typename MxElem<DT>::type *p, int n) {
+  Raw8<DT> r;
   if (n >= 8) {
+    r.w[0] = *reinterpret_cast<const u32x4_u *>(p);
+    if constexpr (DT == F8LIN_FP32) r.w[1] = *reinterpret_cast<const u32x4_u *>(p + 4);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? (uint32_t)p[i] : 0u;
     if constexpr (DT == F8LIN_FP32) {
-      const u32x4 a = *reinterpret_cast<const u32x4_u *>(p), b = *reinterpret_cast<const u32x4_u *>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
+      r.w[0] = u32x4{e[0], e[1], e[2], e[3]};
+      r.w[1] = u32x4{e[4], e[5], e[6], e[7]};
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4_u *>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[2 * i] = elem_f32<DT>(a[i] & 0xFFFFu), v[2 * i + 1] = elem_f32<DT>(a[i] >> 16);
+      r.w[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     }
+  }
+  return r;
+}
+
+// Largest magnitude of pairs of 16-bit elements, per half (integer order of
+// the magnitude bits is the order of the values, NaN last).
+__device__ __forceinline__ uint32_t pair_mag_max(uint32_t m, uint32_t w) {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, m),
+                                                                __builtin_bit_cast(u16x2_t, w & 0x7FFF7FFFu)));
+}
+
+// binary32 bits of the 16-bit magnitude m.
+template <int DT>
+__device__ __forceinline__ uint32_t mag_f32_bits(uint32_t m) {
+  if constexpr (DT == F8LIN_BF16) return m << 16;
+  if constexpr (DT == F8LIN_FP16) return __float_as_uint(f16_bits_to_f32(m));
+  return m;
+}
+
+// Largest magnitude of the eight, as bits of type DT.
+template <int DT>
+__device__ __forceinline__ uint32_t raw_mag(const Raw8<DT> &r) {
+  uint32_t m = 0;
+  if constexpr (DT == F8LIN_FP32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(r.w[0][i] & 0x7FFFFFFFu, r.w[1][i] & 0x7FFFFFFFu));
+    return m;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? elem_f32<DT>(p[i]) : 0.0f;
+    for (int i = 0; i < 4; ++i) m = pair_mag_max(m, r.w[0][i]);
+    return max(m & 0xFFFFu, m >> 16);
+  }
+}
+
+// Two elements (a packed pair) -> two codes in byte `SEL` of r.
+template <int DT, int SEL>
+__device__ __forceinline__ uint32_t cvt_pair(uint32_t r, uint32_t w, float scale) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  if constexpr (DT == F8LIN_BF16)
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2_t, w), scale, SEL);
+  else
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(f16x2_t, w), scale, SEL);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t cvt_pairs(uint32_t a, uint32_t b, uint32_t c, uint32_t d, float scale) {
+  uint32_t r = 0;
+  r = cvt_pair<DT, 0>(r, a, scale);
+  r = cvt_pair<DT, 1>(r, b, scale);
+  r = cvt_pair<DT, 2>(r, c, scale);
+  return cvt_pair<DT, 3>(r, d, scale);
+}
+
+// The eight elements' codes.
+template <int DT>
+__device__ __forceinline__ uint32_t raw_codes(const Raw8<DT> &r, float scale) {
+  if constexpr (DT == F8LIN_FP32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
+    return mx_cvt8(v, scale);
+  } else {
+    return cvt_pairs<DT>(r.w[0][0], r.w[0][1], r.w[0][2], r.w[0][3], scale);
+  }
+}
+
+// Eight values of type DT at p as binary32; `n` of them exist (the rest +0).
+template <int DT>
+__device__ __forceinline__ void load8(const typename MxElem<DT>::type *p, int n, float (&v)[8]) {
+  const Raw8<DT> r = load_raw8<DT>(p, n);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (DT == F8LIN_FP32) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
+    else v[i] = elem_f32<DT>((r.w[0][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
   }
 }
 

@@ -4,18 +4,23 @@
 // needs.  The block arithmetic is in mx_common.h.
 //
 // HBM-bound: es bytes read and 17/32 byte written per element and layout.
-// Work decomposition: one workgroup of 256 threads per 128 x 128 tile.
-//   load : thread t reads 8 consecutive elements of rows t/16 + 16 p: sixteen
-//          lanes cover 128 columns of a row.
-//   rows : a block is four lanes; its maximum meets by two DPP quad
-//          permutations, each lane converts its eight values to one 32-bit
-//          word, and sixteen lanes store 64 contiguous bytes.
+// Rows alone (mx_rows_kernel): a thread takes eight consecutive elements of
+// four rows, all four loads in flight; a block is four lanes, whose maxima
+// meet by two DPP quad permutations.
+// Columns, or both (mx_quantize_kernel): one workgroup of 256 threads per 128
+// x 128 tile, all of its loads in flight at once.
+//   rows : sixteen lanes cover 128 columns of a row and store 64 contiguous
+//          bytes of codes and one word of scales.
 //   cols : the tile goes to LDS as it is; thread t then owns the 32-row block
 //          t % 4 of column pair t / 4: it reads 32 words down the tile, has
 //          both columns' maxima in its own registers, and stores 16 bytes
 //          for each column, four lanes covering 64 contiguous bytes of a
 //          transposed row.  Words are XOR-ed with 16 * (row / 32), so that the
 //          four row blocks that one read touches fall in different banks.
+//   An XCD takes a contiguous run of tiles (workgroup b runs on XCD b % 8),
+//   so that the halves of a 128-byte line of codes meet in one L2.
+// 16-bit elements stay packed pairs throughout: maxima by packed 16-bit max,
+// codes by v_cvt_scalef32_pk_fp4_{bf16,f16}.
 #include <algorithm>
 
 #include "mx_common.h"
@@ -31,118 +36,160 @@ struct QuantJob {
   int64_t rows, cols, ldx;
   f8lin_mxfp4 q, qt;
   float *colsum;
-  int tiles_x, first;
+  int tiles_x, first, log_tx;
 };
 struct QuantJobs {
   QuantJob j[kMxMaxQuant];
   int count;
 };
 
-template <int DT, int RULE, bool ROWS, bool COLS>
+// The scale bytes of the four blocks that sixteen lanes hold (block q in lanes
+// 4 q .. 4 q + 3), as one word in all of them.
+__device__ __forceinline__ int scales_of_16(int e, int q) {
+  int sw = e << (8 * q);
+  sw |= __builtin_amdgcn_mov_dpp(sw, 0x124, 0xF, 0xF, true);         // row_ror 4
+  return sw | __builtin_amdgcn_mov_dpp(sw, 0x128, 0xF, 0xF, true);  // row_ror 8
+}
+
+// Rows alone.  A workgroup covers tx = 2^log_tx chunks of eight elements by
+// kRowsPer * 256 / tx rows.
+constexpr int kRowsPer = 4;
+template <int DT, int RULE>
+__global__ __launch_bounds__(kThreads) void mx_rows_kernel(const QuantJobs jobs) {
+  typedef typename MxElem<DT>::type elem;
+  const int job = jobs.count > 1 && (int)blockIdx.x >= jobs.j[1].first ? 1 : 0;
+  const QuantJob &jb = jobs.j[job];
+  const int local = (int)blockIdx.x - jb.first;
+  const int tx = (int)threadIdx.x & ((1 << jb.log_tx) - 1), ty = (int)threadIdx.x >> jb.log_tx;
+  const int64_t col = ((int64_t)(local % jb.tiles_x) << (jb.log_tx + 3)) + 8 * tx;
+  const int64_t row0 = (int64_t)(local / jb.tiles_x) * (kRowsPer * (kThreads >> jb.log_tx)) + ty;
+  const int have = (int)min((int64_t)8, max((int64_t)0, jb.cols - col));
+  const elem *x = reinterpret_cast<const elem *>(jb.x);
+  Raw8<DT> v[kRowsPer];
+#pragma unroll
+  for (int p = 0; p < kRowsPer; ++p) {
+    const int64_t row = row0 + (int64_t)p * (kThreads >> jb.log_tx);
+    v[p] = load_raw8<DT>(x + row * jb.ldx + col, row < jb.rows ? have : 0);
+  }
+#pragma unroll
+  for (int p = 0; p < kRowsPer; ++p) {
+    const int64_t row = row0 + (int64_t)p * (kThreads >> jb.log_tx);
+    const int e = mx_scale_byte<RULE>(mag_f32_bits<DT>(quad_max(raw_mag<DT>(v[p]))));
+    const uint32_t code = e == kMxNan ? 0u : raw_codes<DT>(v[p], mx_scale_f32(e));
+    const int sw = scales_of_16(e, (tx >> 2) & 3);
+    if (row < jb.rows) {
+      // (a block that starts inside the row is stored whole: its codes past cols are +0)
+      if ((col & ~31) < jb.cols) *reinterpret_cast<uint32_t *>(jb.q.codes + row * jb.q.ld + col / 2) = code;
+      if ((tx & 15) == 0 && col < jb.cols) *reinterpret_cast<int *>(jb.q.scales + row * jb.q.scale_ld + col / 32) = sw;
+    }
+  }
+}
+
+template <int DT, int RULE, bool ROWS>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs jobs) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kWords = DT == F8LIN_FP32 ? 2 : 1;  // 32-bit words of a column pair
-  __shared__ __attribute__((aligned(16))) uint32_t tile[COLS ? kTile * kTile / 2 * kWords : 4];
-  const int job = jobs.count > 1 && (int)blockIdx.x >= jobs.j[1].first ? 1 : 0;
+  constexpr int kPitch = kTile / 2 * kWords;
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * kPitch];
+  const int per = (int)gridDim.x / 8, rem = (int)gridDim.x % 8, xcd = (int)blockIdx.x % 8;
+  const int wg = xcd * per + min(xcd, rem) + (int)blockIdx.x / 8;
+  const int job = jobs.count > 1 && wg >= jobs.j[1].first ? 1 : 0;
   const QuantJob &jb = jobs.j[job];
   const int64_t rows = jb.rows, cols = jb.cols;
-  const int local = (int)blockIdx.x - jb.first;
+  const int local = wg - jb.first;
   const int64_t row0 = (int64_t)(local / jb.tiles_x) * kTile, col0 = (int64_t)(local % jb.tiles_x) * kTile;
   const int t = threadIdx.x, c8 = t & 15;
   const elem *x = reinterpret_cast<const elem *>(jb.x);
   const int64_t gcol = col0 + 8 * c8;
   const int have = (int)min((int64_t)8, max((int64_t)0, cols - gcol));
-
-#pragma unroll 4
-  for (int p = 0; p < 8; ++p) {
-    const int r = (t >> 4) + 16 * p;
-    const int64_t grow = row0 + r;
-    float v[8];
-    load8<DT>(x + grow * jb.ldx + gcol, grow < rows ? have : 0, v);
-    if constexpr (ROWS) {
-      uint32_t m = 0;
+  Raw8<DT> in[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      const int e = mx_scale_byte<RULE>(quad_max(m));
-      const uint32_t code = e == kMxNan ? 0u : mx_cvt8(v, mx_scale_f32(e));
-      // the four blocks' scale bytes of the row meet in one word
-      int sw = e << (8 * (c8 >> 2));
-      sw |= __builtin_amdgcn_mov_dpp(sw, 0x124, 0xF, 0xF, true);  // row_ror 4
-      sw |= __builtin_amdgcn_mov_dpp(sw, 0x128, 0xF, 0xF, true);  // row_ror 8
+  for (int p = 0; p < 8; ++p) {
+    const int64_t grow = row0 + (t >> 4) + 16 * p;
+    in[p] = load_raw8<DT>(x + grow * jb.ldx + gcol, grow < rows ? have : 0);
+  }
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int r = (t >> 4) + 16 * p, rb = r >> 5;
+    const int64_t grow = row0 + r;
+    if constexpr (DT == F8LIN_FP32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4 *>(&tile[r * kPitch + ((8 * c8 + 4 * h) ^ (32 * rb))]) = in[p].w[h];
+    } else {
+      *reinterpret_cast<u32x4 *>(&tile[r * kPitch + ((4 * c8) ^ (16 * rb))]) = in[p].w[0];
+    }
+    if constexpr (ROWS) {
+      const int e = mx_scale_byte<RULE>(mag_f32_bits<DT>(quad_max(raw_mag<DT>(in[p]))));
+      const uint32_t code = e == kMxNan ? 0u : raw_codes<DT>(in[p], mx_scale_f32(e));
+      const int sw = scales_of_16(e, c8 >> 2);
       if (grow < rows) {
-        // (a block that starts inside the row is stored whole: its codes past cols are +0)
         if (col0 + 32 * (c8 >> 2) < cols)
           *reinterpret_cast<uint32_t *>(jb.q.codes + grow * jb.q.ld + col0 / 2 + 4 * c8) = code;
         if (c8 == 0) *reinterpret_cast<int *>(jb.q.scales + grow * jb.q.scale_ld + col0 / 32) = sw;
       }
     }
-    if constexpr (COLS) {
-      const int rb = r >> 5;
-      if constexpr (DT == F8LIN_FP32) {
+  }
+  __syncthreads();
+  const int rb = t & 3, cp = t >> 2;
+  const bool block_ok = row0 + 32 * rb < rows;
+  // the column pair's 32 rows, and its two maxima
+  uint32_t v[kWords][32], m[2] = {0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int w = (8 * c8 + 4 * h) ^ (32 * rb);
-          *reinterpret_cast<u32x4 *>(&tile[r * 128 + w]) =
-              u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
-                    __float_as_uint(v[4 * h + 3])};
-        }
-      } else {
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = f32_to_elem(v[2 * i], DT) | f32_to_elem(v[2 * i + 1], DT) << 16;
-        *reinterpret_cast<u32x4 *>(&tile[r * 64 + ((4 * c8) ^ (16 * rb))]) = w;
-      }
+  for (int i = 0; i < 32; ++i) {
+    const int r = 32 * rb + i;
+    if constexpr (DT == F8LIN_FP32) {
+      const u32x2 w = *reinterpret_cast<const u32x2 *>(&tile[r * kPitch + ((2 * cp) ^ (32 * rb))]);
+      v[0][i] = w.x, v[1][i] = w.y;
+      m[0] = max(m[0], w.x & 0x7FFFFFFFu);
+      m[1] = max(m[1], w.y & 0x7FFFFFFFu);
+    } else {
+      v[0][i] = tile[r * kPitch + (cp ^ (16 * rb))];
+      m[0] = pair_mag_max(m[0], v[0][i]);
     }
   }
-
-  if constexpr (COLS) {
-    __syncthreads();
-    const int rb = t & 3, cp = t >> 2;
-    const bool block_ok = row0 + 32 * rb < rows;
-    float v[2][32];
+  if constexpr (DT != F8LIN_FP32) m[1] = m[0] >> 16, m[0] &= 0xFFFFu;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int r = 32 * rb + i;
+  for (int h = 0; h < 2; ++h) {
+    const int64_t col = col0 + 2 * cp + h;
+    const int e = mx_scale_byte<RULE>(mag_f32_bits<DT>(m[h]));
+    const float s = mx_scale_f32(e);
+    u32x4 out;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
       if constexpr (DT == F8LIN_FP32) {
-        const u32x2 w = *reinterpret_cast<const u32x2 *>(&tile[r * 128 + ((2 * cp) ^ (32 * rb))]);
-        v[0][i] = __uint_as_float(w.x), v[1][i] = __uint_as_float(w.y);
-      } else {
-        const uint32_t w = tile[r * 64 + (cp ^ (16 * rb))];
-        v[0][i] = elem_f32<DT>(w & 0xFFFFu), v[1][i] = elem_f32<DT>(w >> 16);
-      }
-    }
-    float cs[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t col = col0 + 2 * cp + h;
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[h][i]) & 0x7FFFFFFFu);
-      const int e = mx_scale_byte<RULE>(m);
-      u32x4 out;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
         float g[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = v[h][8 * d + i];
-        out[d] = e == kMxNan ? 0u : mx_cvt8(g, mx_scale_f32(e));
-      }
-      int sw = e << (8 * rb);
-      sw |= __builtin_amdgcn_mov_dpp(sw, 0xB1, 0xF, 0xF, true);
-      sw |= __builtin_amdgcn_mov_dpp(sw, 0x4E, 0xF, 0xF, true);
-      if (col < cols) {
-        if (block_ok) *reinterpret_cast<u32x4 *>(jb.qt.codes + col * jb.qt.ld + row0 / 2 + 16 * rb) = out;
-        if (rb == 0) *reinterpret_cast<int *>(jb.qt.scales + col * jb.qt.scale_ld + row0 / 32) = sw;
-      }
-      if (jb.colsum) {
+        for (int i = 0; i < 8; ++i) g[i] = __uint_as_float(v[h][8 * d + i]);
+        out[d] = mx_cvt8(g, s);
+      } else {
+        // the column's elements of two rows side by side
+        constexpr uint32_t kSel[2] = {0x05040100u, 0x07060302u};
+        uint32_t g[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) cs[h] += v[h][i];
-        // the four row blocks in a fixed order: (0 + 1) + (2 + 3)
-        cs[h] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(cs[h]), 0xB1, 0xF, 0xF, true));
-        cs[h] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(cs[h]), 0x4E, 0xF, 0xF, true));
-        if (rb == 0 && col < cols) jb.colsum[(row0 / kTile) * cols + col] = cs[h];
+        for (int i = 0; i < 4; ++i) g[i] = __builtin_amdgcn_perm(v[0][8 * d + 2 * i + 1], v[0][8 * d + 2 * i], kSel[h]);
+        out[d] = cvt_pairs<DT>(g[0], g[1], g[2], g[3], s);
       }
+      if (e == kMxNan) out[d] = 0;
+    }
+    int sw = e << (8 * rb);
+    sw |= __builtin_amdgcn_mov_dpp(sw, 0xB1, 0xF, 0xF, true);
+    sw |= __builtin_amdgcn_mov_dpp(sw, 0x4E, 0xF, 0xF, true);
+    if (col < cols) {
+      if (block_ok) *reinterpret_cast<u32x4 *>(jb.qt.codes + col * jb.qt.ld + row0 / 2 + 16 * rb) = out;
+      if (rb == 0) *reinterpret_cast<int *>(jb.qt.scales + col * jb.qt.scale_ld + row0 / 32) = sw;
+    }
+    if (jb.colsum) {
+      float cs = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if constexpr (DT == F8LIN_FP32) cs += __uint_as_float(v[h][i]);
+        else cs += elem_f32<DT>((v[0][i] >> (16 * h)) & 0xFFFFu);
+      }
+      // the four row blocks in a fixed order: (0 + 1) + (2 + 3)
+      cs += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(cs), 0xB1, 0xF, 0xF, true));
+      cs += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(cs), 0x4E, 0xF, 0xF, true));
+      if (rb == 0 && col < cols) jb.colsum[(row0 / kTile) * cols + col] = cs;
     }
   }
 }
@@ -200,28 +247,38 @@ __global__ __launch_bounds__(kThreads) void mx_dbias_kernel(const float *__restr
 template <int DT, int RULE>
 void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, bool cols, hipStream_t stream) {
   if (rows && cols)
-    mx_quantize_kernel<DT, RULE, true, true><<<grid, kThreads, 0, stream>>>(jobs);
+    mx_quantize_kernel<DT, RULE, true><<<grid, kThreads, 0, stream>>>(jobs);
   else if (rows)
-    mx_quantize_kernel<DT, RULE, true, false><<<grid, kThreads, 0, stream>>>(jobs);
+    mx_rows_kernel<DT, RULE><<<grid, kThreads, 0, stream>>>(jobs);
   else
-    mx_quantize_kernel<DT, RULE, false, true><<<grid, kThreads, 0, stream>>>(jobs);
+    mx_quantize_kernel<DT, RULE, false><<<grid, kThreads, 0, stream>>>(jobs);
 }
 
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_t stream) {
+  const bool rows = ts[0].q.codes != nullptr, cols = ts[0].qt.codes != nullptr;
   QuantJobs jobs = {};
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
     const MxQuant &t = ts[i];
     if (t.rows == 0 || t.cols == 0) continue;
-    const int64_t gx = (t.cols + kTile - 1) / kTile, gy = (t.rows + kTile - 1) / kTile;
+    int64_t gx, gy;
+    int log_tx = 0;
+    if (cols) {
+      gx = (t.cols + kTile - 1) / kTile, gy = (t.rows + kTile - 1) / kTile;
+    } else {
+      // as many threads along a row as it has chunks, 16 to 256
+      log_tx = 4;
+      while (log_tx < 8 && (8 << log_tx) < t.cols) ++log_tx;
+      const int64_t per = kRowsPer * (kThreads >> log_tx);
+      gx = (t.cols + (8 << log_tx) - 1) / (8 << log_tx), gy = (t.rows + per - 1) / per;
+    }
     jobs.j[jobs.count++] =
-        QuantJob{t.x, t.rows, t.cols, t.ldx, t.q, t.qt, t.colsum, (int)gx, (int)total};
+        QuantJob{t.x, t.rows, t.cols, t.ldx, t.q, t.qt, t.colsum, (int)gx, (int)total, log_tx};
     total += gx * gy;
   }
   if (jobs.count == 0) return hipSuccess;
-  const bool rows = ts[0].q.codes != nullptr, cols = ts[0].qt.codes != nullptr;
   const unsigned grid = (unsigned)total;
 #define F8_MX_Q(DT)                                                             \
   if (rule == F8LIN_MX_CEIL)                                                    \

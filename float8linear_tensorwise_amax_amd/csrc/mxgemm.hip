@@ -565,13 +565,9 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
     for (int m = 0; m < P.M; ++m) {
       const elem *x = reinterpret_cast<const elem *>(P.x) + m * P.ldx;
       for (int i = threadIdx.x; i < P.nkb * kBlocksPerK * 4; i += 64 * NW) {  // eight values each, a block per quad
-        float v[8];
-        load8<XDT>(x + 8 * i, P.K - 8 * i, v);
-        uint32_t mag = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mag = max(mag, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-        const int e = mx_scale_byte<RULE>(quad_max(mag));
-        *reinterpret_cast<uint32_t *>(dyn + m * xrow + 4 * i) = e == kMxNan ? 0u : mx_cvt8(v, mx_scale_f32(e));
+        const Raw8<XDT> v = load_raw8<XDT>(x + 8 * i, P.K - 8 * i);
+        const int e = mx_scale_byte<RULE>(mag_f32_bits<XDT>(quad_max(raw_mag<XDT>(v))));
+        *reinterpret_cast<uint32_t *>(dyn + m * xrow + 4 * i) = e == kMxNan ? 0u : raw_codes<XDT>(v, mx_scale_f32(e));
         if ((i & 3) == 0) xs[m * xsrow + (i >> 2)] = (uint8_t)e;
       }
     }
