@@ -129,12 +129,12 @@ struct MxQuant {
   int dtype;
   int64_t rows, cols, ldx;
   f8lin_mxfp4 q, qt;
-  // if set (needs qt): fp32 column sums over each 128-row tile,
+  // if set (needs qt): fp32 column sums over each kMxTile rows,
   // colsum[tile_row * cols + col], for the bias gradient
   float *colsum;
 };
 hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_t stream);
-constexpr int kMxTile = 128;
+constexpr int kMxTile = 128;  // rows of a column sum
 hipError_t launch_mx_dequantize(const f8lin_mxfp4 &q, int64_t rows, int64_t cols, int dtype, void *out,
                                 hipStream_t stream);
 hipError_t launch_mx_dbias(const float *colsum, int64_t tiles, int64_t n, void *db, int dtype, hipStream_t stream);
@@ -166,8 +166,15 @@ struct MxLinear {
 bool mx_linear_fused(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream);
 
-// Row stride (bytes) of the codes of an MXFP4 tensor with n columns.
-inline int64_t mx_ld(int64_t n) { return (n + 31) / 32 * 16; }
+// Row stride (bytes) of the codes of an MXFP4 tensor with n columns.  As with
+// the fp8 copies, rows a multiple of 32 KB apart are slow to write down a
+// column and to contract along (65536 columns: a 4096 x 4096 x 65536 product
+// 541 us, with 128 bytes of padding 477 us; quantising 65536 x 4096 along
+// its columns 166 and 154 us; at 16 KB the padding gains nothing).
+inline int64_t mx_ld(int64_t n) {
+  const int64_t ld = (n + 31) / 32 * 16;
+  return ld > 0 && ld % kTransposeBadStride == 0 ? ld + kTransposePad : ld;
+}
 
 // ---- Gradient norm and clipping
 constexpr int kGradBatch = 96;       // tensors per launch: their table is a kernel argument

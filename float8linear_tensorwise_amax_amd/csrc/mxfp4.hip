@@ -7,16 +7,16 @@
 // Rows alone (mx_rows_kernel): a thread takes eight consecutive elements of
 // four rows, all four loads in flight; a block is four lanes, whose maxima
 // meet by two DPP quad permutations.
-// Columns, or both (mx_quantize_kernel): one workgroup of 256 threads per 128
-// x 128 tile, all of its loads in flight at once.
+// Columns, or both (mx_quantize_kernel): one workgroup per tile of 256 (or 128)
+// rows x 128 columns, a wave per 32 rows, all of its loads in flight at once.
 //   rows : sixteen lanes cover 128 columns of a row and store 64 contiguous
 //          bytes of codes and one word of scales.
 //   cols : the tile goes to LDS as it is; thread t then owns the 32-row block
-//          t % 4 of column pair t / 4: it reads 32 words down the tile, has
+//          t % 8 of column pair t / 8: it reads 32 words down the tile, has
 //          both columns' maxima in its own registers, and stores 16 bytes
-//          for each column, four lanes covering 64 contiguous bytes of a
-//          transposed row.  Words are XOR-ed with 16 * (row / 32), so that the
-//          four row blocks that one read touches fall in different banks.
+//          for each column, eight lanes covering a 128-byte line of a
+//          transposed row.  Words are XOR-ed with 8 * (row / 32), so that the
+//          eight row blocks that one read touches fall in different banks.
 //   An XCD takes a contiguous run of tiles (workgroup b runs on XCD b % 8),
 //   so that the halves of a 128-byte line of codes meet in one L2.
 // 16-bit elements stay packed pairs throughout: maxima by packed 16-bit max,
@@ -28,8 +28,8 @@
 namespace f8lin {
 namespace {
 
-constexpr int kTile = 128;
 constexpr int kThreads = 256;
+constexpr int kTileCols = 128;
 
 struct QuantJob {
   const void *x;
@@ -85,19 +85,21 @@ __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const QuantJobs jobs)
   }
 }
 
-template <int DT, int RULE, bool ROWS>
-__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs jobs) {
+template <int DT, int RULE, bool ROWS, int kRowBlocks>
+__global__ __launch_bounds__(64 * kRowBlocks) void mx_quantize_kernel(const QuantJobs jobs) {
   typedef typename MxElem<DT>::type elem;
+  constexpr int kTileRows = 32 * kRowBlocks;  // a wave per 32 rows
   constexpr int kWords = DT == F8LIN_FP32 ? 2 : 1;  // 32-bit words of a column pair
-  constexpr int kPitch = kTile / 2 * kWords;
-  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * kPitch];
+  constexpr int kPitch = kTileCols / 2 * kWords;
+  constexpr int kSkew = 64 / kRowBlocks;  // words that a row block is set apart by
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTileRows * kPitch];
   const int per = (int)gridDim.x / 8, rem = (int)gridDim.x % 8, xcd = (int)blockIdx.x % 8;
   const int wg = xcd * per + min(xcd, rem) + (int)blockIdx.x / 8;
   const int job = jobs.count > 1 && wg >= jobs.j[1].first ? 1 : 0;
   const QuantJob &jb = jobs.j[job];
   const int64_t rows = jb.rows, cols = jb.cols;
   const int local = wg - jb.first;
-  const int64_t row0 = (int64_t)(local / jb.tiles_x) * kTile, col0 = (int64_t)(local % jb.tiles_x) * kTile;
+  const int64_t row0 = (int64_t)(local / jb.tiles_x) * kTileRows, col0 = (int64_t)(local % jb.tiles_x) * kTileCols;
   const int t = threadIdx.x, c8 = t & 15;
   const elem *x = reinterpret_cast<const elem *>(jb.x);
   const int64_t gcol = col0 + 8 * c8;
@@ -105,19 +107,19 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs j
   Raw8<DT> in[8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
-    const int64_t grow = row0 + (t >> 4) + 16 * p;
+    const int64_t grow = row0 + (t >> 4) + 4 * kRowBlocks * p;
     in[p] = load_raw8<DT>(x + grow * jb.ldx + gcol, grow < rows ? have : 0);
   }
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
-    const int r = (t >> 4) + 16 * p, rb = r >> 5;
+    const int r = (t >> 4) + 4 * kRowBlocks * p, rb = r >> 5;
     const int64_t grow = row0 + r;
     if constexpr (DT == F8LIN_FP32) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4 *>(&tile[r * kPitch + ((8 * c8 + 4 * h) ^ (32 * rb))]) = in[p].w[h];
+        *reinterpret_cast<u32x4 *>(&tile[r * kPitch + ((8 * c8 + 4 * h) ^ (2 * kSkew * rb))]) = in[p].w[h];
     } else {
-      *reinterpret_cast<u32x4 *>(&tile[r * kPitch + ((4 * c8) ^ (16 * rb))]) = in[p].w[0];
+      *reinterpret_cast<u32x4 *>(&tile[r * kPitch + ((4 * c8) ^ (kSkew * rb))]) = in[p].w[0];
     }
     if constexpr (ROWS) {
       const int e = mx_scale_byte<RULE>(mag_f32_bits<DT>(quad_max(raw_mag<DT>(in[p]))));
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs j
     }
   }
   __syncthreads();
-  const int rb = t & 3, cp = t >> 2;
+  const int rb = t % kRowBlocks, cp = t / kRowBlocks;
   const bool block_ok = row0 + 32 * rb < rows;
   // the column pair's 32 rows, and its two maxima
   uint32_t v[kWords][32], m[2] = {0, 0};
@@ -139,12 +141,12 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs j
   for (int i = 0; i < 32; ++i) {
     const int r = 32 * rb + i;
     if constexpr (DT == F8LIN_FP32) {
-      const u32x2 w = *reinterpret_cast<const u32x2 *>(&tile[r * kPitch + ((2 * cp) ^ (32 * rb))]);
+      const u32x2 w = *reinterpret_cast<const u32x2 *>(&tile[r * kPitch + ((2 * cp) ^ (2 * kSkew * rb))]);
       v[0][i] = w.x, v[1][i] = w.y;
       m[0] = max(m[0], w.x & 0x7FFFFFFFu);
       m[1] = max(m[1], w.y & 0x7FFFFFFFu);
     } else {
-      v[0][i] = tile[r * kPitch + (cp ^ (16 * rb))];
+      v[0][i] = tile[r * kPitch + (cp ^ (kSkew * rb))];
       m[0] = pair_mag_max(m[0], v[0][i]);
     }
   }
@@ -172,12 +174,13 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs j
       }
       if (e == kMxNan) out[d] = 0;
     }
-    int sw = e << (8 * rb);
+    int sw = e << (8 * (rb & 3));
     sw |= __builtin_amdgcn_mov_dpp(sw, 0xB1, 0xF, 0xF, true);
     sw |= __builtin_amdgcn_mov_dpp(sw, 0x4E, 0xF, 0xF, true);
     if (col < cols) {
       if (block_ok) *reinterpret_cast<u32x4 *>(jb.qt.codes + col * jb.qt.ld + row0 / 2 + 16 * rb) = out;
-      if (rb == 0) *reinterpret_cast<int *>(jb.qt.scales + col * jb.qt.scale_ld + row0 / 32) = sw;
+      if ((rb & 3) == 0 && block_ok)
+        *reinterpret_cast<int *>(jb.qt.scales + col * jb.qt.scale_ld + row0 / 32 + rb) = sw;
     }
     if (jb.colsum) {
       float cs = 0.0f;
@@ -186,10 +189,10 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const QuantJobs j
         if constexpr (DT == F8LIN_FP32) cs += __uint_as_float(v[h][i]);
         else cs += elem_f32<DT>((v[0][i] >> (16 * h)) & 0xFFFFu);
       }
-      // the four row blocks in a fixed order: (0 + 1) + (2 + 3)
+      // four row blocks (kMxTile rows) in a fixed order: (0 + 1) + (2 + 3)
       cs += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(cs), 0xB1, 0xF, 0xF, true));
       cs += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(cs), 0x4E, 0xF, 0xF, true));
-      if (rb == 0 && col < cols) jb.colsum[(row0 / kTile) * cols + col] = cs;
+      if ((rb & 3) == 0 && col < cols && block_ok) jb.colsum[(row0 / kMxTile + rb / 4) * cols + col] = cs;
     }
   }
 }
@@ -244,20 +247,38 @@ __global__ __launch_bounds__(kThreads) void mx_dbias_kernel(const float *__restr
     reinterpret_cast<uint16_t *>(db)[col] = (uint16_t)o;
 }
 
-template <int DT, int RULE>
-void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, bool cols, hipStream_t stream) {
-  if (rows && cols)
-    mx_quantize_kernel<DT, RULE, true><<<grid, kThreads, 0, stream>>>(jobs);
-  else if (rows)
-    mx_rows_kernel<DT, RULE><<<grid, kThreads, 0, stream>>>(jobs);
+template <int DT, int RULE, int RB>
+void launch_cols(const QuantJobs &jobs, unsigned grid, bool rows, hipStream_t stream) {
+  if (rows)
+    mx_quantize_kernel<DT, RULE, true, RB><<<grid, 64 * RB, 0, stream>>>(jobs);
   else
-    mx_quantize_kernel<DT, RULE, false><<<grid, kThreads, 0, stream>>>(jobs);
+    mx_quantize_kernel<DT, RULE, false, RB><<<grid, 64 * RB, 0, stream>>>(jobs);
+}
+
+template <int DT, int RULE>
+void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, int row_blocks, hipStream_t stream) {
+  if constexpr (DT != F8LIN_FP32) {
+    if (row_blocks == 8) return launch_cols<DT, RULE, 8>(jobs, grid, rows, stream);
+  }
+  if (row_blocks == 4)
+    launch_cols<DT, RULE, 4>(jobs, grid, rows, stream);
+  else
+    mx_rows_kernel<DT, RULE><<<grid, kThreads, 0, stream>>>(jobs);
 }
 
 }  // namespace
 
 hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_t stream) {
   const bool rows = ts[0].q.codes != nullptr, cols = ts[0].qt.codes != nullptr;
+  // 256-row tiles fill whole 128-byte lines of the transposed codes (65536 x
+  // 4096 bf16, both layouts: 187 us, with 128-row tiles 214 us); 128-row
+  // tiles for 32-bit elements, whose tile would take 128 KB of LDS (286 us,
+  // with 256 rows 342 us), and where there are few tiles (256 x 4096 bf16:
+  // 5.6 us, with 256 rows 6.3 us).
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i)
+    tiles += ((ts[i].rows + 255) / 256) * ((ts[i].cols + kTileCols - 1) / kTileCols);
+  const int row_blocks = !cols ? 0 : (ts[0].dtype != F8LIN_FP32 && tiles >= 256) ? 8 : 4;
   QuantJobs jobs = {};
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
@@ -266,7 +287,7 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
     int64_t gx, gy;
     int log_tx = 0;
     if (cols) {
-      gx = (t.cols + kTile - 1) / kTile, gy = (t.rows + kTile - 1) / kTile;
+      gx = (t.cols + kTileCols - 1) / kTileCols, gy = (t.rows + 32 * row_blocks - 1) / (32 * row_blocks);
     } else {
       // as many threads along a row as it has chunks, 16 to 256
       log_tx = 4;
@@ -282,9 +303,9 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
   const unsigned grid = (unsigned)total;
 #define F8_MX_Q(DT)                                                             \
   if (rule == F8LIN_MX_CEIL)                                                    \
-    launch_quant<DT, F8LIN_MX_CEIL>(jobs, grid, rows, cols, stream);            \
+    launch_quant<DT, F8LIN_MX_CEIL>(jobs, grid, rows, row_blocks, stream);      \
   else                                                                          \
-    launch_quant<DT, F8LIN_MX_FLOOR>(jobs, grid, rows, cols, stream)
+    launch_quant<DT, F8LIN_MX_FLOOR>(jobs, grid, rows, row_blocks, stream)
   if (ts[0].dtype == F8LIN_BF16) {
     F8_MX_Q(F8LIN_BF16);
   } else if (ts[0].dtype == F8LIN_FP16) {

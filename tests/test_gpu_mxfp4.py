@@ -93,6 +93,23 @@ def test_quantize(f8lin, mx, rows, cols, dtype, rule):
             check_mx(mx, qt, *mx.quantize(np64(x).T, rule), "columns")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quantize_many_tiles(f8lin, mod, mx, dtype):
+    """Enough tiles for the taller ones, ragged in both directions; and the column sums a bias gradient takes there."""
+    x = draw((4100, 2050), DTYPES[dtype], 7)
+    xd = x.cuda()
+    q, qt = f8lin.new_mxfp4(4100, 2050), f8lin.new_mxfp4(2050, 4100)
+    f8lin.mxfp4_quantize(xd, q, qt)
+    check_mx(mx, q, *mx.quantize(np64(x)), "rows")
+    check_mx(mx, qt, *mx.quantize(np64(x).T), "columns")
+    w = draw((2050, 32), DTYPES[dtype], 8).cuda()
+    b = torch.zeros(2050, dtype=DTYPES[dtype], device="cuda", requires_grad=True)
+    db, = torch.autograd.grad(mod.mxfp4_linear(draw((4100, 32), DTYPES[dtype], 9).cuda(), w, b), b, xd)
+    ref, s = np64(x).sum(0), np.abs(np64(x)).sum(0)
+    tol = 4102 * 2.0 ** -23 * s
+    assert np.all(np.abs(np64(db) - ref) <= tol + out_half_step(np.abs(ref) + tol, DTYPES[dtype]))
+
+
 def all_bf16():
     bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
     x = bits.view(torch.bfloat16)
@@ -231,6 +248,37 @@ def test_gemm_scales_and_bias(f8lin, mx, M, N, K, dtype):
         c = torch.full((M, N), float("nan"), device="cuda", dtype=DTYPES[dtype])
         f8lin.mxfp4_gemm([(a, b, c, bias)])
         check_product(c, av, bv, DTYPES[dtype], None if bias is None else np64(bias), f"{bias_dtype}")
+
+
+# sizes that take each tile and several of them per workgroup, with odd and even numbers of 256-wide K blocks
+MANY = [(4100, 4100, 1000), (4100, 4100, 200), (4096, 4096, 768), (5000, 3900, 513), (2100, 2100, 1300), (1700, 1500, 2050),
+        (70, 20000, 600), (20000, 100, 257), (130, 5000, 1000)]
+
+
+@pytest.mark.parametrize("M,N,K", MANY)
+def test_gemm_many_tiles(f8lin, mx, M, N, K):
+    """Exact sums over many tiles, in the three output types (bf16 and fp16: rounded once from the exact sum)."""
+    gen = torch.Generator(device="cuda").manual_seed(M + N + K)
+    grid = torch.tensor(mx.GRID, device="cuda")
+
+    def operand(rows):
+        nb = -(-K // 32)
+        codes = torch.randint(0, 16, (rows, nb * 32), generator=gen, device="cuda", dtype=torch.uint8)
+        codes[:, K:] = 0
+        scales = torch.full((rows, -(-nb // 16) * 16), 255, dtype=torch.uint8, device="cuda")
+        scales[:, :nb] = 127
+        v = grid[(codes & 7).long()] * (1.0 - 2.0 * (codes >> 3))
+        return f8lin.MXFP4Tensor(codes[:, 0::2] | codes[:, 1::2] << 4, scales, rows, K), v[:, :K]
+
+    (a, av), (b, bv) = operand(M), operand(N)
+    want = av @ bv.t().contiguous()
+    bias = torch.randint(-8, 8, (N,), generator=gen, device="cuda").float()
+    for dtype in DTYPES.values():
+        c = torch.full((M, N), float("nan"), device="cuda", dtype=dtype)
+        f8lin.mxfp4_gemm([(a, b, c)])
+        assert torch.equal(c, want.to(dtype))
+        f8lin.mxfp4_gemm([(a, b, c, bias)])
+        assert torch.equal(c, (want + bias.double()).to(dtype))
 
 
 def test_gemm_workspace_same_bits_every_time(f8lin, mx):
