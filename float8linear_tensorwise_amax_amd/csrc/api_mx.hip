@@ -322,8 +322,8 @@ int grad_impl(const f8lin_grad *list, int count, int norm_type, bool clip, float
   if (!given) add_span(spans, ws, (int64_t)f8lin_grad_workspace_bytes(), true);
   if (spans_clash(spans)) return F8LIN_EINVAL;
   hipStream_t s = (hipStream_t)stream;
-  if (!given) F8_TRY(status_of(launch_grad_norm(list, count, norm_type, (double *)ws, norm, s)));
-  return clip ? status_of(launch_grad_scale(list, count, norm, max_norm, s)) : F8LIN_OK;
+  if (given) return status_of(launch_grad_scale(list, count, norm, max_norm, s));
+  return status_of(launch_grad_norm(list, count, norm_type, (double *)ws, norm, clip, max_norm, s));
 }
 
 }  // namespace

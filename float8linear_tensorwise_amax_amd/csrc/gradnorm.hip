@@ -13,7 +13,9 @@
 // call copies nothing to the device; the tensors are cut into pieces of
 // kPiece elements, dealt to the workgroups round robin.  Longer lists take one
 // launch per table, each adding to the partial results of the one before.
-// The scaling kernel's workgroups reduce the partial results themselves.
+// The scaling kernel's workgroups each reduce the partial results (at most 8
+// KB, from the L2) themselves, so that norm and clipping are two launches: a
+// launch of its own for it took 4 us, more than the rest of a small list.
 #include <algorithm>
 
 #include "mx_common.h"
@@ -24,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPiece = 16384;
 constexpr int kNormGrid = kGradPartials;
+constexpr int kScaleGrid = 2048;
 
 struct GradTable {
   const void *g[kGradBatch];
@@ -103,17 +106,18 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const GradTable tab
   if (threadIdx.x == 0) partials[blockIdx.x] = add ? join<P>(partials[blockIdx.x], s) : s;
 }
 
+// The norm from the first `count` partial results, in every thread.
 template <int P>
-__device__ __forceinline__ float norm_of(const double *partials) {
+__device__ __forceinline__ float norm_of(const double *partials, int count) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < kNormGrid; i += kThreads) s = join<P>(s, partials[i]);
+  for (int i = threadIdx.x; i < count; i += kThreads) s = join<P>(s, partials[i]);
   s = block_join<P>(s);
   return (float)(P == F8LIN_NORM_2 ? sqrt(s) : s);
 }
 
 template <int P>
-__global__ __launch_bounds__(kThreads) void grad_norm_final_kernel(const double *partials, float *norm) {
-  const float n = norm_of<P>(partials);
+__global__ __launch_bounds__(kThreads) void grad_norm_final_kernel(const double *partials, int count, float *norm) {
+  const float n = norm_of<P>(partials, count);
   if (threadIdx.x == 0) norm[0] = n;
 }
 
@@ -152,8 +156,19 @@ __device__ __forceinline__ void piece_scale(const void *g, void *out, int out_dt
   }
 }
 
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable tab, const float *norm, float max_norm) {
-  float c = max_norm / (norm[0] + 1e-6f);
+// P < 0: norm[0] holds the norm; otherwise it comes from the partial results,
+// and the first workgroup writes it there.
+template <int P>
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable tab, const double *partials, int count,
+                                                              float *norm, float max_norm) {
+  float n;
+  if constexpr (P < 0) {
+    n = norm[0];
+  } else {
+    n = norm_of<P>(partials, count);
+    if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = n;
+  }
+  float c = max_norm / (n + 1e-6f);
   c = c > 1.0f ? 1.0f : c;  // (a NaN stays one)
   for (int p = blockIdx.x; p < tab.pieces; p += gridDim.x) {
     const int t = tensor_of(tab, p);
@@ -192,37 +207,57 @@ int fill(GradTable &tab, const f8lin_grad *list, int at, int count, bool outs) {
   return at;
 }
 
+// The norm's partial results; returns how many there are.
 template <int P>
-void launch_norm(const f8lin_grad *list, int count, double *partials, float *norm, hipStream_t stream) {
-  int at = 0;
+int launch_partials(const f8lin_grad *list, int count, double *partials, hipStream_t stream) {
+  int at = 0, grid = kNormGrid;
   bool add = false;
   do {
     GradTable tab = {};
     at = fill(tab, list, at, count, false);
-    grad_norm_kernel<P><<<kNormGrid, kThreads, 0, stream>>>(tab, partials, add ? 1 : 0);
+    // (a list of one table needs no more workgroups than it has pieces)
+    if (!add && at >= count) grid = std::max(1, std::min(tab.pieces, kNormGrid));
+    grad_norm_kernel<P><<<grid, kThreads, 0, stream>>>(tab, partials, add ? 1 : 0);
     add = true;
   } while (at < count);
-  grad_norm_final_kernel<P><<<1, kThreads, 0, stream>>>(partials, norm);
+  return grid;
+}
+
+template <int P>
+void launch_scale(const f8lin_grad *list, int count, const double *partials, int nparts, float *norm, float max_norm,
+                  hipStream_t stream) {
+  int at = 0;
+  do {
+    GradTable tab = {};
+    at = fill(tab, list, at, count, true);
+    const unsigned grid = (unsigned)std::max(1, std::min(tab.pieces, kScaleGrid));
+    grad_scale_kernel<P><<<grid, kThreads, 0, stream>>>(tab, partials, nparts, norm, max_norm);
+  } while (at < count);
+}
+
+template <int P>
+void launch_type(const f8lin_grad *list, int count, double *partials, float *norm, bool clip, float max_norm,
+                 hipStream_t stream) {
+  const int nparts = launch_partials<P>(list, count, partials, stream);
+  if (clip)
+    launch_scale<P>(list, count, partials, nparts, norm, max_norm, stream);
+  else
+    grad_norm_final_kernel<P><<<1, kThreads, 0, stream>>>(partials, nparts, norm);
 }
 
 }  // namespace
 
-hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, double *partials, float *norm,
-                            hipStream_t stream) {
-  if (norm_type == F8LIN_NORM_2) launch_norm<F8LIN_NORM_2>(list, count, partials, norm, stream);
-  else if (norm_type == F8LIN_NORM_1) launch_norm<F8LIN_NORM_1>(list, count, partials, norm, stream);
-  else launch_norm<F8LIN_NORM_INF>(list, count, partials, norm, stream);
+hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, double *partials, float *norm, bool clip,
+                            float max_norm, hipStream_t stream) {
+  if (norm_type == F8LIN_NORM_2) launch_type<F8LIN_NORM_2>(list, count, partials, norm, clip, max_norm, stream);
+  else if (norm_type == F8LIN_NORM_1) launch_type<F8LIN_NORM_1>(list, count, partials, norm, clip, max_norm, stream);
+  else launch_type<F8LIN_NORM_INF>(list, count, partials, norm, clip, max_norm, stream);
   return hipGetLastError();
 }
 
-hipError_t launch_grad_scale(const f8lin_grad *list, int count, const float *norm, float max_norm, hipStream_t stream) {
-  for (int at = 0; at < count;) {
-    GradTable tab = {};
-    at = fill(tab, list, at, count, true);
-    if (tab.count == 0) continue;
-    const unsigned grid = (unsigned)std::min(tab.pieces, 4096);
-    grad_scale_kernel<<<grid, kThreads, 0, stream>>>(tab, norm, max_norm);
-  }
+hipError_t launch_grad_scale(const f8lin_grad *list, int count, float *norm, float max_norm, hipStream_t stream) {
+  if (count == 0) return hipSuccess;
+  launch_scale<-1>(list, count, nullptr, 0, norm, max_norm, stream);
   return hipGetLastError();
 }
 

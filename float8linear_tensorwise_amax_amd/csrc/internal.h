@@ -179,8 +179,10 @@ inline int64_t mx_ld(int64_t n) {
 // ---- Gradient norm and clipping
 constexpr int kGradBatch = 96;       // tensors per launch: their table is a kernel argument
 constexpr int kGradPartials = 1024;  // workgroups of the norm, one binary64 partial result each
-hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, double *partials, float *norm,
-                            hipStream_t stream);
-hipError_t launch_grad_scale(const f8lin_grad *list, int count, const float *norm, float max_norm, hipStream_t stream);
+// The norm into norm[0]; clip: every tensor scaled to max_norm too.
+hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, double *partials, float *norm, bool clip,
+                            float max_norm, hipStream_t stream);
+// The scaling alone, with the norm that norm[0] holds.
+hipError_t launch_grad_scale(const f8lin_grad *list, int count, float *norm, float max_norm, hipStream_t stream);
 
 }  // namespace f8lin

@@ -518,41 +518,46 @@ for _fmt, _cls in ((_MX, MxStruct), (_MX_FWD, MxFwdArgs), (_MX_BWD, MxBwdArgs)):
     assert _fmt.size == ctypes.sizeof(_cls)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current hipStream_t of a device, without a Stream object
+_current_device = torch._C._cuda_getDevice
+
+
 def _call(fn, device: torch.device, stream, *args):
     """Calls fn(*args, stream) with `device` current: the stream is the given one, or the device's current one."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _check(fn(*args, raw))
+    index = device.index
+    raw = _raw_stream(index) if stream is None else _stream(stream)
+    if index == _current_device():
+        status = fn(*args, raw)
     else:
-        _check(fn(*args, raw))
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status:
+        raise F8linError(status)
 
 
-def _dense(t: torch.Tensor, what: str, device: torch.device = None) -> int:
-    """Pointer of a contiguous bf16 / fp16 / fp32 GPU tensor (on `device`, if given)."""
+def _refuse(t: torch.Tensor, what: str, device: Optional[torch.device]):
     if not t.is_cuda:
         raise ValueError("f8lin: tensors must be on the GPU")
     if device is not None and t.device != device:
         raise ValueError(f"f8lin: {what} is on {t.device}, expected {device}")
     if t.dtype not in _DTYPE:
         raise TypeError(f"f8lin: {what} must be bfloat16, float16 or float32, got {t.dtype}")
+
+
+def _dense(t: torch.Tensor, what: str, device: Optional[torch.device] = None) -> int:
+    """Pointer of a contiguous bf16 / fp16 / fp32 GPU tensor (on `device`, if given)."""
+    if not t.is_cuda or t.dtype not in _DTYPE or (device is not None and t.device != device):
+        _refuse(t, what, device)
     if not t.is_contiguous():
         raise ValueError(f"f8lin: {what} must be contiguous")
     return t.data_ptr()
 
 
-def _dense_ld(t: torch.Tensor, what: str, device: torch.device = None):
+def _dense_ld(t: torch.Tensor, what: str, device: Optional[torch.device] = None):
     """(pointer, row stride in elements) of a 2-D bf16 / fp16 / fp32 tensor whose rows are contiguous."""
     if t.is_contiguous():
         return _dense(t, what, device), t.shape[1]
-    if not t.is_cuda:
-        raise ValueError("f8lin: tensors must be on the GPU")
-    if device is not None and t.device != device:
-        raise ValueError(f"f8lin: {what} is on {t.device}, expected {device}")
-    if t.dtype not in _DTYPE:
-        raise TypeError(f"f8lin: {what} must be bfloat16, float16 or float32, got {t.dtype}")
+    _refuse(t, what, device)
     rows, cols = t.shape
     ld = t.stride(0) if rows > 1 else cols
     if t.numel() and ((cols > 1 and t.stride(1) != 1) or ld < cols):

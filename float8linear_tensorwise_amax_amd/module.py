@@ -515,9 +515,9 @@ def get_grad_norm(grads: Iterable[torch.Tensor], norm_type: float = 2.0) -> torc
     if not grads:
         return torch.zeros((), dtype=torch.float32)
     dev = grads[0].device
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
     f8lin.grad_norm(grads, norm, f8lin.new_grad_workspace(dev), norm_type)
-    return norm[0]
+    return norm
 
 
 def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0,
@@ -528,10 +528,10 @@ def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float 
     if not grads:
         return torch.zeros((), dtype=torch.float32), []
     dev = grads[0].device
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
     outs = [torch.empty_like(g, dtype=out_dtype) for g in grads]
     f8lin.grad_clip(grads, max_norm, norm, f8lin.new_grad_workspace(dev), norm_type, outs)
-    return norm[0], outs
+    return norm, outs
 
 
 @torch.no_grad()
@@ -545,7 +545,7 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
         return torch.zeros((), dtype=torch.float32)
     flat = [_dense_copy(g) for g in grads]
     dev = flat[0].device
-    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
     ws = f8lin.new_grad_workspace(dev)
     if error_if_nonfinite:
         f8lin.grad_norm(flat, norm, ws, norm_type)
@@ -558,4 +558,4 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     for g, f in zip(grads, flat):
         if f is not g:
             g.copy_(f)
-    return norm[0]
+    return norm
