@@ -121,39 +121,64 @@ __global__ __launch_bounds__(kThreads) void grad_norm_final_kernel(const double 
   if (threadIdx.x == 0) norm[0] = n;
 }
 
-template <int DI>
-__device__ __forceinline__ void piece_scale(const void *g, void *out, int out_dtype, int64_t begin, int64_t n, float c) {
-  typedef typename MxElem<DI>::type elem;
-  const elem *x = reinterpret_cast<const elem *>(g) + begin;
+// E consecutive elements per thread and step, so that a step's stores are 16
+// bytes a lane and contiguous whatever the types (16-bit gradients into
+// 32-bit outputs with eight elements a lane: 1142 us for 872M elements, with
+// four 995 us); kAhead steps' loads in flight.
+template <int DI, int DO>
+__device__ __forceinline__ void piece_scale(const void *g, void *out, int64_t begin, int64_t n, float c) {
+  typedef typename MxElem<DI>::type ielem;
+  typedef typename MxElem<DO>::type oelem;
+  constexpr int E = DO == F8LIN_FP32 ? 4 : 8, kAhead = 4;
+  constexpr int kInWords = E * (int)sizeof(ielem) / 4, kOutWords = 4;
+  const ielem *x = reinterpret_cast<const ielem *>(g) + begin;
+  oelem *y = reinterpret_cast<oelem *>(out) + begin;
   const int len = (int)min((int64_t)kPiece, n - begin);
-  for (int i = 8 * (int)threadIdx.x; i < len; i += 8 * kThreads) {
-    float v[8];
-    load8<DI>(x + i, len - i, v);
-    uint32_t o[8];
+  const int whole = len / E;  // whole groups of E
+  auto value = [&](const uint32_t(&w)[kInWords], int k) {
+    if constexpr (DI == F8LIN_FP32) return __uint_as_float(w[k]);
+    else return elem_f32<DI>((w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
+  };
+  for (int i0 = threadIdx.x; i0 < whole; i0 += kAhead * kThreads) {
+    uint32_t w[kAhead][kInWords];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = f32_to_elem(v[k] * c, out_dtype);
-    if (out_dtype == F8LIN_FP32) {
-      uint32_t *dst = reinterpret_cast<uint32_t *>(out) + begin + i;
-      if (i + 8 <= len) {
-        reinterpret_cast<u32x4_u *>(dst)[0] = u32x4{o[0], o[1], o[2], o[3]};
-        reinterpret_cast<u32x4_u *>(dst)[1] = u32x4{o[4], o[5], o[6], o[7]};
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * kThreads;
+      if (i >= whole) continue;
+      if constexpr (kInWords == 2) {
+        const u32x2 v = *reinterpret_cast<const u32x2_u *>(x + E * i);
+        w[a][0] = v.x, w[a][1] = v.y;
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (i + k < len) dst[k] = o[k];
-      }
-    } else {
-      uint16_t *dst = reinterpret_cast<uint16_t *>(out) + begin + i;
-      if (i + 8 <= len) {
-        *reinterpret_cast<u32x4_u *>(dst) =
-            u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (i + k < len) dst[k] = (uint16_t)o[k];
+        for (int q = 0; q < kInWords; q += 4) {
+          const u32x4 v = *reinterpret_cast<const u32x4_u *>(x + E * i + q * 4 / (int)sizeof(ielem));
+          w[a][q] = v.x, w[a][q + 1] = v.y, w[a][q + 2] = v.z, w[a][q + 3] = v.w;
+        }
       }
     }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int i = i0 + a * kThreads;
+      uint32_t o[kOutWords];
+#pragma unroll
+      for (int k = 0; k < kOutWords; ++k) {
+        if constexpr (DO == F8LIN_FP32)
+          o[k] = __float_as_uint(value(w[a], k) * c);
+        else
+          o[k] = f32_to_elem(value(w[a], 2 * k) * c, DO) | f32_to_elem(value(w[a], 2 * k + 1) * c, DO) << 16;
+      }
+      if (i < whole) *reinterpret_cast<u32x4_u *>(y + E * i) = u32x4{o[0], o[1], o[2], o[3]};
+    }
   }
+  const int at = whole * E + (int)threadIdx.x;  // fewer than E elements left
+  if (at < len) y[at] = (oelem)f32_to_elem(elem_f32<DI>((uint32_t)x[at]) * c, DO);
+}
+
+template <int DI>
+__device__ __forceinline__ void piece_scale_to(const void *g, void *out, int out_dtype, int64_t begin, int64_t n, float c) {
+  if (out_dtype == F8LIN_BF16) piece_scale<DI, F8LIN_BF16>(g, out, begin, n, c);
+  else if (out_dtype == F8LIN_FP16) piece_scale<DI, F8LIN_FP16>(g, out, begin, n, c);
+  else piece_scale<DI, F8LIN_FP32>(g, out, begin, n, c);
 }
 
 // P < 0: norm[0] holds the norm; otherwise it comes from the partial results,
@@ -170,17 +195,18 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable ta
   }
   float c = max_norm / (n + 1e-6f);
   c = c > 1.0f ? 1.0f : c;  // (a NaN stays one)
-  for (int p = blockIdx.x; p < tab.pieces; p += gridDim.x) {
+  // from the end: what the norm's pass read last is still in the caches
+  for (int p = tab.pieces - 1 - (int)blockIdx.x; p >= 0; p -= (int)gridDim.x) {
     const int t = tensor_of(tab, p);
     // a factor of one leaves a tensor scaled in place as it is
     if (c == 1.0f && tab.g[t] == tab.out[t]) continue;
     const int64_t begin = (int64_t)(p - tab.first[t]) * kPiece;
     if (tab.in_dtype[t] == F8LIN_BF16)
-      piece_scale<F8LIN_BF16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+      piece_scale_to<F8LIN_BF16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
     else if (tab.in_dtype[t] == F8LIN_FP16)
-      piece_scale<F8LIN_FP16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+      piece_scale_to<F8LIN_FP16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
     else
-      piece_scale<F8LIN_FP32>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+      piece_scale_to<F8LIN_FP32>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
   }
 }
 
