@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTileCols = 128;
+constexpr int64_t kFewTiles = 256;  // tiles of 256 x 128 elements: fewer leave CUs idle
 
 struct QuantJob {
   const void *x;
@@ -52,9 +53,9 @@ __device__ __forceinline__ int scales_of_16(int e, int q) {
 }
 
 // Rows alone.  A workgroup covers tx = 2^log_tx chunks of eight elements by
-// kRowsPer * 256 / tx rows.
-constexpr int kRowsPer = 4;
-template <int DT, int RULE>
+// kRowsPer * 256 / tx rows: four rows a thread, or one where that leaves few
+// workgroups.
+template <int DT, int RULE, int kRowsPer>
 __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const QuantJobs jobs) {
   typedef typename MxElem<DT>::type elem;
   const int job = jobs.count > 1 && (int)blockIdx.x >= jobs.j[1].first ? 1 : 0;
@@ -197,38 +198,54 @@ __global__ __launch_bounds__(64 * kRowBlocks) void mx_quantize_kernel(const Quan
   }
 }
 
-// Eight codes (one 32-bit word) per thread back to values of type dt.
-template <int DT>
+// The way back.  E codes per thread, so that its values are one 16-byte store,
+// of kRowsPer rows; a workgroup covers 2^log_tx such groups by kRowsPer * 256 /
+// 2^log_tx rows.
+template <int DT, int kRowsPer>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(f8lin_mxfp4 q, int64_t rows, int64_t cols,
-                                                                 typename MxElem<DT>::type *out) {
-  const int64_t words = (cols + 7) / 8;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * words; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t r = i / words, w = i % words;
-    const uint32_t c = *reinterpret_cast<const uint32_t *>(q.codes + r * q.ld + 4 * w);
-    const int e = q.scales[r * q.scale_ld + w / 4];
-    const float s = mx_scale_f32(e);
-    float v[8];
-    f32x2_t p;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), v[0] = p.x, v[1] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1), v[2] = p.x, v[3] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), v[4] = p.x, v[5] = p.y;
-    p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3), v[6] = p.x, v[7] = p.y;
-    uint32_t o[8];
+                                                                 typename MxElem<DT>::type *out, int tiles_x, int log_tx) {
+  constexpr int E = DT == F8LIN_FP32 ? 4 : 8;
+  const int tx = (int)threadIdx.x & ((1 << log_tx) - 1), ty = (int)threadIdx.x >> log_tx;
+  const int64_t col = ((int64_t)((int)blockIdx.x % tiles_x) * E << log_tx) + E * tx;
+  const int64_t row0 = (int64_t)((int)blockIdx.x / tiles_x) * (kRowsPer * (kThreads >> log_tx)) + ty;
+  if (col >= cols) return;
+  uint32_t code[kRowsPer];
+  int exps[kRowsPer];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = f32_to_elem(e == kMxNan ? __builtin_nanf("") : v[k], DT);
-    typename MxElem<DT>::type *dst = out + r * cols + 8 * w;
-    if (8 * w + 8 <= cols) {
-      if constexpr (DT == F8LIN_FP32) {
-        reinterpret_cast<u32x4_u *>(dst)[0] = u32x4{o[0], o[1], o[2], o[3]};
-        reinterpret_cast<u32x4_u *>(dst)[1] = u32x4{o[4], o[5], o[6], o[7]};
-      } else {
+  for (int p = 0; p < kRowsPer; ++p) {
+    const int64_t row = row0 + (int64_t)p * (kThreads >> log_tx);
+    code[p] = 0, exps[p] = 0;
+    if (row >= rows) continue;
+    const uint8_t *c = q.codes + row * q.ld + col / 2;
+    code[p] = E == 8 ? *reinterpret_cast<const uint32_t *>(c) : *reinterpret_cast<const uint16_t *>(c);
+    exps[p] = q.scales[row * q.scale_ld + col / 32];
+  }
+#pragma unroll
+  for (int p = 0; p < kRowsPer; ++p) {
+    const int64_t row = row0 + (int64_t)p * (kThreads >> log_tx);
+    if (row >= rows) continue;
+    const uint32_t c = code[p];
+    const int e = exps[p];
+    const float s = mx_scale_f32(e);
+    f32x2_t v[4];
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+    uint32_t o[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) o[k] = f32_to_elem(e == kMxNan ? __builtin_nanf("") : v[k >> 1][k & 1], DT);
+    typename MxElem<DT>::type *dst = out + row * cols + col;
+    if (col + E <= cols) {
+      if constexpr (DT == F8LIN_FP32)
+        *reinterpret_cast<u32x4_u *>(dst) = u32x4{o[0], o[1], o[2], o[3]};
+      else
         *reinterpret_cast<u32x4_u *>(dst) =
             u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
-      }
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (8 * w + k < cols) dst[k] = (typename MxElem<DT>::type)o[k];
+      for (int k = 0; k < E; ++k)
+        if (col + k < cols) dst[k] = (typename MxElem<DT>::type)o[k];
     }
   }
 }
@@ -263,7 +280,8 @@ void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, int row_block
   if (row_blocks == 4)
     launch_cols<DT, RULE, 4>(jobs, grid, rows, stream);
   else
-    mx_rows_kernel<DT, RULE><<<grid, kThreads, 0, stream>>>(jobs);
+    row_blocks == 0 ? mx_rows_kernel<DT, RULE, 4><<<grid, kThreads, 0, stream>>>(jobs)
+                    : mx_rows_kernel<DT, RULE, 1><<<grid, kThreads, 0, stream>>>(jobs);
 }
 
 }  // namespace
@@ -278,7 +296,8 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
   int64_t tiles = 0;
   for (int i = 0; i < count; ++i)
     tiles += ((ts[i].rows + 255) / 256) * ((ts[i].cols + kTileCols - 1) / kTileCols);
-  const int row_blocks = !cols ? 0 : (ts[0].dtype != F8LIN_FP32 && tiles >= 256) ? 8 : 4;
+  // (rows alone: 0, or 1 for one row a thread)
+  const int row_blocks = !cols ? (tiles < kFewTiles ? 1 : 0) : (ts[0].dtype != F8LIN_FP32 && tiles >= kFewTiles) ? 8 : 4;
   QuantJobs jobs = {};
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
@@ -292,7 +311,7 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
       // as many threads along a row as it has chunks, 16 to 256
       log_tx = 4;
       while (log_tx < 8 && (8 << log_tx) < t.cols) ++log_tx;
-      const int64_t per = kRowsPer * (kThreads >> log_tx);
+      const int64_t per = (row_blocks ? 1 : 4) * (kThreads >> log_tx);
       gx = (t.cols + (8 << log_tx) - 1) / (8 << log_tx), gy = (t.rows + per - 1) / per;
     }
     jobs.j[jobs.count++] =
@@ -320,14 +339,22 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
 hipError_t launch_mx_dequantize(const f8lin_mxfp4 &q, int64_t rows, int64_t cols, int dtype, void *out,
                                 hipStream_t stream) {
   if (rows == 0 || cols == 0) return hipSuccess;
-  const int64_t work = rows * ((cols + 7) / 8);
-  const unsigned grid = (unsigned)std::min<int64_t>((work + kThreads - 1) / kThreads, 65536);
+  const int64_t per = dtype == F8LIN_FP32 ? 4 : 8;
+  int log_tx = 2;
+  while (log_tx < 8 && (per << log_tx) < cols) ++log_tx;
+  const int64_t gx = (cols + (per << log_tx) - 1) / (per << log_tx), few = rows * cols < kFewTiles * 256 * kTileCols,
+                rows_per = (few ? 1 : 4) * (kThreads >> log_tx);
+  const unsigned grid = (unsigned)(gx * ((rows + rows_per - 1) / rows_per));
+#define F8_MX_D(DT, T)                                                                                        \
+  few ? mx_dequantize_kernel<DT, 1><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx) \
+      : mx_dequantize_kernel<DT, 4><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx)
   if (dtype == F8LIN_BF16)
-    mx_dequantize_kernel<F8LIN_BF16><<<grid, kThreads, 0, stream>>>(q, rows, cols, (uint16_t *)out);
+    F8_MX_D(F8LIN_BF16, uint16_t);
   else if (dtype == F8LIN_FP16)
-    mx_dequantize_kernel<F8LIN_FP16><<<grid, kThreads, 0, stream>>>(q, rows, cols, (uint16_t *)out);
+    F8_MX_D(F8LIN_FP16, uint16_t);
   else
-    mx_dequantize_kernel<F8LIN_FP32><<<grid, kThreads, 0, stream>>>(q, rows, cols, (uint32_t *)out);
+    F8_MX_D(F8LIN_FP32, uint32_t);
+#undef F8_MX_D
   return hipGetLastError();
 }
 
