@@ -64,10 +64,6 @@ int check_dense(const void *p, int dt, int64_t rows, int64_t cols, int64_t ld, i
   return F8LIN_OK;
 }
 
-int check_ws_opt(const void *ws, size_t bytes) {
-  return ws && bytes > 0 && !aligned16(ws) ? F8LIN_EALIGN : F8LIN_OK;
-}
-
 int64_t dbias_tiles(int64_t M) { return M > 0 ? (M + kMxTile - 1) / kMxTile : 0; }
 
 }  // namespace
@@ -120,12 +116,7 @@ int f8lin_mxfp4_dequantize(const f8lin_mxfp4 *q, int64_t rows, int64_t cols, int
   return status_of(launch_mx_dequantize(*q, rows, cols, dtype, out, (hipStream_t)stream));
 }
 
-size_t f8lin_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (bad_matrix(M, N) || bad_size(K)) return 0;
-  return mx_gemm_workspace_bytes(M, N, K);
-}
-
-int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *ws, size_t ws_bytes, void *stream) {
+int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *stream) {
   static_assert(F8LIN_MXFP4_MAX_BATCH == kMxMaxGemms, "batch limit");
   if (!d || count < 1 || count > kMxMaxGemms) return F8LIN_EINVAL;
   Ranges outs, ins;
@@ -143,10 +134,8 @@ int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *ws, size_t
     ins.add(e.bias, e.bias ? e.N * es_of(e.bias_dtype) : 0);
     g[i] = MxGemm{e.a, e.b, e.c, e.bias, e.M, e.N, e.K, e.c_dtype, e.bias_dtype};
   }
-  F8_TRY(check_ws_opt(ws, ws_bytes));
-  outs.add(ws, ws ? (int64_t)ws_bytes : 0);
   if (any_overlap(outs.r, outs.n, ins.r, ins.n)) return F8LIN_EINVAL;
-  return status_of(launch_mx_gemms(g, count, ws, ws ? ws_bytes : 0, (hipStream_t)stream));
+  return status_of(launch_mx_gemms(g, count, (hipStream_t)stream));
 }
 
 int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *p, void *stream) {
@@ -165,10 +154,8 @@ int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *p, void *stream) {
   F8_TRY(check_mx(a.w4, N, K));
   if (quant_w) F8_TRY(check_dense(a.w, a.w_dtype, N, K, K, es_of(a.w_dtype)));
   if (wt) F8_TRY(check_mx(a.w4t, K, N));
-  F8_TRY(check_ws_opt(a.ws, a.ws_bytes));
   Ranges outs, ins;
   outs.add(a.y, M * N * es_of(a.y_dtype));
-  outs.add(a.ws, a.ws ? (int64_t)a.ws_bytes : 0);
   if (!fused) outs.add(a.x4, M, K);
   if (xt) outs.add(a.x4t, K, M);
   (quant_w ? outs : ins).add(a.w4, N, K);
@@ -190,7 +177,7 @@ int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *p, void *stream) {
   F8_TRY(status_of(launch_mx_quantize(q, both ? 2 : 1, a.rule, s)));
   if (quant_w && !both) F8_TRY(status_of(launch_mx_quantize(q + 1, 1, a.rule, s)));
   const MxGemm g = {a.x4, a.w4, a.y, a.bias, M, N, K, a.y_dtype, a.bias_dtype};
-  return status_of(launch_mx_gemms(&g, 1, a.ws, a.ws ? a.ws_bytes : 0, s));
+  return status_of(launch_mx_gemms(&g, 1, s));
 }
 
 int f8lin_mxfp4_forward_fused(int64_t M, int64_t N, int64_t K) { return mx_linear_fused(M, N, K) ? 1 : 0; }
@@ -238,8 +225,6 @@ int f8lin_mxfp4_backward(const f8lin_mxfp4_bwd_args *p, void *stream) {
     outs.add(a.dbias, N * es_of(a.dbias_dtype));
     outs.add(a.dbias_ws, db_ws);
   }
-  F8_TRY(check_ws_opt(a.ws, a.ws_bytes));
-  outs.add(a.ws, a.ws ? (int64_t)a.ws_bytes : 0);
   if (any_overlap(outs.r, outs.n, ins.r, ins.n)) return F8LIN_EINVAL;
 
   hipStream_t s = (hipStream_t)stream;
@@ -251,7 +236,7 @@ int f8lin_mxfp4_backward(const f8lin_mxfp4_bwd_args *p, void *stream) {
   int n = 0;
   if (a.dx) g[n++] = MxGemm{a.dy4, a.w4t, a.dx, nullptr, M, K, N, a.dx_dtype, 0};
   if (a.dw) g[n++] = MxGemm{a.dy4t, a.x4t, a.dw, nullptr, N, K, M, a.dw_dtype, 0};
-  return n ? status_of(launch_mx_gemms(g, n, a.ws, a.ws ? a.ws_bytes : 0, s)) : F8LIN_OK;
+  return n ? status_of(launch_mx_gemms(g, n, s)) : F8LIN_OK;
 }
 
 size_t f8lin_grad_workspace_bytes(void) { return kGradPartials * sizeof(double); }

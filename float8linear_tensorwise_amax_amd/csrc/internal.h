@@ -147,8 +147,7 @@ struct MxGemm {
   int64_t M, N, K;
   int c_dtype, bias_dtype;
 };
-hipError_t launch_mx_gemms(const MxGemm *d, int count, void *ws, size_t ws_bytes, hipStream_t stream);
-size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_gemms(const MxGemm *d, int count, hipStream_t stream);
 
 // Y = X4 . W4^T with X quantised inside the product's kernel (few rows).
 struct MxLinear {

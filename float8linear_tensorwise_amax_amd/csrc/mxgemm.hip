@@ -31,16 +31,16 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 struct MxProblem {
   const uint8_t *a, *as, *b, *bs;
-  void *c;           // splits > 1: splits x (M, N) fp32 partial products
+  void *c;
   const void *bias;
   int64_t lda, lsa, ldb, lsb;
   int M, N, nb;      // nb: MX blocks of K
   int c_dtype, bias_dtype;
-  int tiles, splits, group, group_log;  // output tiles, K ranges, tile-rows per group (a power of two)
-  // divisors: tiles, tiles per group, tile-rows of the last group
+  int nkb;           // K blocks of 128 bytes
+  int tiles, group, group_log;  // output tiles, tile-rows per group (a power of two)
+  // divisors: tiles per group, tile-rows of the last group
   int group_tiles, last_rows, last_group;
-  uint32_t inv_tiles, inv_group_tiles, inv_last_rows;
-  int nkb, pairs;    // K blocks of 128 bytes, and pairs of them
+  uint32_t inv_group_tiles, inv_last_rows;
 };
 struct MxBatch {
   MxProblem p[kMxMaxGemms];
@@ -83,14 +83,13 @@ __device__ __forceinline__ int div_by(int n, int d, uint32_t inv) {
   return n - q * d >= d ? q + 1 : q;
 }
 
-// One output tile (of one K range) of one problem.
+// One output tile of one problem.
 struct Item {
-  int pi, m0, n0, range;
-  int kb0, nkb;  // first K block, number of K blocks (at least one)
-  int nb;        // MX blocks from kb0 to the end of the range
+  int pi, m0, n0;
+  int nkb, nb;  // K blocks (at least one), MX blocks
 };
 
-template <int BM, int BN, int NS, int MINB, int DT, bool SPLIT>
+template <int BM, int BN, int NS, int MINB, int DT>
 __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch) {
   // The problems are read where the launch put them, through the scalar
   // cache (an argument indexed at run time would be copied to scratch).
@@ -119,7 +118,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   const int xcd = (int)blockIdx.x % kXcds;
   const int nwg = (int)gridDim.x, wx = nwg / kXcds + (xcd < nwg % kXcds ? 1 : 0);
   auto share = [&](int i, int &st, int &ln) {
-    const int T = i < batch.count ? batch.p[i].tiles * batch.p[i].splits : 0;
+    const int T = i < batch.count ? batch.p[i].tiles : 0;
     const int per = T / kXcds, rem = T % kXcds;
     st = xcd * per + min(xcd, rem);
     ln = per + (xcd < rem ? 1 : 0);
@@ -134,27 +133,17 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
     w.pi = it < ln0 ? 0 : 1;
     const int t = it < ln0 ? st0 + it : st1 + it - ln0;
     const MxProblemArg &P = batch.p[w.pi];
-    // K ranges hold whole pairs of K blocks (16 bytes of scales)
-    w.range = 0;
-    w.kb0 = 0;
-    int end = P.nkb, local = t;
-    if constexpr (SPLIT) {
-      w.range = div_by(t, P.tiles, P.inv_tiles);
-      local = t - w.range * P.tiles;
-      w.kb0 = w.range * P.pairs / P.splits * 2;
-      end = min((w.range + 1) * P.pairs / P.splits * 2, P.nkb);
-    }
     // groups of `group` tile-rows, each walked column by column, so that the
     // tiles an XCD runs at once form a compact patch whose operand slices its
     // L2 shares
-    const int grp = div_by(local, P.group_tiles, P.inv_group_tiles), in = local - grp * P.group_tiles;
+    const int grp = div_by(t, P.group_tiles, P.inv_group_tiles), in = t - grp * P.group_tiles;
     const bool tail = grp == P.last_group;
     const int rows = tail ? P.last_rows : P.group;
     const int tn = tail ? div_by(in, P.last_rows, P.inv_last_rows) : in >> P.group_log;
     w.m0 = (grp * P.group + in - tn * rows) * BM;
     w.n0 = tn * BN;
-    w.nkb = end - w.kb0;
-    w.nb = min(end * kBlocksPerK, P.nb) - w.kb0 * kBlocksPerK;
+    w.nkb = P.nkb;
+    w.nb = P.nb;
     return w;
   };
   int it = (int)blockIdx.x / kXcds;
@@ -179,10 +168,8 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   auto set_copy_item = [&](bool live) {
     const MxProblemArg &P = batch.p[ci.pi];
     const int rows_a = min(BM, P.M - ci.m0), rows_b = min(BN, P.N - ci.n0);
-    ra = __builtin_amdgcn_make_buffer_rsrc((void *)(P.a + ci.m0 * P.lda + ci.kb0 * kBlockBytes), (short)0,
-                                           rows_a * (int)P.lda - ci.kb0 * kBlockBytes, 0x00020000);
-    rb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.b + ci.n0 * P.ldb + ci.kb0 * kBlockBytes), (short)0,
-                                           rows_b * (int)P.ldb - ci.kb0 * kBlockBytes, 0x00020000);
+    ra = __builtin_amdgcn_make_buffer_rsrc((void *)(P.a + ci.m0 * P.lda), (short)0, rows_a * (int)P.lda, 0x00020000);
+    rb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.b + ci.n0 * P.ldb), (short)0, rows_b * (int)P.ldb, 0x00020000);
     rsa = __builtin_amdgcn_make_buffer_rsrc((void *)(P.as + ci.m0 * P.lsa), (short)0, rows_a * (int)P.lsa, 0x00020000);
     rsb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.bs + ci.n0 * P.lsb), (short)0, rows_b * (int)P.lsb, 0x00020000);
     step_a = 16 * (int)P.lda;
@@ -226,7 +213,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
   auto copy_scales = [&]() {
     const bool even = !(c_kb & 1);
     uint8_t *dst = smem + NS * STB + (even ? (c_pair & (RING - 1)) * SCB : RING * SCB);
-    const int so = (ci.kb0 + c_kb) * kBlocksPerK, odd = even ? 0 : kOutOfRange;
+    const int so = c_kb * kBlocksPerK, odd = even ? 0 : kOutOfRange;
     if constexpr (BM == 256 && BN == 256) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(dst + wave * 1024), 16, (vsa + wave * step_sa) | odd, so,
                                                0, 0);
@@ -304,7 +291,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
     constexpr int ES = DT == F8LIN_FP32 ? 4 : 2;
     const int lane_col = DT == F8LIN_FP32 ? 4 * g : 16 * (g & 1) + 8 * (g >> 1);
     const int left = N - col0 - lane_col;  // columns from this lane's first one to the edge
-    int64_t at = (int64_t)(uintptr_t)P.c + (((SPLIT ? (int64_t)w.range * M : 0) + row0) * N + col0 + lane_col) * ES;
+    int64_t at = (int64_t)(uintptr_t)P.c + ((int64_t)row0 * N + col0 + lane_col) * ES;
     const int64_t step = (int64_t)16 * N * ES;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -449,7 +436,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         v4f init = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (!SPLIT && P.bias) {
+        if (P.bias) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const int col = cur.n0 + wn + 16 * j + 4 * g + v;
@@ -474,7 +461,7 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
 }
 
 // ---- Few rows (M <= 64): bound by reading B once.  A workgroup of NW waves
-// owns 16 rows of B (16 output columns), so N / 16 workgroups stream B; the
+// owns NT x 16 rows of B (output columns), so that many workgroups stream B; the
 // waves split K in 128-byte blocks (wave w takes blocks w, w + NW, ...), load
 // operands straight into registers, U blocks in flight, and their partial
 // sums meet in LDS.  FUSED (X not yet quantised, M <= 16): every workgroup
@@ -489,6 +476,8 @@ struct MxSkinny {
   int c_dtype, bias_dtype;
 };
 constexpr int kSkinnyMaxM = 64;
+// Rows that every workgroup quantises itself (see launch_mx_linear).
+constexpr int kFusedMaxM = 2;
 
 
 // LDS strides of the quantised X: rows 16 bytes apart from a multiple of 128
@@ -497,20 +486,14 @@ __host__ __device__ constexpr int fused_row(int nkb) { return nkb * kBlockBytes 
 __host__ __device__ constexpr int fused_scale_row(int nkb) { return nkb * kBlocksPerK; }
 __host__ __device__ constexpr int fused_bytes(int M, int nkb) { return M * (fused_row(nkb) + fused_scale_row(nkb)); }
 
-#ifndef XU
-#define XU 4
-#define XFM 2
-#define XNW8 512
-#endif
-constexpr int kFusedMaxM = XFM;
-template <int MT, int NW, bool FUSED, int XDT, int RULE>
+template <int MT, int NT, int NW, bool FUSED, int XDT, int RULE>
 __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
-  constexpr int U = MT == 1 ? XU : (MT == 2 ? 4 : 2);
+  constexpr int U = MT <= 2 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16;
-  const int rows_b = min(16, P.N - n0);
+  const int n0 = (int)blockIdx.x * 16 * NT;
+  const int rows_b = min(16 * NT, P.N - n0);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.b + n0 * P.ldb), (short)0,
                                                                       rows_b * (int)P.ldb, 0x00020000);
   const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc((void *)(P.bs + n0 * P.lsb), (short)0,
@@ -540,15 +523,18 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
     if (left <= 4) sel = left <= 0 ? 0x0C0C0C0Cu : (sel & 0xFFu) | 0x0C0C0C00u;
     return (int)__builtin_amdgcn_perm(sc.y, sc.x, sel);
   };
-  v4f acc[MT];
+  v4f acc[MT][NT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4 fb[U][2], fa[FUSED ? 1 : U][MT][2];
-  u32x2 sb[U], sa[FUSED ? 1 : U][MT];
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 fb[U][NT][2], fa[FUSED ? 1 : U][MT][2];
+  u32x2 sb[U][NT], sa[FUSED ? 1 : U][MT];
   auto load_all = [&](int kb0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      load(rb, rsb, (int)P.ldb, (int)P.lsb, r, kb0 + NW * u, fb[u], sb[u]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) load(rb, rsb, (int)P.ldb, (int)P.lsb, 16 * n + r, kb0 + NW * u, fb[u][n], sb[u][n]);
       if constexpr (!FUSED) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) load(ra, rsa, (int)P.lda, (int)P.lsa, 16 * m + r, kb0 + NW * u, fa[u][m], sa[u][m]);
@@ -577,7 +563,9 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kb = kb0 + NW * u;
-      const int sbu = scale(sb[u], kb);
+      int sbu[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sbu[n] = scale(sb[u][n], kb);
       if constexpr (FUSED) {
         fa[0][0][0] = fa[0][0][1] = u32x4{0, 0, 0, 0};
         sa[0][0] = u32x2{0, 0};
@@ -592,10 +580,13 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
       for (int m = 0; m < MT; ++m) {
         const int ua = FUSED ? 0 : u;
         const int sau = scale(sa[ua][m], kb);
-        acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[u][0]), frag8(fa[ua][m][0]), acc[m], 4, 4, 0,
-                                                                  sbu, 0, sau);
-        acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[u][1]), frag8(fa[ua][m][1]), acc[m], 4, 4, 1,
-                                                                  sbu, 1, sau);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[u][n][0]), frag8(fa[ua][m][0]), acc[m][n],
+                                                                       4, 4, 0, sbu[n], 0, sau);
+          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag8(fb[u][n][1]), frag8(fa[ua][m][1]), acc[m][n],
+                                                                       4, 4, 1, sbu[n], 1, sau);
+        }
       }
     }
     kb0 += NW * U;
@@ -605,14 +596,16 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
   __syncthreads();  // (the quantised X is read by all: the partial sums take its place)
   v4f *red = reinterpret_cast<v4f *>(dyn);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) red[(wave * MT + m) * 64 + lane] = acc[m];
-  __syncthreads();
-  if (wave < MT) {
-    const int m = wave;
-    v4f t = red[m * 64 + lane];
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int w = 1; w < NW; ++w) t += red[(w * MT + m) * 64 + lane];
-    const int row = 16 * m + r, col = n0 + 4 * g;
+    for (int n = 0; n < NT; ++n) red[((wave * MT + m) * NT + n) * 64 + lane] = acc[m][n];
+  __syncthreads();
+  for (int i = wave; i < MT * NT; i += NW) {
+    const int m = i / NT, n = i % NT;
+    v4f t = red[i * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) t += red[(w * MT * NT + i) * 64 + lane];
+    const int row = 16 * m + r, col = n0 + 16 * n + 4 * g;
     if (row < P.M) {
 #pragma unroll
       for (int v = 0; v < 4; ++v)
@@ -624,17 +617,6 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
   }
 }
 
-// C = sum over ranges of the fp32 partial products, in range order (+ bias), rounded.
-__global__ __launch_bounds__(256) void mx_split_reduce_kernel(const float *__restrict__ part, int splits, int64_t mn, int N,
-                                                              void *c, int c_dtype, const void *bias, int bias_dtype) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < mn; i += (int64_t)gridDim.x * 256) {
-    float s = part[i];
-    for (int k = 1; k < splits; ++k) s += part[(int64_t)k * mn + i];
-    if (bias) s += load_elem(bias, i % N, bias_dtype);
-    store_elem(c, i, s, c_dtype);
-  }
-}
-
 // K = 0: C is the bias, or zero.
 __global__ __launch_bounds__(256) void mx_fill_kernel(void *c, int c_dtype, int64_t mn, int N, const void *bias,
                                                       int bias_dtype) {
@@ -642,86 +624,102 @@ __global__ __launch_bounds__(256) void mx_fill_kernel(void *c, int c_dtype, int6
     store_elem(c, i, bias ? load_elem(bias, i % N, bias_dtype) : 0.0f, c_dtype);
 }
 
-void set_tiles(MxProblem &p, int bm, int bn, int group_log, int splits) {
+void set_tiles(MxProblem &p, int bm, int bn, int group_log) {
   const int tm = (p.M + bm - 1) / bm, tn = (p.N + bn - 1) / bn;
   auto inv = [](int d) { return (uint32_t)std::min<uint64_t>(0xFFFFFFFFull, (1ull << 32) / (uint64_t)d); };
   p.tiles = tm * tn;
-  p.splits = splits;
   p.group_log = group_log;
   p.group = 1 << group_log;
   p.group_tiles = p.group * tn;
   p.last_rows = tm % p.group ? tm % p.group : p.group;
   p.last_group = (tm - 1) >> group_log;
-  p.inv_tiles = inv(p.tiles);
   p.inv_group_tiles = inv(p.group_tiles);
   p.inv_last_rows = inv(p.last_rows);
-  p.nkb = (p.nb + kBlocksPerK - 1) / kBlocksPerK;
-  p.pairs = (p.nkb + 1) / 2;
 }
 
-template <int BM, int BN, int NS, int MINB, bool SPLIT>
-void launch_tiled(const MxBatch &b, int dt, unsigned grid, hipStream_t stream) {
-  if (SPLIT || dt == F8LIN_FP32)
-    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP32, SPLIT><<<grid, 256, 0, stream>>>(b);
+template <int BM, int BN, int NS, int MINB>
+void launch_tiled(const MxBatch &b, int dt, int64_t tiles, hipStream_t stream) {
+  const unsigned grid = (unsigned)std::min<int64_t>(tiles, MINB * kCUs);
+  if (dt == F8LIN_FP32)
+    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP32><<<grid, 256, 0, stream>>>(b);
   else if (dt == F8LIN_BF16)
-    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_BF16, false><<<grid, 256, 0, stream>>>(b);
+    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_BF16><<<grid, 256, 0, stream>>>(b);
   else
-    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP16, false><<<grid, 256, 0, stream>>>(b);
+    mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP16><<<grid, 256, 0, stream>>>(b);
 }
 
-template <int MT, bool FUSED, int XDT, int RULE>
+template <int MT, int NT, bool FUSED, int XDT, int RULE>
 void launch_skinny_nw(const MxSkinny &k, hipStream_t stream) {
-  const unsigned grid = (unsigned)((k.N + 15) / 16);
+  const unsigned grid = (unsigned)((k.N + 16 * NT - 1) / (16 * NT));
   const size_t x = FUSED ? fused_bytes(k.M, k.nkb) : 0;
-  // eight waves where there are few workgroups
-  if (grid <= XNW8)
-    mx_skinny_kernel<MT, 8, FUSED, XDT, RULE><<<grid, 512, std::max<size_t>(x, 8 * MT * 1024), stream>>>(k);
+  // eight waves where few workgroups have a long contraction (1 x 4096 x
+  // 14336: 10.9 us, with four 12.9 us; 51 x 4800 x 1600: 8.9 us, with four 6.3 us)
+  if (grid <= 2 * kCUs && k.nkb >= 32)
+    mx_skinny_kernel<MT, NT, 8, FUSED, XDT, RULE><<<grid, 512, std::max<size_t>(x, 8 * MT * NT * 1024), stream>>>(k);
   else
-    mx_skinny_kernel<MT, 4, FUSED, XDT, RULE><<<grid, 256, std::max<size_t>(x, 4 * MT * 1024), stream>>>(k);
+    mx_skinny_kernel<MT, NT, 4, FUSED, XDT, RULE><<<grid, 256, std::max<size_t>(x, 4 * MT * NT * 1024), stream>>>(k);
 }
 
 void launch_skinny(const MxProblem &p, hipStream_t stream) {
   MxSkinny k = {};
   k.a = p.a, k.as = p.as, k.b = p.b, k.bs = p.bs, k.c = p.c, k.bias = p.bias;
   k.lda = p.lda, k.lsa = p.lsa, k.ldb = p.ldb, k.lsb = p.lsb;
-  k.M = p.M, k.N = p.N, k.nb = p.nb, k.nkb = (p.nb + kBlocksPerK - 1) / kBlocksPerK;
+  k.M = p.M, k.N = p.N, k.nb = p.nb, k.nkb = p.nkb;
   k.c_dtype = p.c_dtype, k.bias_dtype = p.bias_dtype;
-  switch ((p.M + 15) / 16) {
-    case 1: launch_skinny_nw<1, false, 0, 0>(k, stream); break;
-    case 2: launch_skinny_nw<2, false, 0, 0>(k, stream); break;
-    case 3: launch_skinny_nw<3, false, 0, 0>(k, stream); break;
-    default: launch_skinny_nw<4, false, 0, 0>(k, stream); break;
-  }
+  const int mt = (p.M + 15) / 16;
+  // two column blocks per workgroup halve what is read of A, where enough
+  // workgroups are left (33 x 14336 x 4096: 17.9 us, with one 23.0 us; 64 x
+  // 4096 x 4096: 12.9 us, with one 10.2 us)
+  const bool wide = p.N >= 32 * kCUs;
+  if (mt == 1) launch_skinny_nw<1, 1, false, 0, 0>(k, stream);
+  else if (mt == 2 && wide) launch_skinny_nw<2, 2, false, 0, 0>(k, stream);
+  else if (mt == 2) launch_skinny_nw<2, 1, false, 0, 0>(k, stream);
+  else if (wide) launch_skinny_nw<4, 2, false, 0, 0>(k, stream);
+  else launch_skinny_nw<4, 1, false, 0, 0>(k, stream);
 }
 
-// One launch for problems of one output type.
-void launch_batch(MxBatch &b, int dt, hipStream_t stream) {
-  int64_t big = 0, mid = 0;
-  for (int i = 0; i < b.count; ++i) {
-    big += ((b.p[i].M + 255) / 256) * (int64_t)((b.p[i].N + 255) / 256);
-    mid += ((b.p[i].M + 127) / 128) * (int64_t)((b.p[i].N + 127) / 128);
-  }
-  const int force = getenv("XCFG") ? atoi(getenv("XCFG")) : -1;
-  const int cfg = force >= 0 ? force : big >= kCUs ? 0 : mid > kCUs ? 1 : mid > kCUs / 2 ? 2 : 3;
-  const int bm = cfg == 0 ? 256 : cfg < 3 ? 128 : 64;
+// The tile a problem takes: 0: 256 x 256, one workgroup per CU; 1: 128 x 128,
+// two per CU; 2: the same, one per CU with four stages; 3: 64 x 64, one per CU
+// with eight stages.  The one whose estimated time is least: rounds of
+// workgroups times a cost per round (prologue and stores) and per K block, in
+// microseconds as measured (bf16 output):
+//   4096 x 4096 x 4096       0:  40   1: 49   2: 57   3: 110
+//   4096 x 4096 x 256        0:  17   1: 14   2: 19   3:  29
+//   2048 x 4096 x 4096       0:  36   1: 27   2: 32   3:  58
+//   256 x 4096 x 4096        0:  32   1: 17   2: 18   3:  13
+//   1600 x 1600 x 12288      0:  74   1: 44   2: 38   3:  59
+int tile_for(const MxProblem &p) {
+  auto rounds = [&](int b, int slots) {
+    const int64_t tiles = (int64_t)((p.M + b - 1) / b) * ((p.N + b - 1) / b);
+    return (double)((tiles + slots - 1) / slots);
+  };
+  const double k = p.nkb;
+  const bool spread = rounds(128, kCUs) <= 1.0;  // at most one 128 x 128 tile per CU
+  const double t[4] = {5.5 + rounds(256, kCUs) * (8.5 + 1.75 * k),
+                       3.0 + (spread ? 3.5 + 0.75 * k : rounds(128, 2 * kCUs) * (4.4 + 1.15 * k)),
+                       4.0 + rounds(128, kCUs) * (3.5 + 0.68 * k), 4.5 + rounds(64, kCUs) * (1.7 + 0.36 * k)};
+  return (int)(std::min_element(t, t + 4) - t);
+}
+
+// Problems of one output type and tile in one launch.
+void launch_batch(MxBatch &b, int tile, int dt, hipStream_t stream) {
+  const int bm = tile == 0 ? 256 : tile < 3 ? 128 : 64;
   int64_t tiles = 0;
   for (int i = 0; i < b.count; ++i) {
-    set_tiles(b.p[i], bm, bm, cfg == 0 ? 2 : 3, 1);
+    // groups of 4 tile-rows; of 8 with small tiles, and in long runs of big
+    // ones (65536 x 4096 x 4096: 576 us, with 4 586 us; 8192^3: 256 and 252 us)
+    const bool many = (int64_t)((b.p[i].M + 255) / 256) * ((b.p[i].N + 255) / 256) >= 8 * kCUs;
+    set_tiles(b.p[i], bm, bm, tile == 0 && !many ? 2 : 3);
     tiles += b.p[i].tiles;
   }
-  if (cfg == 0)
-    launch_tiled<256, 256, 2, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
-  else if (cfg == 1)
-    launch_tiled<128, 128, 2, 2, false>(b, dt, (unsigned)std::min<int64_t>(tiles, 2 * kCUs), stream);
-  else if (cfg == 2)
-    launch_tiled<128, 128, 4, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
-  else
-    launch_tiled<64, 64, 8, 1, false>(b, dt, (unsigned)std::min<int64_t>(tiles, kCUs), stream);
+  if (tile == 0) launch_tiled<256, 256, 2, 1>(b, dt, tiles, stream);
+  else if (tile == 1) launch_tiled<128, 128, 2, 2>(b, dt, tiles, stream);
+  else if (tile == 2) launch_tiled<128, 128, 4, 1>(b, dt, tiles, stream);
+  else launch_tiled<64, 64, 8, 1>(b, dt, tiles, stream);
 }
 
 }  // namespace
 
-size_t mx_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 // Few enough rows, and few enough bytes for every workgroup to quantise them
 // itself (at most 35 KB of LDS).
 bool mx_linear_fused(int64_t M, int64_t N, int64_t K) {
@@ -737,9 +735,9 @@ hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream) {
   k.nb = (int)((l.K + kMxBlock - 1) / kMxBlock), k.nkb = (k.nb + kBlocksPerK - 1) / kBlocksPerK;
 #define F8_MX_L(DT)                                              \
   if (l.rule == F8LIN_MX_CEIL)                                   \
-    launch_skinny_nw<1, true, DT, F8LIN_MX_CEIL>(k, stream);     \
+    launch_skinny_nw<1, 1, true, DT, F8LIN_MX_CEIL>(k, stream);     \
   else                                                           \
-    launch_skinny_nw<1, true, DT, F8LIN_MX_FLOOR>(k, stream)
+    launch_skinny_nw<1, 1, true, DT, F8LIN_MX_FLOOR>(k, stream)
   if (l.x_dtype == F8LIN_BF16) {
     F8_MX_L(F8LIN_BF16);
   } else if (l.x_dtype == F8LIN_FP16) {
@@ -751,9 +749,10 @@ hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream_t stream) {
+hipError_t launch_mx_gemms(const MxGemm *d, int count, hipStream_t stream) {
   bool any = false;
-  MxBatch b[3] = {};  // by output type (a problem of few rows has a launch of its own)
+  MxBatch b = {};
+  int tile[kMxMaxGemms], dt[kMxMaxGemms];
   for (int i = 0; i < count; ++i) {
     if (d[i].M == 0 || d[i].N == 0) continue;
     any = true;
@@ -763,8 +762,7 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream
           d[i].c, d[i].c_dtype, mn, (int)d[i].N, d[i].bias, d[i].bias_dtype);
       continue;
     }
-    MxBatch &list = b[d[i].c_dtype];
-    MxProblem &p = list.p[list.count];
+    MxProblem &p = b.p[b.count];
     p.a = d[i].a.codes;
     p.as = d[i].a.scales;
     p.b = d[i].b.codes;
@@ -778,15 +776,23 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, void *, size_t, hipStream
     p.M = (int)d[i].M;
     p.N = (int)d[i].N;
     p.nb = (int)((d[i].K + kMxBlock - 1) / kMxBlock);
+    p.nkb = (p.nb + kBlocksPerK - 1) / kBlocksPerK;
     p.c_dtype = d[i].c_dtype;
     p.bias_dtype = d[i].bias_dtype;
-    if (p.M <= kSkinnyMaxM)
+    if (p.M <= kSkinnyMaxM) {
       launch_skinny(p, stream);
-    else
-      ++list.count;
+    } else {
+      tile[b.count] = tile_for(p);
+      dt[b.count++] = d[i].c_dtype;
+    }
   }
-  for (int dt = 0; dt < 3; ++dt)
-    if (b[dt].count > 0) launch_batch(b[dt], dt, stream);
+  if (b.count == 2 && (tile[0] != tile[1] || dt[0] != dt[1])) {
+    MxBatch second = {};
+    second.p[0] = b.p[1];
+    second.count = b.count = 1;
+    launch_batch(second, tile[1], dt[1], stream);
+  }
+  if (b.count > 0) launch_batch(b, tile[0], dt[0], stream);
   return any ? hipGetLastError() : hipSuccess;
 }
 

@@ -471,15 +471,14 @@ class MxGemmDesc(ctypes.Structure):
 class MxFwdArgs(ctypes.Structure):
     _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("x", _vp), ("w", _vp), ("ldx", _i64), ("y", _vp),
                 ("bias", _vp), ("x_dtype", _int), ("w_dtype", _int), ("y_dtype", _int), ("bias_dtype", _int),
-                ("x4", MxStruct), ("x4t", MxStruct), ("w4", MxStruct), ("w4t", MxStruct), ("rule", _int),
-                ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
+                ("x4", MxStruct), ("x4t", MxStruct), ("w4", MxStruct), ("w4t", MxStruct), ("rule", _int)]
 
 
 class MxBwdArgs(ctypes.Structure):
     _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("dy", _vp), ("lddy", _i64), ("dx", _vp), ("dw", _vp),
                 ("dbias", _vp), ("dy_dtype", _int), ("dx_dtype", _int), ("dw_dtype", _int), ("dbias_dtype", _int),
                 ("x4t", MxStruct), ("w4t", MxStruct), ("dy4", MxStruct), ("dy4t", MxStruct), ("rule", _int),
-                ("dbias_ws", _vp), ("dbias_ws_bytes", ctypes.c_size_t), ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
+                ("dbias_ws", _vp), ("dbias_ws_bytes", ctypes.c_size_t)]
 
 
 class Grad(ctypes.Structure):
@@ -492,9 +491,7 @@ _lib.f8lin_mxfp4_scale_ld.argtypes = [_i64]
 _lib.f8lin_mxfp4_scale_ld.restype = _i64
 _lib.f8lin_mxfp4_quantize.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _vp]
 _lib.f8lin_mxfp4_dequantize.argtypes = [_vp, _i64, _i64, _int, _vp, _vp]
-_lib.f8lin_mxfp4_gemm.argtypes = [_vp, _int, _vp, ctypes.c_size_t, _vp]
-_lib.f8lin_mxfp4_gemm_workspace_bytes.argtypes = [_i64, _i64, _i64]
-_lib.f8lin_mxfp4_gemm_workspace_bytes.restype = ctypes.c_size_t
+_lib.f8lin_mxfp4_gemm.argtypes = [_vp, _int, _vp]
 _lib.f8lin_mxfp4_forward.argtypes = [_vp, _vp]
 _lib.f8lin_mxfp4_forward_fused.argtypes = [_i64, _i64, _i64]
 _lib.f8lin_mxfp4_forward_fused.restype = _int
@@ -512,8 +509,8 @@ for _name in ("f8lin_mxfp4_quantize", "f8lin_mxfp4_dequantize", "f8lin_mxfp4_gem
 
 # The argument structures as bytes: packing one costs a fraction of filling a ctypes.Structure field by field.
 _MX = struct.Struct("@4q")
-_MX_FWD = struct.Struct("@8q4i16qi4x2q")
-_MX_BWD = struct.Struct("@8q4i16qi4x4q")
+_MX_FWD = struct.Struct("@8q4i16qi4x")
+_MX_BWD = struct.Struct("@8q4i16qi4x2q")
 for _fmt, _cls in ((_MX, MxStruct), (_MX_FWD, MxFwdArgs), (_MX_BWD, MxBwdArgs)):
     assert _fmt.size == ctypes.sizeof(_cls)
 
@@ -673,13 +670,9 @@ def mxfp4_dequantize(q: MXFP4Tensor, out: torch.Tensor, stream=None):
     _call(_lib.f8lin_mxfp4_dequantize, out.device, stream, _MX.pack(*q._c), q.rows, q.cols, _DTYPE[out.dtype], p)
 
 
-def mxfp4_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_lib.f8lin_mxfp4_gemm_workspace_bytes(M, N, K))
-
-
-def mxfp4_gemm(items, ws: Optional[torch.Tensor] = None, stream=None):
+def mxfp4_gemm(items, stream=None):
     """One or two products c (M, N) = a (M, K) . b (N, K)^T (+ bias) in one call; items: (a, b, c) or (a, b, c, bias)
-    tuples, a and b MXFP4Tensors.  ws: optional uint8 scratch (the sum of mxfp4_gemm_workspace_bytes)."""
+    tuples, a and b MXFP4Tensors."""
     arr = (MxGemmDesc * max(1, len(items)))()
     dev = None
     for i, item in enumerate(items):
@@ -694,7 +687,7 @@ def mxfp4_gemm(items, ws: Optional[torch.Tensor] = None, stream=None):
                             0 if bias is None else _DTYPE[bias.dtype])
     if dev is None:
         raise ValueError("mxfp4_gemm: no products given")
-    _call(_lib.f8lin_mxfp4_gemm, dev, stream, arr, len(items), _ptr(ws), _nbytes(ws))
+    _call(_lib.f8lin_mxfp4_gemm, dev, stream, arr, len(items))
 
 
 def mxfp4_forward_fused(M: int, N: int, K: int) -> bool:
@@ -703,9 +696,9 @@ def mxfp4_forward_fused(M: int, N: int, K: int) -> bool:
 
 
 def mxfp4_forward(x, w, y, x4: Optional[MXFP4Tensor], w4: MXFP4Tensor, x4t=None, w4t=None, bias=None, rule="floor",
-                  ws: Optional[torch.Tensor] = None, stream=None):
+                  stream=None):
     """y (M, N) = x4 . w4^T (+ bias).  w (N, K): quantised into w4 (and w4t); None: w4 already holds the weight.
-    x4 is scratch unless x4t is asked for; ws: optional scratch of mxfp4_gemm_workspace_bytes(M, N, K)."""
+    x4 (and x4t, if the backward is to follow) receive X's codes."""
     M, K = x.shape
     N = w4.rows
     dev = x.device
@@ -717,7 +710,7 @@ def mxfp4_forward(x, w, y, x4: Optional[MXFP4Tensor], w4: MXFP4Tensor, x4t=None,
                      0 if bias is None else _dense(bias, "bias", dev), _DTYPE[x.dtype],
                      0 if w is None else _DTYPE[w.dtype], _DTYPE[y.dtype], 0 if bias is None else _DTYPE[bias.dtype],
                      *_mx(x4, M, K, "x4", dev), *_mx(x4t, K, M, "x4t", dev), *_mx(w4, N, K, "w4", dev),
-                     *_mx(w4t, K, N, "w4t", dev), _RULE[rule], _ptr(ws) or 0, _nbytes(ws))
+                     *_mx(w4t, K, N, "w4t", dev), _RULE[rule])
     _call(_lib.f8lin_mxfp4_forward, dev, stream, a)
 
 
@@ -725,8 +718,7 @@ def mxfp4_dbias_workspace_bytes(M: int, N: int) -> int:
     return int(_lib.f8lin_mxfp4_dbias_workspace_bytes(M, N))
 
 
-def mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, dbias=None, dbias_ws=None, rule="floor",
-                   ws: Optional[torch.Tensor] = None, stream=None):
+def mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, dbias=None, dbias_ws=None, rule="floor", stream=None):
     """dx (M, K), dw (N, K) and dbias (N) -- each may be None -- of the layer whose forward left x4t (K, M) and
     w4t (K, N).  dy4 (M, N; for dx) and dy4t (N, M; for dw or dbias) receive dY's two layouts; dbias_ws: float32
     scratch of mxfp4_dbias_workspace_bytes(M, N)."""
@@ -742,8 +734,7 @@ def mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, dbias=None, dbias_ws=None, r
     a = _MX_BWD.pack(M, N, K, p, ld, opt(dx, "dx"), opt(dw, "dw"), opt(dbias, "dbias"), _DTYPE[dy.dtype], dt(dx), dt(dw),
                      dt(dbias), *_mx(x4t if dw is not None else None, K, M, "x4t", dev),
                      *_mx(w4t if dx is not None else None, K, N, "w4t", dev), *_mx(dy4, M, N, "dy4", dev),
-                     *_mx(dy4t, N, M, "dy4t", dev), _RULE[rule], _ptr(dbias_ws, torch.float32) or 0, _nbytes(dbias_ws),
-                     _ptr(ws) or 0, _nbytes(ws))
+                     *_mx(dy4t, N, M, "dy4t", dev), _RULE[rule], _ptr(dbias_ws, torch.float32) or 0, _nbytes(dbias_ws))
     _call(_lib.f8lin_mxfp4_backward, dev, stream, a)
 
 

@@ -338,10 +338,6 @@ def sync_float8_amax_and_scale_history(module: nn.Module, check: bool = False) -
 
 # ------------------------------------------------------------------- MXFP4
 
-def _workspace(n: int, device) -> Optional[torch.Tensor]:
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
-
-
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """t as a 2-D tensor with contiguous rows (a copy only where its strides need one)."""
     if t.dim() == 2 and t.is_contiguous():
@@ -364,8 +360,7 @@ class _MXFP4LinearFn(torch.autograd.Function):
         # the transposed copies only for the gradients that will be asked for
         x4t = f8lin.new_mxfp4(K, M, dev) if ctx.needs_input_grad[1] else None
         w4t = f8lin.new_mxfp4(K, N, dev) if ctx.needs_input_grad[0] else None
-        ws = _workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), dev)
-        f8lin.mxfp4_forward(x, w, y, x4, w4, x4t, w4t, None if bias is None else bias.contiguous(), rule, ws)
+        f8lin.mxfp4_forward(x, w, y, x4, w4, x4t, w4t, None if bias is None else bias.contiguous(), rule)
         ctx.save_for_backward(*(q.buffer for q in (x4t, w4t) if q is not None))
         ctx.args = (M, N, K, rule, x.dtype, weight.dtype, None if bias is None else bias.dtype)
         return y
@@ -388,9 +383,7 @@ class _MXFP4LinearFn(torch.autograd.Function):
             db_ws = torch.empty(max(1, f8lin.mxfp4_dbias_workspace_bytes(M, N) // 4), dtype=torch.float32, device=dev)
         dy4 = f8lin.new_mxfp4(M, N, dev) if need_x else None
         dy4t = f8lin.new_mxfp4(N, M, dev) if need_w or need_b else None
-        ws = _workspace((f8lin.mxfp4_gemm_workspace_bytes(M, K, N) if need_x else 0)
-                        + (f8lin.mxfp4_gemm_workspace_bytes(N, K, M) if need_w else 0), dev)
-        f8lin.mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, db, db_ws, rule, ws)
+        f8lin.mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, db, db_ws, rule)
         return dx, dw, db, None
 
 
@@ -418,8 +411,7 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
     y = torch.empty((M, N), dtype=x.dtype, device=x.device)
     fused = f8lin.mxfp4_forward_fused(M, N, K)  # X is quantised inside the product: no buffers
     f8lin.mxfp4_forward(x2, None, y, None if fused else f8lin.new_mxfp4(M, K, x.device), weight,
-                        bias=None if bias is None else bias.contiguous(), rule=rule,
-                        ws=None if fused else _workspace(f8lin.mxfp4_gemm_workspace_bytes(M, N, K), x.device))
+                        bias=None if bias is None else bias.contiguous(), rule=rule)
     return y if x.dim() == 2 else y.reshape(*lead, N)
 
 

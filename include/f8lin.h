@@ -425,11 +425,8 @@ int f8lin_mxfp4_dequantize(const f8lin_mxfp4 *q, int64_t rows, int64_t cols, int
 /* C (M, N) = A (M, K) . B (N, K)^T (+ bias (N), added in fp32 to every row):
  * MXFP4 operands with blocks along K, exact products, fp32 accumulation, one
  * rounding to c_dtype.  bias may be NULL.  K = 0 gives C = bias (or 0).
- * count (1 .. F8LIN_MXFP4_MAX_BATCH) products in one call.
- * ws: optional scratch (NULL = none) of f8lin_mxfp4_gemm_workspace_bytes
- * bytes per product, 16-byte aligned, no initialisation, with which a product
- * of few output tiles and a long contraction is split along K; its partial
- * sums meet in a fixed order (the same bits on every run). */
+ * count (1 .. F8LIN_MXFP4_MAX_BATCH) products in one call, each the same, bit
+ * for bit, as alone. */
 #define F8LIN_MXFP4_MAX_BATCH 2
 typedef struct {
   f8lin_mxfp4 a, b;
@@ -438,8 +435,7 @@ typedef struct {
   int64_t M, N, K;
   int c_dtype, bias_dtype;
 } f8lin_mxfp4_gemm_desc;
-int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *ws, size_t ws_bytes, void *stream);
-size_t f8lin_mxfp4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *stream);
 
 /* Forward of a linear layer with 4-bit operands: Y = X4 . W4^T (+ bias).
  * w != NULL (training): X and W are quantised, x4 / w4 for this product and,
@@ -458,8 +454,6 @@ typedef struct {
   int x_dtype, w_dtype, y_dtype, bias_dtype;
   f8lin_mxfp4 x4, x4t, w4, w4t; /* (M, K), (K, M), (N, K), (K, N) */
   int rule;
-  void *ws; /* optional: f8lin_mxfp4_gemm_workspace_bytes(M, N, K) */
-  size_t ws_bytes;
 } f8lin_mxfp4_fwd_args;
 int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *args, void *stream);
 int f8lin_mxfp4_forward_fused(int64_t M, int64_t N, int64_t K);
@@ -468,9 +462,10 @@ int f8lin_mxfp4_forward_fused(int64_t M, int64_t N, int64_t K);
  *   dX (M, K) = dY4 . W4t^T  (contraction over N)
  *   dW (N, K) = dY4t . X4t^T (contraction over M)
  *   dbias (N) = column sums of dY (not quantised; fp32 in a fixed order)
- * dx, dw and dbias may each be NULL (not computed; dx without dw needs no
- * x4t / dy4t, dw without dx no w4t / dy4).  dbias needs dbias_ws of
- * f8lin_mxfp4_dbias_workspace_bytes(M, N) bytes. */
+ * dx, dw and dbias may each be NULL (not computed).  dx needs dy4 and w4t, dw
+ * needs dy4t and x4t, dbias needs dy4t (its sums are taken on the way) and
+ * dbias_ws of f8lin_mxfp4_dbias_workspace_bytes(M, N) bytes (16-byte aligned,
+ * no initialisation needed). */
 typedef struct {
   int64_t M, N, K;
   const void *dy;
@@ -481,8 +476,6 @@ typedef struct {
   int rule;
   float *dbias_ws;
   size_t dbias_ws_bytes;
-  void *ws; /* optional: f8lin_mxfp4_gemm_workspace_bytes(M, K, N) + ...(N, K, M) */
-  size_t ws_bytes;
 } f8lin_mxfp4_bwd_args;
 int f8lin_mxfp4_backward(const f8lin_mxfp4_bwd_args *args, void *stream);
 size_t f8lin_mxfp4_dbias_workspace_bytes(int64_t M, int64_t N);
