@@ -417,7 +417,8 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
 
 class MXFP4Linear(nn.Module):
     """nn.Linear whose products run in MXFP4 (mxfp4_linear).  freeze() replaces the weight by its 4-bit form, kept in
-    the buffers weight_codes and weight_scales, after which the layer only serves."""
+    the buffers weight_codes and weight_scales, after which the layer only serves: its bias is no longer trained, and
+    an input that needs a gradient is refused.  (A frozen layer's state dict loads into a frozen layer.)"""
 
     def __init__(self, in_features: int, out_features: int, rule: str = "floor", weight: Optional[torch.Tensor] = None,
                  device=None, dtype=torch.bfloat16, bias=False):
@@ -452,16 +453,17 @@ class MXFP4Linear(nn.Module):
         if not self.frozen:
             q = f8lin.new_mxfp4(self.out_features, self.in_features, self.weight.device)
             f8lin.mxfp4_quantize(self.weight.detach().contiguous(), q, None, self.rule)
-            self.weight_codes, self.weight_scales = q.codes.contiguous(), q.scales.contiguous()
+            self.weight_codes, self.weight_scales = q.codes.clone(), q.scales.clone()
             self.weight = None
+            if self.bias is not None:
+                self.bias = nn.Parameter(self.bias.detach(), requires_grad=False)
         return self
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if not self.frozen:
             return mxfp4_linear(x, self.weight, self.bias, self.rule)
         q = f8lin.MXFP4Tensor(self.weight_codes, self.weight_scales, self.out_features, self.in_features)
-        with torch.no_grad():
-            return mxfp4_linear(x, q, self.bias, self.rule)
+        return mxfp4_linear(x, q, self.bias, self.rule)
 
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, bias={self.bias is not None}, "
