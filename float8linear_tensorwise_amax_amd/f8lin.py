@@ -571,7 +571,7 @@ class MXFP4Tensor:
     scales (rows, >= ceil(cols / 32) rounded up to 16) uint8: e8m0, 2^(byte - 127), 255 for NaN
     Both with contiguous rows 16 bytes aligned.  A row's codes and scales are views into what you pass."""
 
-    __slots__ = ("_codes", "_scales", "rows", "cols", "device", "buffer", "_c")
+    __slots__ = ("_codes", "_scales", "rows", "cols", "device", "_buffer", "_at", "_c")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         nb = -(-cols // MXFP4_BLOCK)
@@ -580,7 +580,7 @@ class MXFP4Tensor:
         if not codes.is_cuda or scales.device != codes.device:
             raise ValueError("MXFP4Tensor: codes and scales must be on one GPU")
         self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
-        self.device, self.buffer = codes.device, None
+        self.device, self._buffer = codes.device, None
         if rows and cols:
             (cr, cw), (sr, sw) = codes.shape, scales.shape
             sn = -(-nb // 16) * 16
@@ -594,27 +594,28 @@ class MXFP4Tensor:
             self._c = _NO_MX
 
     @classmethod
-    def _of(cls, buffer: torch.Tensor, rows: int, cols: int, ld: int, scale_ld: int) -> "MXFP4Tensor":
-        """The tensor laid out in one flat buffer: all codes, then all scales."""
+    def _of(cls, buffer: torch.Tensor, at: int, rows: int, cols: int, ld: int, scale_ld: int) -> "MXFP4Tensor":
+        """The tensor whose codes, then scales, lie `at` bytes into a flat buffer."""
         t = cls.__new__(cls)
         t._codes = t._scales = None
-        t.rows, t.cols, t.device, t.buffer = rows, cols, buffer.device, buffer
-        p = buffer.data_ptr()
+        t.rows, t.cols, t.device, t._buffer, t._at = rows, cols, buffer.device, buffer, at
+        p = buffer.data_ptr() + at
         t._c = (p, p + rows * ld, ld, scale_ld)
         return t
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            n, ld = self.rows, self._c[2]
-            self._codes = self.buffer[:n * ld].view(n, ld)
+            n, ld, at = self.rows, self._c[2], self._at
+            self._codes = self._buffer[at:at + n * ld].view(n, ld)
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
             n, ld, sld = self.rows, self._c[2], self._c[3]
-            self._scales = self.buffer[n * ld:n * (ld + sld)].view(n, sld)
+            at = self._at + n * ld
+            self._scales = self._buffer[at:at + n * sld].view(n, sld)
         return self._scales
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
@@ -638,15 +639,23 @@ def _mx(t: Optional[MXFP4Tensor], rows: int, cols: int, what: str, device=None):
     return t._c
 
 
+def new_mxfp4s(shapes, device="cuda", buffer: Optional[torch.Tensor] = None):
+    """(flat buffer, [MXFP4Tensor]): uninitialised tensors of the (rows, cols) shapes, with the library's strides, in
+    one allocation -- or the tensors that such a buffer holds."""
+    ld, sld = _lib.f8lin_mxfp4_ld, _lib.f8lin_mxfp4_scale_ld
+    laid, at = [], 0
+    for rows, cols in shapes:
+        a, b = ld(cols), sld(cols)
+        laid.append((at, rows, cols, a, b))
+        at += rows * (a + b)
+    if buffer is None:
+        buffer = torch.empty(at, dtype=torch.uint8, device=device)
+    return buffer, [MXFP4Tensor._of(buffer, *l) for l in laid]
+
+
 def new_mxfp4(rows: int, cols: int, device="cuda") -> MXFP4Tensor:
     """An uninitialised MXFP4 tensor with the library's strides."""
-    ld, sld = _lib.f8lin_mxfp4_ld(cols), _lib.f8lin_mxfp4_scale_ld(cols)
-    return MXFP4Tensor._of(torch.empty(rows * (ld + sld), dtype=torch.uint8, device=device), rows, cols, ld, sld)
-
-
-def mxfp4_of(buffer: torch.Tensor, rows: int, cols: int) -> MXFP4Tensor:
-    """The (rows, cols) tensor that new_mxfp4 laid out in `buffer` (its .buffer)."""
-    return MXFP4Tensor._of(buffer, rows, cols, _lib.f8lin_mxfp4_ld(cols), _lib.f8lin_mxfp4_scale_ld(cols))
+    return new_mxfp4s(((rows, cols),), device)[1][0]
 
 
 def mxfp4_quantize(x: torch.Tensor, q: Optional[MXFP4Tensor], qt: Optional[MXFP4Tensor] = None, rule="floor",

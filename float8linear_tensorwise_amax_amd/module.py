@@ -348,20 +348,29 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
+def _present(*pairs):
+    """The shapes of the pairs (asked for, shape) that are asked for."""
+    return [shape for ask, shape in pairs if ask]
+
+
 class _MXFP4LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, rule):
         M, K = x.shape
         N = weight.shape[0]
         dev = x.device
-        w = weight.contiguous()
+        need_x, need_w = ctx.needs_input_grad[:2]
         y = torch.empty((M, N), dtype=x.dtype, device=dev)
-        x4, w4 = f8lin.new_mxfp4(M, K, dev), f8lin.new_mxfp4(N, K, dev)
-        # the transposed copies only for the gradients that will be asked for
-        x4t = f8lin.new_mxfp4(K, M, dev) if ctx.needs_input_grad[1] else None
-        w4t = f8lin.new_mxfp4(K, N, dev) if ctx.needs_input_grad[0] else None
-        f8lin.mxfp4_forward(x, w, y, x4, w4, x4t, w4t, None if bias is None else bias.contiguous(), rule)
-        ctx.save_for_backward(*(q.buffer for q in (x4t, w4t) if q is not None))
+        _, (x4, w4) = f8lin.new_mxfp4s(((M, K), (N, K)), dev)
+        x4t = w4t = saved = None
+        if need_x or need_w:  # the transposed copies, for the gradients that will be asked for
+            saved, copies = f8lin.new_mxfp4s(_present((need_w, (K, M)), (need_x, (K, N))), dev)
+            x4t = copies[0] if need_w else None
+            w4t = copies[-1] if need_x else None
+        f8lin.mxfp4_forward(x, weight if weight.is_contiguous() else weight.contiguous(), y, x4, w4, x4t, w4t,
+                            bias if bias is None or bias.is_contiguous() else bias.contiguous(), rule)
+        if saved is not None:
+            ctx.save_for_backward(saved)
         ctx.args = (M, N, K, rule, x.dtype, weight.dtype, None if bias is None else bias.dtype)
         return y
 
@@ -371,19 +380,23 @@ class _MXFP4LinearFn(torch.autograd.Function):
         M, N, K, rule, x_dtype, w_dtype, b_dtype = ctx.args
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         dev = dy.device
-        saved = list(ctx.saved_tensors)
-        x4t = f8lin.mxfp4_of(saved.pop(0), K, M) if need_w else None
-        w4t = f8lin.mxfp4_of(saved.pop(0), K, N) if need_x else None
         dy = _rows(dy)
-        dx = torch.empty((M, K), dtype=x_dtype, device=dev) if need_x else None
-        dw = torch.empty((N, K), dtype=w_dtype, device=dev) if need_w else None
-        db = db_ws = None
+        x4t = w4t = dx = dw = db = db_ws = None
+        if need_x or need_w:
+            copies = f8lin.new_mxfp4s(_present((need_w, (K, M)), (need_x, (K, N))), dev, ctx.saved_tensors[0])[1]
+            x4t = copies[0] if need_w else None
+            w4t = copies[-1] if need_x else None
+        if need_x:
+            dx = torch.empty((M, K), dtype=x_dtype, device=dev)
+        if need_w:
+            dw = torch.empty((N, K), dtype=w_dtype, device=dev)
         if need_b:
             db = torch.empty((N,), dtype=b_dtype, device=dev)
             db_ws = torch.empty(max(1, f8lin.mxfp4_dbias_workspace_bytes(M, N) // 4), dtype=torch.float32, device=dev)
-        dy4 = f8lin.new_mxfp4(M, N, dev) if need_x else None
-        dy4t = f8lin.new_mxfp4(N, M, dev) if need_w or need_b else None
-        f8lin.mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, db, db_ws, rule)
+        cols = need_w or need_b
+        _, copies = f8lin.new_mxfp4s(_present((need_x, (M, N)), (cols, (N, M))), dev)
+        f8lin.mxfp4_backward(dy, x4t, w4t, dx, dw, copies[0] if need_x else None, copies[-1] if cols else None, db, db_ws,
+                             rule)
         return dx, dw, db, None
 
 
@@ -411,7 +424,7 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
     y = torch.empty((M, N), dtype=x.dtype, device=x.device)
     fused = f8lin.mxfp4_forward_fused(M, N, K)  # X is quantised inside the product: no buffers
     f8lin.mxfp4_forward(x2, None, y, None if fused else f8lin.new_mxfp4(M, K, x.device), weight,
-                        bias=None if bias is None else bias.contiguous(), rule=rule)
+                        bias=bias if bias is None or bias.is_contiguous() else bias.contiguous(), rule=rule)
     return y if x.dim() == 2 else y.reshape(*lead, N)
 
 
