@@ -352,7 +352,10 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
     if (++st == NS) break;
     advance();
   }
-  __builtin_amdgcn_s_waitcnt(waitcnt((NS - 1) * NCP, 15));
+  // (with two stages all of them: no stores follow these copies, and the first
+  // block's wait, which allows for a tile's stores, would let the second
+  // block's copies pass)
+  __builtin_amdgcn_s_waitcnt(waitcnt(NS > 2 ? (NS - 1) * NCP : 0, 15));
   __builtin_amdgcn_s_barrier();
   Item cur = decode(it);
   it += wx;
