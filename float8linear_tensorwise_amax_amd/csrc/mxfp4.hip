@@ -250,13 +250,36 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(f8lin_mxfp4 q, 
   }
 }
 
-// Bias gradient from the 128-row column sums, in order of the tiles.
-__global__ __launch_bounds__(kThreads) void mx_dbias_kernel(const float *__restrict__ colsum, int64_t tiles, int64_t n,
-                                                            void *db, int dt) {
-  const int64_t col = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (col >= n) return;
+// Bias gradient from the 128-row column sums.  A workgroup owns 32 columns (a
+// 128-byte line of a tile's sums); 32 groups of threads take every 32nd tile,
+// eight loads in flight each, and meet in LDS in the groups' order.  (65536 x
+// 4096: 4.1 us, with a thread a column 164 us: the loads of 512 tiles one after
+// the other on 16 CUs.)
+constexpr int kDbCols = 32, kDbGroups = 32;
+__global__ __launch_bounds__(kDbCols * kDbGroups) void mx_dbias_kernel(const float *__restrict__ colsum, int64_t tiles,
+                                                                       int64_t n, void *db, int dt) {
+  constexpr int kAhead = 8;
+  __shared__ float part[kDbGroups][kDbCols];
+  const int c = (int)threadIdx.x % kDbCols, grp = (int)threadIdx.x / kDbCols;
+  const int64_t col = (int64_t)blockIdx.x * kDbCols + c;
   float s = 0.0f;
-  for (int64_t i = 0; i < tiles; ++i) s += colsum[i * n + col];
+  if (col < n) {
+    for (int64_t i0 = grp; i0 < tiles; i0 += kAhead * kDbGroups) {
+      float v[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int64_t i = i0 + a * kDbGroups;
+        v[a] = i < tiles ? colsum[i * n + col] : 0.0f;
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) s += v[a];
+    }
+  }
+  part[grp][c] = s;
+  __syncthreads();
+  if (grp != 0 || col >= n) return;
+#pragma unroll
+  for (int g = 1; g < kDbGroups; ++g) s += part[g][c];
   const uint32_t o = f32_to_elem(s, dt);
   if (dt == F8LIN_FP32)
     reinterpret_cast<uint32_t *>(db)[col] = o;
@@ -360,7 +383,8 @@ hipError_t launch_mx_dequantize(const f8lin_mxfp4 &q, int64_t rows, int64_t cols
 
 hipError_t launch_mx_dbias(const float *colsum, int64_t tiles, int64_t n, void *db, int dtype, hipStream_t stream) {
   if (n == 0) return hipSuccess;
-  mx_dbias_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(colsum, tiles, n, db, dtype);
+  mx_dbias_kernel<<<(unsigned)((n + kDbCols - 1) / kDbCols), kDbCols * kDbGroups, 0, stream>>>(colsum, tiles, n, db,
+                                                                                              dtype);
   return hipGetLastError();
 }
 
