@@ -148,7 +148,7 @@ int f8lin_mxfp4_forward(const f8lin_mxfp4_fwd_args *p, void *stream) {
   F8_TRY(check_dense(a.y, a.y_dtype, M, N, N, es_of(a.y_dtype)));
   if (a.bias) F8_TRY(check_dense(a.bias, a.bias_dtype, 1, N, N, es_of(a.bias_dtype)));
   const bool xt = a.x4t.codes != nullptr, quant_w = a.w != nullptr, wt = quant_w && a.w4t.codes != nullptr;
-  const bool fused = !xt && !quant_w && mx_linear_fused(M, N, K);
+  const bool fused = !a.x4.codes && !xt && !quant_w && mx_linear_fused(M, N, K);
   if (!fused) F8_TRY(check_mx(a.x4, M, K));
   if (xt) F8_TRY(check_mx(a.x4t, K, M));
   F8_TRY(check_mx(a.w4, N, K));

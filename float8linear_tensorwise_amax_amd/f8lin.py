@@ -541,6 +541,11 @@ def _refuse(t: torch.Tensor, what: str, device: Optional[torch.device]):
         raise TypeError(f"f8lin: {what} must be bfloat16, float16 or float32, got {t.dtype}")
 
 
+def _same_device(t: Optional[torch.Tensor], what: str, device: torch.device):
+    if t is not None and t.device != device:
+        raise ValueError(f"f8lin: {what} is on {t.device}, expected {device}")
+
+
 def _dense(t: torch.Tensor, what: str, device: Optional[torch.device] = None) -> int:
     """Pointer of a contiguous bf16 / fp16 / fp32 GPU tensor (on `device`, if given)."""
     if not t.is_cuda or t.dtype not in _DTYPE or (device is not None and t.device != device):
@@ -700,14 +705,14 @@ def mxfp4_gemm(items, stream=None):
 
 
 def mxfp4_forward_fused(M: int, N: int, K: int) -> bool:
-    """Whether mxfp4_forward with a quantised weight and no x4t quantises X inside the product (x4 may be None)."""
+    """Whether mxfp4_forward with a quantised weight can quantise X inside the product (x4 and x4t may be None)."""
     return bool(_lib.f8lin_mxfp4_forward_fused(M, N, K))
 
 
 def mxfp4_forward(x, w, y, x4: Optional[MXFP4Tensor], w4: MXFP4Tensor, x4t=None, w4t=None, bias=None, rule="floor",
                   stream=None):
     """y (M, N) = x4 . w4^T (+ bias).  w (N, K): quantised into w4 (and w4t); None: w4 already holds the weight.
-    x4 (and x4t, if the backward is to follow) receive X's codes."""
+    x4 (and x4t, if the backward is to follow) receive X's codes; x4 may be None where mxfp4_forward_fused says so."""
     M, K = x.shape
     N = w4.rows
     dev = x.device
@@ -738,6 +743,7 @@ def mxfp4_backward(dy, x4t, w4t, dx, dw, dy4, dy4t, dbias=None, dbias_ws=None, r
             (dbias is not None and tuple(dbias.shape) != (N,)):
         raise ValueError("mxfp4_backward: shape mismatch")
     p, ld = _dense_ld(dy, "dy")
+    _same_device(dbias_ws, "dbias_ws", dev)
     opt = lambda t, what: 0 if t is None else _dense(t, what, dev)  # noqa: E731
     dt = lambda t: 0 if t is None else _DTYPE[t.dtype]  # noqa: E731
     a = _MX_BWD.pack(M, N, K, p, ld, opt(dx, "dx"), opt(dw, "dw"), opt(dbias, "dbias"), _DTYPE[dy.dtype], dt(dx), dt(dw),
@@ -803,6 +809,7 @@ def grad_norm(grads: Sequence[torch.Tensor], out: torch.Tensor, ws: torch.Tensor
     """out[0] (float32) = the norm of all gradients' elements as one vector; norm_type 2, 1 or inf."""
     code = _norm_type(norm_type)
     tab = _grad_table(grads, None, out.device)
+    _same_device(ws, "ws", out.device)
     _call(_lib.f8lin_grad_norm, out.device, stream, tab.buffer_info()[0], len(grads), code,
           _ptr(out, torch.float32), _ptr(ws), _nbytes(ws))
 
@@ -814,5 +821,6 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor
     min(1, max_norm / (norm + 1e-6)), in place or into outs (laid out alike; any of the three types)."""
     code = _norm_type(norm_type)
     tab = _grad_table(grads, outs, norm.device)
+    _same_device(ws, "ws", norm.device)
     _call(_lib.f8lin_grad_clip, norm.device, stream, tab.buffer_info()[0], len(grads), code, float(max_norm),
           _ptr(norm, torch.float32), 1 if norm_given else 0, _ptr(ws), _nbytes(ws))

@@ -442,8 +442,8 @@ int f8lin_mxfp4_gemm(const f8lin_mxfp4_gemm_desc *d, int count, void *stream);
  * where their codes are not NULL, x4t / w4t for the backward.
  * w == NULL (serving, or a weight quantised before): w4 already holds W and
  * w4t is not touched.  Where f8lin_mxfp4_forward_fused(M, N, K) is nonzero
- * (few rows) and no x4t is asked for, X is then quantised inside the product's
- * kernel and x4 is not used: its pointers may be NULL.
+ * (few rows), x4.codes may then be NULL, with x4t.codes NULL too: X is
+ * quantised inside the product's kernel, to the same codes.
  * Errors as above; nothing is launched on error. */
 typedef struct {
   int64_t M, N, K;

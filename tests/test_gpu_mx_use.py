@@ -269,3 +269,39 @@ def test_wide_and_tall(f8lin, mx):
     c = torch.empty((3, 5), device="cuda")
     f8lin.mxfp4_gemm([(qx, qw, c)])
     check_product(c, mx.rounded(np64(x)), mx.rounded(np64(w)), torch.float32)
+
+
+@pytest.mark.parametrize("m, n", [(1, 1), (129, 33), (4096, 31), (4097, 32), (33000, 65), (140001, 3)])
+def test_bias_gradient_of_many_rows(f8lin, m, n):
+    """The column sums alone, over fewer and more row tiles than the groups that add them up; the same bits twice."""
+    dy = draw((m, n), torch.float32, m + n).cuda()
+    ws = torch.empty(f8lin.mxfp4_dbias_workspace_bytes(m, n) // 4, device="cuda")
+    got = []
+    for _ in range(2):
+        db = torch.full((n,), float("nan"), device="cuda")
+        f8lin.mxfp4_backward(dy, None, None, None, None, None, f8lin.new_mxfp4(n, m), db, ws.fill_(float("nan")))
+        got.append(np64(db))
+    ref = np64(dy).sum(0)
+    # an element passes 32 + 2 additions in its tile, tiles / 32 in its group and 31 joining them, each off by half a
+    # step of at most the sum of magnitudes
+    depth = 34 + -(-m // 128) // 32 + 1 + 31
+    assert np.all(np.abs(got[0] - ref) <= depth * 2.0 ** -24 * 1.01 * np.abs(np64(dy)).sum(0))
+    assert np.array_equal(got[0], got[1])
+
+
+@pytest.mark.parametrize("m", [1, 2, 3])
+def test_codes_of_x_are_left_where_asked_for(f8lin, mx, m):
+    """A forward that is given x4 writes X's codes there, however few the rows; without it the result is the same."""
+    n, k = 96, 333
+    x, w = draw((m, k), torch.bfloat16, m).cuda(), draw((n, k), torch.bfloat16, 7).cuda()
+    w4, x4 = f8lin.new_mxfp4(n, k), f8lin.new_mxfp4(m, k)
+    f8lin.mxfp4_quantize(w, w4)
+    x4.codes.fill_(0xA5), x4.scales.fill_(0xA5)
+    y = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    f8lin.mxfp4_forward(x, None, y, x4, w4)
+    assert np.array_equal(np64(x4.dequantize(torch.float32)), mx.rounded(np64(x)))
+    check_product(y, mx.rounded(np64(x)), mx.rounded(np64(w)), torch.bfloat16)
+    if f8lin.mxfp4_forward_fused(m, n, k):
+        y2 = torch.empty_like(y)
+        f8lin.mxfp4_forward(x, None, y2, None, w4)
+        check_product(y2, mx.rounded(np64(x)), mx.rounded(np64(w)), torch.bfloat16)
