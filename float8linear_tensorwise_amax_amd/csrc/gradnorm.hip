@@ -27,6 +27,9 @@ constexpr int kThreads = 256;
 constexpr int kPiece = 16384;
 constexpr int kNormGrid = kGradPartials;
 constexpr int kScaleGrid = 2048;
+// 16-byte loads a thread has in flight, in both passes (the norm of 872M bf16
+// elements: 290 us or 6.0 TB/s; with one load 349 us)
+constexpr int kAhead = 4;
 
 struct GradTable {
   const void *g[kGradBatch];
@@ -78,15 +81,24 @@ __device__ __forceinline__ double piece_norm(const void *g, int64_t begin, int64
   const int len = (int)min((int64_t)kPiece, n - begin);
   double s = 0.0;
   bool nan = false;
-  for (int i = 8 * (int)threadIdx.x; i < len; i += 8 * kThreads) {
-    float v[8];
-    load8<DT>(x + i, len - i, v);
+  auto add = [&](const Raw8<DT> &r) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (P == F8LIN_NORM_INF) nan = nan || v[k] != v[k];
-      fold<P>(s, v[k]);
+      const float v = raw_value<DT>(r, k);
+      if (P == F8LIN_NORM_INF) nan = nan || v != v;
+      fold<P>(s, v);
     }
+  };
+  constexpr int kStep = 8 * kThreads;
+  int at = 0;
+  for (; at + kAhead * kStep <= len; at += kAhead * kStep) {  // kAhead loads in flight
+    Raw8<DT> r[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) r[a] = load_raw8<DT>(x + at + a * kStep + 8 * (int)threadIdx.x, 8);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) add(r[a]);
   }
+  for (int i = at + 8 * (int)threadIdx.x; i < len; i += kStep) add(load_raw8<DT>(x + i, len - i));
   return nan ? __builtin_nan("") : s;
 }
 
@@ -129,7 +141,7 @@ template <int DI, int DO>
 __device__ __forceinline__ void piece_scale(const void *g, void *out, int64_t begin, int64_t n, float c) {
   typedef typename MxElem<DI>::type ielem;
   typedef typename MxElem<DO>::type oelem;
-  constexpr int E = DO == F8LIN_FP32 ? 4 : 8, kAhead = 4;
+  constexpr int E = DO == F8LIN_FP32 ? 4 : 8;
   constexpr int kInWords = E * (int)sizeof(ielem) / 4, kOutWords = 4;
   const ielem *x = reinterpret_cast<const ielem *>(g) + begin;
   oelem *y = reinterpret_cast<oelem *>(out) + begin;

@@ -189,15 +189,11 @@ __device__ __forceinline__ uint32_t raw_codes(const Raw8<DT> &r, float scale) {
   }
 }
 
-// Eight values of type DT at p as binary32; `n` of them exist (the rest +0).
+// Element i of eight, as binary32.
 template <int DT>
-__device__ __forceinline__ void load8(const typename MxElem<DT>::type *p, int n, float (&v)[8]) {
-  const Raw8<DT> r = load_raw8<DT>(p, n);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (DT == F8LIN_FP32) v[i] = __uint_as_float(r.w[i >> 2][i & 3]);
-    else v[i] = elem_f32<DT>((r.w[0][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-  }
+__device__ __forceinline__ float raw_value(const Raw8<DT> &r, int i) {
+  if constexpr (DT == F8LIN_FP32) return __uint_as_float(r.w[i >> 2][i & 3]);
+  else return elem_f32<DT>((r.w[0][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
 }
 
 }  // namespace f8lin
