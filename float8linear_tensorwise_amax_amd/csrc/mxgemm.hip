@@ -467,7 +467,8 @@ __global__ __launch_bounds__(256, MINB) void mx_gemm_tiled_kernel(const MxBatch)
 // owns NT x 16 rows of B (output columns), so that many workgroups stream B; the
 // waves split K in 128-byte blocks (wave w takes blocks w, w + NW, ...), load
 // operands straight into registers, U blocks in flight, and their partial
-// sums meet in LDS.  FUSED (X not yet quantised, M <= 16): every workgroup
+// sums meet in LDS (1 x 14336 x 4096: 9.7 us or 3.2 TB/s; a read of 32 MB alone
+// takes 10 us here).  FUSED (X not yet quantised, M <= 16): every workgroup
 // quantises X into LDS itself while its first loads of B are under way.
 struct MxSkinny {
   const uint8_t *a, *as, *b, *bs;
@@ -478,15 +479,18 @@ struct MxSkinny {
   int M, N, K, nb, nkb;
   int c_dtype, bias_dtype;
 };
-constexpr int kSkinnyMaxM = 64;
-// Rows that every workgroup quantises itself (see launch_mx_linear).
-constexpr int kFusedMaxM = 2;
 
 
 // LDS strides of the quantised X: rows 16 bytes apart from a multiple of 128
 // (bank conflicts), scales after all codes.
 __host__ __device__ constexpr int fused_row(int nkb) { return nkb * kBlockBytes + 16; }
 __host__ __device__ constexpr int fused_scale_row(int nkb) { return nkb * kBlocksPerK; }
+// log2 of the threads that quantise a row together: 32 items a K block
+__host__ __device__ constexpr int fused_row_log(int nkb, int waves) {
+  int l = 5;
+  while ((32 << (l - 5)) < 32 * nkb && (32 << (l - 5)) < 64 * waves) ++l;
+  return l;
+}
 __host__ __device__ constexpr int fused_bytes(int M, int nkb) { return M * (fused_row(nkb) + fused_scale_row(nkb)); }
 
 template <int MT, int NT, int NW, bool FUSED, int XDT, int RULE>
@@ -551,9 +555,11 @@ __global__ __launch_bounds__(64 * NW) void mx_skinny_kernel(const MxSkinny P) {
   uint8_t *const xs = dyn + P.M * xrow;
   if constexpr (FUSED) {
     typedef typename MxElem<XDT>::type elem;
-    for (int m = 0; m < P.M; ++m) {
+    // eight values each, a block per quad; several rows at once where they are short
+    const int row_log = fused_row_log(P.nkb, NW), row_threads = 1 << row_log;
+    for (int m = (int)threadIdx.x >> row_log; m < P.M; m += (64 * NW) >> row_log) {
       const elem *x = reinterpret_cast<const elem *>(P.x) + m * P.ldx;
-      for (int i = threadIdx.x; i < P.nkb * kBlocksPerK * 4; i += 64 * NW) {  // eight values each, a block per quad
+      for (int i = (int)threadIdx.x & (row_threads - 1); i < P.nkb * kBlocksPerK * 4; i += row_threads) {
         const Raw8<XDT> v = load_raw8<XDT>(x + 8 * i, P.K - 8 * i);
         const int e = mx_scale_byte<RULE>(mag_f32_bits<XDT>(quad_max(raw_mag<XDT>(v))));
         *reinterpret_cast<uint32_t *>(dyn + m * xrow + 4 * i) = e == kMxNan ? 0u : raw_codes<XDT>(v, mx_scale_f32(e));
@@ -651,16 +657,43 @@ void launch_tiled(const MxBatch &b, int dt, int64_t tiles, hipStream_t stream) {
     mx_gemm_tiled_kernel<BM, BN, NS, MINB, F8LIN_FP16><<<grid, 256, 0, stream>>>(b);
 }
 
+// Waves per workgroup: eight where few workgroups have a contraction of more
+// than two rounds of loads (1 x 4096 x 14336: 10.9 us, with four 12.9 us; 51 x
+// 4800 x 1600: 8.9 us, with four 6.3 us; 48 x 8192 x 4096: 14.2 us, with four
+// 15.8 us).
+int skinny_waves(int64_t grid, int64_t nkb, int MT) { return grid <= 2 * kCUs && nkb >= (MT <= 2 ? 32 : 16) ? 8 : 4; }
+
+// Blocks of 16 columns per workgroup: several share what is read of A, but the
+// time is that of the CU with the most blocks (16 rows of X, quantised first:
+// 9216 x 4096 with three 12.0 us, with two 14.6 us; 14336 x 4096 with four 13.8
+// us, three 17.9 us, two 14.9 us, one 17.4 us; 20000 x 4096 with three 18.6
+// us, four 21.4 us).
+int skinny_blocks(int N, int MT, int most) {
+  int best = 1;
+  int64_t least = 0;
+  for (int nt = 1; nt <= most; ++nt) {
+    const int64_t rounds = ((N + 16 * nt - 1) / (16 * nt) + kCUs - 1) / kCUs, cost = rounds * (2 * nt + MT);
+    if (nt == 1 || cost < least) best = nt, least = cost;
+  }
+  return best;
+}
+
 template <int MT, int NT, bool FUSED, int XDT, int RULE>
 void launch_skinny_nw(const MxSkinny &k, hipStream_t stream) {
   const unsigned grid = (unsigned)((k.N + 16 * NT - 1) / (16 * NT));
   const size_t x = FUSED ? fused_bytes(k.M, k.nkb) : 0;
-  // eight waves where few workgroups have a long contraction (1 x 4096 x
-  // 14336: 10.9 us, with four 12.9 us; 51 x 4800 x 1600: 8.9 us, with four 6.3 us)
-  if (grid <= 2 * kCUs && k.nkb >= 32)
+  if (skinny_waves(grid, k.nkb, MT) == 8)
     mx_skinny_kernel<MT, NT, 8, FUSED, XDT, RULE><<<grid, 512, std::max<size_t>(x, 8 * MT * NT * 1024), stream>>>(k);
   else
     mx_skinny_kernel<MT, NT, 4, FUSED, XDT, RULE><<<grid, 256, std::max<size_t>(x, 4 * MT * NT * 1024), stream>>>(k);
+}
+
+// Few enough rows for the skinny kernel: up to 64, or fewer where 64 x 64 tiles
+// would fill the chip as well (in us, with X's quantisation: 64 x 8192 x 4096
+// 15.3, tiled 16.4; 64 x 9216 x 4096 18.4, 16.4; 32 x 11000 x 11000 27.3, 27.6;
+// 32 x 14336 x 4096 18.2, 16.3).
+bool skinny(const MxProblem &p) {
+  return p.M <= 16 || (p.M <= 32 && p.N <= 48 * kCUs) || (p.M <= 64 && p.N <= 32 * kCUs);
 }
 
 void launch_skinny(const MxProblem &p, hipStream_t stream) {
@@ -670,15 +703,20 @@ void launch_skinny(const MxProblem &p, hipStream_t stream) {
   k.M = p.M, k.N = p.N, k.nb = p.nb, k.nkb = p.nkb;
   k.c_dtype = p.c_dtype, k.bias_dtype = p.bias_dtype;
   const int mt = (p.M + 15) / 16;
-  // two column blocks per workgroup halve what is read of A, where enough
-  // workgroups are left (33 x 14336 x 4096: 17.9 us, with one 23.0 us; 64 x
-  // 4096 x 4096: 12.9 us, with one 10.2 us)
-  const bool wide = p.N >= 32 * kCUs;
-  if (mt == 1) launch_skinny_nw<1, 1, false, 0, 0>(k, stream);
-  else if (mt == 2 && wide) launch_skinny_nw<2, 2, false, 0, 0>(k, stream);
-  else if (mt == 2) launch_skinny_nw<2, 1, false, 0, 0>(k, stream);
-  else if (wide) launch_skinny_nw<4, 2, false, 0, 0>(k, stream);
-  else launch_skinny_nw<4, 1, false, 0, 0>(k, stream);
+  const int nt = skinny_blocks(p.N, mt, mt == 1 ? 4 : (mt == 2 ? 3 : 2));
+  if (mt == 1) {
+    if (nt == 1) launch_skinny_nw<1, 1, false, 0, 0>(k, stream);
+    else if (nt == 2) launch_skinny_nw<1, 2, false, 0, 0>(k, stream);
+    else if (nt == 3) launch_skinny_nw<1, 3, false, 0, 0>(k, stream);
+    else launch_skinny_nw<1, 4, false, 0, 0>(k, stream);
+  } else if (mt == 2) {
+    if (nt == 1) launch_skinny_nw<2, 1, false, 0, 0>(k, stream);
+    else if (nt == 2) launch_skinny_nw<2, 2, false, 0, 0>(k, stream);
+    else launch_skinny_nw<2, 3, false, 0, 0>(k, stream);
+  } else {
+    if (nt == 1) launch_skinny_nw<4, 1, false, 0, 0>(k, stream);
+    else launch_skinny_nw<4, 2, false, 0, 0>(k, stream);
+  }
 }
 
 // The tile a problem takes: 0: 256 x 256, one workgroup per CU; 1: 128 x 128,
@@ -723,11 +761,22 @@ void launch_batch(MxBatch &b, int tile, int dt, hipStream_t stream) {
 
 }  // namespace
 
-// Few enough rows, and few enough bytes for every workgroup to quantise them
-// itself (at most 35 KB of LDS).
+// Whether X is quantised by every workgroup of the product itself.  That saves
+// a launch and costs every workgroup the whole of X's arithmetic: the passes
+// that its threads make over a row's items, and one more, for all rows (more
+// where a SIMD runs more than four of its waves).  In us, fused and with a
+// launch of its own (and the count that the rule takes):
+//   1 x 4096 x 4096   5.6, 7.7 (3)     4 x 4096 x 4096   7.5, 8.0 (12)
+//   6 x 4800 x 1600   7.2, 7.5 (12)    8 x 4800 x 1600   8.2, 7.6 (16)
+//   2 x 4096 x 14336 12.0, 13.7 (10)   4 x 4096 x 14336 15.2, 13.8 (20)
+//   2 x 28672 x 4096 18.6, 20.4 (11)   4 x 28672 x 4096 22.1, 20.2 (21)
 bool mx_linear_fused(int64_t M, int64_t N, int64_t K) {
-  const int64_t nkb = (K + 8 * kBlocksPerK * 4 - 1) / (8 * kBlocksPerK * 4);
-  return M > 0 && N > 0 && K > 0 && M <= kFusedMaxM && M * nkb <= 256;
+  if (M <= 0 || N <= 0 || K <= 0 || M > 16) return false;
+  const int64_t nkb = (K + 8 * kBlocksPerK * 4 - 1) / (8 * kBlocksPerK * 4), grid = (N + 15) / 16;
+  const int waves = skinny_waves(grid, nkb, 1);
+  const int64_t at_once = (64 * waves) >> fused_row_log((int)nkb, waves);
+  const int64_t passes = (M + at_once - 1) / at_once * ((32 * nkb + 64 * waves - 1) / (64 * waves) + 1);
+  return passes * std::max<int64_t>(4 * kCUs, grid) <= 12 * 4 * kCUs;
 }
 
 hipError_t launch_mx_linear(const MxLinear &l, hipStream_t stream) {
@@ -782,7 +831,7 @@ hipError_t launch_mx_gemms(const MxGemm *d, int count, hipStream_t stream) {
     p.nkb = (p.nb + kBlocksPerK - 1) / kBlocksPerK;
     p.c_dtype = d[i].c_dtype;
     p.bias_dtype = d[i].bias_dtype;
-    if (p.M <= kSkinnyMaxM) {
+    if (skinny(p)) {
       launch_skinny(p, stream);
     } else {
       tile[b.count] = tile_for(p);

@@ -305,3 +305,25 @@ def test_codes_of_x_are_left_where_asked_for(f8lin, mx, m):
         y2 = torch.empty_like(y)
         f8lin.mxfp4_forward(x, None, y2, None, w4)
         check_product(y2, mx.rounded(np64(x)), mx.rounded(np64(w)), torch.bfloat16)
+
+
+@pytest.mark.parametrize("m, n, k", [
+    (16, 40, 200), (13, 33, 511), (12, 70, 1024), (6, 50, 1600), (4, 50, 4096), (2, 35, 14336), (3, 17, 9),  # X quantised inside
+    (16, 4100, 96), (9, 8200, 96), (16, 12300, 100), (5, 20001, 64),                      # one to four blocks of columns
+    (17, 4100, 96), (17, 8200, 300), (32, 12288, 40), (17, 12289, 36),
+    (33, 4100, 70), (64, 8192, 36), (33, 8193, 36), (49, 600, 4100), (20, 600, 8200)])
+def test_few_rows_against_quantised_weights(mod, f8lin, mx, m, n, k):
+    """Each path that a few rows can take: X quantised inside the product or ahead of it, its splits, the tiled one."""
+    x, w = draw((m, k), torch.bfloat16, m + k).cuda(), draw((n, k), torch.bfloat16, n).cuda()
+    bias = draw((n,), torch.bfloat16, 3).cuda()
+    w4 = f8lin.new_mxfp4(n, k)
+    f8lin.mxfp4_quantize(w, w4)
+    y = mod.mxfp4_linear(x, w4, bias)
+    check_product(y, mx.rounded(np64(x)), mx.rounded(np64(w)), torch.bfloat16, np64(bias))
+
+
+def test_where_x_is_quantised_inside(f8lin):
+    """One row for every weight whose row a workgroup can take on itself; no batch beyond 16 rows, nothing empty."""
+    assert all(f8lin.mxfp4_forward_fused(1, n, k) for n in (1, 4096, 28672) for k in (1, 4096))
+    assert f8lin.mxfp4_forward_fused(16, 64, 256) and not f8lin.mxfp4_forward_fused(17, 64, 256)
+    assert not any(f8lin.mxfp4_forward_fused(*s) for s in ((0, 4, 4), (4, 0, 4), (4, 4, 0), (16, 4096, 4096)))
