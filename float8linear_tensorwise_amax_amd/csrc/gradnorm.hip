@@ -6,7 +6,8 @@
 // elements become NaN and the others 0).
 //
 // HBM-bound: the norm reads every element once, the scaling reads it again
-// and writes it.  Sums are taken in binary64: the square of a 16-bit float is
+// and writes it (872M bf16 elements into fp32: 289 us, 6.0 TB/s, and 982 us,
+// 5.3 TB/s).  Sums are taken in binary64: the square of a 16-bit float is
 // exact in it, cannot overflow or vanish, and the order of a fixed grid is
 // the same on every run (no atomics).
 // Tables of up to kGradBatch tensors go to the kernel as an argument, so a

@@ -4,6 +4,10 @@
 // needs.  The block arithmetic is in mx_common.h.
 //
 // HBM-bound: es bytes read and 17/32 byte written per element and layout.
+// 65536 x 4096 bf16: rows 126 us (5.4 TB/s), columns 145 us (4.7), both 186 us
+// (4.4: it also writes a fifth more than that, as a tile's 8 bytes of a
+// transposed row's scales reach memory as 32), the way back 121 us (5.6); a
+// plain copy moves 5.0-5.3 TB/s on this card.
 // Rows alone (mx_rows_kernel): a thread takes eight consecutive elements of
 // four rows, all four loads in flight; a block is four lanes, whose maxima
 // meet by two DPP quad permutations.

@@ -31,7 +31,8 @@
  *
  * Conventions for every entry point:
  *  - Every data pointer is a DEVICE pointer owned by the caller, 16-byte
- *    aligned, to a row-major contiguous tensor.  bf16 tensors are passed as
+ *    aligned, to a row-major contiguous tensor (the MXFP4 and gradient entry
+ *    points, below, take less alignment, odd sizes and row strides).  bf16 tensors are passed as
  *    their uint16_t bit patterns; fp8 tensors as uint8_t codes.  A data
  *    pointer may be NULL only if its tensor has no elements.
  *  - `stream` is a hipStream_t (NULL = the null stream).  Every call only
@@ -68,8 +69,8 @@ extern "C" {
 typedef enum {
   F8LIN_OK = 0,
   F8LIN_EINVAL = 1,     /* null pointer, bad enum, overlapping buffers, bad count */
-  F8LIN_ESHAPE = 2,     /* negative dimension, above 2^22, or not a multiple of 16 */
-  F8LIN_EALIGN = 3,     /* a pointer not 16-byte aligned */
+  F8LIN_ESHAPE = 2,     /* negative dimension, above 2^22, or not a multiple of 16; a bad stride (MXFP4) */
+  F8LIN_EALIGN = 3,     /* a pointer not aligned (16 bytes; MXFP4 and gradient data: an element) */
   F8LIN_EWORKSPACE = 4, /* workspace missing or smaller than f8lin_workspace_bytes() */
   F8LIN_EHIP = 5        /* a HIP launch failed */
 } f8lin_status;
