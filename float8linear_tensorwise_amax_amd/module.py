@@ -31,6 +31,10 @@ fp16 or fp32.  freeze_mxfp4 keeps only the 4-bit weights, for serving.
 Gradient clipping.  clip_grad_norm_ (in place), clip_grads (into new tensors)
 and get_grad_norm work on a list of gradients after backward.
 
+Both can be captured into a HIP graph, a whole step under autograd too.  As
+with any layer, let no eager graph of the same parameters live on into the
+capture of a backward: its gradient nodes belong to another stream.
+
 Delayed scaling, per role:
   * the scale comes from the largest amax of the previous steps (the
     history), and the cast folds this step's amax into the state;
@@ -550,6 +554,8 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     grads = _gradients(parameters)
     if not grads:
         return torch.zeros((), dtype=torch.float32)
+    if any(st == 0 and n > 1 for g in grads for st, n in zip(g.stride(), g.shape)):
+        raise ValueError("clip_grad_norm_: an expanded gradient cannot be scaled in place")
     flat = [_dense_copy(g) for g in grads]
     dev = flat[0].device
     norm = torch.empty((), dtype=torch.float32, device=dev)

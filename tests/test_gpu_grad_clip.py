@@ -211,3 +211,15 @@ def test_refusals(f8lin, mod):
         f8lin.grad_clip([g], 1.0, norm, ws, outs=[g, g])
     with pytest.raises(ValueError):
         mod.clip_grads([torch.zeros(4), g], 1.0)
+
+
+def test_expanded_gradient_is_refused_in_place(mod):
+    """Nothing is scaled when one of the gradients shares its elements; out of place it counts each of them."""
+    a = torch.nn.Parameter(torch.zeros(4, device="cuda"))
+    b = torch.nn.Parameter(torch.zeros(3, 5, device="cuda"))
+    a.grad, b.grad = torch.full((4,), 2.0, device="cuda"), torch.full((1, 5), 3.0, device="cuda").expand(3, 5)
+    with pytest.raises(ValueError):
+        mod.clip_grad_norm_([a, b], 1.0)
+    assert torch.equal(a.grad, torch.full((4,), 2.0, device="cuda"))
+    norm, out = mod.clip_grads([a.grad, b.grad], 1.0, norm_type=1.0)
+    assert norm.item() == 4 * 2.0 + 15 * 3.0 and out[1].shape == (3, 5)

@@ -327,3 +327,42 @@ def test_where_x_is_quantised_inside(f8lin):
     assert all(f8lin.mxfp4_forward_fused(1, n, k) for n in (1, 4096, 28672) for k in (1, 4096))
     assert f8lin.mxfp4_forward_fused(16, 64, 256) and not f8lin.mxfp4_forward_fused(17, 64, 256)
     assert not any(f8lin.mxfp4_forward_fused(*s) for s in ((0, 4, 4), (4, 0, 4), (4, 4, 0), (16, 4096, 4096)))
+
+
+def test_layer_step_captured(mod, f8lin):
+    """A whole step of layers under autograd -- forward, backward, clipping -- as one graph, replayed on new inputs with
+    eager steps between; the eager graphs of the same leaves are gone before the capture."""
+    model = build(mod, dtype=torch.bfloat16)
+    params = list(model.parameters())
+    x, target = (torch.empty((3, 11, n), dtype=torch.bfloat16, device="cuda") for n in (70, 5))
+
+    def step():
+        y = model(x)
+        grads = torch.autograd.grad(y, params, (y - target).detach())
+        norm, clipped = mod.clip_grads(grads, 0.5, out_dtype=torch.float32)
+        return [y.detach(), norm, *clipped]
+
+    def load(seed):
+        x.copy_(draw(x.shape, x.dtype, seed))
+        target.copy_(draw(target.shape, target.dtype, 100 + seed))
+
+    load(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # warm-up; nothing of it is kept
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(1, 4):
+        load(seed)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.isfinite(t).all() for t in want)
+        for i, (a, b) in enumerate(zip(out, want)):
+            assert torch.equal(a, b), i
