@@ -106,13 +106,17 @@ struct Raw8 {
 };
 
 // Eight elements of type DT at p (any element address); `n` of them exist
-// (the rest read as +0).
-template <int DT>
+// (the rest read as +0).  ONCE: the launch reads them once, so that they need
+// no place in the L2.
+template <int DT, bool ONCE = false>
 __device__ __forceinline__ Raw8<DT> load_raw8(const typename MxElem<DT>::type *p, int n) {
   Raw8<DT> r;
   if (n >= 8) {
-    r.w[0] = *reinterpret_cast<const u32x4_u *>(p);
-    if constexpr (DT == F8LIN_FP32) r.w[1] = *reinterpret_cast<const u32x4_u *>(p + 4);
+#pragma unroll
+    for (int h = 0; h < (DT == F8LIN_FP32 ? 2 : 1); ++h) {
+      const u32x4_u *q = reinterpret_cast<const u32x4_u *>(p + 4 * h);
+      r.w[h] = ONCE ? __builtin_nontemporal_load(q) : *q;
+    }
   } else {
     uint32_t e[8];
 #pragma unroll

@@ -4,10 +4,9 @@
 // needs.  The block arithmetic is in mx_common.h.
 //
 // HBM-bound: es bytes read and 17/32 byte written per element and layout.
-// 65536 x 4096 bf16: rows 126 us (5.4 TB/s), columns 145 us (4.7), both 186 us
-// (4.4: it also writes a fifth more than that, as a tile's 8 bytes of a
-// transposed row's scales reach memory as 32), the way back 121 us (5.6); a
-// plain copy moves 5.0-5.3 TB/s on this card.
+// 65536 x 4096 bf16: rows 109 us (6.2 TB/s), columns 133 us (5.1), both 157 us
+// (5.2), the way back 121 us (5.6); a plain copy moves 5.0-5.3 TB/s on this
+// card and a read alone 6.3.
 // Rows alone (mx_rows_kernel): a thread takes eight consecutive elements of
 // four rows, all four loads in flight; a block is four lanes, whose maxima
 // meet by two DPP quad permutations.
@@ -56,7 +55,8 @@ __device__ __forceinline__ int scales_of_16(int e, int q) {
   return sw | __builtin_amdgcn_mov_dpp(sw, 0x128, 0xF, 0xF, true);  // row_ror 8
 }
 
-// Rows alone.  A workgroup covers tx = 2^log_tx chunks of eight elements by
+// Rows alone; 16-bit X is read past the L2 (65536 x 4096 bf16 109 us, through
+// it 126 us; 3001 x 2504 fp16 8.4 us, through it 7.4 us).  A workgroup covers tx = 2^log_tx chunks of eight elements by
 // kRowsPer * 256 / tx rows: four rows a thread, or one where that leaves few
 // workgroups.
 template <int DT, int RULE, int kRowsPer>
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const QuantJobs jobs)
 #pragma unroll
   for (int p = 0; p < kRowsPer; ++p) {
     const int64_t row = row0 + (int64_t)p * (kThreads >> jb.log_tx);
-    v[p] = load_raw8<DT>(x + row * jb.ldx + col, row < jb.rows ? have : 0);
+    v[p] = load_raw8<DT, DT != F8LIN_FP32>(x + row * jb.ldx + col, row < jb.rows ? have : 0);
   }
 #pragma unroll
   for (int p = 0; p < kRowsPer; ++p) {
@@ -90,7 +90,10 @@ __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const QuantJobs jobs)
   }
 }
 
-template <int DT, int RULE, bool ROWS, int kRowBlocks>
+// ONCE: X is read, and the transposed codes (which a backward reads much later)
+// are written, past the L2, so that the lines that tiles fill together stay
+// there (65536 x 4096 bf16, both layouts: 157 us, otherwise 185 us).
+template <int DT, int RULE, bool ROWS, int kRowBlocks, bool ONCE>
 __global__ __launch_bounds__(64 * kRowBlocks) void mx_quantize_kernel(const QuantJobs jobs) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kTileRows = 32 * kRowBlocks;  // a wave per 32 rows
@@ -121,7 +124,7 @@ __global__ __launch_bounds__(64 * kRowBlocks) void mx_quantize_kernel(const Quan
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t grow = row0 + (t >> 4) + 4 * kRowBlocks * p;
-    in[p] = load_raw8<DT>(x + grow * jb.ldx + gcol, grow < rows ? have : 0);
+    in[p] = load_raw8<DT, ONCE>(x + grow * jb.ldx + gcol, grow < rows ? have : 0);
   }
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
@@ -191,7 +194,11 @@ __global__ __launch_bounds__(64 * kRowBlocks) void mx_quantize_kernel(const Quan
     sw |= __builtin_amdgcn_mov_dpp(sw, 0xB1, 0xF, 0xF, true);
     sw |= __builtin_amdgcn_mov_dpp(sw, 0x4E, 0xF, 0xF, true);
     if (col < cols) {
-      if (block_ok) *reinterpret_cast<u32x4 *>(jb.qt.codes + col * jb.qt.ld + row0 / 2 + 16 * rb) = out;
+      u32x4 *const dst = reinterpret_cast<u32x4 *>(jb.qt.codes + col * jb.qt.ld + row0 / 2 + 16 * rb);
+      if (block_ok) {
+        if constexpr (ROWS && ONCE) __builtin_nontemporal_store(out, dst);
+        else *dst = out;
+      }
       if ((rb & 3) == 0 && block_ok)
         *reinterpret_cast<int *>(jb.qt.scales + col * jb.qt.scale_ld + row0 / 32 + rb) = sw;
     }
@@ -299,21 +306,22 @@ __global__ __launch_bounds__(kDbCols * kDbGroups) void mx_dbias_kernel(const flo
     reinterpret_cast<uint16_t *>(db)[col] = (uint16_t)o;
 }
 
-template <int DT, int RULE, int RB>
+template <int DT, int RULE, int RB, bool ONCE>
 void launch_cols(const QuantJobs &jobs, unsigned grid, bool rows, hipStream_t stream) {
   if (rows)
-    mx_quantize_kernel<DT, RULE, true, RB><<<grid, 64 * RB, 0, stream>>>(jobs);
+    mx_quantize_kernel<DT, RULE, true, RB, ONCE><<<grid, 64 * RB, 0, stream>>>(jobs);
   else
-    mx_quantize_kernel<DT, RULE, false, RB><<<grid, 64 * RB, 0, stream>>>(jobs);
+    mx_quantize_kernel<DT, RULE, false, RB, ONCE><<<grid, 64 * RB, 0, stream>>>(jobs);
 }
 
 template <int DT, int RULE>
-void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, int row_blocks, hipStream_t stream) {
+void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, int row_blocks, bool once, hipStream_t stream) {
   if constexpr (DT != F8LIN_FP32) {
-    if (row_blocks == 8) return launch_cols<DT, RULE, 8>(jobs, grid, rows, stream);
+    if (row_blocks == 8 && once) return launch_cols<DT, RULE, 8, true>(jobs, grid, rows, stream);
+    if (row_blocks == 8) return launch_cols<DT, RULE, 8, false>(jobs, grid, rows, stream);
   }
   if (row_blocks == 4)
-    launch_cols<DT, RULE, 4>(jobs, grid, rows, stream);
+    launch_cols<DT, RULE, 4, false>(jobs, grid, rows, stream);
   else
     row_blocks == 0 ? mx_rows_kernel<DT, RULE, 4><<<grid, kThreads, 0, stream>>>(jobs)
                     : mx_rows_kernel<DT, RULE, 1><<<grid, kThreads, 0, stream>>>(jobs);
@@ -324,7 +332,7 @@ void launch_quant(const QuantJobs &jobs, unsigned grid, bool rows, int row_block
 hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_t stream) {
   const bool rows = ts[0].q.codes != nullptr, cols = ts[0].qt.codes != nullptr;
   // 256-row tiles fill whole 128-byte lines of the transposed codes (65536 x
-  // 4096 bf16, both layouts: 187 us, with 128-row tiles 214 us); 128-row
+  // 4096 bf16, both layouts: 157 us, with 128-row tiles 214 us); 128-row
   // tiles for 32-bit elements, whose tile would take 128 KB of LDS (270 us,
   // with 256 rows 342 us), and where there are few tiles (256 x 4096 bf16:
   // 5.6 us, with 256 rows 6.3 us).
@@ -335,9 +343,13 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
   const int row_blocks = !cols ? (tiles < kFewTiles ? 1 : 0) : (ts[0].dtype != F8LIN_FP32 && tiles >= kFewTiles) ? 8 : 4;
   QuantJobs jobs = {};
   int64_t total = 0;
+  // X past the L2: where its rows are whole 128-byte lines, that no two tiles
+  // share (65535 x 4095 bf16, both layouts: 218 us so, 214 us otherwise)
+  bool once = true;
   for (int i = 0; i < count; ++i) {
     const MxQuant &t = ts[i];
     if (t.rows == 0 || t.cols == 0) continue;
+    once = once && ((uintptr_t)t.x | (uintptr_t)t.ldx * 2) % 128 == 0;
     int64_t gx, gy;
     int log_tx = 0;
     if (cols) {
@@ -357,9 +369,9 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
   const unsigned grid = (unsigned)total;
 #define F8_MX_Q(DT)                                                             \
   if (rule == F8LIN_MX_CEIL)                                                    \
-    launch_quant<DT, F8LIN_MX_CEIL>(jobs, grid, rows, row_blocks, stream);      \
+    launch_quant<DT, F8LIN_MX_CEIL>(jobs, grid, rows, row_blocks, once, stream);      \
   else                                                                          \
-    launch_quant<DT, F8LIN_MX_FLOOR>(jobs, grid, rows, row_blocks, stream)
+    launch_quant<DT, F8LIN_MX_FLOOR>(jobs, grid, rows, row_blocks, once, stream)
   if (ts[0].dtype == F8LIN_BF16) {
     F8_MX_Q(F8LIN_BF16);
   } else if (ts[0].dtype == F8LIN_FP16) {

@@ -366,3 +366,20 @@ def test_layer_step_captured(mod, f8lin):
         assert all(torch.isfinite(t).all() for t in want)
         for i, (a, b) in enumerate(zip(out, want)):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("rows, cols, pad", [(8192, 1024, 0), (8190, 1030, 0), (8192, 1024, 8), (8300, 960, 64), (65536, 128, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_quantize_many_tiles(f8lin, mx, rows, cols, pad, dtype):
+    """Enough tiles for the big ones, X's rows aligned to 128 bytes and not: both layouts at once, and each alone, agree
+    with the oracle bit for bit."""
+    buf = draw((rows, cols + pad), DTYPES[dtype], rows + cols + pad).cuda()
+    x = buf[:, :cols]
+    ref = [mx.rounded(np64(x)), mx.rounded(np64(x).T)]
+    q, qt = f8lin.new_mxfp4(rows, cols), f8lin.new_mxfp4(cols, rows)
+    f8lin.mxfp4_quantize(x, q, qt)
+    for t, want in zip((q, qt), ref):
+        assert np.array_equal(np64(t.dequantize(torch.float32)), want)
+    for i, t in enumerate((f8lin.new_mxfp4(rows, cols), f8lin.new_mxfp4(cols, rows))):
+        f8lin.mxfp4_quantize(x, t if i == 0 else None, t if i == 1 else None)
+        assert np.array_equal(np64(t.dequantize(torch.float32)), ref[i])
