@@ -6,8 +6,8 @@
 // elements become NaN and the others 0).
 //
 // HBM-bound: the norm reads every element once, the scaling reads it again
-// and writes it (872M bf16 elements into fp32: 289 us, 6.0 TB/s, and 982 us,
-// 5.3 TB/s).  Sums are taken in binary64: the square of a 16-bit float is
+// and writes it (872M bf16 elements into fp32: 254 us, 6.9 TB/s, and 970 us,
+// 5.4 TB/s).  Sums are taken in binary64: the square of a 16-bit float is
 // exact in it, cannot overflow or vanish, and the order of a fixed grid is
 // the same on every run (no atomics).
 // Tables of up to kGradBatch tensors go to the kernel as an argument, so a
@@ -29,7 +29,7 @@ constexpr int kPiece = 16384;
 constexpr int kNormGrid = kGradPartials;
 constexpr int kScaleGrid = 2048;
 // 16-byte loads a thread has in flight, in both passes (the norm of 872M bf16
-// elements: 290 us or 6.0 TB/s; with one load 349 us)
+// elements through the caches: 289 us, with one load 349 us)
 constexpr int kAhead = 4;
 
 struct GradTable {
@@ -75,7 +75,7 @@ __device__ __forceinline__ double block_join(double s) {
   return join<P>(join<P>(red[0], red[1]), join<P>(red[2], red[3]));
 }
 
-template <int P, int DT>
+template <int P, int DT, bool PAST>
 __device__ __forceinline__ double piece_norm(const void *g, int64_t begin, int64_t n) {
   typedef typename MxElem<DT>::type elem;
   const elem *x = reinterpret_cast<const elem *>(g) + begin;
@@ -95,7 +95,7 @@ __device__ __forceinline__ double piece_norm(const void *g, int64_t begin, int64
   for (; at + kAhead * kStep <= len; at += kAhead * kStep) {  // kAhead loads in flight
     Raw8<DT> r[kAhead];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) r[a] = load_raw8<DT>(x + at + a * kStep + 8 * (int)threadIdx.x, 8);
+    for (int a = 0; a < kAhead; ++a) r[a] = load_raw8<DT, PAST>(x + at + a * kStep + 8 * (int)threadIdx.x, 8);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) add(r[a]);
   }
@@ -103,16 +103,16 @@ __device__ __forceinline__ double piece_norm(const void *g, int64_t begin, int64
   return nan ? __builtin_nan("") : s;
 }
 
-template <int P>
+template <int P, bool PAST>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const GradTable tab, double *partials, int add) {
   double s = 0.0;
   for (int p = blockIdx.x; p < tab.pieces; p += gridDim.x) {
     const int t = tensor_of(tab, p);
     const int64_t begin = (int64_t)(p - tab.first[t]) * kPiece;
     double v;
-    if (tab.in_dtype[t] == F8LIN_BF16) v = piece_norm<P, F8LIN_BF16>(tab.g[t], begin, tab.n[t]);
-    else if (tab.in_dtype[t] == F8LIN_FP16) v = piece_norm<P, F8LIN_FP16>(tab.g[t], begin, tab.n[t]);
-    else v = piece_norm<P, F8LIN_FP32>(tab.g[t], begin, tab.n[t]);
+    if (tab.in_dtype[t] == F8LIN_BF16) v = piece_norm<P, F8LIN_BF16, PAST>(tab.g[t], begin, tab.n[t]);
+    else if (tab.in_dtype[t] == F8LIN_FP16) v = piece_norm<P, F8LIN_FP16, PAST>(tab.g[t], begin, tab.n[t]);
+    else v = piece_norm<P, F8LIN_FP32, PAST>(tab.g[t], begin, tab.n[t]);
     s = join<P>(s, v);
   }
   s = block_join<P>(s);
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void grad_norm_final_kernel(const double 
 // bytes a lane and contiguous whatever the types (16-bit gradients into
 // 32-bit outputs with eight elements a lane: 1142 us for 872M elements, with
 // four 995 us); kAhead steps' loads in flight.
-template <int DI, int DO>
+template <int DI, int DO, bool PAST>
 __device__ __forceinline__ void piece_scale(const void *g, void *out, int64_t begin, int64_t n, float c) {
   typedef typename MxElem<DI>::type ielem;
   typedef typename MxElem<DO>::type oelem;
@@ -159,12 +159,14 @@ __device__ __forceinline__ void piece_scale(const void *g, void *out, int64_t be
       const int i = i0 + a * kThreads;
       if (i >= whole) continue;
       if constexpr (kInWords == 2) {
-        const u32x2 v = *reinterpret_cast<const u32x2_u *>(x + E * i);
+        const u32x2_u *src = reinterpret_cast<const u32x2_u *>(x + E * i);
+        const u32x2 v = PAST ? __builtin_nontemporal_load(src) : *src;
         w[a][0] = v.x, w[a][1] = v.y;
       } else {
 #pragma unroll
         for (int q = 0; q < kInWords; q += 4) {
-          const u32x4 v = *reinterpret_cast<const u32x4_u *>(x + E * i + q * 4 / (int)sizeof(ielem));
+          const u32x4_u *src = reinterpret_cast<const u32x4_u *>(x + E * i + q * 4 / (int)sizeof(ielem));
+          const u32x4 v = PAST ? __builtin_nontemporal_load(src) : *src;
           w[a][q] = v.x, w[a][q + 1] = v.y, w[a][q + 2] = v.z, w[a][q + 3] = v.w;
         }
       }
@@ -180,23 +182,27 @@ __device__ __forceinline__ void piece_scale(const void *g, void *out, int64_t be
         else
           o[k] = f32_to_elem(value(w[a], 2 * k) * c, DO) | f32_to_elem(value(w[a], 2 * k + 1) * c, DO) << 16;
       }
-      if (i < whole) *reinterpret_cast<u32x4_u *>(y + E * i) = u32x4{o[0], o[1], o[2], o[3]};
+      if (i >= whole) continue;
+      const u32x4 v = {o[0], o[1], o[2], o[3]};
+      u32x4_u *const dst = reinterpret_cast<u32x4_u *>(y + E * i);
+      if constexpr (PAST) __builtin_nontemporal_store(v, dst);
+      else *dst = v;
     }
   }
   const int at = whole * E + (int)threadIdx.x;  // fewer than E elements left
   if (at < len) y[at] = (oelem)f32_to_elem(elem_f32<DI>((uint32_t)x[at]) * c, DO);
 }
 
-template <int DI>
+template <int DI, bool PAST>
 __device__ __forceinline__ void piece_scale_to(const void *g, void *out, int out_dtype, int64_t begin, int64_t n, float c) {
-  if (out_dtype == F8LIN_BF16) piece_scale<DI, F8LIN_BF16>(g, out, begin, n, c);
-  else if (out_dtype == F8LIN_FP16) piece_scale<DI, F8LIN_FP16>(g, out, begin, n, c);
-  else piece_scale<DI, F8LIN_FP32>(g, out, begin, n, c);
+  if (out_dtype == F8LIN_BF16) piece_scale<DI, F8LIN_BF16, PAST>(g, out, begin, n, c);
+  else if (out_dtype == F8LIN_FP16) piece_scale<DI, F8LIN_FP16, PAST>(g, out, begin, n, c);
+  else piece_scale<DI, F8LIN_FP32, PAST>(g, out, begin, n, c);
 }
 
 // P < 0: norm[0] holds the norm; otherwise it comes from the partial results,
 // and the first workgroup writes it there.
-template <int P>
+template <int P, bool PAST>
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable tab, const double *partials, int count,
                                                               float *norm, float max_norm) {
   float n;
@@ -215,11 +221,11 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable ta
     if (c == 1.0f && tab.g[t] == tab.out[t]) continue;
     const int64_t begin = (int64_t)(p - tab.first[t]) * kPiece;
     if (tab.in_dtype[t] == F8LIN_BF16)
-      piece_scale_to<F8LIN_BF16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+      piece_scale_to<F8LIN_BF16, PAST>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
     else if (tab.in_dtype[t] == F8LIN_FP16)
-      piece_scale_to<F8LIN_FP16>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+      piece_scale_to<F8LIN_FP16, PAST>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
     else
-      piece_scale_to<F8LIN_FP32>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
+      piece_scale_to<F8LIN_FP32, PAST>(tab.g[t], tab.out[t], tab.out_dtype[t], begin, tab.n[t], c);
   }
 }
 
@@ -246,8 +252,24 @@ int fill(GradTable &tab, const f8lin_grad *list, int at, int count, bool outs) {
   return at;
 }
 
+// Whether gradients and outputs go past the caches (PAST): where they are more
+// than the 256 MB last-level cache keeps between the two passes.  Clipping
+// bf16 into bf16, past and through them: 256 MB in all 70 and 67 us, 384 MB
+// 103 and 107 us, 1.6 GB 404 and 452 us; into fp32: 192 MB 51 and 46 us, 384
+// MB 96 and 95 us, 576 MB 142 and 153 us.
+constexpr int64_t kCached = (int64_t)320 << 20;
+bool past_caches(const f8lin_grad *list, int count, bool outs) {
+  auto size = [](int64_t n, int dt) { return n * (dt == F8LIN_FP32 ? 4 : 2); };
+  int64_t bytes = 0;
+  for (int i = 0; i < count; ++i) {
+    bytes += size(list[i].n, list[i].dtype);
+    if (outs && list[i].out != list[i].g) bytes += size(list[i].n, list[i].out_dtype);
+  }
+  return bytes > kCached;
+}
+
 // The norm's partial results; returns how many there are.
-template <int P>
+template <int P, bool PAST>
 int launch_partials(const f8lin_grad *list, int count, double *partials, hipStream_t stream) {
   int at = 0, grid = kNormGrid;
   bool add = false;
@@ -256,13 +278,13 @@ int launch_partials(const f8lin_grad *list, int count, double *partials, hipStre
     at = fill(tab, list, at, count, false);
     // (a list of one table needs no more workgroups than it has pieces)
     if (!add && at >= count) grid = std::max(1, std::min(tab.pieces, kNormGrid));
-    grad_norm_kernel<P><<<grid, kThreads, 0, stream>>>(tab, partials, add ? 1 : 0);
+    grad_norm_kernel<P, PAST><<<grid, kThreads, 0, stream>>>(tab, partials, add ? 1 : 0);
     add = true;
   } while (at < count);
   return grid;
 }
 
-template <int P>
+template <int P, bool PAST>
 void launch_scale(const f8lin_grad *list, int count, const double *partials, int nparts, float *norm, float max_norm,
                   hipStream_t stream) {
   int at = 0;
@@ -270,18 +292,27 @@ void launch_scale(const f8lin_grad *list, int count, const double *partials, int
     GradTable tab = {};
     at = fill(tab, list, at, count, true);
     const unsigned grid = (unsigned)std::max(1, std::min(tab.pieces, kScaleGrid));
-    grad_scale_kernel<P><<<grid, kThreads, 0, stream>>>(tab, partials, nparts, norm, max_norm);
+    grad_scale_kernel<P, PAST><<<grid, kThreads, 0, stream>>>(tab, partials, nparts, norm, max_norm);
   } while (at < count);
+}
+
+template <int P, bool PAST>
+void launch_norm(const f8lin_grad *list, int count, double *partials, float *norm, bool clip, float max_norm,
+                 hipStream_t stream) {
+  const int nparts = launch_partials<P, PAST>(list, count, partials, stream);
+  if (clip)
+    launch_scale<P, PAST>(list, count, partials, nparts, norm, max_norm, stream);
+  else
+    grad_norm_final_kernel<P><<<1, kThreads, 0, stream>>>(partials, nparts, norm);
 }
 
 template <int P>
 void launch_type(const f8lin_grad *list, int count, double *partials, float *norm, bool clip, float max_norm,
                  hipStream_t stream) {
-  const int nparts = launch_partials<P>(list, count, partials, stream);
-  if (clip)
-    launch_scale<P>(list, count, partials, nparts, norm, max_norm, stream);
+  if (past_caches(list, count, clip))
+    launch_norm<P, true>(list, count, partials, norm, clip, max_norm, stream);
   else
-    grad_norm_final_kernel<P><<<1, kThreads, 0, stream>>>(partials, nparts, norm);
+    launch_norm<P, false>(list, count, partials, norm, clip, max_norm, stream);
 }
 
 }  // namespace
@@ -296,7 +327,10 @@ hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, do
 
 hipError_t launch_grad_scale(const f8lin_grad *list, int count, float *norm, float max_norm, hipStream_t stream) {
   if (count == 0) return hipSuccess;
-  launch_scale<-1>(list, count, nullptr, 0, norm, max_norm, stream);
+  if (past_caches(list, count, true))
+    launch_scale<-1, true>(list, count, nullptr, 0, norm, max_norm, stream);
+  else
+    launch_scale<-1, false>(list, count, nullptr, 0, norm, max_norm, stream);
   return hipGetLastError();
 }
 

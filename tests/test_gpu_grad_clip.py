@@ -223,3 +223,26 @@ def test_expanded_gradient_is_refused_in_place(mod):
     assert torch.equal(a.grad, torch.full((4,), 2.0, device="cuda"))
     norm, out = mod.clip_grads([a.grad, b.grad], 1.0, norm_type=1.0)
     assert norm.item() == 4 * 2.0 + 15 * 3.0 and out[1].shape == (3, 5)
+
+
+@pytest.mark.parametrize("sizes, dtype, out", [([100_000_003, 70_000_001, 5], torch.bfloat16, None),
+                                               ([60_000_001, 7], torch.float16, torch.float32),
+                                               ([90_000_001], torch.float32, torch.float32)])
+def test_more_than_the_caches_hold(f8lin, mod, sizes, dtype, out):
+    """Big lists, in place (out None) and out of it: the norm against binary64, the clipped gradients bit for bit."""
+    gen = torch.Generator("cuda").manual_seed(len(sizes))
+    grads = [torch.empty(n, dtype=dtype, device="cuda").normal_(0, 0.02, generator=gen) for n in sizes]
+    before = [g.clone() for g in grads]
+    ref = sum(sum((c.double() ** 2).sum().item() for c in g.split(1 << 24)) for g in grads) ** 0.5
+    norm = torch.empty((), device="cuda")
+    f8lin.grad_norm(grads, norm, f8lin.new_grad_workspace())
+    assert abs(norm.item() - ref) <= ref * 2.0 ** -24 * 1.01
+    assert abs(mod.get_grad_norm(grads, math.inf).item() - max(g.abs().max().item() for g in grads)) == 0
+    outs = grads if out is None else [torch.empty_like(g, dtype=out) for g in grads]
+    got = torch.empty((), device="cuda")
+    f8lin.grad_clip(grads, 0.5, got, f8lin.new_grad_workspace(), 2.0, outs=None if out is None else outs)
+    assert torch.equal(got, norm)
+    c = torch.tensor(0.5, device="cuda") / (norm + 1e-6)
+    for g, b, o in zip(grads, before, outs):
+        assert torch.equal(o, (b.float() * c).to(o.dtype))
+        assert out is None or torch.equal(g, b)
