@@ -5,8 +5,8 @@
 //
 // HBM-bound: es bytes read and 17/32 byte written per element and layout.
 // 65536 x 4096 bf16: rows 109 us (6.2 TB/s), columns 133 us (5.1), both 157 us
-// (5.2), the way back 121 us (5.6); a plain copy moves 5.0-5.3 TB/s on this
-// card and a read alone 6.3.
+// (5.2), the way back 103 us (6.6); a plain copy moves 5.0-5.3 TB/s on this
+// card and a read alone 6.3, both through the caches.
 // Rows alone (mx_rows_kernel): a thread takes eight consecutive elements of
 // four rows, all four loads in flight; a block is four lanes, whose maxima
 // meet by two DPP quad permutations.
@@ -34,6 +34,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTileCols = 128;
 constexpr int64_t kFewTiles = 256;  // tiles of 256 x 128 elements: fewer leave CUs idle
+constexpr int64_t kManyTiles = 1280;  // 80 MB of 16-bit elements
 
 struct QuantJob {
   const void *x;
@@ -55,8 +56,9 @@ __device__ __forceinline__ int scales_of_16(int e, int q) {
   return sw | __builtin_amdgcn_mov_dpp(sw, 0x128, 0xF, 0xF, true);  // row_ror 8
 }
 
-// Rows alone; 16-bit X is read past the L2 (65536 x 4096 bf16 109 us, through
-// it 126 us; 3001 x 2504 fp16 8.4 us, through it 7.4 us).  A workgroup covers tx = 2^log_tx chunks of eight elements by
+// Rows alone; in large calls 16-bit X is read past the L2 (65536 x 4096 bf16
+// 109 us, through it 126 us; 3001 x 2504 fp16 8.4 us, through it 7.4 us).  A
+// workgroup covers tx = 2^log_tx chunks of eight elements by
 // kRowsPer * 256 / tx rows: four rows a thread, or one where that leaves few
 // workgroups.
 template <int DT, int RULE, int kRowsPer>
@@ -74,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const QuantJobs jobs)
 #pragma unroll
   for (int p = 0; p < kRowsPer; ++p) {
     const int64_t row = row0 + (int64_t)p * (kThreads >> jb.log_tx);
-    v[p] = load_raw8<DT, DT != F8LIN_FP32>(x + row * jb.ldx + col, row < jb.rows ? have : 0);
+    v[p] = load_raw8<DT, DT != F8LIN_FP32 && kRowsPer == 4>(x + row * jb.ldx + col, row < jb.rows ? have : 0);
   }
 #pragma unroll
   for (int p = 0; p < kRowsPer; ++p) {
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(64 * kRowBlocks) void mx_quantize_kernel(const Quan
 // The way back.  E codes per thread, so that its values are one 16-byte store,
 // of kRowsPer rows; a workgroup covers 2^log_tx such groups by kRowsPer * 256 /
 // 2^log_tx rows.
-template <int DT, int kRowsPer>
+template <int DT, int kRowsPer, bool PAST>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(f8lin_mxfp4 q, int64_t rows, int64_t cols,
                                                                  typename MxElem<DT>::type *out, int tiles_x, int log_tx) {
   constexpr int E = DT == F8LIN_FP32 ? 4 : 8;
@@ -256,11 +258,11 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(f8lin_mxfp4 q, 
     for (int k = 0; k < E; ++k) o[k] = f32_to_elem(e == kMxNan ? __builtin_nanf("") : v[k >> 1][k & 1], DT);
     typename MxElem<DT>::type *dst = out + row * cols + col;
     if (col + E <= cols) {
-      if constexpr (DT == F8LIN_FP32)
-        *reinterpret_cast<u32x4_u *>(dst) = u32x4{o[0], o[1], o[2], o[3]};
-      else
-        *reinterpret_cast<u32x4_u *>(dst) =
-            u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+      u32x4 v;
+      if constexpr (DT == F8LIN_FP32) v = u32x4{o[0], o[1], o[2], o[3]};
+      else v = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+      if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_u *>(dst));
+      else *reinterpret_cast<u32x4_u *>(dst) = v;
     } else {
 #pragma unroll
       for (int k = 0; k < E; ++k)
@@ -344,8 +346,12 @@ hipError_t launch_mx_quantize(const MxQuant *ts, int count, int rule, hipStream_
   QuantJobs jobs = {};
   int64_t total = 0;
   // X past the L2: where its rows are whole 128-byte lines, that no two tiles
-  // share (65535 x 4095 bf16, both layouts: 218 us so, 214 us otherwise)
-  bool once = true;
+  // share (65535 x 4095 bf16, both layouts: 218 us so, 214 us otherwise), and
+  // there is more of it than the caches may hold from whoever wrote it (an
+  // element-wise launch, the forward and another one: 8192 x 4096 x 4096, 96
+  // MB in X and W, 159 us, otherwise 166 us; 4096 x 4096 x 4096, 64 MB, 92 and
+  // 90 us).
+  bool once = tiles >= kManyTiles;
   for (int i = 0; i < count; ++i) {
     const MxQuant &t = ts[i];
     if (t.rows == 0 || t.cols == 0) continue;
@@ -392,9 +398,13 @@ hipError_t launch_mx_dequantize(const f8lin_mxfp4 &q, int64_t rows, int64_t cols
   const int64_t gx = (cols + (per << log_tx) - 1) / (per << log_tx), few = rows * cols < kFewTiles * 256 * kTileCols,
                 rows_per = (few ? 1 : 4) * (kThreads >> log_tx);
   const unsigned grid = (unsigned)(gx * ((rows + rows_per - 1) / rows_per));
-#define F8_MX_D(DT, T)                                                                                        \
-  few ? mx_dequantize_kernel<DT, 1><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx) \
-      : mx_dequantize_kernel<DT, 4><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx)
+  // an output that the caches cannot hold for its reader goes past them (65536
+  // x 4096 bf16 103 us, through them 122 us)
+  const bool past = rows * cols * (dtype == F8LIN_FP32 ? 4 : 2) > (int64_t)320 << 20;
+#define F8_MX_D(DT, T)                                                                                             \
+  past  ? mx_dequantize_kernel<DT, 4, true><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx) \
+  : few ? mx_dequantize_kernel<DT, 1, false><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx) \
+        : mx_dequantize_kernel<DT, 4, false><<<grid, kThreads, 0, stream>>>(q, rows, cols, (T *)out, (int)gx, log_tx)
   if (dtype == F8LIN_BF16)
     F8_MX_D(F8LIN_BF16, uint16_t);
   else if (dtype == F8LIN_FP16)

@@ -383,3 +383,28 @@ def test_quantize_many_tiles(f8lin, mx, rows, cols, pad, dtype):
     for i, t in enumerate((f8lin.new_mxfp4(rows, cols), f8lin.new_mxfp4(cols, rows))):
         f8lin.mxfp4_quantize(x, t if i == 0 else None, t if i == 1 else None)
         assert np.array_equal(np64(t.dequantize(torch.float32)), ref[i])
+
+
+@pytest.mark.parametrize("rows, cols", [(163840, 1088), (163841, 1090)])
+def test_more_than_the_caches_hold(f8lin, rows, cols):
+    """A large tensor, its rows aligned to 128 bytes and not, against the same in pieces: codes, scales and values."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    q, qt, alone, back = (f8lin.new_mxfp4(*s) for s in ((rows, cols), (cols, rows), (rows, cols), (cols, rows)))
+    f8lin.mxfp4_quantize(x, q, qt)
+    f8lin.mxfp4_quantize(x, alone)
+    f8lin.mxfp4_quantize(x, None, back)
+    values = q.dequantize()
+    cb, step = -(-cols // 32), 4096
+    for r0 in range(0, rows, step):
+        n = min(step, rows - r0)
+        p, pt = f8lin.new_mxfp4(n, cols), f8lin.new_mxfp4(cols, n)
+        f8lin.mxfp4_quantize(x[r0:r0 + n], p, pt)
+        nb = -(-n // 32)
+        for t in (q, alone):
+            assert torch.equal(t.codes[r0:r0 + n, :16 * cb], p.codes[:, :16 * cb])
+            assert torch.equal(t.scales[r0:r0 + n, :cb], p.scales[:, :cb])
+        for t in (qt, back):
+            assert torch.equal(t.codes[:, r0 // 2:r0 // 2 + 16 * nb], pt.codes[:, :16 * nb])
+            assert torch.equal(t.scales[:, r0 // 32:r0 // 32 + nb], pt.scales[:, :nb])
+        assert torch.equal(values[r0:r0 + n], p.dequantize())
