@@ -357,25 +357,31 @@ def _present(*pairs):
     return [shape for ask, shape in pairs if ask]
 
 
+def _mxfp4_forward(x, weight, bias, rule, need_x, need_w):
+    """(y, buffer of the transposed copies that the gradients asked for will need, or None)."""
+    M, K = x.shape
+    N = weight.shape[0]
+    dev = x.device
+    y = torch.empty((M, N), dtype=x.dtype, device=dev)
+    _, (x4, w4) = f8lin.new_mxfp4s(((M, K), (N, K)), dev)
+    x4t = w4t = saved = None
+    if need_x or need_w:
+        saved, copies = f8lin.new_mxfp4s(_present((need_w, (K, M)), (need_x, (K, N))), dev)
+        x4t = copies[0] if need_w else None
+        w4t = copies[-1] if need_x else None
+    f8lin.mxfp4_forward(x, weight if weight.is_contiguous() else weight.contiguous(), y, x4, w4, x4t, w4t,
+                        bias if bias is None or bias.is_contiguous() else bias.contiguous(), rule)
+    return y, saved
+
+
 class _MXFP4LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, rule):
-        M, K = x.shape
-        N = weight.shape[0]
-        dev = x.device
-        need_x, need_w = ctx.needs_input_grad[:2]
-        y = torch.empty((M, N), dtype=x.dtype, device=dev)
-        _, (x4, w4) = f8lin.new_mxfp4s(((M, K), (N, K)), dev)
-        x4t = w4t = saved = None
-        if need_x or need_w:  # the transposed copies, for the gradients that will be asked for
-            saved, copies = f8lin.new_mxfp4s(_present((need_w, (K, M)), (need_x, (K, N))), dev)
-            x4t = copies[0] if need_w else None
-            w4t = copies[-1] if need_x else None
-        f8lin.mxfp4_forward(x, weight if weight.is_contiguous() else weight.contiguous(), y, x4, w4, x4t, w4t,
-                            bias if bias is None or bias.is_contiguous() else bias.contiguous(), rule)
+        y, saved = _mxfp4_forward(x, weight, bias, rule, *ctx.needs_input_grad[:2])
         if saved is not None:
             ctx.save_for_backward(saved)
-        ctx.args = (M, N, K, rule, x.dtype, weight.dtype, None if bias is None else bias.dtype)
+        ctx.args = (x.shape[0], weight.shape[0], x.shape[1], rule, x.dtype, weight.dtype,
+                    None if bias is None else bias.dtype)
         return y
 
     @staticmethod
@@ -421,7 +427,9 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
     # (an empty last dimension leaves reshape nothing to infer the rows from)
     x2 = _rows(x) if x.numel() else x.reshape(lead.numel(), K)
     if not packed:
-        return _MXFP4LinearFn.apply(x2, weight, bias, rule).reshape(*lead, N)
+        if torch.is_grad_enabled():
+            return _MXFP4LinearFn.apply(x2, weight, bias, rule).reshape(*lead, N)
+        return _mxfp4_forward(x2, weight, bias, rule, False, False)[0].reshape(*lead, N)
     if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):
         raise RuntimeError("mxfp4_linear: a quantised weight has no backward; call it under torch.no_grad()")
     M = x2.shape[0]

@@ -408,3 +408,22 @@ def test_more_than_the_caches_hold(f8lin, rows, cols):
             assert torch.equal(t.codes[:, r0 // 2:r0 // 2 + 16 * nb], pt.codes[:, :16 * nb])
             assert torch.equal(t.scales[:, r0 // 32:r0 // 32 + nb], pt.scales[:, :nb])
         assert torch.equal(values[r0:r0 + n], p.dequantize())
+
+
+def test_no_transposed_copies_without_gradients(mod, f8lin, mx, monkeypatch):
+    """Under no_grad a trainable layer quantises for its product alone; with gradients for one operand, only for that."""
+    layer = mod.MXFP4Linear(70, 50, device="cuda", dtype=torch.float32, bias=True)
+    x = draw((9, 70), torch.float32, 5).cuda()
+    made, real = [], f8lin.new_mxfp4s
+    monkeypatch.setattr(f8lin, "new_mxfp4s", lambda shapes, *a: made.extend(shapes) or real(shapes, *a))
+    with torch.no_grad():
+        y = layer(x)
+    assert sorted(made) == [(9, 70), (50, 70)] and not y.requires_grad
+    made.clear()
+    z = layer(x)
+    assert torch.equal(z, y) and sorted(made) == [(9, 70), (50, 70), (70, 9)]
+    made.clear()
+    layer.weight.requires_grad_(False)
+    z = layer(x.clone().requires_grad_())
+    assert torch.equal(z, y) and sorted(made) == [(9, 70), (50, 70), (70, 50)]
+    check_product(y, mx.rounded(np64(x)), mx.rounded(np64(layer.weight)), torch.float32, np64(layer.bias))
