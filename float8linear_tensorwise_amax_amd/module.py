@@ -53,6 +53,7 @@ from typing import Dict, Iterable, List, Optional, Tuple, Union
 
 import torch
 import torch.nn as nn
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import f8lin
@@ -352,6 +353,14 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
+def _refuse_tangents(what: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Raises where a tensor has a forward-mode tangent: a call that takes no part in autograd would drop it, and its
+    result would read as having a derivative of zero."""
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{what} has no forward-mode derivative")
+
+
 def _present(*pairs):
     """The shapes of the pairs (asked for, shape) that are asked for."""
     return [shape for ask, shape in pairs if ask]
@@ -416,7 +425,8 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
 
     weight a (out, in) tensor: it is quantised by the call, and the call is differentiable in x, weight and bias
     (the two backward products run in MXFP4 too, on operands quantised along their own contractions).
-    weight an f8lin.MXFP4Tensor of (out, in): for serving; x must not need a gradient."""
+    weight an f8lin.MXFP4Tensor of (out, in): for serving; x must not need a gradient.
+    Forward-mode derivatives are refused (NotImplementedError), whatever the grad mode."""
     if not x.is_cuda:
         raise RuntimeError("mxfp4_linear runs on the GPU only (libf8lin has no CPU path)")
     packed = isinstance(weight, f8lin.MXFP4Tensor)
@@ -426,9 +436,10 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
     lead = x.shape[:-1]
     # (an empty last dimension leaves reshape nothing to infer the rows from)
     x2 = _rows(x) if x.numel() else x.reshape(lead.numel(), K)
+    if not packed and torch.is_grad_enabled():
+        return _MXFP4LinearFn.apply(x2, weight, bias, rule).reshape(*lead, N)
+    _refuse_tangents("mxfp4_linear", x, bias, None if packed else weight)
     if not packed:
-        if torch.is_grad_enabled():
-            return _MXFP4LinearFn.apply(x2, weight, bias, rule).reshape(*lead, N)
         return _mxfp4_forward(x2, weight, bias, rule, False, False)[0].reshape(*lead, N)
     if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):
         raise RuntimeError("mxfp4_linear: a quantised weight has no backward; call it under torch.no_grad()")

@@ -1,0 +1,31 @@
+"""The MXFP4 and clipping module surface without a GPU: the library's calls are replaced by stubs that fill their
+outputs, and tensors say that they are on a GPU."""
+import pytest
+import torch
+import torch.nn as nn
+from torch.autograd import forward_ad
+
+from float8linear_tensorwise_amax_amd import f8lin
+from float8linear_tensorwise_amax_amd import module as m
+
+
+@pytest.fixture
+def stubbed(monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(f8lin, "mxfp4_forward", lambda x, w, y, *a, **k: y.fill_(3.0))
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("packed, dual", [(True, "x"), (True, "bias"), (False, "x"), (False, "weight"), (False, "bias")])
+def test_a_forward_mode_tangent_is_refused(stubbed, packed, grad, dual):
+    """A linear that takes no part in autograd would drop a tangent, which reads as a derivative of zero."""
+    ts = {"x": torch.ones(2, 3, 64), "weight": torch.ones(5, 64), "bias": torch.ones(5)}
+    packed_w = f8lin.new_mxfp4(5, 64, "cpu")
+    with forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        plain = packed_w if packed else ts["weight"]
+        assert m.mxfp4_linear(ts["x"], plain, ts["bias"]).shape == (2, 3, 5)  # no tangent: as ever
+        ts[dual] = forward_ad.make_dual(ts[dual], torch.ones_like(ts[dual]))
+        with pytest.raises(NotImplementedError):
+            m.mxfp4_linear(ts["x"], packed_w if packed else ts["weight"], ts["bias"])
+    with torch.inference_mode():  # no derivative of any kind there
+        assert m.mxfp4_linear(torch.ones(2, 64), packed_w if packed else torch.ones(5, 64)).shape == (2, 5)
