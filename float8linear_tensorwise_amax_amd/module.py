@@ -540,7 +540,10 @@ def _gradients(parameters: Union[torch.Tensor, Iterable[torch.Tensor]]) -> List[
 
 
 def get_grad_norm(grads: Iterable[torch.Tensor], norm_type: float = 2.0) -> torch.Tensor:
-    """The norm (2, 1 or inf) of all the gradients' elements as one vector: a float32 scalar on their GPU."""
+    """The norm (2, 1 or inf) of all the gradients' elements as one vector: a float32 scalar on their GPU, outside any
+    autograd graph (a forward-mode tangent is refused)."""
+    grads = list(grads)
+    _refuse_tangents("get_grad_norm", *grads)
     grads = [_dense_copy(g) for g in grads]
     if not grads:
         return torch.zeros((), dtype=torch.float32)
@@ -553,7 +556,10 @@ def get_grad_norm(grads: Iterable[torch.Tensor], norm_type: float = 2.0) -> torc
 def clip_grads(grads: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0,
                out_dtype: Optional[torch.dtype] = None) -> Tuple[torch.Tensor, List[torch.Tensor]]:
     """(norm, clipped): the gradients times min(1, max_norm / (norm + 1e-6)) in new tensors (of out_dtype, e.g.
-    float32 for a full-precision optimiser behind 16-bit gradients; default their own)."""
+    float32 for a full-precision optimiser behind 16-bit gradients; default their own), outside any autograd graph (a
+    forward-mode tangent is refused)."""
+    grads = list(grads)
+    _refuse_tangents("clip_grads", *grads)
     grads = [_dense_copy(g) for g in grads]
     if not grads:
         return torch.zeros((), dtype=torch.float32), []
@@ -573,6 +579,7 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
     grads = _gradients(parameters)
     if not grads:
         return torch.zeros((), dtype=torch.float32)
+    _refuse_tangents("clip_grad_norm_", *grads)
     if any(st == 0 and n > 1 for g in grads for st, n in zip(g.stride(), g.shape)):
         raise ValueError("clip_grad_norm_: an expanded gradient cannot be scaled in place")
     flat = [_dense_copy(g) for g in grads]

@@ -29,3 +29,19 @@ def test_a_forward_mode_tangent_is_refused(stubbed, packed, grad, dual):
             m.mxfp4_linear(ts["x"], packed_w if packed else ts["weight"], ts["bias"])
     with torch.inference_mode():  # no derivative of any kind there
         assert m.mxfp4_linear(torch.ones(2, 64), packed_w if packed else torch.ones(5, 64)).shape == (2, 5)
+
+
+def test_a_tangent_of_a_gradient_is_refused(monkeypatch):
+    """The norm and the clipped gradients would come back without it; in place it would stay unscaled."""
+    monkeypatch.setattr(f8lin, "grad_norm", lambda grads, out, *a, **k: out.fill_(1.0))
+    monkeypatch.setattr(f8lin, "grad_clip", lambda grads, max_norm, norm, *a, **k: norm.fill_(1.0))
+    plain, p = torch.ones(4), nn.Parameter(torch.ones(4))
+    with forward_ad.dual_level():
+        p.grad = plain.clone()
+        assert m.get_grad_norm([plain]) == 1 and m.clip_grads([plain], 1.0)[0] == 1 and m.clip_grad_norm_([p], 1.0) == 1
+        dual = forward_ad.make_dual(torch.ones(4), torch.ones(4))
+        p.grad = dual
+        for call in (lambda: m.get_grad_norm([plain, dual]), lambda: m.clip_grads([plain, dual], 1.0),
+                     lambda: m.clip_grad_norm_([p], 1.0)):
+            with pytest.raises(NotImplementedError):
+                call()
