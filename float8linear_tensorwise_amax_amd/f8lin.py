@@ -4,7 +4,9 @@ Argument marshalling only: every step of the path runs in the library's HIP
 kernels.  PyTorch supplies device memory (tensors) and streams; this module
 checks dtypes / devices / contiguity, passes raw pointers and the current HIP
 stream, and raises F8linError on a non-zero status.  Importing it fails
-loudly if the library is not built -- there is no fallback.
+loudly if the library is not built -- there is no fallback.  Outputs are
+written behind autograd's back: only grad_norm and grad_clip, whose tensors
+are gradients, move the version counters of what they write.
 """
 import array
 import ctypes
@@ -812,6 +814,7 @@ def grad_norm(grads: Sequence[torch.Tensor], out: torch.Tensor, ws: torch.Tensor
     _same_device(ws, "ws", out.device)
     _call(_lib.f8lin_grad_norm, out.device, stream, tab.buffer_info()[0], len(grads), code,
           _ptr(out, torch.float32), _ptr(ws), _nbytes(ws))
+    torch.autograd.graph.increment_version(out)
 
 
 def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor, ws: Optional[torch.Tensor],
@@ -824,3 +827,5 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor
     _same_device(ws, "ws", norm.device)
     _call(_lib.f8lin_grad_clip, norm.device, stream, tab.buffer_info()[0], len(grads), code, float(max_norm),
           _ptr(norm, torch.float32), 1 if norm_given else 0, _ptr(ws), _nbytes(ws))
+    written = list(grads if outs is None else outs)
+    torch.autograd.graph.increment_version(written if norm_given else written + [norm])

@@ -45,3 +45,31 @@ def test_a_tangent_of_a_gradient_is_refused(monkeypatch):
                      lambda: m.clip_grad_norm_([p], 1.0)):
             with pytest.raises(NotImplementedError):
                 call()
+
+
+def test_written_gradients_count_as_changed(monkeypatch):
+    """The library writes through pointers: the version counters, by which autograd finds a saved tensor that was
+    changed, are moved for every tensor that a call writes and for none that it reads."""
+    monkeypatch.setattr(f8lin, "_ptr", lambda t, dtype=None: 0 if t is None else t.data_ptr())
+    monkeypatch.setattr(f8lin, "_call", lambda *a: None)
+    grads, outs = [torch.ones(4), torch.ones(3, 2).t()], [torch.ones(4), torch.ones(3, 2).t()]
+    norm, ws = torch.zeros(1), torch.zeros(f8lin.grad_workspace_bytes(), dtype=torch.uint8)
+
+    def moved(*args, call=f8lin.grad_clip, **kw):
+        ts = (*grads, *outs, norm)
+        before = [t._version for t in ts]
+        call(*args, **kw)
+        return [t._version > b for t, b in zip(ts, before)]
+
+    assert moved(grads, 1.0, norm, ws) == [True, True, False, False, True]
+    assert moved(grads, 1.0, norm, ws, outs=outs) == [False, False, True, True, True]
+    assert moved(grads, 1.0, norm, None, outs=outs, norm_given=True) == [False, False, True, True, False]
+    assert moved(grads, norm, ws, call=f8lin.grad_norm) == [False] * 4 + [True]
+    p = nn.Parameter(torch.ones(4))
+    p.grad = torch.ones(4)
+    saved = (p.grad.requires_grad_() * torch.ones(4, requires_grad=True)).sum()  # keeps p.grad for its backward
+    m.clip_grad_norm_([p], 1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.backward()
+    with torch.inference_mode():  # (tensors that count no versions)
+        f8lin.grad_clip([torch.ones(4)], 1.0, torch.zeros(1), ws)
