@@ -508,15 +508,21 @@ class MXFP4Linear(nn.Module):
 
 def convert_to_mxfp4_training(module: nn.Module, rule: str = "floor", module_filter_fn=None) -> nn.Module:
     """Replaces every nn.Linear (that module_filter_fn(fqn, module) accepts, if given) by an MXFP4Linear sharing its
-    weight and bias Parameters.  Returns the module."""
+    weight and bias Parameters.  A linear that stands in several places becomes one MXFP4Linear in all of them; the
+    filter is asked for each (for the places inside a shared parent, once, under that parent's first name).  Returns the
+    module."""
     if type(module) is nn.Linear:
         raise ValueError("convert the parent module, not a bare nn.Linear")
-    for fqn, child in list(module.named_modules()):
-        if type(child) is nn.Linear and (module_filter_fn is None or module_filter_fn(fqn, child)):
-            parent, _, name = fqn.rpartition(".")
-            setattr(module.get_submodule(parent), name,
-                    MXFP4Linear(child.in_features, child.out_features, rule, weight=child.weight,
-                                bias=child.bias if child.bias is not None else False))
+    made: Dict[nn.Linear, MXFP4Linear] = {}
+    for prefix, parent in list(module.named_modules()):
+        # (not named_children, which names a child once)
+        for name, child in list(parent._modules.items()):
+            fqn = f"{prefix}.{name}" if prefix else name
+            if type(child) is nn.Linear and (module_filter_fn is None or module_filter_fn(fqn, child)):
+                if child not in made:
+                    made[child] = MXFP4Linear(child.in_features, child.out_features, rule, weight=child.weight,
+                                              bias=child.bias if child.bias is not None else False)
+                setattr(parent, name, made[child])
     return module
 
 

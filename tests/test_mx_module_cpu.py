@@ -73,3 +73,31 @@ def test_written_gradients_count_as_changed(monkeypatch):
         saved.backward()
     with torch.inference_mode():  # (tensors that count no versions)
         f8lin.grad_clip([torch.ones(4)], 1.0, torch.zeros(1), ws)
+
+
+class Holder(nn.Module):
+    def __init__(self, **children):
+        super().__init__()
+        for name, child in children.items():
+            self.add_module(name, child)
+
+
+def test_a_shared_linear_is_converted_everywhere():
+    """One linear under several parents, twice under one, and inside a shared parent: one layer in all the places."""
+    lin, other = nn.Linear(8, 8), nn.Linear(8, 4)
+    inner = Holder(c=other)
+    model = Holder(a=Holder(l=lin), b=Holder(l=lin, again=lin), s=inner, t=inner)
+    m.convert_to_mxfp4_training(model, "ceil")
+    layers = [model.a.l, model.b.l, model.b.again]
+    assert all(isinstance(l, m.MXFP4Linear) and l is layers[0] and l.rule == "ceil" for l in layers)
+    assert layers[0].weight is lin.weight and isinstance(model.t.c, m.MXFP4Linear) and model.t.c is model.s.c
+    assert not any(type(l) is nn.Linear for l in model.modules())
+    assert len(list(model.parameters())) == 4
+
+    # each place is asked for by name, a shared parent's places under its first name
+    seen = []
+    lin = nn.Linear(8, 8)
+    inner = Holder(c=lin)
+    model = Holder(a=Holder(l=lin), s=inner, t=inner)
+    m.convert_to_mxfp4_training(model, module_filter_fn=lambda fqn, child: seen.append(fqn) or fqn != "a.l")
+    assert seen == ["a.l", "s.c"] and model.a.l is lin and isinstance(model.t.c, m.MXFP4Linear)
