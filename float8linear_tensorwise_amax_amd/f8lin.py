@@ -534,6 +534,14 @@ def _call(fn, device: torch.device, stream, *args):
         raise F8linError(status)
 
 
+def _stream_object(stream, device: torch.device) -> torch.cuda.Stream:
+    """The stream as an object that torch allocates under (ExternalStream would take a handle of 0 for no stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = _stream(stream)
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
 def _refuse(t: torch.Tensor, what: str, device: Optional[torch.device]):
     if not t.is_cuda:
         raise ValueError("f8lin: tensors must be on the GPU")
@@ -626,8 +634,17 @@ class MXFP4Tensor:
         return self._scales
 
     def dequantize(self, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
-        """The values this tensor stands for, rounded to `dtype`."""
-        out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.device)
+        """The values this tensor stands for, rounded to `dtype`.  A given stream owns the result's memory, as of a tensor
+        made under it; the current stream may read it once it has waited for that stream."""
+        if stream is None:
+            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.device)
+        else:
+            stream = _stream_object(stream, self.device)
+            with torch.cuda.stream(stream):
+                out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.device)
+            current = torch.cuda.current_stream(self.device)
+            if stream != current:
+                out.record_stream(current)
         mxfp4_dequantize(self, out, stream)
         return out
 
