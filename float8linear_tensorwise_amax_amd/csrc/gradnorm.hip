@@ -3,7 +3,7 @@
 //   n = sqrt(sum g^2), sum |g| or max |g| over every element of every tensor;
 //   c = min(1, max_norm / (n + 1e-6)) in binary32;  out = c * g, rounded once.
 // A NaN anywhere makes n and c NaN; an Inf makes n Inf and c 0 (so that Inf
-// elements become NaN and the others 0).
+// elements become NaN and the others 0), unless max_norm is Inf too: then c is 1.
 //
 // HBM-bound: the norm reads every element once, the scaling reads it again
 // and writes it (872M bf16 elements into fp32: 254 us, 6.9 TB/s, and 970 us,
@@ -214,6 +214,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable ta
   }
   float c = max_norm / (n + 1e-6f);
   c = c > 1.0f ? 1.0f : c;  // (a NaN stays one)
+  if (max_norm == __builtin_inff() && n == max_norm) c = 1.0f;  // (no limit: Inf / Inf above)
   // from the end: what the norm's pass read last is still in the caches
   for (int p = tab.pieces - 1 - (int)blockIdx.x; p >= 0; p -= (int)gridDim.x) {
     const int t = tensor_of(tab, p);

@@ -838,7 +838,8 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor
               norm_type: float = 2.0, outs: Optional[Sequence[torch.Tensor]] = None, norm_given: bool = False,
               stream=None):
     """norm[0] (float32) = the norm as grad_norm gives it (norm_given: it is read instead), then every gradient times
-    min(1, max_norm / (norm + 1e-6)), in place or into outs (laid out alike; any of the three types)."""
+    min(1, max_norm / (norm + 1e-6)), in place or into outs (laid out alike; any of the three types).  max_norm may be
+    inf: no limit."""
     code = _norm_type(norm_type)
     tab = _grad_table(grads, outs, norm.device)
     _same_device(ws, "ws", norm.device)

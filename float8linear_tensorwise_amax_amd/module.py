@@ -581,7 +581,8 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
                     error_if_nonfinite: bool = False) -> torch.Tensor:
     """Scales the parameters' gradients in place so that the norm of all of them together is at most max_norm;
     returns the norm they had.  A NaN norm makes every gradient NaN; error_if_nonfinite=True reads the norm back
-    instead (a host synchronisation) and raises before anything is scaled."""
+    instead (a host synchronisation) and raises before anything is scaled.  max_norm=inf only measures the norm.  A
+    gradient may be there once: a parameter listed twice is refused."""
     grads = _gradients(parameters)
     if not grads:
         return torch.zeros((), dtype=torch.float32)

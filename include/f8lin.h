@@ -510,7 +510,8 @@ size_t f8lin_grad_workspace_bytes(void);
  * NULL), then for every tensor
  *   out = c * g,  c = min(1, max_norm / (norm + 1e-6))
  * in fp32, rounded once to out_dtype.  c is NaN with a NaN norm and 0 with an
- * infinite one (so Inf elements become NaN, the others 0).  max_norm >= 0.
+ * infinite one (so Inf elements become NaN, the others 0).  max_norm >= 0; an
+ * infinite one is no limit: c is 1 with any norm but NaN.
  * A tensor may not be listed twice. */
 int f8lin_grad_clip(const f8lin_grad *list, int count, int norm_type, float max_norm, float *norm, int norm_given,
                     void *ws, size_t ws_bytes, void *stream);
