@@ -665,7 +665,7 @@ def _mx(t: Optional[MXFP4Tensor], rows: int, cols: int, what: str, device=None):
 
 def new_mxfp4s(shapes, device="cuda", buffer: Optional[torch.Tensor] = None):
     """(flat buffer, [MXFP4Tensor]): uninitialised tensors of the (rows, cols) shapes, with the library's strides, in
-    one allocation -- or the tensors that such a buffer holds."""
+    one allocation -- or the tensors that such a buffer (flat, contiguous, 16-byte aligned, as long or longer) holds."""
     ld, sld = _lib.f8lin_mxfp4_ld, _lib.f8lin_mxfp4_scale_ld
     laid, at = [], 0
     for rows, cols in shapes:
@@ -674,6 +674,9 @@ def new_mxfp4s(shapes, device="cuda", buffer: Optional[torch.Tensor] = None):
         at += rows * (a + b)
     if buffer is None:
         buffer = torch.empty(at, dtype=torch.uint8, device=device)
+    elif (buffer.dtype != torch.uint8 or buffer.dim() != 1 or buffer.numel() < at or not buffer.is_contiguous()
+          or buffer.data_ptr() % 16):
+        raise ValueError(f"new_mxfp4s: these tensors need a flat, contiguous, 16-byte aligned uint8 buffer of {at} bytes")
     return buffer, [MXFP4Tensor._of(buffer, *l) for l in laid]
 
 

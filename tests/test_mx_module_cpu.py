@@ -101,3 +101,20 @@ def test_a_shared_linear_is_converted_everywhere():
     model = Holder(a=Holder(l=lin), s=inner, t=inner)
     m.convert_to_mxfp4_training(model, module_filter_fn=lambda fqn, child: seen.append(fqn) or fqn != "a.l")
     assert seen == ["a.l", "s.c"] and model.a.l is lin and isinstance(model.t.c, m.MXFP4Linear)
+
+
+def test_tensors_in_a_given_buffer():
+    """They lie inside it, or it is refused: their addresses go to the kernels as they are."""
+    shapes = ((3, 100), (100, 3))
+    buffer, made = f8lin.new_mxfp4s(shapes, "cpu")
+    again, same = f8lin.new_mxfp4s(shapes, "cpu", buffer)
+    assert again is buffer and [t._c for t in same] == [t._c for t in made]
+    assert [t.codes.shape for t in same] == [(3, 64), (100, 16)] and same[1].scales.data_ptr() + 1600 == \
+        buffer.data_ptr() + buffer.numel()
+    larger = torch.empty(buffer.numel() + 64, dtype=torch.uint8)
+    assert len(f8lin.new_mxfp4s(shapes, "cpu", larger)[1]) == 2
+    for bad in (buffer[:-1], larger[8:8 + buffer.numel()], larger.view(-1, 16), larger[::2].expand(buffer.numel() // 2 + 32),
+                torch.empty(2 * buffer.numel(), dtype=torch.uint8)[::2], buffer.view(torch.int8), buffer[:0]):
+        with pytest.raises(ValueError):
+            f8lin.new_mxfp4s(shapes, "cpu", bad)
+    assert f8lin.new_mxfp4s(((0, 5), (5, 0)), "cpu", buffer[:0])[1][1].codes.shape == (5, 0)
