@@ -22,13 +22,13 @@
 //     16-column blocks gives every lane eight adjacent columns.
 // Measured (bf16 output, random codes): 8192^3 254 us (4.3 PFLOP/s), 65536 x
 // 4096 x 4096 575 us (3.8), 4096 x 4096 x 65536 462 us (4.8), 4096^3 40 us.
-// Bound by power: the matrix cores fed from registers alone reach 7.1 PFLOP/s
-// on such codes (9.8 on zeros; 6.3 with 32 x 32 x 64 instructions), and the
-// loop keeps them busy for 56% of its cycles at 1.93 GHz of 2.4.  What saved
-// cycles (other slots for reads and copies, waves set apart, skewed starts)
-// gave them back in clock.  256 x 256 with four waves reads least LDS per MFMA:
-// 16 KB per 64 of them.  Short contractions pay for each tile's 128 KB of
-// stores; few tiles for their first loads' latency.
+// The matrix cores are busy for 56% of the cycles at 8192^3 and 45% at 8192 x
+// 14336 x 4096, at 1.93 GHz of 2.4.  A K block of a 256 x 256 tile takes 1.75
+// us, where its 128 MFMAs a wave of 16 cycles take 1.06; what each round of
+// tiles costs besides (first loads, 128 KB of stores a tile) is 8.5 us, 23% of
+// it at K = 4096.  Other spacings of the reads and copies in the K block were
+// within 1%, waves set apart and skewed starts 1-4% slower.  256 x 256 with
+// four waves reads least LDS per MFMA: 16 KB per 64 of them.
 #include <algorithm>
 
 #include "mx_common.h"
@@ -667,16 +667,22 @@ void launch_tiled(const MxBatch &b, int dt, int64_t tiles, hipStream_t stream) {
 }
 
 // Waves per workgroup: eight where few workgroups have a contraction of more
-// than two rounds of loads (1 x 4096 x 14336: 10.9 us, with four 12.9 us; 51 x
-// 4800 x 1600: 8.9 us, with four 6.3 us; 48 x 8192 x 4096: 14.2 us, with four
-// 15.8 us).
+// than two rounds of loads (products back to back, cold weights; 1 x 4096 x
+// 14336 with X quantised inside 10.3 us, with four 11.9 us; 48 x 8192 x 4096
+// 11.0 us, with four 12.4 us; 16 x 4800 x 1600 5.9 us, with four 4.9 us; 51 x
+// 4800 x 1600 6.7 us, with four 6.4 us; 4 x 4096 x 4096, X inside, 7.1 us, with
+// the four that the rule takes 7.6 us).
 int skinny_waves(int64_t grid, int64_t nkb, int MT) { return grid <= 2 * kCUs && nkb >= (MT <= 2 ? 32 : 16) ? 8 : 4; }
 
 // Blocks of 16 columns per workgroup: several share what is read of A, but the
-// time is that of the CU with the most blocks (16 rows of X, quantised first:
-// 9216 x 4096 with three 12.0 us, with two 14.6 us; 14336 x 4096 with four 13.8
-// us, three 17.9 us, two 14.9 us, one 17.4 us; 20000 x 4096 with three 18.6
-// us, four 21.4 us).
+// time is that of the CU with the most blocks (products back to back, cold
+// weights; 16 rows: 9216 x 4096 with three 8.8 us, one 11.3 us, two 11.4 us;
+// 14336 x 4096 with four 10.5 us, two 11.6 us, one 14.0 us, three 14.4 us; 51
+// rows: 8192 x 4096 with two 11.2 us, one 16.3 us).  Several workgroups that
+// fit on a CU at once count as rounds all the same, which short contractions
+// do not bear out: 51 x 4800 x 1600 with the two that the rule takes 6.4 us,
+// with one 6.1 us; 33 x 4800 x 1600 6.1 and 5.9 us; 64 x 6400 x 1600 6.8 and
+// 7.0 us; 16 x 4800 x 1600 4.9 and 5.1 us.
 int skinny_blocks(int N, int MT, int most) {
   int best = 1;
   int64_t least = 0;

@@ -688,7 +688,8 @@ def new_mxfp4(rows: int, cols: int, device="cuda") -> MXFP4Tensor:
 def mxfp4_quantize(x: torch.Tensor, q: Optional[MXFP4Tensor], qt: Optional[MXFP4Tensor] = None, rule="floor",
                    stream=None):
     """x (rows, cols) -> q (rows, cols), blocks along the rows, and / or qt (cols, rows), the transposed tensor with
-    blocks along x's columns.  rule: "floor" (exponent of the largest magnitude) or "ceil" (nothing saturates)."""
+    blocks along x's columns.  rule, with m a block's largest magnitude: "floor" (exponent floor(log2 m) - 2) or "ceil"
+    (ceil(log2(m / 6)): nothing saturates)."""
     if x.dim() != 2:
         raise ValueError("mxfp4_quantize takes a 2-D tensor")
     rows, cols = x.shape

@@ -381,7 +381,8 @@ int f8lin_delayed_update(const f8lin_state *states, int n_states, int32_t *statu
  * scales themselves, at twice the fp8 rate.
  *    m    = max |x| of the block
  *    FLOOR: e - 127 = floor(log2 m) - 2
- *    CEIL : e - 127 = the smallest integer with m <= 6 * 2^(e - 127)
+ *    CEIL : e - 127 = the smallest integer with m <= 6 * 2^(e - 127), that is
+ *           ceil(log2(m / 6)) (not ceil(log2 m) - 2, which others call "ceil")
  *           (both clamped to e >= 0; m = 0 gives e = 0)
  *    code = RNE_sat(x * 2^(127 - e)): ties to the even mantissa, magnitudes
  *           above 6 become 6 (FLOOR rule only), the sign of zero is kept
