@@ -10,6 +10,7 @@ namespace f8lin {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 22;        // per matrix dimension (32-bit tile offsets)
 constexpr int64_t kMaxElems = (int64_t)1 << 40;      // per tensor
+constexpr int64_t kMaxBytes = (int64_t)1 << 60;      // rows times stride (no overflow in a tensor's span)
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 

@@ -184,4 +184,29 @@ hipError_t launch_grad_norm(const f8lin_grad *list, int count, int norm_type, do
 // The scaling alone, with the norm that norm[0] holds.
 hipError_t launch_grad_scale(const f8lin_grad *list, int count, float *norm, float max_norm, hipStream_t stream);
 
+// ---- Layer norm
+struct LayerNormFwd {
+  const void *x;
+  int64_t rows, cols, ldx;
+  const void *weight, *bias;  // (cols) or null
+  int weight_dtype, bias_dtype;
+  float eps;
+  void *y;            // (rows, cols)
+  float *mean, *rstd; // (rows), or both null
+  float *amax;        // max |y| after rounding, or null
+};
+struct LayerNormBwd {
+  const void *dy, *x;
+  int64_t rows, cols, lddy, ldx;
+  const void *weight;
+  int weight_dtype;
+  const float *mean, *rstd;
+  void *dx;     // (rows, cols) of x's type, or null
+  float *part;  // ln_parts(rows, cols) x 2 x cols partial sums of dw and db, or null
+};
+int ln_parts(int64_t rows, int64_t cols);
+hipError_t launch_layer_norm_forward(const LayerNormFwd &a, int x_dtype, int y_dtype, hipStream_t stream);
+hipError_t launch_layer_norm_backward(const LayerNormBwd &a, int x_dtype, int dy_dtype, void *dw, int dw_dtype, void *db,
+                                      int db_dtype, hipStream_t stream);
+
 }  // namespace f8lin

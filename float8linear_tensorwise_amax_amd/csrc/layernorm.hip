@@ -1,0 +1,483 @@
+// Layer norm of the rows of a matrix, forward and backward:
+//   mean = sum(x) / n,  rstd = 1 / sqrt(sum((x - mean)^2) / n + eps),  xhat = (x - mean) * rstd
+//   y  = xhat * w + b
+//   dx = rstd * (g - sum(g) / n - xhat * sum(g * xhat) / n),  g = dy * w
+//   dw = sum over rows of dy * xhat,  db = sum over rows of dy
+//
+// HBM-bound: the forward reads x and writes y once, the backward reads x and
+// dy and writes dx once.  A row stays in the registers of the wave (or of the
+// workgroup) that normalises it, so that the mean, the centred squares and
+// the output are three passes over registers, not memory; only rows of more
+// than kRowMax values are read again.  Everything is computed in binary32
+// from the values as read, and rounded once.  The backward's workgroups keep
+// dw and db of their rows in registers too and leave one partial sum each,
+// which a second launch adds in a fixed order (no atomics: the same bits on
+// every run).
+#include <algorithm>
+
+#include "mx_common.h"
+
+namespace f8lin {
+namespace {
+
+// Sum over the G threads of a row (G = 64: a wave; else the workgroup), the
+// same in all of them.  `slot` keeps consecutive sums apart in the LDS.
+template <int G, int S>
+__device__ __forceinline__ void row_sum(float (&v)[S], float (*red)[S]) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) v[s] += __shfl_xor(v[s], off, 64);
+  }
+  if constexpr (G > 64) {
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) red[threadIdx.x >> 6][s] = v[s];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < G / 64; ++w) t += red[w][s];
+      v[s] = t;
+    }
+  }
+}
+
+// Eight parameters from column c as binary32; `n` of them exist.
+__device__ __forceinline__ void load_param8(const void *p, int dt, int64_t c, int n, float (&v)[8]) {
+  if (dt == F8LIN_FP32) {
+    const Raw8<F8LIN_FP32> r = load_raw8<F8LIN_FP32>(reinterpret_cast<const uint32_t *>(p) + c, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = raw_value<F8LIN_FP32>(r, e);
+  } else if (dt == F8LIN_BF16) {
+    const Raw8<F8LIN_BF16> r = load_raw8<F8LIN_BF16>(reinterpret_cast<const uint16_t *>(p) + c, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = raw_value<F8LIN_BF16>(r, e);
+  } else {
+    const Raw8<F8LIN_FP16> r = load_raw8<F8LIN_FP16>(reinterpret_cast<const uint16_t *>(p) + c, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = raw_value<F8LIN_FP16>(r, e);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void *p, int64_t at, int n, float (&v)[8]) {
+  const Raw8<DT> r = load_raw8<DT>(reinterpret_cast<const typename MxElem<DT>::type *>(p) + at, n);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = raw_value<DT>(r, e);
+}
+
+// Stores the first n of eight values, rounded to DT; returns the largest
+// magnitude stored, as binary32 bits (NaN above all).
+template <int DT>
+__device__ __forceinline__ uint32_t store8(void *p, int64_t at, int n, const float (&v)[8], bool mag) {
+  typedef typename MxElem<DT>::type elem;
+  elem *const y = reinterpret_cast<elem *>(p) + at;
+  uint32_t o[8], m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = f32_to_elem(v[e], DT);
+  if (mag) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) m = max(m, __float_as_uint(elem_f32<DT>(o[e])) & 0x7FFFFFFFu);
+  }
+  if (n >= 8) {
+    if constexpr (DT == F8LIN_FP32) {
+      reinterpret_cast<u32x4_u *>(y)[0] = u32x4{o[0], o[1], o[2], o[3]};
+      reinterpret_cast<u32x4_u *>(y)[1] = u32x4{o[4], o[5], o[6], o[7]};
+    } else {
+      *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) y[e] = (elem)o[e];
+  }
+  return m;
+}
+
+// Folds this wave's largest magnitude into the amax word (the order of the
+// bits is the order of the values).
+__device__ __forceinline__ void fold_amax(float *amax, uint32_t m) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+  uint32_t *const word = reinterpret_cast<uint32_t *>(amax);
+  if ((threadIdx.x & 63) == 0 && m > __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+    __hip_atomic_fetch_max(word, m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ void ln_clear_kernel(float *word) { *word = 0.0f; }
+
+// Rows of up to 8 * C * G values: G threads a row, C chunks of 8 a thread.
+template <int XT, int YT, int G, int C>
+__global__ __launch_bounds__(G > 256 ? G : 256) void ln_forward_kernel(const LayerNormFwd a) {
+  __shared__ float red[2][16][1];
+  constexpr int kRows = G == 64 ? 4 : 1;  // rows of a workgroup
+  const int lane = G == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * kRows + (G == 64 ? threadIdx.x >> 6 : 0);
+  if (G == 64 && row >= a.rows) return;  // (no barrier below for G = 64)
+  const int cols = (int)a.cols;
+  const int64_t at = row * a.ldx;
+  float v[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (c * G + lane);
+    if (col < cols) load8<XT>(a.x, at + col, cols - col, v[c]);
+    else
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = 0.0f;
+  }
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] += v[c][e];
+  row_sum<G, 1>(s, red[0]);
+  const float mean = s[0] / (float)cols;
+  float q[1] = {0.0f};
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int n = cols - 8 * (c * G + lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[c][e] = e < n ? v[c][e] - mean : 0.0f;
+      q[0] = fmaf(v[c][e], v[c][e], q[0]);
+    }
+  }
+  row_sum<G, 1>(q, red[1]);
+  const float rstd = 1.0f / sqrtf(q[0] / (float)cols + a.eps);
+  if (a.mean && lane == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (c * G + lane), n = cols - col;
+    if (n <= 0) break;
+    float w[8], b[8];
+    if (a.weight) load_param8(a.weight, a.weight_dtype, col, n, w);
+    if (a.bias) load_param8(a.bias, a.bias_dtype, col, n, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[c][e] *= rstd;
+      if (a.weight) v[c][e] *= w[e];
+      if (a.bias) v[c][e] += b[e];
+    }
+    m = max(m, store8<YT>(a.y, row * a.cols + col, n, v[c], a.amax != nullptr));
+  }
+  if (a.amax) fold_amax(a.amax, m);
+}
+
+// Rows of any length: the row is read three times (from the L2, where it fits).
+template <int XT, int YT>
+__global__ __launch_bounds__(1024) void ln_forward_wide_kernel(const LayerNormFwd a) {
+  __shared__ float red[2][16][1];
+  const int64_t row = blockIdx.x, at = row * a.ldx, cols = a.cols;
+  float v[8];
+  float s[1] = {0.0f}, q[1] = {0.0f};
+  for (int64_t col = 8 * (int64_t)threadIdx.x; col < cols; col += 8 * 1024) {
+    load8<XT>(a.x, at + col, (int)min((int64_t)8, cols - col), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] += v[e];
+  }
+  row_sum<1024, 1>(s, red[0]);
+  const float mean = s[0] / (float)cols;
+  for (int64_t col = 8 * (int64_t)threadIdx.x; col < cols; col += 8 * 1024) {
+    const int n = (int)min((int64_t)8, cols - col);
+    load8<XT>(a.x, at + col, n, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) q[0] = fmaf(v[e] - mean, v[e] - mean, q[0]);
+  }
+  row_sum<1024, 1>(q, red[1]);
+  const float rstd = 1.0f / sqrtf(q[0] / (float)cols + a.eps);
+  if (a.mean && threadIdx.x == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  uint32_t m = 0;
+  for (int64_t col = 8 * (int64_t)threadIdx.x; col < cols; col += 8 * 1024) {
+    const int n = (int)min((int64_t)8, cols - col);
+    float w[8], b[8];
+    load8<XT>(a.x, at + col, n, v);
+    if (a.weight) load_param8(a.weight, a.weight_dtype, col, n, w);
+    if (a.bias) load_param8(a.bias, a.bias_dtype, col, n, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = (v[e] - mean) * rstd;
+      if (a.weight) v[e] *= w[e];
+      if (a.bias) v[e] += b[e];
+    }
+    m = max(m, store8<YT>(a.y, row * cols + col, n, v, a.amax != nullptr));
+  }
+  if (a.amax) fold_amax(a.amax, m);
+}
+
+// One row's dx; dw and db of the rows of a workgroup in registers.
+template <int XT, int YT, int G, int C>
+__global__ __launch_bounds__(G > 256 ? G : 256) void ln_backward_kernel(const LayerNormBwd a, int64_t rows_each) {
+  constexpr int kRows = G == 64 ? 4 : 1;
+  __shared__ float red[2][16][2];
+  __shared__ float join[G == 64 ? 2 * 8 * 64 * C : 1];
+  const int wave = threadIdx.x >> 6;
+  const int lane = G == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int cols = (int)a.cols;
+  const float inv = 1.0f / (float)cols;
+  const bool params = a.part != nullptr;
+  float w[C][8], dw[C][8], db[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (c * G + lane);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[c][e] = 1.0f, dw[c][e] = 0.0f, db[c][e] = 0.0f;
+    if (a.weight && col < cols) load_param8(a.weight, a.weight_dtype, col, cols - col, w[c]);
+  }
+  const int64_t first = (int64_t)blockIdx.x * rows_each, last = min(a.rows, first + rows_each);
+  int parity = 0;
+  for (int64_t row = first + (G == 64 ? wave : 0); row < last; row += kRows) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float x[C][8], d[C][8];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = 8 * (c * G + lane), n = cols - col;
+      if (n > 0) {
+        load8<XT>(a.x, row * a.ldx + col, n, x[c]);
+        load8<YT>(a.dy, row * a.lddy + col, n, d[c]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[c][e] = d[c][e] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int n = cols - 8 * (c * G + lane);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // (a column past the end: nothing of the row's mean gets in)
+        const float xh = e < n ? (x[c][e] - mean) * rstd : 0.0f, g = d[c][e] * w[c][e];
+        x[c][e] = xh;
+        s[0] += g;
+        s[1] = fmaf(g, xh, s[1]);
+        dw[c][e] = fmaf(d[c][e], xh, dw[c][e]);
+        db[c][e] += d[c][e];
+      }
+    }
+    if (!a.dx) continue;
+    row_sum<G, 2>(s, red[parity]);
+    parity ^= 1;  // (the other buffer: a wave may still read this one)
+    const float m0 = s[0] * inv, m1 = s[1] * inv;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = 8 * (c * G + lane), n = cols - col;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = rstd * (d[c][e] * w[c][e] - m0 - x[c][e] * m1);
+      if (n > 0) store8<XT>(a.dx, row * a.cols + col, n, o, false);
+    }
+  }
+  if (!params) return;
+  float *const part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+  if constexpr (G == 64) {
+    // the four waves' sums, in their order
+    for (int t = 0; t < 4; ++t) {
+      if (wave == t) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float *const j0 = join + (c * 8 + e) * 64 + lane, *const j1 = j0 + 8 * 64 * C;
+            if (t > 0) dw[c][e] += *j0, db[c][e] += *j1;
+            *j0 = dw[c][e], *j1 = db[c][e];
+          }
+      }
+      __syncthreads();
+    }
+    if (wave != 3) return;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = 8 * (c * G + lane), n = cols - col;
+    if (n > 0) {
+      store8<F8LIN_FP32>(part, col, n, dw[c], false);
+      store8<F8LIN_FP32>(part + a.cols, col, n, db[c], false);
+    }
+  }
+}
+
+// Rows of any length, dx alone.
+template <int XT, int YT>
+__global__ __launch_bounds__(1024) void ln_backward_wide_kernel(const LayerNormBwd a) {
+  __shared__ float red[16][2];
+  const int64_t row = blockIdx.x, cols = a.cols;
+  const float mean = a.mean[row], rstd = a.rstd[row], inv = 1.0f / (float)cols;
+  float s[2] = {0.0f, 0.0f}, x[8], d[8], w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+  for (int64_t col = 8 * (int64_t)threadIdx.x; col < cols; col += 8 * 1024) {
+    const int n = (int)min((int64_t)8, cols - col);
+    load8<XT>(a.x, row * a.ldx + col, n, x);
+    load8<YT>(a.dy, row * a.lddy + col, n, d);
+    if (a.weight) load_param8(a.weight, a.weight_dtype, col, n, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e >= n) continue;
+      const float g = d[e] * w[e];
+      s[0] += g;
+      s[1] = fmaf(g, (x[e] - mean) * rstd, s[1]);
+    }
+  }
+  row_sum<1024, 2>(s, red);
+  const float m0 = s[0] * inv, m1 = s[1] * inv;
+  for (int64_t col = 8 * (int64_t)threadIdx.x; col < cols; col += 8 * 1024) {
+    const int n = (int)min((int64_t)8, cols - col);
+    load8<XT>(a.x, row * a.ldx + col, n, x);
+    load8<YT>(a.dy, row * a.lddy + col, n, d);
+    if (a.weight) load_param8(a.weight, a.weight_dtype, col, n, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = rstd * (d[e] * w[e] - m0 - (x[e] - mean) * rstd * m1);
+    store8<XT>(a.dx, row * cols + col, n, x, false);
+  }
+}
+
+// Rows of any length, dw and db of rows_each rows for 2048 columns a workgroup.
+template <int XT, int YT>
+__global__ __launch_bounds__(256) void ln_param_kernel(const LayerNormBwd a, int64_t rows_each, int col_blocks) {
+  const int64_t block = blockIdx.x / col_blocks;
+  const int64_t col = 8 * ((int64_t)(blockIdx.x % col_blocks) * 256 + threadIdx.x);
+  if (col >= a.cols) return;
+  const int n = (int)min((int64_t)8, a.cols - col);
+  float dw[8], db[8], x[8], d[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.0f;
+  const int64_t first = block * rows_each, last = min(a.rows, first + rows_each);
+  for (int64_t row = first; row < last; ++row) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    load8<XT>(a.x, row * a.ldx + col, n, x);
+    load8<YT>(a.dy, row * a.lddy + col, n, d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dw[e] = fmaf(d[e], (x[e] - mean) * rstd, dw[e]);
+      db[e] += d[e];
+    }
+  }
+  float *const part = a.part + block * 2 * a.cols;
+  store8<F8LIN_FP32>(part, col, n, dw, false);
+  store8<F8LIN_FP32>(part + a.cols, col, n, db, false);
+}
+
+// dw[c], db[c] = the sums of `parts` partial sums, in a fixed order: 64 columns
+// a workgroup, 16 waves over the partial sums.
+__global__ __launch_bounds__(1024) void ln_join_kernel(const float *part, int parts, int64_t cols, void *dw, int dw_dtype,
+                                                       void *db, int db_dtype) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t blocks = (cols + 63) / 64;
+  const bool bias = blockIdx.x >= blocks;
+  const int64_t col = (int64_t)(blockIdx.x - (bias ? blocks : 0)) * 64 + lane;
+  void *const out = bias ? db : dw;
+  if (!out) return;
+  const int dt = bias ? db_dtype : dw_dtype;
+  const int64_t ld = 2 * cols;
+  float s = 0.0f;
+  if (col < cols) {
+    const float *p = part + (bias ? cols : 0) + col;
+    for (int i = wave; i < parts; i += 16) s += p[i * ld];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || col >= cols) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += red[i][lane];
+  const uint32_t o = f32_to_elem(s, dt);
+  if (dt == F8LIN_FP32) reinterpret_cast<uint32_t *>(out)[col] = o;
+  else reinterpret_cast<uint16_t *>(out)[col] = (uint16_t)o;
+}
+
+template <int XT, int YT>
+void forward_typed(const LayerNormFwd &a, hipStream_t s) {
+  const unsigned rows = (unsigned)a.rows, quads = (unsigned)((a.rows + 3) / 4);
+  if (a.cols <= 512) ln_forward_kernel<XT, YT, 64, 1><<<quads, 256, 0, s>>>(a);
+  else if (a.cols <= 1024) ln_forward_kernel<XT, YT, 64, 2><<<quads, 256, 0, s>>>(a);
+  else if (a.cols <= 2048) ln_forward_kernel<XT, YT, 64, 4><<<quads, 256, 0, s>>>(a);
+  else if (a.cols <= 4096) ln_forward_kernel<XT, YT, 256, 2><<<rows, 256, 0, s>>>(a);
+  else if (a.cols <= 8192) ln_forward_kernel<XT, YT, 256, 4><<<rows, 256, 0, s>>>(a);
+  else if (a.cols <= 16384) ln_forward_kernel<XT, YT, 1024, 2><<<rows, 1024, 0, s>>>(a);
+  else ln_forward_wide_kernel<XT, YT><<<rows, 1024, 0, s>>>(a);
+}
+
+template <int XT, int YT>
+void backward_typed(const LayerNormBwd &a, hipStream_t s) {
+  const int parts = ln_parts(a.rows, a.cols);
+  const int64_t each = (a.rows + parts - 1) / parts;
+  if (a.cols <= 512) ln_backward_kernel<XT, YT, 64, 1><<<parts, 256, 0, s>>>(a, each);
+  else if (a.cols <= 1024) ln_backward_kernel<XT, YT, 64, 2><<<parts, 256, 0, s>>>(a, each);
+  else if (a.cols <= 2048) ln_backward_kernel<XT, YT, 64, 4><<<parts, 256, 0, s>>>(a, each);
+  else if (a.cols <= 4096) ln_backward_kernel<XT, YT, 256, 2><<<parts, 256, 0, s>>>(a, each);
+  else if (a.cols <= 8192) ln_backward_kernel<XT, YT, 256, 4><<<parts, 256, 0, s>>>(a, each);
+  else if (a.cols <= 16384) ln_backward_kernel<XT, YT, 1024, 2><<<parts, 1024, 0, s>>>(a, each);
+  else {
+    if (a.dx) ln_backward_wide_kernel<XT, YT><<<(unsigned)a.rows, 1024, 0, s>>>(a);
+    const int blocks = (int)((a.cols + 2047) / 2048);
+    if (a.part) ln_param_kernel<XT, YT><<<(unsigned)parts * blocks, 256, 0, s>>>(a, each, blocks);
+  }
+}
+
+template <int XT>
+void forward_by_y(const LayerNormFwd &a, int y_dtype, hipStream_t s) {
+  if constexpr (XT == F8LIN_FP32) {
+    if (y_dtype == F8LIN_BF16) return forward_typed<XT, F8LIN_BF16>(a, s);
+    if (y_dtype == F8LIN_FP16) return forward_typed<XT, F8LIN_FP16>(a, s);
+  }
+  forward_typed<XT, XT>(a, s);
+}
+template <int XT>
+void backward_by_y(const LayerNormBwd &a, int dy_dtype, hipStream_t s) {
+  if constexpr (XT == F8LIN_FP32) {
+    if (dy_dtype == F8LIN_BF16) return backward_typed<XT, F8LIN_BF16>(a, s);
+    if (dy_dtype == F8LIN_FP16) return backward_typed<XT, F8LIN_FP16>(a, s);
+  }
+  backward_typed<XT, XT>(a, s);
+}
+
+}  // namespace
+
+int ln_parts(int64_t rows, int64_t cols) {
+  // rows a partial sum covers at least, so that writing and reading it is not
+  // the larger part
+  const int64_t most = cols <= 2048 ? (rows + 7) / 8 : (rows + 3) / 4;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 512));
+}
+
+hipError_t launch_layer_norm_forward(const LayerNormFwd &a, int x_dtype, int y_dtype, hipStream_t stream) {
+  if (!a.amax && (a.rows == 0 || a.cols == 0)) return hipSuccess;
+  if (a.amax) ln_clear_kernel<<<1, 1, 0, stream>>>(a.amax);
+  if (a.rows > 0 && a.cols > 0) {
+    if (x_dtype == F8LIN_BF16) forward_by_y<F8LIN_BF16>(a, y_dtype, stream);
+    else if (x_dtype == F8LIN_FP16) forward_by_y<F8LIN_FP16>(a, y_dtype, stream);
+    else forward_by_y<F8LIN_FP32>(a, y_dtype, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_layer_norm_backward(const LayerNormBwd &a, int x_dtype, int dy_dtype, void *dw, int dw_dtype, void *db,
+                                      int db_dtype, hipStream_t stream) {
+  if (a.cols == 0 || (a.rows == 0 && !dw && !db)) return hipSuccess;
+  // (no rows: the parameters' gradients are zero)
+  const int parts = a.rows > 0 ? ln_parts(a.rows, a.cols) : 0;
+  if (parts) {
+    if (x_dtype == F8LIN_BF16) backward_by_y<F8LIN_BF16>(a, dy_dtype, stream);
+    else if (x_dtype == F8LIN_FP16) backward_by_y<F8LIN_FP16>(a, dy_dtype, stream);
+    else backward_by_y<F8LIN_FP32>(a, dy_dtype, stream);
+  }
+  if (dw || db)
+    ln_join_kernel<<<2 * (unsigned)((a.cols + 63) / 64), 1024, 0, stream>>>(a.part, parts, a.cols, dw, dw_dtype, db,
+                                                                            db_dtype);
+  return hipGetLastError();
+}
+
+}  // namespace f8lin

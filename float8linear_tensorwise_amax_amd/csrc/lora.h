@@ -1,0 +1,81 @@
+// The low-rank adapters' launchers and the layout of their plan.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace f8lin {
+
+constexpr int kLoraTile = 64;            // rows of a tile
+constexpr int kLoraMaxAdapters = 2047;   // of a plan: 16 waves' counts of each fit the LDS
+constexpr int kLoraMaxRank = 256;
+constexpr int kLoraMagic = 0x4C6F5241;
+
+__host__ __device__ inline int lora_rank_pad(int rank) { return (rank + 15) / 16 * 16; }
+__host__ __device__ inline int64_t lora_max_tiles(int64_t tokens, int64_t adapters) {
+  const int64_t groups = tokens < adapters + 1 ? tokens : adapters + 1;
+  return (tokens + kLoraTile - 1) / kLoraTile + groups;
+}
+// Words before the tiles, and before the tokens' order.
+__host__ __device__ inline int64_t lora_tiles_at(int64_t adapters) { return (4 + adapters + 2 + 3) / 4 * 4; }
+__host__ __device__ inline int64_t lora_order_at(int64_t tokens, int64_t adapters) {
+  return lora_tiles_at(adapters) + 4 * lora_max_tiles(tokens, adapters);
+}
+__host__ __device__ inline int64_t lora_plan_words(int64_t tokens, int64_t adapters) {
+  return lora_order_at(tokens, adapters) + 2 * tokens;
+}
+
+struct LoraDown {
+  const int *plan;
+  int tokens, adapters, rank;
+  const void *x;  // (tokens, cols)
+  int64_t ldx, cols;
+  const void *w;        // (adapters, rank, cols) or (adapters, cols, rank)
+  const float *scales;  // (adapters) or null
+  float *h;             // parts x tokens x lora_rank_pad(rank)
+  int parts;
+};
+struct LoraUp {
+  const int *plan;
+  int tokens, adapters, rank;
+  const float *h;  // as left by down
+  int parts;
+  float *sum;  // if set: the parts' sum, tokens x lora_rank_pad(rank)
+  const void *w;  // (adapters, cols, rank) or (adapters, rank, cols)
+  const void *base;
+  int64_t ldbase, cols;
+  void *y;
+  int64_t ldy;
+};
+struct LoraOuterSide {
+  const void *x;  // (tokens, cols)
+  int64_t ldx, cols;
+  const float *h;  // tokens x lora_rank_pad(rank)
+  void *d;         // (adapters, rank, cols), or (adapters, cols, rank) where d_t; null: not computed
+  int d_t;
+  float *part;  // 2 * chunks x rank x cols
+  int blocks;   // (set by the launch)
+  int64_t join_blocks;
+};
+struct LoraOuter {
+  const int *plan;
+  int tokens, adapters, rank;
+  int chunk, chunks;  // sorted positions a workgroup takes, and how many such
+  LoraOuterSide side[2];
+  int units;  // (set by the launch)
+};
+
+// Parts the columns of a down product are split into, and the positions of an
+// outer product's chunk.
+int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank);
+int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank);
+hipError_t launch_lora_plan(const void *index, bool wide, int tokens, int adapters, int *plan, hipStream_t stream);
+hipError_t launch_lora_down(const LoraDown &a, int dtype, bool w_t, hipStream_t stream);
+hipError_t launch_lora_up(const LoraUp &a, int dtype, bool w_t, hipStream_t stream);
+// a.sum alone: the parts' sum.
+hipError_t launch_lora_sum(const LoraUp &a, hipStream_t stream);
+hipError_t launch_lora_outer(const LoraOuter &a, int dtype, hipStream_t stream);
+
+}  // namespace f8lin

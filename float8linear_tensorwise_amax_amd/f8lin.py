@@ -851,3 +851,246 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor
           _ptr(norm, torch.float32), 1 if norm_given else 0, _ptr(ws), _nbytes(ws))
     written = list(grads if outs is None else outs)
     torch.autograd.graph.increment_version(written if norm_given else written + [norm])
+
+
+# -------------------------------------------------------------- layer norm
+
+class LayerNormFwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("x", _vp), ("ldx", _i64), ("weight", _vp), ("bias", _vp), ("y", _vp),
+                ("mean", _vp), ("rstd", _vp), ("y_amax", _vp), ("x_dtype", _int), ("weight_dtype", _int),
+                ("bias_dtype", _int), ("y_dtype", _int), ("eps", ctypes.c_float)]
+
+
+class LayerNormBwdArgs(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("dy", _vp), ("x", _vp), ("lddy", _i64), ("ldx", _i64),
+                ("weight", _vp), ("mean", _vp), ("rstd", _vp), ("dx", _vp), ("dweight", _vp), ("dbias", _vp),
+                ("dy_dtype", _int), ("x_dtype", _int), ("weight_dtype", _int), ("dweight_dtype", _int),
+                ("dbias_dtype", _int), ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
+
+
+_LN_FWD = struct.Struct("@10q4if4x")
+_LN_BWD = struct.Struct("@12q5i4x2q")
+for _fmt, _cls in ((_LN_FWD, LayerNormFwdArgs), (_LN_BWD, LayerNormBwdArgs)):
+    assert _fmt.size == ctypes.sizeof(_cls)
+
+_lib.f8lin_layer_norm_forward.argtypes = [_vp, _vp]
+_lib.f8lin_layer_norm_backward.argtypes = [_vp, _vp]
+_lib.f8lin_layer_norm_workspace_bytes.argtypes = [_i64, _i64]
+_lib.f8lin_layer_norm_workspace_bytes.restype = ctypes.c_size_t
+for _name in ("f8lin_layer_norm_forward", "f8lin_layer_norm_backward"):
+    getattr(_lib, _name).restype = _int
+
+
+def _f32(t: Optional[torch.Tensor], n: int, what: str, device: torch.device) -> int:
+    """Pointer of a contiguous float32 tensor of n elements on `device` (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.device != device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"f8lin: {what} must be a contiguous float32 tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _vector(t: Optional[torch.Tensor], n: int, what: str, device: torch.device):
+    """(pointer, dtype code) of a contiguous bf16 / fp16 / fp32 vector of n elements on `device` (0, 0 for None)."""
+    if t is None:
+        return 0, 0
+    if t.numel() != n:
+        raise ValueError(f"f8lin: {what} must have {n} elements, got {tuple(t.shape)}")
+    return _dense(t, what, device), _DTYPE[t.dtype]
+
+
+def _pair_types(x: torch.Tensor, y: torch.Tensor, what: str):
+    if y.dtype != x.dtype and x.dtype != torch.float32:
+        raise TypeError(f"f8lin: {what} must be {x.dtype} like x (only a float32 x allows another type), got {y.dtype}")
+
+
+def layer_norm_forward(x, y, weight=None, bias=None, eps: float = 1e-5, mean=None, rstd=None, y_amax=None, stream=None):
+    """y (rows, cols) = the layer norm of each row of x, times weight plus bias (each (cols) or None).  mean and rstd:
+    float32 (rows) each, for the backward, or both None.  y_amax: optional float32 tensor that receives max |y|."""
+    if x.dim() != 2 or y.shape != x.shape:
+        raise ValueError("layer_norm_forward: x and y must be 2-D tensors of one shape")
+    rows, cols = x.shape
+    px, ldx = _dense_ld(x, "x")
+    dev = x.device
+    py = _dense(y, "y", dev)
+    if y.dtype is not x.dtype:
+        _pair_types(x, y, "y")
+    pw, wt = _vector(weight, cols, "weight", dev)
+    pb, bt = _vector(bias, cols, "bias", dev)
+    a = _LN_FWD.pack(rows, cols, px, ldx, pw, pb, py, _f32(mean, rows, "mean", dev), _f32(rstd, rows, "rstd", dev),
+                     _f32(y_amax, 1, "y_amax", dev), _DTYPE[x.dtype], wt, bt, _DTYPE[y.dtype], eps)
+    _call(_lib.f8lin_layer_norm_forward, dev, stream, a)
+
+
+def layer_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_lib.f8lin_layer_norm_workspace_bytes(rows, cols))
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, ws=None, stream=None):
+    """dx (rows, cols; x's type), dweight (cols) and dbias (cols) -- each may be None -- from dy, x, weight (or None) and
+    the forward's mean and rstd.  ws: layer_norm_workspace_bytes(rows, cols) bytes, for dweight or dbias."""
+    if x.dim() != 2 or dy.shape != x.shape or (dx is not None and dx.shape != x.shape):
+        raise ValueError("layer_norm_backward: dy, x and dx must be 2-D tensors of one shape")
+    rows, cols = x.shape
+    px, ldx = _dense_ld(x, "x")
+    dev = x.device
+    pdy, lddy = _dense_ld(dy, "dy", dev)
+    _pair_types(x, dy, "dy")
+    pdx = 0 if dx is None else _dense(dx, "dx", dev)
+    if dx is not None and dx.dtype != x.dtype:
+        raise TypeError(f"f8lin: dx must be {x.dtype} like x, got {dx.dtype}")
+    pw, wt = _vector(weight, cols, "weight", dev)
+    pdw, dwt = _vector(dweight, cols, "dweight", dev)
+    pdb, dbt = _vector(dbias, cols, "dbias", dev)
+    _same_device(ws, "ws", dev)
+    a = _LN_BWD.pack(rows, cols, pdy, px, lddy, ldx, pw, _f32(mean, rows, "mean", dev), _f32(rstd, rows, "rstd", dev),
+                     pdx, pdw, pdb, _DTYPE[dy.dtype], _DTYPE[x.dtype], wt, dwt, dbt, _ptr(ws) or 0, _nbytes(ws))
+    _call(_lib.f8lin_layer_norm_backward, dev, stream, a)
+
+
+# ------------------------------------------------------- low-rank adapters
+
+LORA_MAX_ADAPTERS = 2047
+LORA_MAX_RANK = 256
+
+
+class LoraFwdArgs(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("K", _i64), ("N", _i64), ("x", _vp), ("a", _vp), ("b", _vp), ("base", _vp),
+                ("ldx", _i64), ("ldbase", _i64), ("y", _vp), ("scales", _vp), ("plan", _vp), ("h", _vp), ("ws", _vp),
+                ("ws_bytes", ctypes.c_size_t), ("rank", _int), ("adapters", _int), ("dtype", _int)]
+
+
+class LoraBwdArgs(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("K", _i64), ("N", _i64), ("dy", _vp), ("x", _vp), ("a", _vp), ("b", _vp),
+                ("lddy", _i64), ("ldx", _i64), ("scales", _vp), ("h", _vp), ("plan", _vp), ("dx", _vp), ("da", _vp),
+                ("db", _vp), ("ws", _vp), ("ws_bytes", ctypes.c_size_t), ("rank", _int), ("adapters", _int),
+                ("dtype", _int)]
+
+
+_LORA_FWD = struct.Struct("@15q3i4x")
+_LORA_BWD = struct.Struct("@17q3i4x")
+for _fmt, _cls in ((_LORA_FWD, LoraFwdArgs), (_LORA_BWD, LoraBwdArgs)):
+    assert _fmt.size == ctypes.sizeof(_cls)
+
+_lib.f8lin_lora_plan_bytes.argtypes = [_i64, _int]
+_lib.f8lin_lora_plan.argtypes = [_vp, _int, _i64, _int, _vp, ctypes.c_size_t, _vp]
+_lib.f8lin_lora_forward.argtypes = [_vp, _vp]
+_lib.f8lin_lora_backward.argtypes = [_vp, _vp]
+for _name in ("f8lin_lora_forward_workspace_bytes", "f8lin_lora_backward_workspace_bytes"):
+    getattr(_lib, _name).argtypes = [_i64, _i64, _i64, _int, _int]
+    getattr(_lib, _name).restype = ctypes.c_size_t
+_lib.f8lin_lora_plan_bytes.restype = ctypes.c_size_t
+for _name in ("f8lin_lora_plan", "f8lin_lora_forward", "f8lin_lora_backward"):
+    getattr(_lib, _name).restype = _int
+
+
+class LoraPlan:
+    """The buffer of a plan (lora_plan writes it) for a batch of `tokens` tokens over `adapters` adapters."""
+
+    __slots__ = ("tokens", "adapters", "device", "buffer")
+
+    def __init__(self, tokens: int, adapters: int, device="cuda", buffer: Optional[torch.Tensor] = None):
+        """buffer: an int32 tensor to use instead of a new one."""
+        if not 1 <= adapters <= LORA_MAX_ADAPTERS:
+            raise ValueError(f"f8lin: a plan holds 1 to {LORA_MAX_ADAPTERS} adapters, got {adapters}")
+        need = int(_lib.f8lin_lora_plan_bytes(tokens, adapters))
+        if need == 0:
+            raise ValueError(f"f8lin: a plan holds 0 to 2^22 tokens, got {tokens}")
+        if buffer is None:
+            buffer = torch.empty(need // 4, dtype=torch.int32, device=device)
+        elif buffer.dtype != torch.int32 or not buffer.is_contiguous() or buffer.numel() < need // 4 or not buffer.is_cuda:
+            raise ValueError(f"f8lin: this plan needs a contiguous int32 GPU buffer of {need // 4} elements")
+        self.tokens, self.adapters, self.device, self.buffer = tokens, adapters, buffer.device, buffer
+
+
+def lora_plan(index: torch.Tensor, plan: LoraPlan, stream=None):
+    """Writes the plan of a batch: index (tokens) int32 or int64 holds each token's adapter, a value outside
+    0 .. adapters - 1 none."""
+    if index.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"f8lin: index must be int32 or int64, got {index.dtype}")
+    if index.numel() != plan.tokens:
+        raise ValueError(f"f8lin: the plan is of {plan.tokens} tokens, got {index.numel()} indices")
+    p = _ptr(index) or 0
+    if index.device != plan.device:
+        raise ValueError(f"f8lin: index is on {index.device}, the plan on {plan.device}")
+    _call(_lib.f8lin_lora_plan, plan.device, stream, p, index.element_size(), plan.tokens, plan.adapters,
+          plan.buffer.data_ptr(), 4 * plan.buffer.numel())
+    torch.autograd.graph.increment_version(plan.buffer)
+
+
+def lora_forward_workspace_bytes(T: int, K: int, N: int, rank: int, adapters: int) -> int:
+    return int(_lib.f8lin_lora_forward_workspace_bytes(T, K, N, rank, adapters))
+
+
+def lora_backward_workspace_bytes(T: int, K: int, N: int, rank: int, adapters: int) -> int:
+    return int(_lib.f8lin_lora_backward_workspace_bytes(T, K, N, rank, adapters))
+
+
+def lora_h_elements(T: int, rank: int) -> int:
+    """Float32 elements of the inner products that lora_forward keeps for lora_backward."""
+    return T * (-(-rank // 16) * 16)
+
+
+def _lora_sizes(x_rows: int, K: int, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan):
+    """(rank, N) of adapters a (adapters, rank, K), b (adapters, N, rank) beside the plan."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != plan.adapters or b.shape[0] != plan.adapters or \
+            a.shape[2] != K or b.shape[2] != a.shape[1]:
+        raise ValueError(f"f8lin: adapters must be ({plan.adapters}, rank, {K}) and ({plan.adapters}, N, rank), got "
+                         f"{tuple(a.shape)} and {tuple(b.shape)}")
+    if not 1 <= a.shape[1] <= LORA_MAX_RANK:
+        raise ValueError(f"f8lin: the rank must be 1 to {LORA_MAX_RANK}, got {a.shape[1]}")
+    if x_rows != plan.tokens:
+        raise ValueError(f"f8lin: the plan is of {plan.tokens} tokens, got {x_rows} rows")
+    return a.shape[1], b.shape[1]
+
+
+def _one_dtype(dtype: torch.dtype, **tensors):
+    for what, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"f8lin: {what} must be {dtype} like x, got {t.dtype}")
+
+
+def lora_forward(base, x, a, b, scales, plan: LoraPlan, y, h=None, ws=None, stream=None):
+    """y (T, N) = base (T, N; None: 0) + what each token's adapter adds: scales[i] * (x[t] . a[i]^T) . b[i]^T.
+    scales: float32 (adapters), or None for 1.  h: optional float32 tensor of lora_h_elements(T, rank) that receives the
+    inner products for lora_backward.  ws: lora_forward_workspace_bytes(T, K, N, rank, adapters) bytes.  y may be base."""
+    T, K = x.shape
+    rank, N = _lora_sizes(T, K, a, b, plan)
+    if tuple(y.shape) != (T, N) or (base is not None and base.shape != y.shape):
+        raise ValueError("lora_forward: shape mismatch")
+    px, ldx = _dense_ld(x, "x")
+    dev = x.device
+    _one_dtype(x.dtype, a=a, b=b, base=base, y=y)
+    pbase, ldbase = (0, 0) if base is None else _dense_ld(base, "base", dev)
+    if plan.device != dev:
+        raise ValueError(f"f8lin: the plan is on {plan.device}, expected {dev}")
+    _same_device(ws, "ws", dev)
+    args = _LORA_FWD.pack(T, K, N, px, _dense(a, "a", dev), _dense(b, "b", dev), pbase, ldx, ldbase, _dense(y, "y", dev),
+                          _f32(scales, plan.adapters, "scales", dev), plan.buffer.data_ptr(),
+                          0 if h is None else _f32(h, lora_h_elements(T, rank), "h", dev), _ptr(ws) or 0, _nbytes(ws),
+                          rank, plan.adapters, _DTYPE[x.dtype])
+    _call(_lib.f8lin_lora_forward, dev, stream, args)
+
+
+def lora_backward(dy, x, a, b, scales, plan: LoraPlan, h, dx=None, da=None, db=None, ws=None, stream=None):
+    """dx (T, K), da like a and db like b -- each may be None -- of lora_forward; h as it left it (needed for db).
+    ws: lora_backward_workspace_bytes(T, K, N, rank, adapters) bytes."""
+    T, K = x.shape
+    rank, N = _lora_sizes(T, K, a, b, plan)
+    if tuple(dy.shape) != (T, N) or (dx is not None and dx.shape != x.shape) or \
+            (da is not None and da.shape != a.shape) or (db is not None and db.shape != b.shape):
+        raise ValueError("lora_backward: shape mismatch")
+    px, ldx = _dense_ld(x, "x")
+    dev = x.device
+    _one_dtype(x.dtype, dy=dy, a=a, b=b, dx=dx, da=da, db=db)
+    pdy, lddy = _dense_ld(dy, "dy", dev)
+    if plan.device != dev:
+        raise ValueError(f"f8lin: the plan is on {plan.device}, expected {dev}")
+    _same_device(ws, "ws", dev)
+    opt = lambda t, what: 0 if t is None else _dense(t, what, dev)  # noqa: E731
+    args = _LORA_BWD.pack(T, K, N, pdy, px, _dense(a, "a", dev), _dense(b, "b", dev), lddy, ldx,
+                          _f32(scales, plan.adapters, "scales", dev),
+                          0 if h is None else _f32(h, lora_h_elements(T, rank), "h", dev), plan.buffer.data_ptr(),
+                          opt(dx, "dx"), opt(da, "da"), opt(db, "db"), _ptr(ws) or 0, _nbytes(ws), rank, plan.adapters,
+                          _DTYPE[x.dtype])
+    _call(_lib.f8lin_lora_backward, dev, stream, args)

@@ -31,7 +31,14 @@ fp16 or fp32.  freeze_mxfp4 keeps only the 4-bit weights, for serving.
 Gradient clipping.  clip_grad_norm_ (in place), clip_grads (into new tensors)
 and get_grad_norm work on a list of gradients after backward.
 
-Both can be captured into a HIP graph, a whole step under autograd too.  As
+Layer norm.  layer_norm / LayerNorm / convert_layer_norm: the norm in front of
+a block's linears, forward and backward.
+
+Low-rank adapters.  lora_add / LoraLinear / convert_to_lora put adapters
+beside a shared projection (any of the linears above); a batch mixes requests
+of many adapters, and a LoraBatch says which token uses which.
+
+All of them can be captured into a HIP graph, a whole step under autograd too.  As
 with any layer, let no eager graph of the same parameters live on into the
 capture of a backward: its gradient nodes belong to another stream.
 
@@ -605,3 +612,275 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
         if f is not g:
             g.copy_(f)
     return norm
+
+
+# -------------------------------------------------------------- layer norm
+
+def _vector_of(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return t if t is None or t.is_contiguous() else t.contiguous()
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, out_dtype):
+        rows, cols = x.shape
+        dev = x.device
+        weight = _vector_of(weight)
+        y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
+        f8lin.layer_norm_forward(x, y, weight, _vector_of(bias), eps, stats[0], stats[1])
+        ctx.save_for_backward(x, weight, stats)
+        ctx.b_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, stats = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        rows, cols = x.shape
+        dev = x.device
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=dev) if need_x else None
+        dw = torch.empty((cols,), dtype=weight.dtype, device=dev) if need_w else None
+        db = torch.empty((cols,), dtype=ctx.b_dtype, device=dev) if need_b else None
+        ws = None
+        if need_w or need_b:
+            ws = torch.empty(f8lin.layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        f8lin.layer_norm_backward(_rows(dy), x, weight, stats[0], stats[1], dx, dw, db, ws)
+        return dx, dw, db, None, None
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """The layer norm of x over its last dimension, times weight plus bias (vectors of that length, of any of the three
+    types, or None): (x - mean) / sqrt(var + eps) * weight + bias, computed in float32 and rounded once.
+
+    The result has x's dtype, or with a float32 x the given out_dtype (bfloat16 for the linears behind a float32
+    residual stream, say).  Differentiable once in x, weight and bias; forward-mode derivatives are refused
+    (NotImplementedError)."""
+    if not x.is_cuda:
+        raise RuntimeError("layer_norm runs on the GPU only (libf8lin has no CPU path)")
+    if x.dim() < 1:
+        raise ValueError("layer_norm needs a dimension to normalise over")
+    cols = x.shape[-1]
+    for what, t in (("weight", weight), ("bias", bias)):
+        if t is not None and tuple(t.shape) != (cols,):
+            raise ValueError(f"{what} must have shape ({cols},), got {tuple(t.shape)}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    dtype = x.dtype if out_dtype is None else out_dtype
+    if dtype != x.dtype and (x.dtype != torch.float32 or dtype not in f8lin._DTYPE):
+        raise TypeError(f"out_dtype must be {x.dtype} (only a float32 x allows another type), got {dtype}")
+    # (an empty last dimension leaves reshape nothing to infer the rows from)
+    x2 = _rows(x) if x.numel() else x.reshape(x.shape[:-1].numel(), cols)
+    if torch.is_grad_enabled():
+        y = _LayerNormFn.apply(x2, weight, bias, eps, dtype)
+    else:
+        _refuse_tangents("layer_norm", x, weight, bias)
+        y = torch.empty(x2.shape, dtype=dtype, device=x.device)
+        f8lin.layer_norm_forward(x2, y, _vector_of(weight), _vector_of(bias), eps)
+    return y if x.dim() == 2 else y.reshape(x.shape)
+
+
+class LayerNorm(nn.Module):
+    """nn.LayerNorm on this library's kernels (layer_norm).  weight and bias: True (new), False (none), or existing
+    tensors / Parameters to share."""
+
+    def __init__(self, normalized_shape, eps: float = 1e-5, weight=True, bias=True, device=None, dtype=torch.float32):
+        super().__init__()
+        shape = (normalized_shape,) if isinstance(normalized_shape, int) else tuple(normalized_shape)
+        if not shape:
+            raise ValueError("LayerNorm needs a shape to normalise over")
+        self.normalized_shape, self.eps = shape, eps
+        for name, given, fill in (("weight", weight, 1.0), ("bias", bias, 0.0)):
+            if isinstance(given, torch.Tensor):
+                if tuple(given.shape) != shape:
+                    raise ValueError(f"{name} must have shape {shape}")
+                given = given if isinstance(given, nn.Parameter) else nn.Parameter(given)
+            elif given:
+                given = nn.Parameter(torch.full(shape, fill, device=device, dtype=dtype))
+            else:
+                given = None
+            self.register_parameter(name, given)
+
+    def forward(self, x: torch.Tensor, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+        n = len(self.normalized_shape)
+        if tuple(x.shape[-n:]) != self.normalized_shape:
+            raise ValueError(f"expected last dimensions {self.normalized_shape}, got {tuple(x.shape)}")
+        if n == 1:
+            return layer_norm(x, self.weight, self.bias, self.eps, out_dtype)
+        flat = [None if p is None else p.reshape(-1) for p in (self.weight, self.bias)]
+        lead = x.shape[:-n]
+        return layer_norm(x.reshape(lead.numel(), -1) if x.numel() else x.reshape(lead.numel(), self._numel()), *flat,
+                          self.eps, out_dtype).reshape(x.shape)
+
+    def _numel(self) -> int:
+        return torch.Size(self.normalized_shape).numel()
+
+    def extra_repr(self):
+        return (f"{self.normalized_shape}, eps={self.eps}, weight={self.weight is not None}, "
+                f"bias={self.bias is not None}")
+
+
+def _swap(module: nn.Module, accepts, make, module_filter_fn) -> nn.Module:
+    """Replaces every child that `accepts` and the filter take by make(child); a child that stands in several places is
+    made once.  What lies inside a LoraLinear is left as it is."""
+    made: Dict[nn.Module, nn.Module] = {}
+    for prefix, parent in list(module.named_modules()):
+        if isinstance(parent, LoraLinear):
+            continue
+        # (not named_children, which names a child once)
+        for name, child in list(parent._modules.items()):
+            fqn = f"{prefix}.{name}" if prefix else name
+            if child is not None and accepts(child) and (module_filter_fn is None or module_filter_fn(fqn, child)):
+                if child not in made:
+                    made[child] = make(child)
+                setattr(parent, name, made[child])
+    return module
+
+
+def convert_layer_norm(module: nn.Module, module_filter_fn=None) -> nn.Module:
+    """Replaces every nn.LayerNorm (that module_filter_fn(fqn, module) accepts, if given) by a LayerNorm sharing its
+    weight and bias Parameters; one that stands in several places becomes one in all of them.  Returns the module."""
+    if type(module) is nn.LayerNorm:
+        raise ValueError("convert the parent module, not a bare nn.LayerNorm")
+    return _swap(module, lambda m: type(m) is nn.LayerNorm,
+                 lambda m: LayerNorm(m.normalized_shape, m.eps, m.weight if m.weight is not None else False,
+                                     m.bias if m.bias is not None else False), module_filter_fn)
+
+
+# ------------------------------------------------------- low-rank adapters
+
+class LoraBatch:
+    """Which token of a batch uses which adapter, sorted on the GPU once for all the projections that the batch passes.
+
+    index: int32 or int64 tensor on the GPU, one entry a token (any shape; the tokens in its order); a value outside
+    0 .. adapters - 1 means no adapter.  Tokens may come in any order."""
+
+    def __init__(self, index: torch.Tensor, adapters: int):
+        if not index.is_cuda:
+            raise RuntimeError("LoraBatch runs on the GPU only (libf8lin has no CPU path)")
+        self.plan = f8lin.LoraPlan(index.numel(), adapters, index.device)
+        f8lin.lora_plan(index if index.is_contiguous() else index.contiguous(), self.plan)
+
+    tokens = property(lambda self: self.plan.tokens)
+    adapters = property(lambda self: self.plan.adapters)
+
+    def update(self, index: torch.Tensor) -> "LoraBatch":
+        """Another batch of as many tokens, in place (in a captured graph: from what index holds at the replay)."""
+        f8lin.lora_plan(index if index.is_contiguous() else index.contiguous(), self.plan)
+        return self
+
+
+def _lora_forward(base, x, a, b, plan, scales, keep):
+    T, K = x.shape
+    rank, N = f8lin._lora_sizes(T, K, a, b, plan)
+    dev = x.device
+    y = torch.empty((T, N), dtype=x.dtype, device=dev)
+    h = torch.empty(f8lin.lora_h_elements(T, rank), dtype=torch.float32, device=dev) if keep else None
+    ws = torch.empty(f8lin.lora_forward_workspace_bytes(T, K, N, rank, plan.adapters), dtype=torch.uint8, device=dev)
+    f8lin.lora_forward(base, x, a, b, scales, plan, y, h, ws)
+    return y, h
+
+
+class _LoraAddFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, base, x, a, b, plan, scales):
+        a, b = a.contiguous(), b.contiguous()
+        y, h = _lora_forward(base, x, a, b, plan, scales, ctx.needs_input_grad[3])
+        ctx.save_for_backward(x, a, b, h, plan.buffer, scales)
+        ctx.sizes = plan.tokens, plan.adapters
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        need_base, need_x, need_a, need_b = ctx.needs_input_grad[:4]
+        dx = da = db = None
+        if need_x or need_a or need_b:
+            x, a, b, h, buffer, scales = ctx.saved_tensors
+            plan = f8lin.LoraPlan(*ctx.sizes, buffer=buffer)
+            (T, K), (adapters, N, rank) = x.shape, b.shape
+            dx = torch.empty((T, K), dtype=x.dtype, device=x.device) if need_x else None
+            da = torch.empty_like(a) if need_a else None
+            db = torch.empty_like(b) if need_b else None
+            ws = torch.empty(f8lin.lora_backward_workspace_bytes(T, K, N, rank, adapters), dtype=torch.uint8,
+                             device=x.device)
+            f8lin.lora_backward(_rows(dy), x, a, b, scales, plan, h, dx, da, db, ws)
+        return dy if need_base else None, dx, da, db, None, None
+
+
+def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, batch: LoraBatch,
+             scales: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A shared projection's output with each token's low-rank adapter added:
+        y[t] = base[t] + scales[i] * (x[t] . a[i]^T) . b[i]^T     for a token t of adapter i, base[t] without one.
+
+    base (..., N) and x (..., K) with batch.tokens tokens; a (adapters, rank, K), b (adapters, N, rank); all of one
+    dtype.  scales: float32 (adapters) or None (1), outside the graph.  Differentiable once in base, x, a and b (an
+    adapter that no token uses gets a gradient of zero); forward-mode derivatives are refused (NotImplementedError)."""
+    if not x.is_cuda:
+        raise RuntimeError("lora_add runs on the GPU only (libf8lin has no CPU path)")
+    if x.dim() < 1 or base.shape[:-1] != x.shape[:-1] or b.dim() != 3 or base.shape[-1] != b.shape[1]:
+        raise ValueError(f"base must be x's tokens by the adapters' N, got {tuple(base.shape)} beside {tuple(x.shape)} "
+                         f"and {tuple(b.shape)}")
+    if scales is not None and scales.requires_grad:
+        raise ValueError("scales take no part in the graph: detach them")
+    lead = x.shape[:-1]
+    flat = lambda t: _rows(t) if t.numel() else t.reshape(lead.numel(), t.shape[-1])  # noqa: E731
+    base2, x2 = flat(base), flat(x)
+    if torch.is_grad_enabled():
+        y = _LoraAddFn.apply(base2, x2, a, b, batch.plan, scales)
+    else:
+        _refuse_tangents("lora_add", base, x, a, b)
+        y = _lora_forward(base2, x2, a.contiguous(), b.contiguous(), batch.plan, scales, False)[0]
+    return y if base.dim() == 2 else y.reshape(base.shape)
+
+
+class LoraLinear(nn.Module):
+    """A linear layer with low-rank adapters beside it: base(x), then lora_add for the batch set in `batch` (a
+    LoraBatch; None: the base alone).  base: nn.Linear, Float8Linear or MXFP4Linear (also a frozen one, for serving).
+    lora_a starts random and lora_b at zero, so that a new adapter adds nothing.  They are kept in `dtype` (default: the
+    weight's, bfloat16 beside a frozen one) and used in the base output's."""
+
+    def __init__(self, base: nn.Module, adapters: int, rank: int, scale: float = 1.0, dtype: Optional[torch.dtype] = None):
+        super().__init__()
+        if not 1 <= adapters <= f8lin.LORA_MAX_ADAPTERS or not 1 <= rank <= f8lin.LORA_MAX_RANK:
+            raise ValueError(f"adapters must be 1 to {f8lin.LORA_MAX_ADAPTERS} and rank 1 to {f8lin.LORA_MAX_RANK}, got "
+                             f"{adapters} and {rank}")
+        self.base, self.adapters, self.rank = base, adapters, rank
+        self.in_features, self.out_features = base.in_features, base.out_features
+        weight = base.weight if base.weight is not None else base.weight_codes
+        if dtype is None:
+            dtype = weight.dtype if weight.is_floating_point() else torch.bfloat16
+        a = torch.empty((adapters, rank, self.in_features), dtype=dtype, device=weight.device)
+        self.lora_a = nn.Parameter(a.normal_(std=self.in_features ** -0.5))
+        self.lora_b = nn.Parameter(torch.zeros((adapters, self.out_features, rank), dtype=dtype, device=weight.device))
+        self.register_buffer("lora_scales", torch.full((adapters,), scale, dtype=torch.float32, device=weight.device))
+        self.batch: Optional[LoraBatch] = None
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        y = self.base(x)
+        if self.batch is None:
+            return y
+        return lora_add(y, x.to(y.dtype), self.lora_a.to(y.dtype), self.lora_b.to(y.dtype), self.batch, self.lora_scales)
+
+    def extra_repr(self):
+        return f"adapters={self.adapters}, rank={self.rank}"
+
+
+def convert_to_lora(module: nn.Module, adapters: int, rank: int, scale: float = 1.0, module_filter_fn=None) -> nn.Module:
+    """Puts adapters beside every nn.Linear, Float8Linear and MXFP4Linear (that module_filter_fn(fqn, module) accepts, if
+    given) and takes that layer's own parameters out of training.  A linear that stands in several places has one set of
+    adapters.  Returns the module."""
+    kinds = (nn.Linear, Float8Linear, MXFP4Linear)
+    if type(module) in kinds:
+        raise ValueError("convert the parent module, not a bare linear")
+    return _swap(module, lambda m: type(m) in kinds,
+                 lambda m: LoraLinear(m.requires_grad_(False), adapters, rank, scale), module_filter_fn)
+
+
+def set_lora_batch(module: nn.Module, batch: Optional[LoraBatch]) -> None:
+    """The batch that every LoraLinear of the module serves next (None: the bases alone)."""
+    for m in module.modules():
+        if isinstance(m, LoraLinear):
+            m.batch = batch

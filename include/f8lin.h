@@ -517,6 +517,109 @@ size_t f8lin_grad_workspace_bytes(void);
 int f8lin_grad_clip(const f8lin_grad *list, int count, int norm_type, float max_norm, float *norm, int norm_given,
                     void *ws, size_t ws_bytes, void *stream);
 
+/* ============================================================= layer norm
+ * Of every row x of n = cols values, in binary32 from the values as read,
+ * rounded once:
+ *   mean = sum(x) / n,  rstd = 1 / sqrt(sum((x - mean)^2) / n + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ * Any sizes, x with a row stride.  weight and bias may be NULL (1 and 0) and
+ * are of any type; y has x's type, or with fp32 x any.  mean and rstd, (rows)
+ * each, are what the backward needs (both NULL: not kept).  y_amax, if set,
+ * receives max |y| of the rounded values (NaN above all, 0 for no element):
+ * for bf16 y what a following f8lin_forward with x_amax_given takes.
+ * eps >= 0.  A row with an Inf or NaN is NaN as a whole, and no other row.
+ * Errors as above: EINVAL, ESHAPE, EALIGN, nothing launched on error. */
+typedef struct {
+  int64_t rows, cols;
+  const void *x; /* (rows, cols) */
+  int64_t ldx;   /* elements; 0: cols */
+  const void *weight, *bias; /* (cols) or NULL */
+  void *y;                   /* (rows, cols) */
+  float *mean, *rstd, *y_amax;
+  int x_dtype, weight_dtype, bias_dtype, y_dtype;
+  float eps;
+} f8lin_layer_norm_fwd_args;
+int f8lin_layer_norm_forward(const f8lin_layer_norm_fwd_args *args, void *stream);
+
+/* Its backward, with g = dy * weight and xhat = (x - mean) * rstd:
+ *   dx = rstd * (g - sum(g) / n - xhat * sum(g * xhat) / n)   of x's type
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * each may be NULL.  Sums in fp32 in a fixed order.  dweight or dbias need ws:
+ * f8lin_layer_norm_workspace_bytes(rows, cols) bytes, 16-byte aligned, no
+ * initialisation needed, one for each call that may overlap another. */
+typedef struct {
+  int64_t rows, cols;
+  const void *dy, *x;
+  int64_t lddy, ldx; /* elements; 0: cols */
+  const void *weight;
+  const float *mean, *rstd;
+  void *dx, *dweight, *dbias;
+  int dy_dtype, x_dtype, weight_dtype, dweight_dtype, dbias_dtype;
+  float *ws;
+  size_t ws_bytes;
+} f8lin_layer_norm_bwd_args;
+int f8lin_layer_norm_backward(const f8lin_layer_norm_bwd_args *args, void *stream);
+size_t f8lin_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* ====================================================== low-rank adapters
+ * Beside a shared projection, whatever computed it: its output `base` (T, N)
+ * plus what each token's own adapter adds.  Token t of adapter i
+ * (0 <= i < adapters, 1 .. 2047 of them, of rank 1 .. 256) gets
+ *   y[t] = base[t] + scales[i] * (x[t] . A_i^T) . B_i^T
+ * A (adapters, rank, K), B (adapters, N, rank), contiguous, of x's type, as
+ * are base and y; scales fp32 or NULL (1).  The inner product of a token is
+ * kept in fp32.  A token without an adapter gets base[t] and nothing is read
+ * of its x; base NULL: 0.
+ *
+ * The plan says which tokens an adapter has.  Made once per batch from
+ * index (T), int32 or int64 (index_bytes 4 or 8) on the device -- a value
+ * outside 0 .. adapters - 1 is no adapter -- it serves every projection of a
+ * model, and tokens may come in any order.  Buffer: f8lin_lora_plan_bytes
+ * (tokens, adapters) bytes, 16-byte aligned.  A call whose tokens or adapters
+ * are not the plan's writes nothing.
+ * Errors: EINVAL, ESHAPE, EALIGN, EWORKSPACE, before anything is launched. */
+size_t f8lin_lora_plan_bytes(int64_t tokens, int adapters); /* 0: refused sizes */
+int f8lin_lora_plan(const void *index, int index_bytes, int64_t tokens, int adapters, void *plan, size_t plan_bytes,
+                    void *stream);
+
+/* Forward.  y may be base itself (ldbase = N).  h, if set, receives the inner
+ * products times their scale for the backward: T x (rank rounded up to 16)
+ * fp32, in the plan's order.  ws: f8lin_lora_forward_workspace_bytes bytes,
+ * 16-byte aligned, no initialisation needed. */
+typedef struct {
+  int64_t tokens, K, N;
+  const void *x, *a, *b, *base;
+  int64_t ldx, ldbase; /* elements; 0: K, N */
+  void *y;             /* (T, N) */
+  const float *scales;
+  const void *plan;
+  float *h;
+  void *ws;
+  size_t ws_bytes;
+  int rank, adapters, dtype;
+} f8lin_lora_fwd_args;
+int f8lin_lora_forward(const f8lin_lora_fwd_args *args, void *stream);
+size_t f8lin_lora_forward_workspace_bytes(int64_t T, int64_t K, int64_t N, int rank, int adapters);
+
+/* Backward (base's gradient is dy itself), with G[t] = scales[i] dy[t] . B_i:
+ *   dx[t] = G[t] . A_i (0 without an adapter),  dA_i = sum of G[t]^T x[t],
+ *   dB_i = sum of dy[t]^T h[t]   over the adapter's tokens (none: 0),
+ * each may be NULL.  dx needs a and b, da needs x and b, db needs h.  Sums in
+ * fp32 in a fixed order.  ws: f8lin_lora_backward_workspace_bytes bytes. */
+typedef struct {
+  int64_t tokens, K, N;
+  const void *dy, *x, *a, *b;
+  int64_t lddy, ldx; /* elements; 0: N, K */
+  const float *scales, *h;
+  const void *plan;
+  void *dx, *da, *db; /* (T, K), (adapters, rank, K), (adapters, N, rank) */
+  void *ws;
+  size_t ws_bytes;
+  int rank, adapters, dtype;
+} f8lin_lora_bwd_args;
+int f8lin_lora_backward(const f8lin_lora_bwd_args *args, void *stream);
+size_t f8lin_lora_backward_workspace_bytes(int64_t T, int64_t K, int64_t N, int rank, int adapters);
+
 #ifdef __cplusplus
 }
 #endif
