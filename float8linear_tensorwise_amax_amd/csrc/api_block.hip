@@ -150,31 +150,34 @@ int check_ws(const void *ws, size_t bytes, int64_t need) {
   return aligned16(ws) ? F8LIN_OK : F8LIN_EALIGN;
 }
 
-// What the calls keep in their workspace, in bytes from its start.
+// What the calls keep in their workspace, in bytes from its start: H's parts,
+// or H by position and then its exponents; in the backward G's, G by rank, and
+// the partial sums of dA and dB.
 struct LoraWs {
+  bool split;
   int parts;
-  int64_t h_bytes, sum_at, part_a_at, part_b_at, bytes;
+  int64_t h_bytes, exps_at, ht_at, part_a_at, part_b_at, bytes;
   int chunk, chunks;
 };
+int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
 int64_t h_bytes_of(int64_t T, int rank) { return T * lora_rank_pad(rank) * 4; }
-LoraWs lora_forward_ws(int64_t T, int64_t K, int rank, int adapters) {
+LoraWs lora_forward_ws(int64_t T, int64_t cols, int rank, int adapters) {
   LoraWs w = {};
-  w.parts = lora_parts(T, adapters, K, rank);
+  w.split = lora_split(T);
+  w.parts = lora_parts(T, adapters, cols, rank);
   w.h_bytes = h_bytes_of(T, rank);
-  w.bytes = w.parts * w.h_bytes;
+  w.exps_at = w.parts * w.h_bytes;
+  w.bytes = w.exps_at + (w.split ? 0 : up16((rank + 63) / 64 * T * 4));
   return w;
 }
 LoraWs lora_backward_ws(int64_t T, int64_t K, int64_t N, int rank, int adapters) {
-  LoraWs w = {};
-  w.parts = lora_parts(T, adapters, N, rank);
-  w.h_bytes = h_bytes_of(T, rank);
-  w.sum_at = w.parts * w.h_bytes;
+  LoraWs w = lora_forward_ws(T, N, rank, adapters);
+  w.ht_at = w.bytes;
   w.chunk = lora_chunk(T, K, N, rank);
   w.chunks = (int)((T + w.chunk - 1) / w.chunk);
-  w.part_a_at = w.sum_at + (w.parts > 1 ? w.h_bytes : 0);
+  w.part_a_at = w.ht_at + w.h_bytes;
   // (one chunk: nothing reaches over several)
   const int64_t slots = w.chunks > 1 ? 2 * (int64_t)w.chunks : 0;
-  auto up16 = [](int64_t b) { return (b + 15) / 16 * 16; };
   w.part_b_at = w.part_a_at + up16(slots * rank * K * 4);
   w.bytes = w.part_b_at + up16(slots * rank * N * 4);
   return w;
@@ -209,25 +212,25 @@ int f8lin_lora_forward(const f8lin_lora_fwd_args *p, void *stream) {
   if (a.scales && !aligned4(a.scales)) return F8LIN_EALIGN;
   F8_TRY(check_plan(a.plan));
   const LoraWs w = lora_forward_ws(T, K, a.rank, a.adapters);
-  const bool direct = a.h && w.parts == 1;  // H needs no workspace
-  const int64_t need = direct ? 0 : w.bytes;
-  F8_TRY(check_ws(a.ws, a.ws_bytes, need));
+  F8_TRY(check_ws(a.ws, a.ws_bytes, w.bytes));
   if (!aligned16(a.h)) return F8LIN_EALIGN;
   const Range y = span(a.y, a.dtype, T, N, N), base = span(a.base, a.dtype, T, N, ldb);
   // (y may be base itself)
   const bool same = a.base == a.y && ldb == N;
-  const Range outs[] = {y, {a.h, a.h ? w.h_bytes : 0}, {a.ws, need}};
+  const Range outs[] = {y, {a.h, a.h ? w.h_bytes : 0}, {a.ws, w.bytes}};
   const Range ins[] = {span(a.x, a.dtype, T, K, ldx), span(a.a, a.dtype, per, K, K), span(a.b, a.dtype, per, N, N),
                        {a.scales, a.scales ? 4 * (int64_t)a.adapters : 0},
                        {a.plan, (int64_t)f8lin_lora_plan_bytes(T, a.adapters)}, same ? Range{nullptr, 0} : base};
   if (any_overlap(outs, 3, ins, 6)) return F8LIN_EINVAL;
   if (T == 0 || N == 0) return F8LIN_OK;
   hipStream_t s = (hipStream_t)stream;
-  float *const h = direct ? a.h : (float *)a.ws;
-  const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, a.x, ldx, K, a.a, a.scales, h, w.parts};
+  const bool split = w.split;
+  int *const exps = (int *)((uint8_t *)a.ws + w.exps_at);
+  const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, a.x, ldx, K, a.a, a.scales,
+                      split ? nullptr : (uint32_t *)a.ws, (uint32_t *)a.h, exps, split ? (float *)a.ws : nullptr, w.parts};
   F8_TRY(status_of(launch_lora_down(d, a.dtype, false, s)));
-  const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, h, w.parts, direct ? nullptr : a.h, a.b, a.base,
-                    ldb, N, a.y, N};
+  const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, split ? nullptr : (const uint32_t *)a.ws, exps,
+                    split ? (const float *)a.ws : nullptr, w.parts, a.b, a.base, ldb, N, a.y, N};
   return status_of(launch_lora_up(u, a.dtype, false, s));
 }
 
@@ -264,20 +267,21 @@ int f8lin_lora_backward(const f8lin_lora_bwd_args *p, void *stream) {
   if (any_overlap(outs, 4, ins, 7)) return F8LIN_EINVAL;
   hipStream_t s = (hipStream_t)stream;
   uint8_t *const ws = (uint8_t *)a.ws;
-  float *const parts = (float *)ws, *const sum = w.parts > 1 ? (float *)(ws + w.sum_at) : parts;
+  const bool split = w.split;
+  int *const exps = (int *)(ws + w.exps_at);
+  uint32_t *const gt = (uint32_t *)(ws + w.ht_at);
   if (g) {
-    const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, a.dy, lddy, N, a.b, a.scales, parts, w.parts};
+    const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, a.dy, lddy, N, a.b, a.scales,
+                        split ? nullptr : (uint32_t *)ws, a.da ? gt : nullptr, exps, split ? (float *)ws : nullptr, w.parts};
     F8_TRY(status_of(launch_lora_down(d, a.dtype, true, s)));
-    // dx, and the sum of G's parts; with dx not asked for the sum is all that is left to take
-    const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, parts, w.parts, w.parts > 1 ? sum : nullptr, a.a,
-                      nullptr, K, K, a.dx, K};
+    const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, split ? nullptr : (const uint32_t *)ws, exps,
+                      split ? (const float *)ws : nullptr, w.parts, a.a, nullptr, K, K, a.dx, K};
     if (a.dx) F8_TRY(status_of(launch_lora_up(u, a.dtype, true, s)));
-    else if (w.parts > 1) F8_TRY(status_of(launch_lora_sum(u, s)));
   }
   if (!a.da && !a.db) return F8LIN_OK;
   LoraOuter o = {(const int *)a.plan, (int)T, a.adapters, a.rank, w.chunk, w.chunks, {}, 0};
-  o.side[0] = LoraOuterSide{a.x, ldx, K, sum, a.da, 0, (float *)(ws + w.part_a_at), 0, 0};
-  o.side[1] = LoraOuterSide{a.dy, lddy, N, a.h, a.db, 1, (float *)(ws + w.part_b_at), 0, 0};
+  o.side[0] = LoraOuterSide{a.x, ldx, K, gt, a.da, 0, (float *)(ws + w.part_a_at), 0, 0};
+  o.side[1] = LoraOuterSide{a.dy, lddy, N, (const uint32_t *)a.h, a.db, 1, (float *)(ws + w.part_b_at), 0, 0};
   return status_of(launch_lora_outer(o, a.dtype, s));
 }
 

@@ -8,15 +8,19 @@
 
 namespace f8lin {
 
-constexpr int kLoraTile = 64;            // rows of a tile
 constexpr int kLoraMaxAdapters = 2047;   // of a plan: 16 waves' counts of each fit the LDS
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraMagic = 0x4C6F5241;
 
 __host__ __device__ inline int lora_rank_pad(int rank) { return (rank + 15) / 16 * 16; }
+// Rows of a tile: few tokens are mostly single ones of many adapters, or need
+// more workgroups than 64-row tiles give.
+__host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
 __host__ __device__ inline int64_t lora_max_tiles(int64_t tokens, int64_t adapters) {
-  const int64_t groups = tokens < adapters + 1 ? tokens : adapters + 1;
-  return (tokens + kLoraTile - 1) / kLoraTile + groups;
+  const int64_t groups = tokens < adapters + 1 ? tokens : adapters + 1, rows = lora_tile(tokens);
+  // (a group's last tile may be short; a token is in one tile)
+  const int64_t most = (tokens + rows - 1) / rows + groups;
+  return most < tokens ? most : tokens;
 }
 // Words before the tiles, and before the tokens' order.
 __host__ __device__ inline int64_t lora_tiles_at(int64_t adapters) { return (4 + adapters + 2 + 3) / 4 * 4; }
@@ -34,15 +38,23 @@ struct LoraDown {
   int64_t ldx, cols;
   const void *w;        // (adapters, rank, cols) or (adapters, cols, rank)
   const float *scales;  // (adapters) or null
-  float *h;             // parts x tokens x lora_rank_pad(rank)
+  // H as the later products take it: by position, tokens x rank_pad (h, with
+  // fp16 data beside its exponents, one for 64 ranks of a position: rank / 64
+  // rounded up x tokens), and by rank, rank_pad x tokens (ht); either may be
+  // null.  Only with lora_split: parts_out, the parts' sums in binary32, parts
+  // x tokens x rank_pad, in place of h.
+  uint32_t *h, *ht;
+  int *exponents;
+  float *parts_out;
   int parts;
 };
 struct LoraUp {
   const int *plan;
   int tokens, adapters, rank;
-  const float *h;  // as left by down
+  const uint32_t *h;  // as left by down, or null:
+  const int *exponents;
+  const float *parts_in;  // the parts' sums
   int parts;
-  float *sum;  // if set: the parts' sum, tokens x lora_rank_pad(rank)
   const void *w;  // (adapters, cols, rank) or (adapters, rank, cols)
   const void *base;
   int64_t ldbase, cols;
@@ -52,7 +64,7 @@ struct LoraUp {
 struct LoraOuterSide {
   const void *x;  // (tokens, cols)
   int64_t ldx, cols;
-  const float *h;  // tokens x lora_rank_pad(rank)
+  const uint32_t *ht;  // H's final form by rank
   void *d;         // (adapters, rank, cols), or (adapters, cols, rank) where d_t; null: not computed
   int d_t;
   float *part;  // 2 * chunks x rank x cols
@@ -64,18 +76,18 @@ struct LoraOuter {
   int tokens, adapters, rank;
   int chunk, chunks;  // sorted positions a workgroup takes, and how many such
   LoraOuterSide side[2];
-  int units;  // (set by the launch)
+  int units, across;  // (set by the launch)
 };
 
-// Parts the columns of a down product are split into, and the positions of an
-// outer product's chunk.
+// Whether H passes between the products as sums of parts (16-row tiles), into
+// how many parts the columns of a down product are then split, and the
+// positions of an outer product's chunk.
+inline bool lora_split(int64_t tokens) { return lora_tile(tokens) == 16; }
 int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank);
 int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank);
 hipError_t launch_lora_plan(const void *index, bool wide, int tokens, int adapters, int *plan, hipStream_t stream);
 hipError_t launch_lora_down(const LoraDown &a, int dtype, bool w_t, hipStream_t stream);
 hipError_t launch_lora_up(const LoraUp &a, int dtype, bool w_t, hipStream_t stream);
-// a.sum alone: the parts' sum.
-hipError_t launch_lora_sum(const LoraUp &a, hipStream_t stream);
 hipError_t launch_lora_outer(const LoraOuter &a, int dtype, hipStream_t stream);
 
 }  // namespace f8lin

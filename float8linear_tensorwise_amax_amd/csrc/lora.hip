@@ -37,8 +37,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = kLoraTile;
-
 // ---------------------------------------------------------------- plan
 
 // The buffer's words: {magic, tokens, adapters, tiles}, starts[adapters + 2]
@@ -72,6 +70,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
   __shared__ int starts[MAXA + 2], tile_first[MAXA + 2];
   __shared__ int sums[2][WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tile_rows = lora_tile(tokens);
   const int groups = adapters + 1;  // the last: no adapter
   for (int i = tid; i < WAVES * (MAXA + 1); i += kThreads) (&count[0][0])[i] = 0;
   __syncthreads();
@@ -110,7 +109,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) n += count[w][a];
     }
-    const int nt = (n + kTile - 1) / kTile;
+    const int nt = (n + tile_rows - 1) / tile_rows;
     int s = n, st = nt;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -166,8 +165,8 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
       if (tile_first[mid] <= i) lo = mid;
       else hi = mid - 1;
     }
-    const int p = starts[lo] + (i - tile_first[lo]) * kTile;
-    tiles[i] = i32x4{lo, p, min(kTile, starts[lo + 1] - p), 0};
+    const int p = starts[lo] + (i - tile_first[lo]) * tile_rows;
+    tiles[i] = i32x4{lo, p, min(tile_rows, starts[lo + 1] - p), 0};
   }
   if (tid == 0) *reinterpret_cast<i32x4 *>(plan) = i32x4{kLoraMagic, tokens, adapters, tiles_before};
 }
@@ -296,17 +295,52 @@ __device__ __forceinline__ void split_f16(u32x4 f, u32x4 &hi, u32x4 &lo) {
   split8(v, hi, lo);
 }
 
+// ---------------------------------------------------------------- intermediates
+
+// A value of H as the products over tokens take it: for the 16-bit types a
+// bf16 in the high half and what it left over, as another, in the low one.
+template <int DT>
+__device__ __forceinline__ uint32_t h_word(float v) {
+  if constexpr (DT == F8LIN_FP32) return __float_as_uint(v);
+  const uint32_t hi = f32_to_bf16_rne(v);
+  return hi << 16 | f32_to_bf16_rne(left_over(v, __uint_as_float(hi << 16)));
+}
+// The same for the products over ranks: with fp16 operands two fp16 values of
+// v * 2^-e, e by the largest value of a token's block of 64 ranks (2^-24 of
+// that value is the least that is kept).
+template <int DT>
+__device__ __forceinline__ uint32_t up_word(float v, int e) {
+  if constexpr (DT != F8LIN_FP16) return h_word<DT>(v);
+  v = ldexpf(v, -e);
+  const _Float16 hi = (_Float16)v;
+  const float left = isfinite((float)hi) ? v - (float)hi : 0.0f;
+  return (uint32_t)__builtin_bit_cast(uint16_t, hi) << 16 | __builtin_bit_cast(uint16_t, (_Float16)left);
+}
+// e for the largest magnitude's bits: it becomes a value of 2^13 to 2^14.
+__device__ __forceinline__ int up_exponent(uint32_t mag) {
+  const int field = (int)(mag >> 23);
+  return field == 0 || field == 255 ? 0 : field - 127 - 13;
+}
+// The high (or low) halves of eight such words, as a fragment.
+__device__ __forceinline__ u32x4 h_halves(u32x4 a, u32x4 b, bool high) {
+  const uint32_t sel = high ? 0x07060302u : 0x05040100u;
+  return u32x4{__builtin_amdgcn_perm(a.y, a.x, sel), __builtin_amdgcn_perm(a.w, a.z, sel),
+               __builtin_amdgcn_perm(b.y, b.x, sel), __builtin_amdgcn_perm(b.w, b.z, sel)};
+}
+
 // ---------------------------------------------------------------- down
 
-// H[part][position][r] = scale * sum over part's columns of X[t][c] * W(r, c),
-// W (R, C) as rows, or (C, R) where W_T.  A workgroup takes 64 rows, 16 * NT
-// ranks and one part of the columns, 64 (32 in binary32: 128 bytes a row) at a
-// time, dealt to its four waves.
-template <int DT, int NT, bool W_T>
-__global__ __launch_bounds__(256) void lora_down_kernel(const LoraDown a) {
+// H[position][r] = scale * sum over columns of X[t][c] * W(r, c), W (R, C) as
+// rows, or (C, R) where W_T.  A workgroup takes a tile of up to 16 * M rows,
+// 16 * NT ranks and one part of the columns, 64 (32 in binary32: 128 bytes a
+// row) at a time, dealt to its waves, whose sums meet in the LDS.  With one
+// part H is written as the later products take it, by position (h) and by rank
+// (ht); else each part's sum in binary32, by position.
+template <int DT, int NT, bool W_T, int M, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a) {
   typedef typename MxElem<DT>::type elem;
-  constexpr int E = kE<DT>, kBlock = 8 * E, RB = 16 * NT;
-  __shared__ float red[3][kTile][RB + 1];
+  constexpr int E = kE<DT>, kBlock = 8 * E, RB = 16 * NT, kRows = 16 * M, kThreads = 64 * WAVES;
+  __shared__ float red[WAVES][kRows][RB + 1];
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int rblocks = (a.rank + RB - 1) / RB, per_tile = rblocks * a.parts;
@@ -314,23 +348,24 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraDown a) {
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
   const int blocks = (int)((C + kBlock - 1) / kBlock), part_blocks = (blocks + a.parts - 1) / a.parts;
+  const int rp = lora_rank_pad(a.rank);
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[id / per_tile];
     const int sub = (int)(id % per_tile), part = sub % a.parts, r0 = sub / a.parts * RB;
     if (tile.x >= a.adapters) break;  // (tokens without an adapter come last)
     const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
-    const elem *x[4];
+    const elem *x[M];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < M; ++m)
       x[m] = reinterpret_cast<const elem *>(a.x) + (int64_t)order[tile.y + min(16 * m + i, tile.z - 1)] * a.ldx;
     const int groups = (tile.z + 15) >> 4;
-    v4f acc[4][NT];
+    v4f acc[M][NT];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[m][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int b1 = min(blocks, (part + 1) * part_blocks);
-    for (int b = part * part_blocks + wave; b < b1; b += 4) {
+    for (int b = part * part_blocks + wave; b < b1; b += WAVES) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t c = (int64_t)b * kBlock + (2 * g + h) * E;
@@ -351,7 +386,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraDown a) {
           for (int j = 0; j < NT; ++j) wf[j] = pick<DT, NT>(rows, j);
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < M; ++m) {
           if (m >= groups) break;
           const u32x4 xf = load_frag<DT>(x[m] + c, left);
 #pragma unroll
@@ -359,52 +394,284 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraDown a) {
         }
       }
     }
-    // the four waves' sums, in their order
-    auto rank_of = [&](int j, int q) { return W_T ? (4 * g + q) * NT + j : 16 * j + 4 * g + q; };
     __syncthreads();  // (of the last tile's reads)
-    if (wave > 0) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) red[wave - 1][16 * m + i][rank_of(j, q)] = acc[m][j][q];
-    }
+        for (int q = 0; q < 4; ++q) red[wave][16 * m + i][W_T ? (4 * g + q) * NT + j : 16 * j + 4 * g + q] = acc[m][j][q];
     __syncthreads();
-    if (wave == 0) {
-      const float s = a.scales ? a.scales[tile.x] : 1.0f;
-      const int rp = lora_rank_pad(a.rank);
-      float *const out = a.h + (int64_t)part * a.tokens * rp;
+    // the waves' sums, in their order; a thread's values are of one row
+    const float s = a.scales ? a.scales[tile.x] : 1.0f;
+    constexpr int kEach = kRows * RB / kThreads, kLanes = RB / kEach;  // values a thread, threads a row
+    const int row = threadIdx.x / kLanes, rl = threadIdx.x % kLanes;
+    float v[kEach];
+    uint32_t mag = 0;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (16 * m + i >= tile.z) continue;
-        float *const row = out + (int64_t)(tile.y + 16 * m + i) * rp + r0;
+    for (int k = 0; k < kEach; ++k) {
+      const int r = rl + kLanes * k;
+      v[k] = red[0][row][r];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int t = 1; t < WAVES; ++t) v[k] += red[t][row][r];
+      // (past the rank: zero, also where x is not finite)
+      v[k] = r0 + r < a.rank ? s * v[k] : 0.0f;
+      mag = max(mag, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+    }
+    int e = 0;
+    if constexpr (DT == F8LIN_FP16) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = rank_of(j, q);
-            float v = acc[m][j][q];
+      for (int off = 1; off < kLanes; off <<= 1) mag = max(mag, (uint32_t)__shfl_xor((int)mag, off, 64));
+      e = up_exponent(mag);
+      if (a.h && row < tile.z && rl == 0) a.exponents[(int64_t)(r0 / 64) * a.tokens + tile.y + row] = e;
+    }
 #pragma unroll
-            for (int t = 0; t < 3; ++t) v += red[t][16 * m + i][r];
-            // (past the rank: zero, also where x is not finite)
-            if (r0 + r < rp) row[r] = r0 + r < a.rank ? s * v : 0.0f;
-          }
+    for (int k = 0; k < kEach; ++k) {
+      const int r = rl + kLanes * k;
+      const int64_t to = (int64_t)(tile.y + row) * rp + r0 + r;
+      if (row < tile.z && r0 + r < rp) {
+        if (a.parts_out) a.parts_out[(int64_t)part * a.tokens * rp + to] = v[k];
+        else if (a.h) a.h[to] = up_word<DT>(v[k], e);
+      }
+      if (!a.parts_out && a.ht) red[0][row][r] = __uint_as_float(h_word<DT>(v[k]));  // (this thread's own)
+    }
+    if (!a.parts_out && a.ht) {
+      __syncthreads();
+      for (int at = threadIdx.x; at < kRows * RB; at += kThreads) {
+        const int row = at % kRows, r = at / kRows;
+        if (row < tile.z && r0 + r < rp) a.ht[(int64_t)(r0 + r) * a.tokens + tile.y + row] = __float_as_uint(red[0][row][r]);
       }
     }
   }
+}
+
+// Sums the parts that a split down product left, in their order, into H by
+// rank.
+template <int DT>
+__global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
+  __shared__ uint32_t turn[16][17];
+  const int rp = lora_rank_pad(a.rank), tr = threadIdx.x & 15, tp = threadIdx.x >> 4;
+  const int64_t ld = (int64_t)a.tokens * rp, rblocks = rp / 16;
+  const int r = (int)(blockIdx.x % rblocks) * 16, p = (int)(blockIdx.x / rblocks) * 16;
+  if (p + tp < a.tokens) {
+    const float *const from = a.parts_out + (int64_t)(p + tp) * rp + r + tr;
+    float v = from[0];
+    for (int k = 1; k < a.parts; ++k) v += from[k * ld];
+    const uint32_t w = h_word<DT>(v);
+    turn[tp][tr] = w;
+  }
+  __syncthreads();
+  if (p + tr < a.tokens) a.ht[(int64_t)(r + tp) * a.tokens + p + tr] = turn[tr][tp];
 }
 
 // ---------------------------------------------------------------- up
 
 // Y[t][c] = base[t][c] + sum over r of H[position][r] * W(c, r), W (C, R) as
 // rows, or (R, C) where W_T; base may be missing.  A wave takes 64 columns of
-// up to 64 rows; lane (i, g) ends with 16 consecutive columns of rows i, i +
-// 16, ...: row 4 * p + q of operand tile j stands for column 4 * (4 * p + q) + j.
+// up to 16 * M rows, a workgroup 256; lane (i, g) ends with row i of each
+// group of 16 and, in operand tiles of 16 columns each, 16-byte pieces of
+// columns that its neighbours of the same row continue to 64 bytes: in the
+// 16-bit types row 4 p + q of tile j stands for column 32 (j / 2) + 8 p + 2 q
+// + j % 2, in binary32 for 16 j + 4 p + q.
+
+// W's fragments for 16 ranks from r0, 64 columns from c0.
 template <int DT, bool W_T>
-__global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
+__device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, int rank, int64_t C, int64_t c0, int r0,
+                                           u32x4 (&wf)[4]) {
+  constexpr int E = kE<DT>;
+  constexpr bool F32 = DT == F8LIN_FP32;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  // this lane's ranks: E of 16 (in the 16-bit types lanes of g and g + 2 hold the same, for H's two halves)
+  const int rg = r0 + (F32 ? g : (g & 1)) * E;
+  if constexpr (!W_T) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = c0 + (F32 ? 16 * j + i : 32 * (j >> 1) + 2 * i + (j & 1));
+      wf[j] = load_frag<DT>(w + min(c, C - 1) * rank + rg, c < C ? rank - rg : 0);
+    }
+  } else if constexpr (F32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = c0 + 16 * j + i;
+#pragma unroll
+      for (int e = 0; e < E; ++e) wf[j][e] = rg + e < rank && c < C ? w[(int64_t)(rg + e) * C + c] : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int jj = 0; jj < 2; ++jj) {
+      Few<DT, 2> rows[E];
+      const int64_t c = c0 + 32 * jj + 2 * i;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        rows[e] = load_few<DT, 2>(w + (int64_t)(rg + e) * C + c, rg + e < rank ? (int)max((int64_t)0, min((int64_t)2, C - c)) : 0);
+      wf[2 * jj] = pick<DT, 2>(rows, 0);
+      wf[2 * jj + 1] = pick<DT, 2>(rows, 1);
+    }
+  }
+}
+// base's pieces of one row.
+template <int DT>
+__device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, bool in, int64_t c0, u32x4 (&raw)[16 / kE<DT>]) {
+  constexpr int E = kE<DT>;
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int h = 0; h < 16 / E; ++h) {
+    const int64_t c = c0 + 4 * E * h + E * g;
+    raw[h] = u32x4{0, 0, 0, 0};
+    if (a.base && in) raw[h] = load_frag<DT>(reinterpret_cast<const typename MxElem<DT>::type *>(a.base) + t * a.ldbase + c, a.cols - c);
+  }
+}
+// One row's pieces of y.
+template <int DT>
+__device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapted, int64_t c0, const u32x4 (&raw)[16 / kE<DT>],
+                                         const v4f (&acc)[4]) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>;
+  constexpr bool F32 = DT == F8LIN_FP32;
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int h = 0; h < 16 / E; ++h) {
+    const int64_t c = c0 + 4 * E * h + E * g;
+    const int n = (int)max((int64_t)0, min((int64_t)E, a.cols - c));
+    if (n == 0) break;
+    elem *const y = reinterpret_cast<elem *>(a.y) + t * a.ldy + c;
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint32_t bits = F32 ? raw[h][e & 3] : (raw[h][e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+      const float v = F32 ? acc[h & 3][e & 3] : acc[(2 * h + (e & 1)) & 3][e >> 1];
+      // (a token without an adapter keeps base's bits)
+      o[e] = adapted ? f32_to_elem(a.base ? elem_f32<DT>(bits) + v : v, DT) : bits;
+    }
+    if (n == E) {
+      if constexpr (F32) *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0], o[1], o[2], o[3]};
+      else
+        *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < n) y[e] = (elem)o[e];
+    }
+  }
+}
+// H's fragment of 16 ranks for one row (position p).
+template <int DT>
+__device__ __forceinline__ u32x4 up_h(const LoraUp &a, int p, int rp, int r0) {
+  constexpr int E = kE<DT>;
+  const int g = (threadIdx.x & 63) >> 4;
+  const uint32_t *const h = a.h + (int64_t)p * rp + r0 + (DT == F8LIN_FP32 ? g : (g & 1)) * E;
+  if constexpr (DT == F8LIN_FP32) return *reinterpret_cast<const u32x4 *>(h);
+  else return h_halves(*reinterpret_cast<const u32x4 *>(h), *reinterpret_cast<const u32x4 *>(h + 4), g < 2);
+}
+
+// Tiles of 64 rows, H in its final form.  Up to 64 ranks (NB blocks of 16): W
+// stays in registers, the rows pass by in groups of 16, the next group's base
+// and H on their way.  NB = 0: any rank, 64 at a time, all rows' sums kept.
+template <int DT, bool W_T, int NB>
+__global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
+  typedef typename MxElem<DT>::type elem;
+  constexpr int kPieces = 16 / kE<DT>;
+  const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15;
+  const int64_t C = a.cols;
+  const int cblocks = (int)((C + 255) / 256);
+  const int64_t total = (int64_t)tiles * cblocks;
+  const int *const order = plan_order(a.plan, a.tokens, a.adapters);
+  const int rp = lora_rank_pad(a.rank);
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const i32x4 tile = plan_tiles(a.plan, a.adapters)[id / cblocks];
+    const int64_t c0 = (id % cblocks) * 256 + 64 * wave;
+    if (c0 >= C) continue;
+    const bool adapted = tile.x < a.adapters;
+    const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
+    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto position = [&](int m) { return tile.y + min(16 * m + i, tile.z - 1); };
+    auto scale = [&](v4f (&acc)[4], int m, int block) {
+      if constexpr (DT == F8LIN_FP16) {
+        const float f = ldexpf(1.0f, a.exponents[(int64_t)block * a.tokens + position(m)]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] *= f;
+      }
+    };
+    if constexpr (NB > 0) {
+      u32x4 wf[NB][4];
+      if (adapted) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) up_weights<DT, W_T>(w, a.rank, C, c0, 16 * k, wf[k]);
+      }
+      u32x4 raw[2][kPieces], hf[2][NB];
+      int64_t t[2];
+      const int groups = (tile.z + 15) >> 4;
+      auto load = [&](int m, int b) {
+        t[b] = order[position(m)];
+        up_base<DT>(a, t[b], 16 * m + i < tile.z, c0, raw[b]);
+        if (adapted) {
+#pragma unroll
+          for (int k = 0; k < NB; ++k) hf[b][k] = 16 * k < rp ? up_h<DT>(a, position(m), rp, 16 * k) : u32x4{0, 0, 0, 0};
+        }
+      };
+      load(0, 0);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m >= groups) break;
+        if (m + 1 < groups) load(m + 1, (m + 1) & 1);
+        v4f acc[4] = {zero, zero, zero, zero};
+        if (adapted) {
+#pragma unroll
+          for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = mma<DT>(wf[k][j], hf[m & 1][k], acc[j]);
+          scale(acc, m, 0);
+        }
+        if (16 * m + i < tile.z) up_store<DT>(a, t[m & 1], adapted, c0, raw[m & 1], acc);
+      }
+    } else {
+      v4f sum[4][4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[m][j] = zero;
+      for (int r0 = 0; adapted && r0 < rp; r0 += 64) {
+        v4f acc[4][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[m][j] = zero;
+        for (int r = r0; r < min(rp, r0 + 64); r += 16) {
+          u32x4 wf[4];
+          up_weights<DT, W_T>(w, a.rank, C, c0, r, wf);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const u32x4 hf = up_h<DT>(a, position(m), rp, r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[m][j] = mma<DT>(wf[j], hf, acc[m][j]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          scale(acc[m], m, r0 / 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[m][j] += acc[m][j];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (16 * m + i >= tile.z) break;
+        const int64_t t = order[position(m)];
+        u32x4 raw[kPieces];
+        up_base<DT>(a, t, true, c0, raw);
+        up_store<DT>(a, t, adapted, c0, raw, sum[m]);
+      }
+    }
+  }
+}
+
+// Tiles of 16 rows, H as the sums of its parts.
+template <int DT, bool W_T>
+__global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
+  typedef typename MxElem<DT>::type elem;
+  constexpr int E = kE<DT>;
+  constexpr bool F32 = DT == F8LIN_FP32;
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int64_t C = a.cols;
@@ -416,116 +683,49 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[id / cblocks];
     const int64_t c0 = (id % cblocks) * 256 + 64 * wave;
-    const int groups = (tile.z + 15) >> 4;
-    v4f acc[4][4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    if (tile.x < a.adapters) {
+    if (c0 >= C) continue;
+    const bool adapted = tile.x < a.adapters, in = i < tile.z;
+    const int p = tile.y + min(i, tile.z - 1);
+    const int64_t t = order[p];
+    u32x4 raw[16 / E];
+    up_base<DT>(a, t, in, c0, raw);
+    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    v4f acc[4] = {zero, zero, zero, zero};
+    if (adapted) {
       const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
-      const bool keep = a.sum && id % cblocks == 0 && wave == 0;
       for (int r0 = 0; r0 < rp; r0 += 16) {
-        // this lane's ranks: E of 16 (in the 16-bit types lanes of g and g + 2 hold the same, for H's two halves)
-        const int rg = r0 + (DT == F8LIN_FP32 ? g : (g & 1)) * E;
-        u32x4 wf[4];
-        if constexpr (!W_T) {
+        u32x4 wf[4], wl[4];
+        up_weights<DT, W_T>(w, a.rank, C, c0, r0, wf);
+        u32x4 hw[E / 4];
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) {
+          const float *const from = a.parts_in + (int64_t)p * rp + r0 + (F32 ? g : (g & 1)) * E + 4 * e;
+          v4f s = *reinterpret_cast<const v4f *>(from);
+          for (int k = 1; k < a.parts; ++k) s += *reinterpret_cast<const v4f *>(from + k * part_ld);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) hw[e][k] = h_word<DT>(s[k]);
+        }
+        if constexpr (F32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mma<DT>(wf[j], hw[0], acc[j]);
+        } else {
+          if constexpr (DT == F8LIN_FP16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split_f16(wf[j], wf[j], wl[j]);
+          }
+          const u32x4 hf = h_halves(hw[0], hw[E / 4 - 1], g < 2);
+          // (an infinite H meets the operand's main half only: the other is often zero)
+          const u32x4 finite = DT == F8LIN_FP16 ? no_inf(hf) : hf;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int64_t c = c0 + 4 * i + j;
-            wf[j] = load_frag<DT>(w + min(c, C - 1) * a.rank + rg, c < C ? a.rank - rg : 0);
-          }
-        } else {
-          Few<DT, 4> rows[E];
-          const int64_t c = c0 + 4 * i;
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            rows[e] = load_few<DT, 4>(w + (int64_t)(rg + e) * C + c, rg + e < a.rank ? (int)min((int64_t)4, C - c) : 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) wf[j] = pick<DT, 4>(rows, j);
-        }
-        u32x4 wl[4];
-        if constexpr (DT == F8LIN_FP16) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) split_f16(wf[j], wf[j], wl[j]);
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (m >= groups) break;
-          const int p = tile.y + min(16 * m + i, tile.z - 1);
-          const float *const h = a.h + (int64_t)p * rp + rg;
-          float v[E];
-#pragma unroll
-          for (int e = 0; e < E; e += 4) {
-            v4f s = *reinterpret_cast<const v4f *>(h + e);
-            for (int k = 1; k < a.parts; ++k) s += *reinterpret_cast<const v4f *>(h + k * part_ld + e);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[e + k] = s[k];
-            if (keep && (DT == F8LIN_FP32 || g < 2) && 16 * m + i < tile.z)
-              *reinterpret_cast<v4f *>(a.sum + (int64_t)p * rp + rg + e) = s;
-          }
-          if constexpr (DT == F8LIN_FP32) {
-            const u32x4 hf = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[m][j] = mma<DT>(wf[j], hf, acc[m][j]);
-          } else {
-            u32x4 hi, lo;
-            split8(v, hi, lo);
-            const u32x4 hf = g < 2 ? hi : lo;
-            // (an infinite H meets the operand's main half only: the other is often zero)
-            const u32x4 finite = DT == F8LIN_FP16 ? no_inf(hf) : hf;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[m][j] = mma<F8LIN_BF16>(wf[j], hf, acc[m][j]);
-              if constexpr (DT == F8LIN_FP16) acc[m][j] = mma<F8LIN_BF16>(wl[j], finite, acc[m][j]);
-            }
+            acc[j] = mma<F8LIN_BF16>(wf[j], hf, acc[j]);
+            if constexpr (DT == F8LIN_FP16) acc[j] = mma<F8LIN_BF16>(wl[j], finite, acc[j]);
           }
         }
       }
     }
-    const int64_t c = c0 + 16 * g;
-    const int n = (int)max((int64_t)0, min((int64_t)16, C - c));
-    if (n == 0) continue;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if (16 * m + i >= tile.z) break;
-      const int64_t t = order[tile.y + 16 * m + i];
-      elem *const y = reinterpret_cast<elem *>(a.y) + t * a.ldy + c;
-      const elem *const base = a.base ? reinterpret_cast<const elem *>(a.base) + t * a.ldbase + c : nullptr;
-#pragma unroll
-      for (int h = 0; h < 16; h += E) {
-        if (h >= n) break;
-        const u32x4 raw = base ? load_frag<DT>(base + h, n - h) : u32x4{0, 0, 0, 0};
-        uint32_t o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t bits = DT == F8LIN_FP32 ? raw[e & 3] : (raw[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-          const float v = acc[m][(h + e) & 3][(h + e) >> 2];
-          // (a token without an adapter keeps base's bits)
-          o[e] = tile.x < a.adapters ? f32_to_elem(base ? elem_f32<DT>(bits) + v : v, DT) : bits;
-        }
-        if (n - h >= E) {
-          if constexpr (DT == F8LIN_FP32) *reinterpret_cast<u32x4_u *>(y + h) = u32x4{o[0], o[1], o[2], o[3]};
-          else
-            *reinterpret_cast<u32x4_u *>(y + h) =
-                u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4 % E] | o[5 % E] << 16, o[6 % E] | o[7 % E] << 16};
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (h + e < n) y[h + e] = (elem)o[e];
-        }
-      }
-    }
+    if (in) up_store<DT>(a, t, adapted, c0, raw, acc);
   }
-}
-
-// The sum of H's parts, in their order.
-__global__ __launch_bounds__(256) void lora_sum_kernel(const float *h, int parts, int64_t n, float *sum) {
-  const int64_t at = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);  // (n is a multiple of 16)
-  if (at >= n) return;
-  v4f s = *reinterpret_cast<const v4f *>(h + at);
-  for (int k = 1; k < parts; ++k) s += *reinterpret_cast<const v4f *>(h + k * n + at);
-  *reinterpret_cast<v4f *>(sum + at) = s;
 }
 
 // ---------------------------------------------------------------- outer
@@ -533,10 +733,16 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const float *h, int parts
 // D_i(c, r) = sum over adapter i's positions p of X[order[p]][c] * H[p][r], as
 // (R, C), or (C, R) where d_t.  A wave takes 16 * E columns (lane i the
 // contiguous block of E at E * i, which become E operand tiles), 16 * NT ranks
-// and `chunk` sorted positions, which may hold several adapters.  An adapter
+// (NT: 1 or 2) and `chunk` sorted positions, which may hold several adapters.  An adapter
 // that lies within one chunk is written as it is; one that reaches over
 // several leaves a binary32 partial sum for each (slot 2 * chunk, or 2 * chunk
 // + 1 in the chunk where it begins), which lora_outer_join_kernel adds up.
+// Each step's loads are on their way while the step before is multiplied.
+template <int DT, int NT>
+struct OuterStep {
+  Few<DT, kE<DT>> rows[kE<DT>];
+  u32x4 h[NT][kE<DT> / 4];
+};
 template <int DT, int NT>
 __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
   typedef typename MxElem<DT>::type elem;
@@ -549,15 +755,20 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
   const int rp = lora_rank_pad(a.rank);
   const int adapted = starts[a.adapters];
   int id = blockIdx.x;
-  const LoraOuterSide &side = id < a.side[0].blocks * a.units ? a.side[0] : a.side[1];
-  if (id >= a.side[0].blocks * a.units) id -= a.side[0].blocks * a.units;
-  // columns fastest: the workgroups of a chunk read the same H
-  const int64_t c0 = (int64_t)(id % side.blocks) * 4 * kCols + wave * kCols + E * i;
-  const int unit = id / side.blocks, chunk = unit % a.chunks, r0 = unit / a.chunks * 16 * NT;
+  const bool second = id >= a.side[0].blocks * a.units;
+  if (second) id -= a.side[0].blocks * a.units;
+  const LoraOuterSide &side = second ? a.side[1] : a.side[0];
+  // a workgroup's waves: `across` blocks of ranks of the same columns, which they so read once; columns fastest: the
+  // workgroups of a chunk read the same H
+  const int across = a.across;
+  const int64_t cw = ((int64_t)(id % side.blocks) * (4 / across) + wave / across) * kCols, c0 = cw + E * i;
+  const int unit = id / side.blocks, chunk = unit % a.chunks, r0 = (unit / a.chunks * across + wave % across) * 16 * NT;
   const int64_t C = side.cols;
+  if (cw >= C || r0 >= a.rank) return;
   const int64_t first = (int64_t)chunk * a.chunk;
   const int end = (int)min((int64_t)adapted, first + a.chunk);
   const int cn = (int)max((int64_t)0, min((int64_t)E, C - c0));
+  const elem *const xc = reinterpret_cast<const elem *>(side.x) + c0;
   for (int p0 = (int)min((int64_t)adapted, first); p0 < end;) {
     const int ad = owner[p0], p1 = min(end, starts[ad + 1]);
     v4f acc[E][NT];
@@ -565,66 +776,88 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
     for (int c = 0; c < E; ++c)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[c][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = p0; p < p1; p += kStep) {
-      Few<DT, E> rows[E];
-      float h[NT][E];
+    // (nothing behind the adapter's tokens gets in, whatever it holds)
+    auto load = [&](int p, OuterStep<DT, NT> &s) {
+      const int at = p + g * E;
+      if (p + kStep <= p1) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int at = p + g * E + e;
-        const bool in = at < p1;  // (nothing behind the adapter's tokens gets in, whatever it holds)
-        const int64_t t = in ? order[at] : 0;
-        rows[e] = load_few<DT, E>(reinterpret_cast<const elem *>(side.x) + t * side.ldx + c0, in ? cn : 0);
+        for (int e = 0; e < E; ++e) s.rows[e] = load_few<DT, E>(xc + (int64_t)order[at + e] * side.ldx, cn);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const int r = r0 + 16 * j + i;
-          h[j][e] = in && r < rp ? side.h[(int64_t)at * rp + r] : 0.0f;
+          const int r = min(r0 + 16 * j + i, rp - 1);  // (past the padded rank: not stored)
+#pragma unroll
+          for (int k = 0; k < E / 4; ++k)
+            s.h[j][k] = *reinterpret_cast<const u32x4_u *>(side.ht + (int64_t)r * a.tokens + at + 4 * k);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const bool in = at + e < p1;
+          s.rows[e] = load_few<DT, E>(xc + (in ? (int64_t)order[at + e] * side.ldx : 0), in ? cn : 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int r = min(r0 + 16 * j + i, rp - 1);
+#pragma unroll
+          for (int e = 0; e < E; ++e) s.h[j][e >> 2][e & 3] = at + e < p1 ? side.ht[(int64_t)r * a.tokens + at + e] : 0u;
         }
       }
-      u32x4 hi[NT], lo[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if constexpr (DT == F8LIN_FP32)
-          hi[j] = u32x4{__float_as_uint(h[j][0]), __float_as_uint(h[j][1]), __float_as_uint(h[j][2]), __float_as_uint(h[j][3])};
-        else split8(h[j], hi[j], lo[j]);
-      }
+    };
+    auto multiply = [&](const OuterStep<DT, NT> &s) {
 #pragma unroll
       for (int c = 0; c < E; ++c) {
-        u32x4 xf = pick<DT, E>(rows, c);
+        u32x4 xf = pick<DT, E>(s.rows, c);
         if constexpr (DT == F8LIN_FP32) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) acc[c][j] = mma<DT>(xf, hi[j], acc[c][j]);
+          for (int j = 0; j < NT; ++j) acc[c][j] = mma<DT>(xf, s.h[j][0], acc[c][j]);
         } else {
           u32x4 xl;
           if constexpr (DT == F8LIN_FP16) split_f16(xf, xf, xl);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            acc[c][j] = mma<F8LIN_BF16>(xf, hi[j], acc[c][j]);
-            acc[c][j] = mma<F8LIN_BF16>(xf, lo[j], acc[c][j]);
-            if constexpr (DT == F8LIN_FP16) acc[c][j] = mma<F8LIN_BF16>(xl, hi[j], acc[c][j]);
+            const u32x4 hi = h_halves(s.h[j][0], s.h[j][E / 4 - 1], true), lo = h_halves(s.h[j][0], s.h[j][E / 4 - 1], false);
+            acc[c][j] = mma<F8LIN_BF16>(xf, hi, acc[c][j]);
+            acc[c][j] = mma<F8LIN_BF16>(xf, lo, acc[c][j]);
+            if constexpr (DT == F8LIN_FP16) acc[c][j] = mma<F8LIN_BF16>(xl, hi, acc[c][j]);
           }
         }
       }
+    };
+    OuterStep<DT, NT> s0, s1;
+    load(p0, s0);
+    for (int p = p0; p < p1; p += 2 * kStep) {
+      if (p + kStep < p1) load(p + kStep, s1);
+      multiply(s0);
+      if (p + kStep >= p1) break;
+      if (p + 2 * kStep < p1) load(p + 2 * kStep, s0);
+      multiply(s1);
     }
     // lane (i, g) holds rank r0 + 16 j + i of columns E * (4 g + q) + c of the wave's
     const bool whole = starts[ad] >= first && starts[ad + 1] <= first + a.chunk;
     const int slot = 2 * chunk + (starts[ad] >= first ? 1 : 0);
     const int64_t elems = (int64_t)a.rank * C;
-    auto put = [&](int64_t at, float v) {
-      if (!whole) side.part[(int64_t)slot * elems + at] = v;
-      else if constexpr (DT == F8LIN_FP32) reinterpret_cast<float *>(side.d)[(int64_t)ad * elems + at] = v;
-      else reinterpret_cast<uint16_t *>(side.d)[(int64_t)ad * elems + at] = (uint16_t)f32_to_elem(v, DT);
-    };
+    float *const part = side.part + (int64_t)slot * elems;
+    elem *const d = reinterpret_cast<elem *>(side.d) + (int64_t)ad * elems;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r = r0 + 16 * j + i;
       if (r >= a.rank) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
+        const int col = (int)cw + E * (4 * g + q), n = (int)min((int64_t)E, C - col);
+        // (a side has at most 256 * 2^22 elements: 32-bit offsets)
+        uint32_t at = side.d_t ? (uint32_t)col * a.rank + r : (uint32_t)r * (uint32_t)C + col;
+        const uint32_t step = side.d_t ? a.rank : 1;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < E; ++c) {
-          const int64_t col = c0 - E * i + E * (4 * g + q) + c;
-          if (col < C) put(side.d_t ? col * a.rank + r : (int64_t)r * C + col, acc[c][j][q]);
+          for (int c = 0; c < E; ++c, at += step)
+            if (c < n) d[at] = (elem)f32_to_elem(acc[c][j][q], DT);
+        } else {
+#pragma unroll
+          for (int c = 0; c < E; ++c, at += step)
+            if (c < n) part[at] = acc[c][j][q];
         }
+      }
     }
     p0 = p1;
   }
@@ -669,29 +902,44 @@ unsigned grid_of(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, 
 // Ranks of 16 a workgroup takes: one, two or four.
 int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 
-template <int DT, bool W_T>
-void down_typed(const LoraDown &a, hipStream_t s) {
+template <int DT, bool W_T, int M, int WAVES>
+void down_rows(const LoraDown &a, hipStream_t s) {
   const int nt = rank_tiles(a.rank), rblocks = (a.rank + 16 * nt - 1) / (16 * nt);
   const unsigned grid = grid_of(lora_max_tiles(a.tokens, a.adapters) * rblocks * a.parts);
-  if (nt == 1) lora_down_kernel<DT, 1, W_T><<<grid, 256, 0, s>>>(a);
-  else if (nt == 2) lora_down_kernel<DT, 2, W_T><<<grid, 256, 0, s>>>(a);
-  else lora_down_kernel<DT, 4, W_T><<<grid, 256, 0, s>>>(a);
+  if (nt == 1) lora_down_kernel<DT, 1, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
+  else if (nt == 2) lora_down_kernel<DT, 2, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
+  else lora_down_kernel<DT, 4, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
 }
 template <int DT>
-void down_by_layout(const LoraDown &a, bool w_t, hipStream_t s) {
-  if (w_t) down_typed<DT, true>(a, s);
-  else down_typed<DT, false>(a, s);
+void down_typed(const LoraDown &a, bool w_t, hipStream_t s) {
+  if (lora_tile(a.tokens) == 16) {
+    if (w_t) down_rows<DT, true, 1, 4>(a, s);
+    else down_rows<DT, false, 1, 4>(a, s);
+  } else {
+    if (w_t) down_rows<DT, true, 4, 8>(a, s);
+    else down_rows<DT, false, 4, 8>(a, s);
+  }
+  if (a.parts_out && a.ht) {
+    const int64_t grid = (int64_t)((a.tokens + 15) / 16) * (lora_rank_pad(a.rank) / 16);
+    lora_sum_kernel<DT><<<(unsigned)grid, 256, 0, s>>>(a);
+  }
 }
-template <int DT>
-void up_by_layout(const LoraUp &a, bool w_t, hipStream_t s) {
+template <int DT, bool W_T>
+void up_typed(const LoraUp &a, hipStream_t s) {
   const unsigned grid = grid_of(lora_max_tiles(a.tokens, a.adapters) * ((a.cols + 255) / 256));
-  if (w_t) lora_up_kernel<DT, true><<<grid, 256, 0, s>>>(a);
-  else lora_up_kernel<DT, false><<<grid, 256, 0, s>>>(a);
+  if (a.parts_in) lora_up_few_kernel<DT, W_T><<<grid, 256, 0, s>>>(a);
+  else if (a.rank <= 16) lora_up_kernel<DT, W_T, 1><<<grid, 256, 0, s>>>(a);
+  else if (a.rank <= 32) lora_up_kernel<DT, W_T, 2><<<grid, 256, 0, s>>>(a);
+  else if (a.rank <= 64) lora_up_kernel<DT, W_T, 4><<<grid, 256, 0, s>>>(a);
+  else lora_up_kernel<DT, W_T, 0><<<grid, 256, 0, s>>>(a);
 }
 template <int DT>
 void outer_typed(LoraOuter a, hipStream_t s) {
-  const int nt = rank_tiles(a.rank), rblocks = (a.rank + 16 * nt - 1) / (16 * nt);
-  const int64_t cols = 4 * 16 * kE<DT>;
+  const int nt = a.rank <= 16 ? 1 : 2;
+  int rblocks = (a.rank + 16 * nt - 1) / (16 * nt);
+  a.across = rblocks > 2 ? 4 : rblocks;
+  rblocks = (rblocks + a.across - 1) / a.across;
+  const int64_t cols = 4 / a.across * 16 * kE<DT>;
   a.units = a.chunks * rblocks;
   for (int i = 0; i < 2; ++i) {
     a.side[i].blocks = a.side[i].d ? (int)((a.side[i].cols + cols - 1) / cols) : 0;
@@ -700,8 +948,7 @@ void outer_typed(LoraOuter a, hipStream_t s) {
   const int64_t grid = (int64_t)(a.side[0].blocks + a.side[1].blocks) * a.units;
   if (grid > 0) {
     if (nt == 1) lora_outer_kernel<DT, 1><<<(unsigned)grid, 256, 0, s>>>(a);
-    else if (nt == 2) lora_outer_kernel<DT, 2><<<(unsigned)grid, 256, 0, s>>>(a);
-    else lora_outer_kernel<DT, 4><<<(unsigned)grid, 256, 0, s>>>(a);
+    else lora_outer_kernel<DT, 2><<<(unsigned)grid, 256, 0, s>>>(a);
   }
   const int64_t joins = (a.side[0].join_blocks + a.side[1].join_blocks) * a.adapters;
   if (joins > 0) lora_outer_join_kernel<DT><<<grid_of(joins), 256, 0, s>>>(a);
@@ -710,10 +957,11 @@ void outer_typed(LoraOuter a, hipStream_t s) {
 }  // namespace
 
 int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank) {
+  if (!lora_split(tokens)) return 1;
   // enough workgroups for the chip, each with two 64-column blocks a wave at least
   const int64_t groups = std::max<int64_t>(1, lora_max_tiles(tokens, adapters)) * ((rank + 63) / 64);
-  const int64_t want = (1024 + groups - 1) / groups, most = (cols + 511) / 512;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 16));
+  const int64_t want = (512 + groups - 1) / groups, most = (cols + 511) / 512;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 8));
 }
 
 int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank) {
@@ -731,23 +979,17 @@ hipError_t launch_lora_plan(const void *index, bool wide, int tokens, int adapte
 
 hipError_t launch_lora_down(const LoraDown &a, int dtype, bool w_t, hipStream_t stream) {
   if (a.tokens == 0) return hipSuccess;
-  if (dtype == F8LIN_BF16) down_by_layout<F8LIN_BF16>(a, w_t, stream);
-  else if (dtype == F8LIN_FP16) down_by_layout<F8LIN_FP16>(a, w_t, stream);
-  else down_by_layout<F8LIN_FP32>(a, w_t, stream);
+  if (dtype == F8LIN_BF16) down_typed<F8LIN_BF16>(a, w_t, stream);
+  else if (dtype == F8LIN_FP16) down_typed<F8LIN_FP16>(a, w_t, stream);
+  else down_typed<F8LIN_FP32>(a, w_t, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_up(const LoraUp &a, int dtype, bool w_t, hipStream_t stream) {
   if (a.tokens == 0 || a.cols == 0) return hipSuccess;
-  if (dtype == F8LIN_BF16) up_by_layout<F8LIN_BF16>(a, w_t, stream);
-  else if (dtype == F8LIN_FP16) up_by_layout<F8LIN_FP16>(a, w_t, stream);
-  else up_by_layout<F8LIN_FP32>(a, w_t, stream);
-  return hipGetLastError();
-}
-
-hipError_t launch_lora_sum(const LoraUp &a, hipStream_t stream) {
-  const int64_t n = (int64_t)a.tokens * lora_rank_pad(a.rank);
-  if (n > 0) lora_sum_kernel<<<(unsigned)((n + 1023) / 1024), 256, 0, stream>>>(a.h, a.parts, n, a.sum);
+  if (dtype == F8LIN_BF16) w_t ? up_typed<F8LIN_BF16, true>(a, stream) : up_typed<F8LIN_BF16, false>(a, stream);
+  else if (dtype == F8LIN_FP16) w_t ? up_typed<F8LIN_FP16, true>(a, stream) : up_typed<F8LIN_FP16, false>(a, stream);
+  else w_t ? up_typed<F8LIN_FP32, true>(a, stream) : up_typed<F8LIN_FP32, false>(a, stream);
   return hipGetLastError();
 }
 

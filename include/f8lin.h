@@ -584,7 +584,7 @@ int f8lin_lora_plan(const void *index, int index_bytes, int64_t tokens, int adap
 
 /* Forward.  y may be base itself (ldbase = N).  h, if set, receives the inner
  * products times their scale for the backward: T x (rank rounded up to 16)
- * fp32, in the plan's order.  ws: f8lin_lora_forward_workspace_bytes bytes,
+ * words in a form of its own.  ws: f8lin_lora_forward_workspace_bytes bytes,
  * 16-byte aligned, no initialisation needed. */
 typedef struct {
   int64_t tokens, K, N;

@@ -41,9 +41,9 @@ def plan_reference(index, adapters):
     i = np.where((index >= 0) & (index < adapters), index, adapters)
     order = np.argsort(i, kind="stable")
     starts = np.searchsorted(i[order], np.arange(adapters + 2))
-    tiles = []
+    tiles, rows = [], 16 if len(index) <= 1024 else 64
     for a in range(adapters + 1):
-        tiles += [(a, p, min(64, starts[a + 1] - p), 0) for p in range(starts[a], starts[a + 1], 64)]
+        tiles += [(a, p, min(rows, starts[a + 1] - p), 0) for p in range(starts[a], starts[a + 1], rows)]
     return order, starts, tiles, i[order]
 
 
