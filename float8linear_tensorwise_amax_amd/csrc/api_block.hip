@@ -151,7 +151,7 @@ int check_ws(const void *ws, size_t bytes, int64_t need) {
 }
 
 // What the calls keep in their workspace, in bytes from its start: H's parts,
-// or H by position and then its exponents; in the backward G's, G by rank, and
+// or H in fragments and then its exponents; in the backward G's, G by rank, and
 // the partial sums of dA and dB.
 struct LoraWs {
   bool split;
@@ -166,7 +166,8 @@ LoraWs lora_forward_ws(int64_t T, int64_t cols, int rank, int adapters) {
   w.split = lora_split(T);
   w.parts = lora_parts(T, adapters, cols, rank);
   w.h_bytes = h_bytes_of(T, rank);
-  w.exps_at = w.parts * w.h_bytes;
+  w.exps_at = w.split ? w.parts * w.h_bytes
+                      : lora_max_tiles(T, adapters) * lora_tile(T) * (int64_t)lora_rank_pad(rank) * 4;
   w.bytes = w.exps_at + (w.split ? 0 : up16((rank + 63) / 64 * T * 4));
   return w;
 }
@@ -225,11 +226,12 @@ int f8lin_lora_forward(const f8lin_lora_fwd_args *p, void *stream) {
   if (T == 0 || N == 0) return F8LIN_OK;
   hipStream_t s = (hipStream_t)stream;
   const bool split = w.split;
+  const int tiles = (int)lora_max_tiles(T, a.adapters);
   int *const exps = (int *)((uint8_t *)a.ws + w.exps_at);
-  const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, a.x, ldx, K, a.a, a.scales,
+  const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, a.x, ldx, K, a.a, a.scales,
                       split ? nullptr : (uint32_t *)a.ws, (uint32_t *)a.h, exps, split ? (float *)a.ws : nullptr, w.parts};
   F8_TRY(status_of(launch_lora_down(d, a.dtype, false, s)));
-  const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, split ? nullptr : (const uint32_t *)a.ws, exps,
+  const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, split ? nullptr : (const uint32_t *)a.ws, exps,
                     split ? (const float *)a.ws : nullptr, w.parts, a.b, a.base, ldb, N, a.y, N};
   return status_of(launch_lora_up(u, a.dtype, false, s));
 }
@@ -268,13 +270,14 @@ int f8lin_lora_backward(const f8lin_lora_bwd_args *p, void *stream) {
   hipStream_t s = (hipStream_t)stream;
   uint8_t *const ws = (uint8_t *)a.ws;
   const bool split = w.split;
+  const int tiles = (int)lora_max_tiles(T, a.adapters);
   int *const exps = (int *)(ws + w.exps_at);
   uint32_t *const gt = (uint32_t *)(ws + w.ht_at);
   if (g) {
-    const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, a.dy, lddy, N, a.b, a.scales,
+    const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, a.dy, lddy, N, a.b, a.scales,
                         split ? nullptr : (uint32_t *)ws, a.da ? gt : nullptr, exps, split ? (float *)ws : nullptr, w.parts};
     F8_TRY(status_of(launch_lora_down(d, a.dtype, true, s)));
-    const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, split ? nullptr : (const uint32_t *)ws, exps,
+    const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, split ? nullptr : (const uint32_t *)ws, exps,
                       split ? (const float *)ws : nullptr, w.parts, a.a, nullptr, K, K, a.dx, K};
     if (a.dx) F8_TRY(status_of(launch_lora_up(u, a.dtype, true, s)));
   }

@@ -33,15 +33,15 @@ __host__ __device__ inline int64_t lora_plan_words(int64_t tokens, int64_t adapt
 
 struct LoraDown {
   const int *plan;
-  int tokens, adapters, rank;
+  int tokens, adapters, rank, max_tiles;
   const void *x;  // (tokens, cols)
   int64_t ldx, cols;
   const void *w;        // (adapters, rank, cols) or (adapters, cols, rank)
   const float *scales;  // (adapters) or null
-  // H as the later products take it: by position, tokens x rank_pad (h, with
-  // fp16 data beside its exponents, one for 64 ranks of a position: rank / 64
-  // rounded up x tokens), and by rank, rank_pad x tokens (ht); either may be
-  // null.  Only with lora_split: parts_out, the parts' sums in binary32, parts
+  // H as the later products take it: in the up product's operand fragments, a
+  // tile after the other, max_tiles x 64 x rank_pad (h, with fp16 data beside
+  // its exponents, one for 64 ranks of a position: rank / 64 rounded up x
+  // tokens), and by rank, rank_pad x tokens (ht); either may be null.  Only with lora_split: parts_out, the parts' sums in binary32, parts
   // x tokens x rank_pad, in place of h.
   uint32_t *h, *ht;
   int *exponents;
@@ -50,7 +50,7 @@ struct LoraDown {
 };
 struct LoraUp {
   const int *plan;
-  int tokens, adapters, rank;
+  int tokens, adapters, rank, max_tiles;
   const uint32_t *h;  // as left by down, or null:
   const int *exponents;
   const float *parts_in;  // the parts' sums

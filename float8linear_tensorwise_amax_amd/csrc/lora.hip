@@ -35,13 +35,19 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+#ifndef DW
+#define DW 4
+#endif
+#ifndef ROT
+#define ROT 5
+#endif
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- plan
 
 // The buffer's words: {magic, tokens, adapters, tiles}, starts[adapters + 2]
 // (first sorted position of each adapter; then of the tokens without one, and
-// the end), tiles {adapter, position, rows, 0}, order[tokens] (token of each
+// the end), tiles {adapter, position, rows, first token}, order[tokens] (token of each
 // sorted position), owner[tokens] (its adapter).
 __device__ __forceinline__ const int *plan_starts(const int *p) { return p + 4; }
 __device__ __forceinline__ const i32x4 *plan_tiles(const int *p, int adapters) {
@@ -156,6 +162,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
       if (lane == 0) count[wave][av] = at + __builtin_popcountll(same);
     });
   }
+  __syncthreads();  // (order, by other waves)
   for (int a = tid; a <= groups; a += kThreads) plan[4 + a] = starts[a];
   i32x4 *const tiles = reinterpret_cast<i32x4 *>(plan + lora_tiles_at(adapters));
   for (int i = tid; i < tiles_before; i += kThreads) {
@@ -166,7 +173,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
       else hi = mid - 1;
     }
     const int p = starts[lo] + (i - tile_first[lo]) * tile_rows;
-    tiles[i] = i32x4{lo, p, min(tile_rows, starts[lo + 1] - p), 0};
+    tiles[i] = i32x4{lo, p, min(tile_rows, starts[lo + 1] - p), order[p]};
   }
   if (tid == 0) *reinterpret_cast<i32x4 *>(plan) = i32x4{kLoraMagic, tokens, adapters, tiles_before};
 }
@@ -240,6 +247,11 @@ __device__ __forceinline__ Few<DT, V> load_few(const typename MxElem<DT>::type *
     }
   }
   return f;
+}
+// V elements at p, all there.
+template <int DT, int V>
+__device__ __forceinline__ Few<DT, V> load_whole(const typename MxElem<DT>::type *p) {
+  return load_few<DT, V>(p, V);
 }
 // Element j of each of kE rows, packed as a fragment.
 template <int DT, int V>
@@ -336,6 +348,16 @@ __device__ __forceinline__ u32x4 h_halves(u32x4 a, u32x4 b, bool high) {
 // row) at a time, dealt to its waves, whose sums meet in the LDS.  With one
 // part H is written as the later products take it, by position (h) and by rank
 // (ht); else each part's sum in binary32, by position.
+//
+// Each step's loads are on their way while the step before is multiplied;
+// only blocks that reach past the columns (or ranks that are no whole loads)
+// are loaded value by value.
+template <int DT, int NT, bool W_T, int M>
+struct DownStep {
+  u32x4 x[2][M];
+  u32x4 w[2][NT];               // !W_T
+  Few<DT, NT> rows[2][kE<DT>];  // W_T
+};
 template <int DT, int NT, bool W_T, int M, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a) {
   typedef typename MxElem<DT>::type elem;
@@ -343,56 +365,86 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
   __shared__ float red[WAVES][kRows][RB + 1];
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int rblocks = (a.rank + RB - 1) / RB, per_tile = rblocks * a.parts;
-  const int64_t total = (int64_t)tiles * per_tile;
+  const int part = blockIdx.x, r0 = blockIdx.z * RB;
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
   const int blocks = (int)((C + kBlock - 1) / kBlock), part_blocks = (blocks + a.parts - 1) / a.parts;
   const int rp = lora_rank_pad(a.rank);
-  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const i32x4 tile = plan_tiles(a.plan, a.adapters)[id / per_tile];
-    const int sub = (int)(id % per_tile), part = sub % a.parts, r0 = sub / a.parts * RB;
-    if (tile.x >= a.adapters) break;  // (tokens without an adapter come last)
+  const bool whole_ranks = !W_T || a.rank % NT == 0;
+  // (the tile's words are read beside the count: there is room for as many as the grid has)
+  for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
+    const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
+    if (at >= tiles || tile.x >= a.adapters) break;  // (tokens without an adapter come last)
     const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
     const elem *x[M];
 #pragma unroll
     for (int m = 0; m < M; ++m)
       x[m] = reinterpret_cast<const elem *>(a.x) + (int64_t)order[tile.y + min(16 * m + i, tile.z - 1)] * a.ldx;
-    const int groups = (tile.z + 15) >> 4;
     v4f acc[M][NT];
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[m][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const int b1 = min(blocks, (part + 1) * part_blocks);
-    for (int b = part * part_blocks + wave; b < b1; b += WAVES) {
+    // Ranks past the end read a row (or a place in one) that is there: their sums are dropped below.
+    auto load = [&](int b, DownStep<DT, NT, W_T, M> &s) {
+      const int64_t c0 = (int64_t)b * kBlock + 2 * g * E;
+      if (whole_ranks && (int64_t)(b + 1) * kBlock <= C) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t c = (int64_t)b * kBlock + (2 * g + h) * E;
-        const int64_t left = C - c;  // (may be 0 or less)
-        u32x4 wf[NT];
-        if constexpr (!W_T) {
+        for (int h = 0; h < 2; ++h) {
+          const int64_t c = c0 + h * E;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const int r = r0 + 16 * j + i;
-            wf[j] = load_frag<DT>(w + (int64_t)min(r, a.rank - 1) * C + c, r < a.rank ? left : 0);
+          for (int m = 0; m < M; ++m) s.x[h][m] = *reinterpret_cast<const u32x4_u *>(x[m] + c);
+          if constexpr (!W_T) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              s.w[h][j] = *reinterpret_cast<const u32x4_u *>(w + (int64_t)min(r0 + 16 * j + i, a.rank - 1) * C + c);
+          } else {
+            const int r = r0 + i * NT;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s.rows[h][e] = load_whole<DT, NT>(w + (c + e) * a.rank + (r < a.rank ? r : 0));
           }
-        } else {
-          Few<DT, NT> rows[E];
-          const int r = r0 + i * NT;
-#pragma unroll
-          for (int e = 0; e < E; ++e) rows[e] = load_few<DT, NT>(w + (c + e) * a.rank + r, e < left ? a.rank - r : 0);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) wf[j] = pick<DT, NT>(rows, j);
         }
+      } else {
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          if (m >= groups) break;
-          const u32x4 xf = load_frag<DT>(x[m] + c, left);
+        for (int h = 0; h < 2; ++h) {
+          const int64_t c = c0 + h * E, left = C - c;  // (may be 0 or less)
 #pragma unroll
-          for (int j = 0; j < NT; ++j) acc[m][j] = mma<DT>(wf[j], xf, acc[m][j]);
+          for (int m = 0; m < M; ++m) s.x[h][m] = load_frag<DT>(x[m] + c, left);
+          if constexpr (!W_T) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) s.w[h][j] = load_frag<DT>(w + (int64_t)min(r0 + 16 * j + i, a.rank - 1) * C + c, left);
+          } else {
+            const int r = r0 + i * NT;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s.rows[h][e] = load_few<DT, NT>(w + (c + e) * a.rank + r, e < left ? a.rank - r : 0);
+          }
         }
       }
+    };
+    auto multiply = [&](const DownStep<DT, NT, W_T, M> &s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          u32x4 wf;
+          if constexpr (W_T) wf = pick<DT, NT>(s.rows[h], j);
+          else wf = s.w[h][j];
+#pragma unroll
+          for (int m = 0; m < M; ++m) acc[m][j] = mma<DT>(wf, s.x[h][m], acc[m][j]);
+        }
+    };
+    // tiles start at different columns, so that rows a power of two apart do not meet at the same channels
+    const int b0 = part * part_blocks, nb = min(blocks, b0 + part_blocks) - b0;
+    const int turn = nb > 0 ? (int)((uint32_t)at * ROT % (uint32_t)nb) : 0;
+    auto block = [&](int b) { return b0 + (b + turn < nb ? b + turn : b + turn - nb); };
+    DownStep<DT, NT, W_T, M> s0, s1;
+    if (wave < nb) load(block(wave), s0);
+    for (int b = wave; b < nb; b += 2 * WAVES) {
+      if (b + WAVES < nb) load(block(b + WAVES), s1);
+      multiply(s0);
+      if (b + WAVES >= nb) break;
+      if (b + 2 * WAVES < nb) load(block(b + 2 * WAVES), s0);
+      multiply(s1);
     }
     __syncthreads();  // (of the last tile's reads)
 #pragma unroll
@@ -402,43 +454,59 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
 #pragma unroll
         for (int q = 0; q < 4; ++q) red[wave][16 * m + i][W_T ? (4 * g + q) * NT + j : 16 * j + 4 * g + q] = acc[m][j][q];
     __syncthreads();
-    // the waves' sums, in their order; a thread's values are of one row
+    // the waves' sums, in their order: a thread takes E consecutive ranks of a row at a time
     const float s = a.scales ? a.scales[tile.x] : 1.0f;
-    constexpr int kEach = kRows * RB / kThreads, kLanes = RB / kEach;  // values a thread, threads a row
-    const int row = threadIdx.x / kLanes, rl = threadIdx.x % kLanes;
-    float v[kEach];
-    uint32_t mag = 0;
+    constexpr int kPer = RB / E;  // threads a row
+    for (int it = threadIdx.x; it < kRows * kPer; it += kThreads) {
+      const int row = it / kPer, r = it % kPer * E;
+      float v[E];
+      uint32_t mag = 0;
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int r = rl + kLanes * k;
-      v[k] = red[0][row][r];
+      for (int k = 0; k < E; ++k) {
+        v[k] = red[0][row][r + k];
 #pragma unroll
-      for (int t = 1; t < WAVES; ++t) v[k] += red[t][row][r];
-      // (past the rank: zero, also where x is not finite)
-      v[k] = r0 + r < a.rank ? s * v[k] : 0.0f;
-      mag = max(mag, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-    }
-    int e = 0;
-    if constexpr (DT == F8LIN_FP16) {
-#pragma unroll
-      for (int off = 1; off < kLanes; off <<= 1) mag = max(mag, (uint32_t)__shfl_xor((int)mag, off, 64));
-      e = up_exponent(mag);
-      if (a.h && row < tile.z && rl == 0) a.exponents[(int64_t)(r0 / 64) * a.tokens + tile.y + row] = e;
-    }
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int r = rl + kLanes * k;
-      const int64_t to = (int64_t)(tile.y + row) * rp + r0 + r;
-      if (row < tile.z && r0 + r < rp) {
-        if (a.parts_out) a.parts_out[(int64_t)part * a.tokens * rp + to] = v[k];
-        else if (a.h) a.h[to] = up_word<DT>(v[k], e);
+        for (int t = 1; t < WAVES; ++t) v[k] += red[t][row][r + k];
+        // (past the rank: zero, also where x is not finite)
+        v[k] = r0 + r + k < a.rank ? s * v[k] : 0.0f;
+        mag = max(mag, __float_as_uint(v[k]) & 0x7FFFFFFFu);
       }
-      if (!a.parts_out && a.ht) red[0][row][r] = __uint_as_float(h_word<DT>(v[k]));  // (this thread's own)
+      int e = 0;
+      if constexpr (DT == F8LIN_FP16) {
+#pragma unroll
+        for (int off = 1; off < kPer; off <<= 1) mag = max(mag, (uint32_t)__shfl_xor((int)mag, off, 64));
+        e = up_exponent(mag);
+        if (a.h && row < tile.z && r == 0) a.exponents[(int64_t)(r0 / 64) * a.tokens + tile.y + row] = e;
+      }
+      if (row < tile.z && r0 + r < rp) {
+        if (a.parts_out) {
+          float *const to = a.parts_out + ((int64_t)part * a.tokens + tile.y + row) * rp + r0 + r;
+#pragma unroll
+          for (int k = 0; k < E; k += 4) *reinterpret_cast<v4f *>(to + k) = v4f{v[k], v[k + 1], v[k + 2], v[k + 3]};
+        } else if (a.h) {
+          // its place in the fragment of 16 rows and 16 ranks
+          u32x4 *const to = reinterpret_cast<u32x4 *>(a.h) + ((int64_t)(at * M + row / 16) * (rp / 16) + (r0 + r) / 16) * 64;
+          const int lane_to = row % 16 + 16 * (r / E % (16 / E));
+          uint32_t o[E];
+#pragma unroll
+          for (int k = 0; k < E; ++k) o[k] = up_word<DT>(v[k], e);
+          if constexpr (DT == F8LIN_FP32) {
+            to[lane_to] = u32x4{o[0], o[1], o[2], o[3]};
+          } else {
+            const u32x4 lo = {o[0], o[1], o[2], o[3]}, hi = {o[4 % E], o[5 % E], o[6 % E], o[7 % E]};
+            to[lane_to] = h_halves(lo, hi, true);
+            to[lane_to + 32] = h_halves(lo, hi, false);
+          }
+        }
+      }
+      if (a.ht) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) red[0][row][r + k] = __uint_as_float(h_word<DT>(v[k]));  // (this thread's own)
+      }
     }
     if (!a.parts_out && a.ht) {
       __syncthreads();
-      for (int at = threadIdx.x; at < kRows * RB; at += kThreads) {
-        const int row = at % kRows, r = at / kRows;
+      for (int it = threadIdx.x; it < kRows * RB; it += kThreads) {
+        const int row = it % kRows, r = it / kRows;
         if (row < tile.z && r0 + r < rp) a.ht[(int64_t)(r0 + r) * a.tokens + tile.y + row] = __float_as_uint(red[0][row][r]);
       }
     }
@@ -474,8 +542,9 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
 // 16-bit types row 4 p + q of tile j stands for column 32 (j / 2) + 8 p + 2 q
 // + j % 2, in binary32 for 16 j + 4 p + q.
 
-// W's fragments for 16 ranks from r0, 64 columns from c0.
-template <int DT, bool W_T>
+// W's fragments for 16 ranks from r0, 64 columns from c0 (FULL: all there).
+// What lies past the ranks is zero, whatever the memory holds: H is zero there.
+template <int DT, bool W_T, bool FULL>
 __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, int rank, int64_t C, int64_t c0, int r0,
                                            u32x4 (&wf)[4]) {
   constexpr int E = kE<DT>;
@@ -487,14 +556,18 @@ __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, i
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + (F32 ? 16 * j + i : 32 * (j >> 1) + 2 * i + (j & 1));
-      wf[j] = load_frag<DT>(w + min(c, C - 1) * rank + rg, c < C ? rank - rg : 0);
+      if (FULL && r0 + 16 <= rank) wf[j] = *reinterpret_cast<const u32x4_u *>(w + c * rank + rg);
+      else wf[j] = load_frag<DT>(w + min(c, C - 1) * rank + rg, c < C ? rank - rg : 0);
     }
   } else if constexpr (F32) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + 16 * j + i;
 #pragma unroll
-      for (int e = 0; e < E; ++e) wf[j][e] = rg + e < rank && c < C ? w[(int64_t)(rg + e) * C + c] : 0u;
+      for (int e = 0; e < E; ++e) {
+        const uint32_t v = w[(int64_t)min(rg + e, rank - 1) * C + (FULL ? c : min(c, C - 1))];
+        wf[j][e] = rg + e < rank ? v : 0u;
+      }
     }
   } else {
 #pragma unroll
@@ -502,27 +575,37 @@ __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, i
       Few<DT, 2> rows[E];
       const int64_t c = c0 + 32 * jj + 2 * i;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        rows[e] = load_few<DT, 2>(w + (int64_t)(rg + e) * C + c, rg + e < rank ? (int)max((int64_t)0, min((int64_t)2, C - c)) : 0);
+      for (int e = 0; e < E; ++e) {
+        const typename MxElem<DT>::type *const from = w + (int64_t)min(rg + e, rank - 1) * C + c;
+        if constexpr (FULL) rows[e] = load_whole<DT, 2>(from);
+        else rows[e] = load_few<DT, 2>(from, (int)max((int64_t)0, min((int64_t)2, C - c)));
+        if (rg + e >= rank) rows[e].w[0] = 0u;
+      }
       wf[2 * jj] = pick<DT, 2>(rows, 0);
       wf[2 * jj + 1] = pick<DT, 2>(rows, 1);
     }
   }
 }
-// base's pieces of one row.
-template <int DT>
-__device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, bool in, int64_t c0, u32x4 (&raw)[16 / kE<DT>]) {
+// base's pieces of one row (FULL: all there).
+template <int DT, bool FULL>
+__device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, int64_t c0, u32x4 (&raw)[16 / kE<DT>]) {
   constexpr int E = kE<DT>;
   const int g = (threadIdx.x & 63) >> 4;
+  const typename MxElem<DT>::type *const base = reinterpret_cast<const typename MxElem<DT>::type *>(a.base) + t * a.ldbase;
+  if (!a.base) {
+#pragma unroll
+    for (int h = 0; h < 16 / E; ++h) raw[h] = u32x4{0, 0, 0, 0};
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < 16 / E; ++h) {
     const int64_t c = c0 + 4 * E * h + E * g;
-    raw[h] = u32x4{0, 0, 0, 0};
-    if (a.base && in) raw[h] = load_frag<DT>(reinterpret_cast<const typename MxElem<DT>::type *>(a.base) + t * a.ldbase + c, a.cols - c);
+    if constexpr (FULL) raw[h] = *reinterpret_cast<const u32x4_u *>(base + c);
+    else raw[h] = load_frag<DT>(base + c, a.cols - c);
   }
 }
 // One row's pieces of y.
-template <int DT>
+template <int DT, bool FULL>
 __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapted, int64_t c0, const u32x4 (&raw)[16 / kE<DT>],
                                          const v4f (&acc)[4]) {
   typedef typename MxElem<DT>::type elem;
@@ -532,7 +615,7 @@ __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapte
 #pragma unroll
   for (int h = 0; h < 16 / E; ++h) {
     const int64_t c = c0 + 4 * E * h + E * g;
-    const int n = (int)max((int64_t)0, min((int64_t)E, a.cols - c));
+    const int n = FULL ? E : (int)max((int64_t)0, min((int64_t)E, a.cols - c));
     if (n == 0) break;
     elem *const y = reinterpret_cast<elem *>(a.y) + t * a.ldy + c;
     uint32_t o[8];
@@ -554,177 +637,206 @@ __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapte
     }
   }
 }
-// H's fragment of 16 ranks for one row (position p).
-template <int DT>
-__device__ __forceinline__ u32x4 up_h(const LoraUp &a, int p, int rp, int r0) {
-  constexpr int E = kE<DT>;
-  const int g = (threadIdx.x & 63) >> 4;
-  const uint32_t *const h = a.h + (int64_t)p * rp + r0 + (DT == F8LIN_FP32 ? g : (g & 1)) * E;
-  if constexpr (DT == F8LIN_FP32) return *reinterpret_cast<const u32x4 *>(h);
-  else return h_halves(*reinterpret_cast<const u32x4 *>(h), *reinterpret_cast<const u32x4 *>(h + 4), g < 2);
-}
-
 // Tiles of 64 rows, H in its final form.  Up to 64 ranks (NB blocks of 16): W
 // stays in registers, the rows pass by in groups of 16, the next group's base
 // and H on their way.  NB = 0: any rank, 64 at a time, all rows' sums kept.
-template <int DT, bool W_T, int NB>
-__global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
+template <int DT, bool W_T, int NB, bool FULL>
+__device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, int64_t c0) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kPieces = 16 / kE<DT>;
-  const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15;
+  const int i = threadIdx.x & 15;
   const int64_t C = a.cols;
-  const int cblocks = (int)((C + 255) / 256);
-  const int64_t total = (int64_t)tiles * cblocks;
-  const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   const int rp = lora_rank_pad(a.rank);
-  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const i32x4 tile = plan_tiles(a.plan, a.adapters)[id / cblocks];
-    const int64_t c0 = (id % cblocks) * 256 + 64 * wave;
-    if (c0 >= C) continue;
-    const bool adapted = tile.x < a.adapters;
-    const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
-    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto position = [&](int m) { return tile.y + min(16 * m + i, tile.z - 1); };
-    auto scale = [&](v4f (&acc)[4], int m, int block) {
-      if constexpr (DT == F8LIN_FP16) {
-        const float f = ldexpf(1.0f, a.exponents[(int64_t)block * a.tokens + position(m)]);
+  const bool adapted = tile.x < a.adapters;
+  const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
+  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto position = [&](int m) { return tile.y + min(16 * m + i, tile.z - 1); };
+  // H's fragments of the tile, of groups of 16 rows and blocks of 16 ranks; what belongs to rows that are not there is
+  // whatever the memory holds, and goes to no row that is
+  const u32x4 *const h = reinterpret_cast<const u32x4 *>(a.h) + (int64_t)at * 4 * (rp / 16) * 64 + (threadIdx.x & 63);
+  auto scale = [&](v4f (&acc)[4], int exponent) {
+    if constexpr (DT == F8LIN_FP16) {
+      const float f = ldexpf(1.0f, exponent);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] *= f;
+      for (int j = 0; j < 4; ++j) acc[j] *= f;
+    }
+  };
+  if (!adapted) {  // y is base
+#pragma unroll 1
+    for (int m = 0; 16 * m < tile.z; ++m) {
+      const int64_t t = order[position(m)];
+      u32x4 raw[kPieces];
+      const v4f acc[4] = {zero, zero, zero, zero};
+      up_base<DT, FULL>(a, t, c0, raw);
+      if (16 * m + i < tile.z) up_store<DT, FULL>(a, t, false, c0, raw, acc);
+    }
+    return;
+  }
+  if constexpr (NB > 0) {
+    u32x4 wf[NB][4];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) up_weights<DT, W_T, FULL>(w, a.rank, C, c0, min(16 * k, rp - 16), wf[k]);
+    u32x4 raw[2][kPieces], hf[2][NB];
+    int64_t t[2];
+    int exponent[2];
+    const int groups = (tile.z + 15) >> 4;
+    auto load = [&](int m, int b) {
+      t[b] = order[position(m)];
+      up_base<DT, FULL>(a, t[b], c0, raw[b]);
+      if constexpr (DT == F8LIN_FP16) exponent[b] = a.exponents[position(m)];
+      // (a block past the padded ranks: some other's, times zero)
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        hf[b][k] = h[(m * (rp / 16) + min(k, rp / 16 - 1)) * 64];
+        if (16 * k >= rp) hf[b][k] = u32x4{0, 0, 0, 0};
       }
     };
-    if constexpr (NB > 0) {
-      u32x4 wf[NB][4];
-      if (adapted) {
+    load(0, 0);
 #pragma unroll
-        for (int k = 0; k < NB; ++k) up_weights<DT, W_T>(w, a.rank, C, c0, 16 * k, wf[k]);
-      }
-      u32x4 raw[2][kPieces], hf[2][NB];
-      int64_t t[2];
-      const int groups = (tile.z + 15) >> 4;
-      auto load = [&](int m, int b) {
-        t[b] = order[position(m)];
-        up_base<DT>(a, t[b], 16 * m + i < tile.z, c0, raw[b]);
-        if (adapted) {
+    for (int m = 0; m < 4; ++m) {
+      if (m >= groups) break;
+      if (m + 1 < groups) load(m + 1, (m + 1) & 1);
+      v4f acc[4] = {zero, zero, zero, zero};
 #pragma unroll
-          for (int k = 0; k < NB; ++k) hf[b][k] = 16 * k < rp ? up_h<DT>(a, position(m), rp, 16 * k) : u32x4{0, 0, 0, 0};
-        }
-      };
-      load(0, 0);
+      for (int k = 0; k < NB; ++k)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (m >= groups) break;
-        if (m + 1 < groups) load(m + 1, (m + 1) & 1);
-        v4f acc[4] = {zero, zero, zero, zero};
-        if (adapted) {
+        for (int j = 0; j < 4; ++j) acc[j] = mma<DT>(wf[k][j], hf[m & 1][k], acc[j]);
+      scale(acc, exponent[m & 1]);
+      if (16 * m + i < tile.z) up_store<DT, FULL>(a, t[m & 1], true, c0, raw[m & 1], acc);
+    }
+  } else {
+    v4f sum[4][4];
 #pragma unroll
-          for (int k = 0; k < NB; ++k)
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = mma<DT>(wf[k][j], hf[m & 1][k], acc[j]);
-          scale(acc, m, 0);
-        }
-        if (16 * m + i < tile.z) up_store<DT>(a, t[m & 1], adapted, c0, raw[m & 1], acc);
-      }
-    } else {
-      v4f sum[4][4];
+      for (int j = 0; j < 4; ++j) sum[m][j] = zero;
+    for (int r0 = 0; r0 < rp; r0 += 64) {
+      v4f acc[4][4];
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[m][j] = zero;
-      for (int r0 = 0; adapted && r0 < rp; r0 += 64) {
-        v4f acc[4][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][j] = zero;
-        for (int r = r0; r < min(rp, r0 + 64); r += 16) {
-          u32x4 wf[4];
-          up_weights<DT, W_T>(w, a.rank, C, c0, r, wf);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const u32x4 hf = up_h<DT>(a, position(m), rp, r);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[m][j] = mma<DT>(wf[j], hf, acc[m][j]);
-          }
-        }
+        for (int j = 0; j < 4; ++j) acc[m][j] = zero;
+      for (int r = r0; r < min(rp, r0 + 64); r += 16) {
+        u32x4 wf[4];
+        up_weights<DT, W_T, FULL>(w, a.rank, C, c0, r, wf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          scale(acc[m], m, r0 / 64);
+          const u32x4 hf = h[(m * (rp / 16) + r / 16) * 64];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sum[m][j] += acc[m][j];
+          for (int j = 0; j < 4; ++j) acc[m][j] = mma<DT>(wf[j], hf, acc[m][j]);
         }
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        if (16 * m + i >= tile.z) break;
-        const int64_t t = order[position(m)];
-        u32x4 raw[kPieces];
-        up_base<DT>(a, t, true, c0, raw);
-        up_store<DT>(a, t, adapted, c0, raw, sum[m]);
+        if constexpr (DT == F8LIN_FP16) scale(acc[m], a.exponents[(int64_t)(r0 / 64) * a.tokens + position(m)]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[m][j] += acc[m][j];
       }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t t = order[position(m)];
+      u32x4 raw[kPieces];
+      up_base<DT, FULL>(a, t, c0, raw);
+      if (16 * m + i < tile.z) up_store<DT, FULL>(a, t, true, c0, raw, sum[m]);
     }
   }
 }
 
+template <int DT, bool W_T, int NB>
+__global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
+  const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
+  const int64_t C = a.cols;
+  const int *const order = plan_order(a.plan, a.tokens, a.adapters);
+  const int64_t c0 = (int64_t)blockIdx.x * 256 + 64 * (threadIdx.x >> 6);
+  if (c0 >= C) return;
+  for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
+    const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
+    if (at >= tiles) break;
+    if (c0 + 64 <= C) up_tile<DT, W_T, NB, true>(a, tile, at, order, c0);
+    else up_tile<DT, W_T, NB, false>(a, tile, at, order, c0);
+  }
+}
+
 // Tiles of 16 rows, H as the sums of its parts.
-template <int DT, bool W_T>
-__global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
+template <int DT, bool W_T, int G, bool FULL>
+__device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, const int *order, int64_t c0) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>;
   constexpr bool F32 = DT == F8LIN_FP32;
-  const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int64_t C = a.cols;
-  const int cblocks = (int)((C + 255) / 256);
-  const int64_t total = (int64_t)tiles * cblocks;
-  const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   const int rp = lora_rank_pad(a.rank);
   const int64_t part_ld = (int64_t)a.tokens * rp;
-  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const i32x4 tile = plan_tiles(a.plan, a.adapters)[id / cblocks];
-    const int64_t c0 = (id % cblocks) * 256 + 64 * wave;
-    if (c0 >= C) continue;
-    const bool adapted = tile.x < a.adapters, in = i < tile.z;
-    const int p = tile.y + min(i, tile.z - 1);
-    const int64_t t = order[p];
-    u32x4 raw[16 / E];
-    up_base<DT>(a, t, in, c0, raw);
-    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    v4f acc[4] = {zero, zero, zero, zero};
-    if (adapted) {
-      const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
-      for (int r0 = 0; r0 < rp; r0 += 16) {
-        u32x4 wf[4], wl[4];
-        up_weights<DT, W_T>(w, a.rank, C, c0, r0, wf);
-        u32x4 hw[E / 4];
+  const bool adapted = tile.x < a.adapters;
+  const int p = tile.y + min(i, tile.z - 1);
+  const int64_t t = tile.z == 1 ? tile.w : order[p];
+  u32x4 raw[G][16 / E];
 #pragma unroll
-        for (int e = 0; e < E / 4; ++e) {
-          const float *const from = a.parts_in + (int64_t)p * rp + r0 + (F32 ? g : (g & 1)) * E + 4 * e;
-          v4f s = *reinterpret_cast<const v4f *>(from);
-          for (int k = 1; k < a.parts; ++k) s += *reinterpret_cast<const v4f *>(from + k * part_ld);
+  for (int k = 0; k < G; ++k) up_base<DT, FULL>(a, t, c0 + 64 * k, raw[k]);
+  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  v4f acc[G][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) hw[e][k] = h_word<DT>(s[k]);
-        }
-        if constexpr (F32) {
+  for (int k = 0; k < G; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = mma<DT>(wf[j], hw[0], acc[j]);
-        } else {
-          if constexpr (DT == F8LIN_FP16) {
+    for (int j = 0; j < 4; ++j) acc[k][j] = zero;
+  if (adapted) {
+    const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
+    for (int r0 = 0; r0 < rp; r0 += 16) {
+      u32x4 wf[G][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split_f16(wf[j], wf[j], wl[j]);
-          }
-          const u32x4 hf = h_halves(hw[0], hw[E / 4 - 1], g < 2);
-          // (an infinite H meets the operand's main half only: the other is often zero)
-          const u32x4 finite = DT == F8LIN_FP16 ? no_inf(hf) : hf;
+      for (int k = 0; k < G; ++k) up_weights<DT, W_T, FULL>(w, a.rank, C, c0 + 64 * k, r0, wf[k]);
+      u32x4 hw[E / 4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[j] = mma<F8LIN_BF16>(wf[j], hf, acc[j]);
-            if constexpr (DT == F8LIN_FP16) acc[j] = mma<F8LIN_BF16>(wl[j], finite, acc[j]);
-          }
-        }
+      for (int e = 0; e < E / 4; ++e) {
+        const float *const from = a.parts_in + (int64_t)p * rp + r0 + (F32 ? g : (g & 1)) * E + 4 * e;
+        v4f s = *reinterpret_cast<const v4f *>(from);
+#pragma unroll 4
+        for (int k = 1; k < a.parts; ++k) s += *reinterpret_cast<const v4f *>(from + k * part_ld);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) hw[e][k] = h_word<DT>(s[k]);
       }
+      const u32x4 hf = F32 ? hw[0] : h_halves(hw[0], hw[E / 4 - 1], g < 2);
+      // (an infinite H meets the operand's main half only: the other is often zero)
+      const u32x4 finite = DT == F8LIN_FP16 ? no_inf(hf) : hf;
+#pragma unroll
+      for (int k = 0; k < G; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (F32) {
+            acc[k][j] = mma<DT>(wf[k][j], hf, acc[k][j]);
+          } else if constexpr (DT == F8LIN_FP16) {
+            u32x4 whi, wlo;
+            split_f16(wf[k][j], whi, wlo);
+            acc[k][j] = mma<F8LIN_BF16>(whi, hf, acc[k][j]);
+            acc[k][j] = mma<F8LIN_BF16>(wlo, finite, acc[k][j]);
+          } else {
+            acc[k][j] = mma<F8LIN_BF16>(wf[k][j], hf, acc[k][j]);
+          }
+        }
     }
-    if (in) up_store<DT>(a, t, adapted, c0, raw, acc);
+  }
+  if (i < tile.z) {
+#pragma unroll
+    for (int k = 0; k < G; ++k) up_store<DT, FULL>(a, t, adapted, c0 + 64 * k, raw[k], acc[k]);
+  }
+}
+
+template <int DT, bool W_T, int G>
+__global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
+  const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
+  const int64_t C = a.cols;
+  const int *const order = plan_order(a.plan, a.tokens, a.adapters);
+  const int64_t c0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 64 * G;
+  if (c0 >= C) return;
+  for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
+    const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
+    if (at >= tiles) break;
+    if (c0 + 64 * G <= C) up_few_tile<DT, W_T, G, true>(a, tile, order, c0);
+    else {
+#pragma unroll 1
+      for (int64_t c = c0; c < min(C, c0 + 64 * G); c += 64) up_few_tile<DT, W_T, 1, false>(a, tile, order, c);
+    }
   }
 }
 
@@ -744,7 +856,7 @@ struct OuterStep {
   u32x4 h[NT][kE<DT> / 4];
 };
 template <int DT, int NT>
-__global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
+__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const LoraOuter a) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>, kCols = 16 * E, kStep = 4 * E;
   if (plan_tile_count(a.plan, a.tokens, a.adapters) < 0) return;
@@ -761,6 +873,12 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
   // a workgroup's waves: `across` blocks of ranks of the same columns, which they so read once; columns fastest: the
   // workgroups of a chunk read the same H
   const int across = a.across;
+#if 1
+  { // rounds of 8 units, one per XCD
+    const int per = 8 * side.blocks, round = id / per, in = id % per, n = min(8, a.units - 8 * round);
+    id = (8 * round + in % n) * side.blocks + in / n;
+  }
+#endif
   const int64_t cw = ((int64_t)(id % side.blocks) * (4 / across) + wave / across) * kCols, c0 = cw + E * i;
   const int unit = id / side.blocks, chunk = unit % a.chunks, r0 = (unit / a.chunks * across + wave % across) * 16 * NT;
   const int64_t C = side.cols;
@@ -768,6 +886,7 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
   const int64_t first = (int64_t)chunk * a.chunk;
   const int end = (int)min((int64_t)adapted, first + a.chunk);
   const int cn = (int)max((int64_t)0, min((int64_t)E, C - c0));
+  const bool full = cw + kCols <= C;
   const elem *const xc = reinterpret_cast<const elem *>(side.x) + c0;
   for (int p0 = (int)min((int64_t)adapted, first); p0 < end;) {
     const int ad = owner[p0], p1 = min(end, starts[ad + 1]);
@@ -779,9 +898,12 @@ __global__ __launch_bounds__(256) void lora_outer_kernel(const LoraOuter a) {
     // (nothing behind the adapter's tokens gets in, whatever it holds)
     auto load = [&](int p, OuterStep<DT, NT> &s) {
       const int at = p + g * E;
-      if (p + kStep <= p1) {
+      if (p + kStep <= p1 && full) {
+        int t[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s.rows[e] = load_few<DT, E>(xc + (int64_t)order[at + e] * side.ldx, cn);
+        for (int e = 0; e < E; ++e) t[e] = order[at + e];
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.rows[e] = load_whole<DT, E>(xc + (int64_t)t[e] * side.ldx);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int r = min(r0 + 16 * j + i, rp - 1);  // (past the padded rank: not stored)
@@ -902,10 +1024,13 @@ unsigned grid_of(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, 
 // Ranks of 16 a workgroup takes: one, two or four.
 int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 
+// Tiles along the grid's y (which the kernels stride over).
+dim3 tile_grid(int64_t x, int max_tiles, int z) { return dim3((unsigned)x, (unsigned)std::min(max_tiles, 65535), (unsigned)z); }
+
 template <int DT, bool W_T, int M, int WAVES>
 void down_rows(const LoraDown &a, hipStream_t s) {
   const int nt = rank_tiles(a.rank), rblocks = (a.rank + 16 * nt - 1) / (16 * nt);
-  const unsigned grid = grid_of(lora_max_tiles(a.tokens, a.adapters) * rblocks * a.parts);
+  const dim3 grid = tile_grid(a.parts, a.max_tiles, rblocks);
   if (nt == 1) lora_down_kernel<DT, 1, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
   else if (nt == 2) lora_down_kernel<DT, 2, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
   else lora_down_kernel<DT, 4, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
@@ -916,8 +1041,8 @@ void down_typed(const LoraDown &a, bool w_t, hipStream_t s) {
     if (w_t) down_rows<DT, true, 1, 4>(a, s);
     else down_rows<DT, false, 1, 4>(a, s);
   } else {
-    if (w_t) down_rows<DT, true, 4, 8>(a, s);
-    else down_rows<DT, false, 4, 8>(a, s);
+    if (w_t) down_rows<DT, true, 4, DW>(a, s);
+    else down_rows<DT, false, 4, DW>(a, s);
   }
   if (a.parts_out && a.ht) {
     const int64_t grid = (int64_t)((a.tokens + 15) / 16) * (lora_rank_pad(a.rank) / 16);
@@ -926,8 +1051,15 @@ void down_typed(const LoraDown &a, bool w_t, hipStream_t s) {
 }
 template <int DT, bool W_T>
 void up_typed(const LoraUp &a, hipStream_t s) {
-  const unsigned grid = grid_of(lora_max_tiles(a.tokens, a.adapters) * ((a.cols + 255) / 256));
-  if (a.parts_in) lora_up_few_kernel<DT, W_T><<<grid, 256, 0, s>>>(a);
+  const dim3 grid = tile_grid((a.cols + 255) / 256, a.max_tiles, 1);
+  if (a.parts_in) {
+#ifndef FG
+#define FG 4
+#endif
+    if (FG > 1 && (int64_t)grid.x * a.max_tiles >= 1024)
+      lora_up_few_kernel<DT, W_T, FG><<<tile_grid((a.cols + 256 * FG - 1) / (256 * FG), a.max_tiles, 1), 256, 0, s>>>(a);
+    else lora_up_few_kernel<DT, W_T, 1><<<grid, 256, 0, s>>>(a);
+  }
   else if (a.rank <= 16) lora_up_kernel<DT, W_T, 1><<<grid, 256, 0, s>>>(a);
   else if (a.rank <= 32) lora_up_kernel<DT, W_T, 2><<<grid, 256, 0, s>>>(a);
   else if (a.rank <= 64) lora_up_kernel<DT, W_T, 4><<<grid, 256, 0, s>>>(a);
@@ -960,13 +1092,19 @@ int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank) {
   if (!lora_split(tokens)) return 1;
   // enough workgroups for the chip, each with two 64-column blocks a wave at least
   const int64_t groups = std::max<int64_t>(1, lora_max_tiles(tokens, adapters)) * ((rank + 63) / 64);
-  const int64_t want = (512 + groups - 1) / groups, most = (cols + 511) / 512;
+  #ifndef PW
+#define PW 256
+#endif
+  const int64_t want = (PW + groups - 1) / groups, most = (cols + 511) / 512;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 8));
 }
 
 int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank) {
   const int64_t per_chunk = ((K + 511) / 512 + (N + 511) / 512) * ((rank + 63) / 64);
-  const int64_t chunks = std::max<int64_t>(1, 2048 / std::max<int64_t>(1, per_chunk));
+  #ifndef OW
+#define OW 512
+#endif
+  const int64_t chunks = std::max<int64_t>(1, OW / std::max<int64_t>(1, per_chunk));
   const int64_t each = ((tokens + chunks - 1) / chunks + 31) / 32 * 32;
   return (int)std::min<int64_t>(4096, std::max<int64_t>(128, each));
 }

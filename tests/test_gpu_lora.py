@@ -43,7 +43,7 @@ def plan_reference(index, adapters):
     starts = np.searchsorted(i[order], np.arange(adapters + 2))
     tiles, rows = [], 16 if len(index) <= 1024 else 64
     for a in range(adapters + 1):
-        tiles += [(a, p, min(rows, starts[a + 1] - p), 0) for p in range(starts[a], starts[a + 1], rows)]
+        tiles += [(a, p, min(rows, starts[a + 1] - p), order[p]) for p in range(starts[a], starts[a + 1], rows)]
     return order, starts, tiles, i[order]
 
 
