@@ -12,7 +12,8 @@ constexpr int kLoraMaxAdapters = 2047;   // of a plan: 16 waves' counts of each 
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraMagic = 0x4C6F5241;
 
-__host__ __device__ inline int lora_rank_pad(int rank) { return (rank + 15) / 16 * 16; }
+// Ranks of H: 16, or blocks of 32.
+__host__ __device__ inline int lora_rank_pad(int rank) { return rank <= 16 ? 16 : (rank + 31) / 32 * 32; }
 // Rows of a tile: few tokens are mostly single ones of many adapters, or need
 // more workgroups than 64-row tiles give.
 __host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
@@ -76,7 +77,7 @@ struct LoraOuter {
   int tokens, adapters, rank;
   int chunk, chunks;  // sorted positions a workgroup takes, and how many such
   LoraOuterSide side[2];
-  int units, across;  // (set by the launch)
+  int units, across, split;  // (set by the launch)
 };
 
 // Whether H passes between the products as sums of parts (16-row tiles), into

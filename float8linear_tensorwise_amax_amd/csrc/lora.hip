@@ -28,16 +28,13 @@
 #include <algorithm>
 
 #include "lora.h"
-#include "mx_common.h"
+#include "rows.h"
 
 namespace f8lin {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-#ifndef DW
-#define DW 4
-#endif
 #ifndef ROT
 #define ROT 5
 #endif
@@ -200,58 +197,28 @@ __device__ __forceinline__ v4f mma(u32x4 a, u32x4 b, v4f c) {
   }
 }
 
-// kE values at p, of which n exist (the others are 0).
+// The same with 8 bytes of a 16-bit type along a contraction of 16.
 template <int DT>
-__device__ __forceinline__ u32x4 load_frag(const typename MxElem<DT>::type *p, int64_t n) {
-  if (n >= kE<DT>) return *reinterpret_cast<const u32x4_u *>(p);
-  uint32_t e[8];
-#pragma unroll
-  for (int i = 0; i < kE<DT>; ++i) e[i] = i < n ? (uint32_t)p[i] : 0u;
-  if constexpr (DT == F8LIN_FP32) return u32x4{e[0], e[1], e[2], e[3]};
-  else return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+__device__ __forceinline__ v4f mma16(u32x2 a, u32x2 b, v4f c) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+  if constexpr (DT == F8LIN_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0, 0);
 }
 
-// V consecutive elements (V = 1, 2, 4, 8 16-bit ones or 1, 2, 4 binary32 ones)
-// as words; a word holds two 16-bit elements, or a lone one in its low half.
-template <int DT, int V>
-struct Few {
-  static constexpr int kWords = DT == F8LIN_FP32 ? V : (V + 1) / 2;
-  uint32_t w[kWords];
-};
-template <int DT, int V>
-__device__ __forceinline__ Few<DT, V> load_few(const typename MxElem<DT>::type *p, int n) {
-  Few<DT, V> f;
-  constexpr int kW = Few<DT, V>::kWords;
-  if (n >= V) {
-    if constexpr (DT != F8LIN_FP32 && V == 1) {
-      f.w[0] = *p;
-    } else if constexpr (kW == 1) {
-      typedef uint32_t u32_u __attribute__((aligned(2)));
-      f.w[0] = *reinterpret_cast<const u32_u *>(p);
-    } else if constexpr (kW == 2) {
-      const u32x2 v = *reinterpret_cast<const u32x2_u *>(p);
-      f.w[0] = v.x, f.w[1] = v.y;
-    } else {
-      const u32x4 v = *reinterpret_cast<const u32x4_u *>(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f.w[i] = v[i];
-    }
-  } else {
-    uint32_t e[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = i < n ? (uint32_t)p[i] : 0u;
-#pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      if constexpr (DT == F8LIN_FP32) f.w[i] = e[i];
-      else f.w[i] = e[2 * i] | (2 * i + 1 < V ? e[(2 * i + 1) % V] << 16 : 0u);
-    }
-  }
-  return f;
+template <int DT>
+__device__ __forceinline__ u32x4 frag_of(const Few<DT, kE<DT>> &f) {
+  return u32x4{f.w[0], f.w[1], f.w[2], f.w[3]};
 }
-// V elements at p, all there.
-template <int DT, int V>
-__device__ __forceinline__ Few<DT, V> load_whole(const typename MxElem<DT>::type *p) {
-  return load_few<DT, V>(p, V);
+
+// Element j of each of four rows, packed.
+template <int V>
+__device__ __forceinline__ u32x2 pick4(const Few<F8LIN_BF16, V> &a, const Few<F8LIN_BF16, V> &b, const Few<F8LIN_BF16, V> &c,
+                                       const Few<F8LIN_BF16, V> &d, int j) {
+  const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+  return u32x2{__builtin_amdgcn_perm(b.w[j >> 1], a.w[j >> 1], sel), __builtin_amdgcn_perm(d.w[j >> 1], c.w[j >> 1], sel)};
 }
 // Element j of each of kE rows, packed as a fragment.
 template <int DT, int V>
@@ -280,31 +247,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float left_over(float a, float rounded) {
   return (__float_as_uint(rounded) & 0x7F800000u) == 0x7F800000u ? 0.0f : a - rounded;
 }
-// Eight values as bf16 plus bf16.
-__device__ __forceinline__ void split8(const float (&v)[8], u32x4 &hi, u32x4 &lo) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-    lo[e] = pack_bf16(left_over(v[2 * e], bf16_lo(hi[e])), left_over(v[2 * e + 1], bf16_hi(hi[e])));
-  }
-}
-// Pairs of bf16 with infinities and NaN as zeros.
-__device__ __forceinline__ u32x4 no_inf(u32x4 f) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if ((f[e] & 0x7F80u) == 0x7F80u) f[e] &= 0xFFFF0000u;
-    if ((f[e] & 0x7F800000u) == 0x7F800000u) f[e] &= 0x0000FFFFu;
-  }
+// A pair of bf16 with infinities and NaN as zeros.
+__device__ __forceinline__ uint32_t no_inf(uint32_t f) {
+  if ((f & 0x7F80u) == 0x7F80u) f &= 0xFFFF0000u;
+  if ((f & 0x7F800000u) == 0x7F800000u) f &= 0x0000FFFFu;
   return f;
 }
-__device__ __forceinline__ void split_f16(u32x4 f, u32x4 &hi, u32x4 &lo) {
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[2 * e] = f16_bits_to_f32(f[e] & 0xFFFFu);
-    v[2 * e + 1] = f16_bits_to_f32(f[e] >> 16);
-  }
-  split8(v, hi, lo);
+// A pair of fp16 as pairs of bf16: rounded, and what that left over.
+__device__ __forceinline__ void split_f16(uint32_t f, uint32_t &hi, uint32_t &lo) {
+  const float a = f16_bits_to_f32(f & 0xFFFFu), b = f16_bits_to_f32(f >> 16);
+  hi = pack_bf16(a, b);
+  lo = pack_bf16(left_over(a, bf16_lo(hi)), left_over(b, bf16_hi(hi)));
 }
 
 // ---------------------------------------------------------------- intermediates
@@ -349,32 +302,35 @@ __device__ __forceinline__ u32x4 h_halves(u32x4 a, u32x4 b, bool high) {
 // part H is written as the later products take it, by position (h) and by rank
 // (ht); else each part's sum in binary32, by position.
 //
-// Each step's loads are on their way while the step before is multiplied;
-// only blocks that reach past the columns (or ranks that are no whole loads)
-// are loaded value by value.
+// Each step's loads are on their way while the step before is multiplied.  The
+// last block of columns ends with the row, what it shares with the one before
+// taken as zero (SMALL, fewer columns than a block: an element at a time).
 template <int DT, int NT, bool W_T, int M>
 struct DownStep {
-  u32x4 x[2][M];
-  u32x4 w[2][NT];               // !W_T
-  Few<DT, NT> rows[2][kE<DT>];  // W_T
+  Few<DT, kE<DT>> x[2][M];
+  Few<DT, kE<DT>> w[2][W_T ? 1 : NT];  // !W_T
+  Few<DT, NT> rows[2][kE<DT>];         // W_T
 };
-template <int DT, int NT, bool W_T, int M, int WAVES>
+template <int DT, int NT, bool W_T, int M, int WAVES, bool SMALL>
 __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>, kBlock = 8 * E, RB = 16 * NT, kRows = 16 * M, kThreads = 64 * WAVES;
   __shared__ float red[WAVES][kRows][RB + 1];
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
-  const int part = blockIdx.x, r0 = blockIdx.z * RB;
+  // (a tile's rows are dealt to as many workgroups as M leaves)
+  const int part = blockIdx.x % a.parts, first_row = blockIdx.x / a.parts * kRows, r0 = blockIdx.z * RB;
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
   const int blocks = (int)((C + kBlock - 1) / kBlock), part_blocks = (blocks + a.parts - 1) / a.parts;
-  const int rp = lora_rank_pad(a.rank);
+  const int rp = lora_rank_pad(a.rank), tile_rows = lora_tile(a.tokens);
   const bool whole_ranks = !W_T || a.rank % NT == 0;
   // (the tile's words are read beside the count: there is room for as many as the grid has)
   for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
-    const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
+    i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles || tile.x >= a.adapters) break;  // (tokens without an adapter come last)
+    tile.y += first_row, tile.z -= first_row;
+    if (tile.z <= 0) continue;
     const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
     const elem *x[M];
 #pragma unroll
@@ -387,36 +343,50 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
       for (int j = 0; j < NT; ++j) acc[m][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     // Ranks past the end read a row (or a place in one) that is there: their sums are dropped below.
     auto load = [&](int b, DownStep<DT, NT, W_T, M> &s) {
-      const int64_t c0 = (int64_t)b * kBlock + 2 * g * E;
-      if (whole_ranks && (int64_t)(b + 1) * kBlock <= C) {
+      const bool last = !SMALL && (int64_t)(b + 1) * kBlock > C;
+      const int64_t at0 = (int64_t)b * kBlock, c0 = (last ? C - kBlock : at0) + 2 * g * E;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t c = c0 + h * E;
+      for (int h = 0; h < 2; ++h) {
+        const int64_t c = c0 + h * E;
 #pragma unroll
-          for (int m = 0; m < M; ++m) s.x[h][m] = *reinterpret_cast<const u32x4_u *>(x[m] + c);
-          if constexpr (!W_T) {
+        for (int m = 0; m < M; ++m) s.x[h][m] = SMALL ? load_each<DT, E>(x[m], c, C) : load_whole<DT, E>(x[m] + c);
+        if constexpr (!W_T) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-              s.w[h][j] = *reinterpret_cast<const u32x4_u *>(w + (int64_t)min(r0 + 16 * j + i, a.rank - 1) * C + c);
+          for (int j = 0; j < NT; ++j) {
+            const elem *const row = w + (int64_t)min(r0 + 16 * j + i, a.rank - 1) * C;
+            s.w[h][j] = SMALL ? load_each<DT, E>(row, c, C) : load_whole<DT, E>(row + c);
+          }
+        } else {
+          const int r = r0 + i * NT;
+          if (whole_ranks) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              s.rows[h][e] = load_whole<DT, NT>(w + (SMALL ? min(c + e, C - 1) : c + e) * a.rank + (r < a.rank ? r : 0));
           } else {
-            const int r = r0 + i * NT;
 #pragma unroll
-            for (int e = 0; e < E; ++e) s.rows[h][e] = load_whole<DT, NT>(w + (c + e) * a.rank + (r < a.rank ? r : 0));
+            for (int e = 0; e < E; ++e)
+              s.rows[h][e] = load_to_end<DT, NT>(w + (SMALL ? min(c + e, C - 1) : c + e) * a.rank, r, a.rank);
+          }
+          if constexpr (SMALL) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (c + e >= C) clear<DT, NT>(s.rows[h][e]);
           }
         }
-      } else {
+      }
+      if (last) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t c = c0 + h * E, left = C - c;  // (may be 0 or less)
+          const int shared = (int)(at0 - (c0 + h * E));
 #pragma unroll
-          for (int m = 0; m < M; ++m) s.x[h][m] = load_frag<DT>(x[m] + c, left);
+          for (int m = 0; m < M; ++m) clear_first<DT, E>(s.x[h][m], shared);
           if constexpr (!W_T) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) s.w[h][j] = load_frag<DT>(w + (int64_t)min(r0 + 16 * j + i, a.rank - 1) * C + c, left);
+            for (int j = 0; j < NT; ++j) clear_first<DT, E>(s.w[h][j], shared);
           } else {
-            const int r = r0 + i * NT;
 #pragma unroll
-            for (int e = 0; e < E; ++e) s.rows[h][e] = load_few<DT, NT>(w + (c + e) * a.rank + r, e < left ? a.rank - r : 0);
+            for (int e = 0; e < E; ++e)
+              if (e < shared) clear<DT, NT>(s.rows[h][e]);
           }
         }
       }
@@ -428,9 +398,9 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
         for (int j = 0; j < NT; ++j) {
           u32x4 wf;
           if constexpr (W_T) wf = pick<DT, NT>(s.rows[h], j);
-          else wf = s.w[h][j];
+          else wf = frag_of<DT>(s.w[h][j]);
 #pragma unroll
-          for (int m = 0; m < M; ++m) acc[m][j] = mma<DT>(wf, s.x[h][m], acc[m][j]);
+          for (int m = 0; m < M; ++m) acc[m][j] = mma<DT>(wf, frag_of<DT>(s.x[h][m]), acc[m][j]);
         }
     };
     // tiles start at different columns, so that rows a power of two apart do not meet at the same channels
@@ -483,18 +453,25 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
 #pragma unroll
           for (int k = 0; k < E; k += 4) *reinterpret_cast<v4f *>(to + k) = v4f{v[k], v[k + 1], v[k + 2], v[k + 3]};
         } else if (a.h) {
-          // its place in the fragment of 16 rows and 16 ranks
-          u32x4 *const to = reinterpret_cast<u32x4 *>(a.h) + ((int64_t)(at * M + row / 16) * (rp / 16) + (r0 + r) / 16) * 64;
-          const int lane_to = row % 16 + 16 * (r / E % (16 / E));
+          // its place among the fragments of 16 rows: 1 KB for 16 ranks (of up to 16 a lane's 8 bytes of high halves and
+          // 8 of low ones; else 1 KB of high halves of 32 ranks, then 1 KB of low ones)
+          const int group = (at * tile_rows + first_row + row) / 16, rr = r0 + r;
+          u32x4 *const to = reinterpret_cast<u32x4 *>(a.h) + (int64_t)group * (rp / 16) * 64 + row % 16;
           uint32_t o[E];
 #pragma unroll
           for (int k = 0; k < E; ++k) o[k] = up_word<DT>(v[k], e);
           if constexpr (DT == F8LIN_FP32) {
-            to[lane_to] = u32x4{o[0], o[1], o[2], o[3]};
+            to[rr / 16 * 64 + rr % 16 / 4 * 16] = u32x4{o[0], o[1], o[2], o[3]};
           } else {
-            const u32x4 lo = {o[0], o[1], o[2], o[3]}, hi = {o[4 % E], o[5 % E], o[6 % E], o[7 % E]};
-            to[lane_to] = h_halves(lo, hi, true);
-            to[lane_to + 32] = h_halves(lo, hi, false);
+            const u32x4 first = {o[0], o[1], o[2], o[3]}, second = {o[4 % E], o[5 % E], o[6 % E], o[7 % E]};
+            const u32x4 hi = h_halves(first, second, true), lo = h_halves(first, second, false);
+            if (rp == 16) {
+              to[rr / 4 * 16] = u32x4{hi.x, hi.y, lo.x, lo.y};
+              to[rr / 4 * 16 + 16] = u32x4{hi.z, hi.w, lo.z, lo.w};
+            } else {
+              to[rr / 32 * 128 + rr % 32 / 8 * 16] = hi;
+              to[rr / 32 * 128 + rr % 32 / 8 * 16 + 64] = lo;
+            }
           }
         }
       }
@@ -542,53 +519,91 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
 // 16-bit types row 4 p + q of tile j stands for column 32 (j / 2) + 8 p + 2 q
 // + j % 2, in binary32 for 16 j + 4 p + q.
 
-// W's fragments for 16 ranks from r0, 64 columns from c0 (FULL: all there).
-// What lies past the ranks is zero, whatever the memory holds: H is zero there.
-template <int DT, bool W_T, bool FULL>
+// W's fragments for KB ranks from r0 and 64 columns from c0 (SMALL: fewer may
+// be there).  KB = 32: 8 ranks a lane, 16: 4 (binary32: always 16 ranks, 4 a
+// lane).  What lies past the ranks is zero, whatever the memory holds: H is
+// zero there.
+template <int DT, int KB>
+struct UpFrag {
+  static constexpr int kPer = DT == F8LIN_FP32 ? 4 : KB / 4, kWords = DT == F8LIN_FP32 ? 4 : kPer / 2;
+  uint32_t w[kWords];
+};
+template <int DT, int KB>
+__device__ __forceinline__ v4f up_mma(const UpFrag<DT, KB> &f, const uint32_t *h, v4f c) {
+  if constexpr (UpFrag<DT, KB>::kWords == 2) return mma16<DT>(u32x2{f.w[0], f.w[1]}, u32x2{h[0], h[1]}, c);
+  else return mma<DT>(u32x4{f.w[0], f.w[1], f.w[2], f.w[3]}, u32x4{h[0], h[1], h[2], h[3]}, c);
+}
+template <int DT, bool W_T, bool SMALL, int KB>
 __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, int rank, int64_t C, int64_t c0, int r0,
-                                           u32x4 (&wf)[4]) {
-  constexpr int E = kE<DT>;
+                                           UpFrag<DT, KB> (&wf)[4]) {
   constexpr bool F32 = DT == F8LIN_FP32;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-  // this lane's ranks: E of 16 (in the 16-bit types lanes of g and g + 2 hold the same, for H's two halves)
-  const int rg = r0 + (F32 ? g : (g & 1)) * E;
+  constexpr int P = UpFrag<DT, KB>::kPer, kWords = UpFrag<DT, KB>::kWords;  // ranks a lane, and their words
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, rg = r0 + P * g;
   if constexpr (!W_T) {
+    // (columns past the end read the last one's: they are not stored)
+    const typename MxElem<DT>::type *row[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + (F32 ? 16 * j + i : 32 * (j >> 1) + 2 * i + (j & 1));
-      if (FULL && r0 + 16 <= rank) wf[j] = *reinterpret_cast<const u32x4_u *>(w + c * rank + rg);
-      else wf[j] = load_frag<DT>(w + min(c, C - 1) * rank + rg, c < C ? rank - rg : 0);
+      row[j] = w + (SMALL ? min(c, C - 1) : c) * rank;
     }
+    Few<DT, P> f[4];
+    if (r0 + 4 * P <= rank) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = load_whole<DT, P>(row[j] + rg);
+    } else if (rank >= P) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = load_to_end<DT, P>(row[j], rg, rank);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = load_each<DT, P>(row[j], rg, rank);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) wf[j].w[k] = f[j].w[k];
   } else if constexpr (F32) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + 16 * j + i;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t v = w[(int64_t)min(rg + e, rank - 1) * C + (FULL ? c : min(c, C - 1))];
-        wf[j][e] = rg + e < rank ? v : 0u;
+      for (int e = 0; e < P; ++e) {
+        const uint32_t v = w[(int64_t)min(rg + e, rank - 1) * C + (SMALL ? min(c, C - 1) : c)];
+        wf[j].w[e] = rg + e < rank ? v : 0u;
       }
     }
   } else {
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj) {
-      Few<DT, 2> rows[E];
+      Few<F8LIN_BF16, 2> rows[P];
       const int64_t c = c0 + 32 * jj + 2 * i;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const typename MxElem<DT>::type *const from = w + (int64_t)min(rg + e, rank - 1) * C + c;
-        if constexpr (FULL) rows[e] = load_whole<DT, 2>(from);
-        else rows[e] = load_few<DT, 2>(from, (int)max((int64_t)0, min((int64_t)2, C - c)));
-        if (rg + e >= rank) rows[e].w[0] = 0u;
+      for (int e = 0; e < P; ++e) {
+        const typename MxElem<DT>::type *const from = w + (int64_t)min(rg + e, rank - 1) * C;
+        rows[e] = SMALL ? load_each<F8LIN_BF16, 2>(from, c, C) : load_whole<F8LIN_BF16, 2>(from + c);
+        rows[e].w[0] = rg + e < rank ? rows[e].w[0] : 0u;
       }
-      wf[2 * jj] = pick<DT, 2>(rows, 0);
-      wf[2 * jj + 1] = pick<DT, 2>(rows, 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < P; e += 4) {
+          const u32x2 f = pick4<2>(rows[e], rows[e + 1], rows[e + 2], rows[e + 3], j);
+          wf[2 * jj + j].w[e / 2] = f.x, wf[2 * jj + j].w[e / 2 + 1] = f.y;
+        }
     }
   }
 }
-// base's pieces of one row (FULL: all there).
-template <int DT, bool FULL>
-__device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, int64_t c0, u32x4 (&raw)[16 / kE<DT>]) {
+// The 64 columns of a wave: from c0, or for the last ones those that end with
+// the row, of which only the ones from `own` on are stored (C >= 64).
+struct UpCols {
+  int64_t c0, own;
+};
+__device__ __forceinline__ UpCols up_cols(int64_t c0, int64_t C) {
+  return UpCols{C >= 64 ? min(c0, C - 64) : c0, c0};
+}
+// base's pieces of one row.
+template <int DT, bool SMALL>
+__device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, const UpCols &cols, u32x4 (&raw)[16 / kE<DT>]) {
   constexpr int E = kE<DT>;
   const int g = (threadIdx.x & 63) >> 4;
   const typename MxElem<DT>::type *const base = reinterpret_cast<const typename MxElem<DT>::type *>(a.base) + t * a.ldbase;
@@ -599,24 +614,21 @@ __device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, int64_t c0, 
   }
 #pragma unroll
   for (int h = 0; h < 16 / E; ++h) {
-    const int64_t c = c0 + 4 * E * h + E * g;
-    if constexpr (FULL) raw[h] = *reinterpret_cast<const u32x4_u *>(base + c);
-    else raw[h] = load_frag<DT>(base + c, a.cols - c);
+    const int64_t c = cols.c0 + 4 * E * h + E * g;
+    raw[h] = frag_of<DT>(SMALL ? load_each<DT, E>(base, c, a.cols) : load_whole<DT, E>(base + c));
   }
 }
 // One row's pieces of y.
-template <int DT, bool FULL>
-__device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapted, int64_t c0, const u32x4 (&raw)[16 / kE<DT>],
-                                         const v4f (&acc)[4]) {
+template <int DT, bool SMALL>
+__device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapted, const UpCols &cols,
+                                         const u32x4 (&raw)[16 / kE<DT>], const v4f (&acc)[4]) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>;
   constexpr bool F32 = DT == F8LIN_FP32;
   const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int h = 0; h < 16 / E; ++h) {
-    const int64_t c = c0 + 4 * E * h + E * g;
-    const int n = FULL ? E : (int)max((int64_t)0, min((int64_t)E, a.cols - c));
-    if (n == 0) break;
+    const int64_t c = cols.c0 + 4 * E * h + E * g;
     elem *const y = reinterpret_cast<elem *>(a.y) + t * a.ldy + c;
     uint32_t o[8];
 #pragma unroll
@@ -626,24 +638,51 @@ __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapte
       // (a token without an adapter keeps base's bits)
       o[e] = adapted ? f32_to_elem(a.base ? elem_f32<DT>(bits) + v : v, DT) : bits;
     }
-    if (n == E) {
+    const bool whole = SMALL ? c + E <= a.cols : c >= cols.own;
+    if (whole) {
       if constexpr (F32) *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0], o[1], o[2], o[3]};
       else
         *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e < n) y[e] = (elem)o[e];
+        if (SMALL ? c + e < a.cols : c + e >= cols.own) y[e] = (elem)o[e];
     }
   }
 }
-// Tiles of 64 rows, H in its final form.  Up to 64 ranks (NB blocks of 16): W
+// Tiles of 64 rows, H in its final form.  Up to 64 ranks (NB blocks of KB): W
 // stays in registers, the rows pass by in groups of 16, the next group's base
 // and H on their way.  NB = 0: any rank, 64 at a time, all rows' sums kept.
-template <int DT, bool W_T, int NB, bool FULL>
-__device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, int64_t c0) {
+
+// H's fragments of 16 rows and KB ranks: high and low halves (binary32: itself).
+template <int DT, int KB>
+struct UpH {
+  static constexpr int kWords = DT == F8LIN_FP32 ? 4 : KB / 4;
+  uint32_t w[kWords];
+};
+template <int DT, int KB>
+__device__ __forceinline__ void up_h(const u32x4 *h, int block, UpH<DT, KB> &f) {
+  const u32x4 v = h[block * (DT != F8LIN_FP32 && KB == 32 ? 128 : 64)];
+  f.w[0] = v.x, f.w[1] = v.y, f.w[2] = v.z, f.w[3] = v.w;
+  if constexpr (UpH<DT, KB>::kWords == 8) {
+    const u32x4 lo = h[block * 128 + 64];
+    f.w[4] = lo.x, f.w[5] = lo.y, f.w[6] = lo.z, f.w[7] = lo.w;
+  }
+}
+template <int DT, int KB>
+__device__ __forceinline__ void up_products(const UpFrag<DT, KB> (&wf)[4], const UpH<DT, KB> &h, v4f (&acc)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    acc[j] = up_mma<DT, KB>(wf[j], h.w, acc[j]);
+    if constexpr (DT != F8LIN_FP32) acc[j] = up_mma<DT, KB>(wf[j], h.w + KB / 8, acc[j]);
+  }
+}
+
+template <int DT, bool W_T, int NB, int KB, bool SMALL>
+__device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, const UpCols cols) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kPieces = 16 / kE<DT>;
+  constexpr int kRanks = DT == F8LIN_FP32 ? 16 : KB;  // of a block
   const int i = threadIdx.x & 15;
   const int64_t C = a.cols;
   const int rp = lora_rank_pad(a.rank);
@@ -651,9 +690,9 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
   const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
   const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
   auto position = [&](int m) { return tile.y + min(16 * m + i, tile.z - 1); };
-  // H's fragments of the tile, of groups of 16 rows and blocks of 16 ranks; what belongs to rows that are not there is
-  // whatever the memory holds, and goes to no row that is
+  // (what belongs to rows that are not there is whatever the memory holds, and goes to no row that is)
   const u32x4 *const h = reinterpret_cast<const u32x4 *>(a.h) + (int64_t)at * 4 * (rp / 16) * 64 + (threadIdx.x & 63);
+  const int h_ld = rp / 16 * 64;
   auto scale = [&](v4f (&acc)[4], int exponent) {
     if constexpr (DT == F8LIN_FP16) {
       const float f = ldexpf(1.0f, exponent);
@@ -667,29 +706,26 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
       const int64_t t = order[position(m)];
       u32x4 raw[kPieces];
       const v4f acc[4] = {zero, zero, zero, zero};
-      up_base<DT, FULL>(a, t, c0, raw);
-      if (16 * m + i < tile.z) up_store<DT, FULL>(a, t, false, c0, raw, acc);
+      up_base<DT, SMALL>(a, t, cols, raw);
+      if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t, false, cols, raw, acc);
     }
     return;
   }
   if constexpr (NB > 0) {
-    u32x4 wf[NB][4];
+    UpFrag<DT, KB> wf[NB][4];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) up_weights<DT, W_T, FULL>(w, a.rank, C, c0, min(16 * k, rp - 16), wf[k]);
-    u32x4 raw[2][kPieces], hf[2][NB];
+    for (int k = 0; k < NB; ++k) up_weights<DT, W_T, SMALL, KB>(w, a.rank, C, cols.c0, kRanks * k, wf[k]);
+    u32x4 raw[2][kPieces];
+    UpH<DT, KB> hf[2][NB];
     int64_t t[2];
     int exponent[2];
     const int groups = (tile.z + 15) >> 4;
     auto load = [&](int m, int b) {
       t[b] = order[position(m)];
-      up_base<DT, FULL>(a, t[b], c0, raw[b]);
+      up_base<DT, SMALL>(a, t[b], cols, raw[b]);
       if constexpr (DT == F8LIN_FP16) exponent[b] = a.exponents[position(m)];
-      // (a block past the padded ranks: some other's, times zero)
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        hf[b][k] = h[(m * (rp / 16) + min(k, rp / 16 - 1)) * 64];
-        if (16 * k >= rp) hf[b][k] = u32x4{0, 0, 0, 0};
-      }
+      for (int k = 0; k < NB; ++k) up_h<DT, KB>(h + m * h_ld, k, hf[b][k]);
     };
     load(0, 0);
 #pragma unroll
@@ -698,11 +734,9 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
       if (m + 1 < groups) load(m + 1, (m + 1) & 1);
       v4f acc[4] = {zero, zero, zero, zero};
 #pragma unroll
-      for (int k = 0; k < NB; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mma<DT>(wf[k][j], hf[m & 1][k], acc[j]);
+      for (int k = 0; k < NB; ++k) up_products<DT, KB>(wf[k], hf[m & 1][k], acc);
       scale(acc, exponent[m & 1]);
-      if (16 * m + i < tile.z) up_store<DT, FULL>(a, t[m & 1], true, c0, raw[m & 1], acc);
+      if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t[m & 1], true, cols, raw[m & 1], acc);
     }
   } else {
     v4f sum[4][4];
@@ -716,14 +750,14 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][j] = zero;
-      for (int r = r0; r < min(rp, r0 + 64); r += 16) {
-        u32x4 wf[4];
-        up_weights<DT, W_T, FULL>(w, a.rank, C, c0, r, wf);
+      for (int r = r0; r < min(rp, r0 + 64); r += kRanks) {
+        UpFrag<DT, KB> wf[4];
+        up_weights<DT, W_T, SMALL, KB>(w, a.rank, C, cols.c0, r, wf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const u32x4 hf = h[(m * (rp / 16) + r / 16) * 64];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][j] = mma<DT>(wf[j], hf, acc[m][j]);
+          UpH<DT, KB> hf;
+          up_h<DT, KB>(h + m * h_ld, r / kRanks, hf);
+          up_products<DT, KB>(wf, hf, acc[m]);
         }
       }
 #pragma unroll
@@ -737,13 +771,13 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
     for (int m = 0; m < 4; ++m) {
       const int64_t t = order[position(m)];
       u32x4 raw[kPieces];
-      up_base<DT, FULL>(a, t, c0, raw);
-      if (16 * m + i < tile.z) up_store<DT, FULL>(a, t, true, c0, raw, sum[m]);
+      up_base<DT, SMALL>(a, t, cols, raw);
+      if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t, true, cols, raw, sum[m]);
     }
   }
 }
 
-template <int DT, bool W_T, int NB>
+template <int DT, bool W_T, int NB, int KB, bool SMALL>
 __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
@@ -753,16 +787,15 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
   for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles) break;
-    if (c0 + 64 <= C) up_tile<DT, W_T, NB, true>(a, tile, at, order, c0);
-    else up_tile<DT, W_T, NB, false>(a, tile, at, order, c0);
+    up_tile<DT, W_T, NB, KB, SMALL>(a, tile, at, order, up_cols(c0, C));
   }
 }
 
 // Tiles of 16 rows, H as the sums of its parts.
-template <int DT, bool W_T, int G, bool FULL>
+template <int DT, bool W_T, int G, int KB, bool SMALL>
 __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, const int *order, int64_t c0) {
   typedef typename MxElem<DT>::type elem;
-  constexpr int E = kE<DT>;
+  constexpr int E = kE<DT>, P = UpFrag<DT, KB>::kPer;
   constexpr bool F32 = DT == F8LIN_FP32;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int64_t C = a.cols;
@@ -773,7 +806,7 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
   const int64_t t = tile.z == 1 ? tile.w : order[p];
   u32x4 raw[G][16 / E];
 #pragma unroll
-  for (int k = 0; k < G; ++k) up_base<DT, FULL>(a, t, c0 + 64 * k, raw[k]);
+  for (int k = 0; k < G; ++k) up_base<DT, SMALL>(a, t, up_cols(c0 + 64 * k, C), raw[k]);
   const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
   v4f acc[G][4];
 #pragma unroll
@@ -782,47 +815,59 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
     for (int j = 0; j < 4; ++j) acc[k][j] = zero;
   if (adapted) {
     const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
-    for (int r0 = 0; r0 < rp; r0 += 16) {
-      u32x4 wf[G][4];
+    for (int r0 = 0; r0 < rp; r0 += 4 * P) {
+      UpFrag<DT, KB> wf[G][4];
 #pragma unroll
-      for (int k = 0; k < G; ++k) up_weights<DT, W_T, FULL>(w, a.rank, C, c0 + 64 * k, r0, wf[k]);
-      u32x4 hw[E / 4];
+      for (int k = 0; k < G; ++k) up_weights<DT, W_T, SMALL, KB>(w, a.rank, C, up_cols(c0 + 64 * k, C).c0, r0, wf[k]);
+      uint32_t hw[P];
 #pragma unroll
-      for (int e = 0; e < E / 4; ++e) {
-        const float *const from = a.parts_in + (int64_t)p * rp + r0 + (F32 ? g : (g & 1)) * E + 4 * e;
+      for (int e = 0; e < P; e += 4) {
+        const float *const from = a.parts_in + (int64_t)p * rp + r0 + P * g + e;
         v4f s = *reinterpret_cast<const v4f *>(from);
 #pragma unroll 4
         for (int k = 1; k < a.parts; ++k) s += *reinterpret_cast<const v4f *>(from + k * part_ld);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) hw[e][k] = h_word<DT>(s[k]);
+        for (int k = 0; k < 4; ++k) hw[e + k] = h_word<DT>(s[k]);
       }
-      const u32x4 hf = F32 ? hw[0] : h_halves(hw[0], hw[E / 4 - 1], g < 2);
-      // (an infinite H meets the operand's main half only: the other is often zero)
-      const u32x4 finite = DT == F8LIN_FP16 ? no_inf(hf) : hf;
+      if constexpr (F32) {
 #pragma unroll
-      for (int k = 0; k < G; ++k)
+        for (int k = 0; k < G; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (F32) {
-            acc[k][j] = mma<DT>(wf[k][j], hf, acc[k][j]);
-          } else if constexpr (DT == F8LIN_FP16) {
-            u32x4 whi, wlo;
-            split_f16(wf[k][j], whi, wlo);
-            acc[k][j] = mma<F8LIN_BF16>(whi, hf, acc[k][j]);
-            acc[k][j] = mma<F8LIN_BF16>(wlo, finite, acc[k][j]);
-          } else {
-            acc[k][j] = mma<F8LIN_BF16>(wf[k][j], hf, acc[k][j]);
-          }
+          for (int j = 0; j < 4; ++j) acc[k][j] = up_mma<DT, KB>(wf[k][j], hw, acc[k][j]);
+      } else {
+        uint32_t hi[P / 2], lo[P / 2], finite[P / 2];
+#pragma unroll
+        for (int e = 0; e < P / 2; ++e) {
+          hi[e] = __builtin_amdgcn_perm(hw[2 * e + 1], hw[2 * e], 0x07060302u);
+          lo[e] = __builtin_amdgcn_perm(hw[2 * e + 1], hw[2 * e], 0x05040100u);
+          // (an infinite H meets an fp16 operand's main half only: the other is often zero)
+          finite[e] = no_inf(hi[e]);
         }
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            UpFrag<F8LIN_BF16, KB> f, left;
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) {
+              f.w[e] = wf[k][j].w[e];
+              if constexpr (DT == F8LIN_FP16) split_f16(wf[k][j].w[e], f.w[e], left.w[e]);
+            }
+            acc[k][j] = up_mma<F8LIN_BF16, KB>(f, hi, acc[k][j]);
+            acc[k][j] = up_mma<F8LIN_BF16, KB>(f, lo, acc[k][j]);
+            if constexpr (DT == F8LIN_FP16) acc[k][j] = up_mma<F8LIN_BF16, KB>(left, finite, acc[k][j]);
+          }
+      }
     }
   }
   if (i < tile.z) {
 #pragma unroll
-    for (int k = 0; k < G; ++k) up_store<DT, FULL>(a, t, adapted, c0 + 64 * k, raw[k], acc[k]);
+    for (int k = 0; k < G; ++k)
+      if (c0 + 64 * k < C) up_store<DT, SMALL>(a, t, adapted, up_cols(c0 + 64 * k, C), raw[k], acc[k]);
   }
 }
 
-template <int DT, bool W_T, int G>
+template <int DT, bool W_T, int G, int KB, bool SMALL>
 __global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
@@ -832,11 +877,7 @@ __global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
   for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles) break;
-    if (c0 + 64 * G <= C) up_few_tile<DT, W_T, G, true>(a, tile, order, c0);
-    else {
-#pragma unroll 1
-      for (int64_t c = c0; c < min(C, c0 + 64 * G); c += 64) up_few_tile<DT, W_T, 1, false>(a, tile, order, c);
-    }
+    up_few_tile<DT, W_T, G, KB, SMALL>(a, tile, order, c0);
   }
 }
 
@@ -855,10 +896,11 @@ struct OuterStep {
   Few<DT, kE<DT>> rows[kE<DT>];
   u32x4 h[NT][kE<DT> / 4];
 };
-template <int DT, int NT>
+template <int DT, int NT, bool SMALL>
 __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const LoraOuter a) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>, kCols = 16 * E, kStep = 4 * E;
+  __shared__ v4f join[4][E * NT][64];
   if (plan_tile_count(a.plan, a.tokens, a.adapters) < 0) return;
   const int *const starts = plan_starts(a.plan);
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
@@ -870,24 +912,26 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
   const bool second = id >= a.side[0].blocks * a.units;
   if (second) id -= a.side[0].blocks * a.units;
   const LoraOuterSide &side = second ? a.side[1] : a.side[0];
-  // a workgroup's waves: `across` blocks of ranks of the same columns, which they so read once; columns fastest: the
-  // workgroups of a chunk read the same H
-  const int across = a.across;
-#if 1
-  { // rounds of 8 units, one per XCD
+  // a workgroup's waves: `across` blocks of ranks of the same columns and tokens, times `split` parts of the tokens,
+  // whose sums meet in the LDS, times blocks of columns; columns fastest: the workgroups of a chunk read the same H,
+  // and rounds of 8 units, one an XCD, so that a row's columns are read through one L2
+  const int across = a.across, split = a.split, side_by_side = 4 / (across * split);
+  {
     const int per = 8 * side.blocks, round = id / per, in = id % per, n = min(8, a.units - 8 * round);
     id = (8 * round + in % n) * side.blocks + in / n;
   }
-#endif
-  const int64_t cw = ((int64_t)(id % side.blocks) * (4 / across) + wave / across) * kCols, c0 = cw + E * i;
-  const int unit = id / side.blocks, chunk = unit % a.chunks, r0 = (unit / a.chunks * across + wave % across) * 16 * NT;
   const int64_t C = side.cols;
-  if (cw >= C || r0 >= a.rank) return;
+  // the wave's columns: the last ones end with the row, and only those from `own` on are stored
+  const int64_t own = ((int64_t)(id % side.blocks) * side_by_side + wave / (across * split)) * kCols;
+  const int64_t cw = SMALL ? own : min(own, C - kCols), c0 = cw + E * i;
+  const int unit = id / side.blocks, chunk = unit % a.chunks;
+  const int r0 = (unit / a.chunks * across + wave % across) * 16 * NT, turn = wave / across % split;
+  if (split == 1 && own >= C) return;
   const int64_t first = (int64_t)chunk * a.chunk;
   const int end = (int)min((int64_t)adapted, first + a.chunk);
-  const int cn = (int)max((int64_t)0, min((int64_t)E, C - c0));
-  const bool full = cw + kCols <= C;
-  const elem *const xc = reinterpret_cast<const elem *>(side.x) + c0;
+  const uint32_t *ht[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) ht[j] = side.ht + (int64_t)min(r0 + 16 * j + i, rp - 1) * a.tokens;  // (past the ranks: not stored)
   for (int p0 = (int)min((int64_t)adapted, first); p0 < end;) {
     const int ad = owner[p0], p1 = min(end, starts[ad + 1]);
     v4f acc[E][NT];
@@ -898,31 +942,28 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
     // (nothing behind the adapter's tokens gets in, whatever it holds)
     auto load = [&](int p, OuterStep<DT, NT> &s) {
       const int at = p + g * E;
-      if (p + kStep <= p1 && full) {
-        int t[E];
+      const bool inside = p + kStep <= p1;
+      const elem *row[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) t[e] = order[at + e];
+      for (int e = 0; e < E; ++e) row[e] = reinterpret_cast<const elem *>(side.x) + (int64_t)order[min(at + e, p1 - 1)] * side.ldx;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s.rows[e] = load_whole<DT, E>(xc + (int64_t)t[e] * side.ldx);
+      for (int e = 0; e < E; ++e) s.rows[e] = SMALL ? load_each<DT, E>(row[e], c0, C) : load_whole<DT, E>(row[e] + c0);
+      if (inside) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int r = min(r0 + 16 * j + i, rp - 1);  // (past the padded rank: not stored)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int k = 0; k < E / 4; ++k)
-            s.h[j][k] = *reinterpret_cast<const u32x4_u *>(side.ht + (int64_t)r * a.tokens + at + 4 * k);
-        }
+          for (int k = 0; k < E / 4; ++k) s.h[j][k] = *reinterpret_cast<const u32x4_u *>(ht[j] + at + 4 * k);
       } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const bool in = at + e < p1;
-          s.rows[e] = load_few<DT, E>(xc + (in ? (int64_t)order[at + e] * side.ldx : 0), in ? cn : 0);
-        }
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int r = min(r0 + 16 * j + i, rp - 1);
+          for (int e = 0; e < E; ++e) {
+            const uint32_t v = ht[j][min(at + e, p1 - 1)];
+            s.h[j][e >> 2][e & 3] = at + e < p1 ? v : 0u;
+          }
 #pragma unroll
-          for (int e = 0; e < E; ++e) s.h[j][e >> 2][e & 3] = at + e < p1 ? side.ht[(int64_t)r * a.tokens + at + e] : 0u;
-        }
+        for (int e = 0; e < E; ++e)
+          if (at + e >= p1) clear<DT, E>(s.rows[e]);
       }
     };
     auto multiply = [&](const OuterStep<DT, NT> &s) {
@@ -934,7 +975,14 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
           for (int j = 0; j < NT; ++j) acc[c][j] = mma<DT>(xf, s.h[j][0], acc[c][j]);
         } else {
           u32x4 xl;
-          if constexpr (DT == F8LIN_FP16) split_f16(xf, xf, xl);
+          if constexpr (DT == F8LIN_FP16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t hi, lo;
+              split_f16(xf[e], hi, lo);
+              xf[e] = hi, xl[e] = lo;
+            }
+          }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             const u32x4 hi = h_halves(s.h[j][0], s.h[j][E / 4 - 1], true), lo = h_halves(s.h[j][0], s.h[j][E / 4 - 1], false);
@@ -946,13 +994,34 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
       }
     };
     OuterStep<DT, NT> s0, s1;
-    load(p0, s0);
-    for (int p = p0; p < p1; p += 2 * kStep) {
-      if (p + kStep < p1) load(p + kStep, s1);
+    const int step = split * kStep, q0 = p0 + turn * kStep;
+    if (q0 < p1) load(q0, s0);
+    for (int p = q0; p < p1; p += 2 * step) {
+      if (p + step < p1) load(p + step, s1);
       multiply(s0);
-      if (p + kStep >= p1) break;
-      if (p + 2 * kStep < p1) load(p + 2 * kStep, s0);
+      if (p + step >= p1) break;
+      if (p + 2 * step < p1) load(p + 2 * step, s0);
       multiply(s1);
+    }
+    // the token parts' sums, in their order
+    if (split > 1) {
+      __syncthreads();  // (of the last adapter's reads)
+      if (turn > 0) {
+#pragma unroll
+        for (int c = 0; c < E; ++c)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) join[wave][c * NT + j][lane] = acc[c][j];
+      }
+      __syncthreads();
+      if (turn > 0) {
+        p0 = p1;
+        continue;
+      }
+      for (int t = 1; t < split; ++t)
+#pragma unroll
+        for (int c = 0; c < E; ++c)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[c][j] += join[wave + t * across][c * NT + j][lane];
     }
     // lane (i, g) holds rank r0 + 16 j + i of columns E * (4 g + q) + c of the wave's
     const bool whole = starts[ad] >= first && starts[ad + 1] <= first + a.chunk;
@@ -966,18 +1035,18 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
       if (r >= a.rank) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int col = (int)cw + E * (4 * g + q), n = (int)min((int64_t)E, C - col);
+        const int col = (int)cw + E * (4 * g + q), n = (int)min((int64_t)E, C - col), n0 = (int)own - col;
         // (a side has at most 256 * 2^22 elements: 32-bit offsets)
         uint32_t at = side.d_t ? (uint32_t)col * a.rank + r : (uint32_t)r * (uint32_t)C + col;
         const uint32_t step = side.d_t ? a.rank : 1;
         if (whole) {
 #pragma unroll
           for (int c = 0; c < E; ++c, at += step)
-            if (c < n) d[at] = (elem)f32_to_elem(acc[c][j][q], DT);
+            if (c >= n0 && c < n) d[at] = (elem)f32_to_elem(acc[c][j][q], DT);
         } else {
 #pragma unroll
           for (int c = 0; c < E; ++c, at += step)
-            if (c < n) part[at] = acc[c][j][q];
+            if (c >= n0 && c < n) part[at] = acc[c][j][q];
         }
       }
     }
@@ -1024,63 +1093,101 @@ unsigned grid_of(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, 
 // Ranks of 16 a workgroup takes: one, two or four.
 int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 
+// How an outer product's four waves lie, and blocks of ranks beside them.
+struct LoraOuterShape {
+  int across, split, side_by_side, rblocks;
+};
+#ifndef OS
+#define OS 32768
+#endif
+LoraOuterShape lora_outer_shape(int64_t tokens, int rank) {
+  LoraOuterShape o;
+  const int blocks = rank <= 16 ? 1 : (rank + 31) / 32;
+  o.across = blocks > 2 ? 4 : blocks;
+  o.rblocks = (blocks + o.across - 1) / o.across;
+  // many tokens: waves side by side, so that a workgroup reads 1 KB of a row; else parts of the tokens, so that there
+  // are fewer chunks for the same number of waves
+  o.split = tokens >= OS ? 1 : 4 / o.across;
+  o.side_by_side = 4 / (o.across * o.split);
+  return o;
+}
+
 // Tiles along the grid's y (which the kernels stride over).
 dim3 tile_grid(int64_t x, int max_tiles, int z) { return dim3((unsigned)x, (unsigned)std::min(max_tiles, 65535), (unsigned)z); }
 
-template <int DT, bool W_T, int M, int WAVES>
+template <int DT, bool W_T, int M, bool SMALL>
 void down_rows(const LoraDown &a, hipStream_t s) {
   const int nt = rank_tiles(a.rank), rblocks = (a.rank + 16 * nt - 1) / (16 * nt);
-  const dim3 grid = tile_grid(a.parts, a.max_tiles, rblocks);
-  if (nt == 1) lora_down_kernel<DT, 1, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
-  else if (nt == 2) lora_down_kernel<DT, 2, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
-  else lora_down_kernel<DT, 4, W_T, M, WAVES><<<grid, 64 * WAVES, 0, s>>>(a);
+  const dim3 grid = tile_grid(a.parts * (lora_tile(a.tokens) / (16 * M)), a.max_tiles, rblocks);
+  if (nt == 1) lora_down_kernel<DT, 1, W_T, M, 4, SMALL><<<grid, 256, 0, s>>>(a);
+  else if (nt == 2) lora_down_kernel<DT, 2, W_T, M, 4, SMALL><<<grid, 256, 0, s>>>(a);
+  else lora_down_kernel<DT, 4, W_T, M, 4, SMALL><<<grid, 256, 0, s>>>(a);
 }
-template <int DT>
-void down_typed(const LoraDown &a, bool w_t, hipStream_t s) {
-  if (lora_tile(a.tokens) == 16) {
-    if (w_t) down_rows<DT, true, 1, 4>(a, s);
-    else down_rows<DT, false, 1, 4>(a, s);
-  } else {
-    if (w_t) down_rows<DT, true, 4, DW>(a, s);
-    else down_rows<DT, false, 4, DW>(a, s);
-  }
+#ifndef DM
+#define DM 512
+#endif
+template <int DT, bool W_T>
+void down_typed(const LoraDown &a, hipStream_t s) {
+  // 64 rows a workgroup read W once for four times the rows; fewer where that leaves the chip empty
+  const int64_t groups = (int64_t)a.max_tiles * ((a.rank + 63) / 64);
+  if (a.cols < 8 * kE<DT>) down_rows<DT, W_T, 1, true>(a, s);
+  else if (lora_tile(a.tokens) == 16 || groups < DM / 4) down_rows<DT, W_T, 1, false>(a, s);
+  else if (groups < DM) down_rows<DT, W_T, 2, false>(a, s);
+  else down_rows<DT, W_T, 4, false>(a, s);
   if (a.parts_out && a.ht) {
     const int64_t grid = (int64_t)((a.tokens + 15) / 16) * (lora_rank_pad(a.rank) / 16);
     lora_sum_kernel<DT><<<(unsigned)grid, 256, 0, s>>>(a);
   }
 }
+#ifndef FG
+#define FG 2
+#endif
 template <int DT, bool W_T>
 void up_typed(const LoraUp &a, hipStream_t s) {
-  const dim3 grid = tile_grid((a.cols + 255) / 256, a.max_tiles, 1);
+  constexpr int kTwo = DT == F8LIN_FP32 ? 2 : 1;  // (its blocks have 16 ranks)
+  auto grid = [&](int groups) { return tile_grid((a.cols + 256 * groups - 1) / (256 * groups), a.max_tiles, 1); };
+  const bool small = a.cols < 64;
   if (a.parts_in) {
-#ifndef FG
-#define FG 4
-#endif
-    if (FG > 1 && (int64_t)grid.x * a.max_tiles >= 1024)
-      lora_up_few_kernel<DT, W_T, FG><<<tile_grid((a.cols + 256 * FG - 1) / (256 * FG), a.max_tiles, 1), 256, 0, s>>>(a);
-    else lora_up_few_kernel<DT, W_T, 1><<<grid, 256, 0, s>>>(a);
+    const bool many = (a.cols + 255) / 256 * a.max_tiles >= 1024;
+    if (a.rank <= 16) {
+      if (small) lora_up_few_kernel<DT, W_T, 1, 16, true><<<grid(1), 256, 0, s>>>(a);
+      else if (many) lora_up_few_kernel<DT, W_T, FG, 16, false><<<grid(FG), 256, 0, s>>>(a);
+      else lora_up_few_kernel<DT, W_T, 1, 16, false><<<grid(1), 256, 0, s>>>(a);
+    } else {
+      if (small) lora_up_few_kernel<DT, W_T, 1, 32, true><<<grid(1), 256, 0, s>>>(a);
+      else lora_up_few_kernel<DT, W_T, 1, 32, false><<<grid(1), 256, 0, s>>>(a);
+    }
+  } else if (a.rank <= 16) {
+    if (small) lora_up_kernel<DT, W_T, 1, 16, true><<<grid(1), 256, 0, s>>>(a);
+    else lora_up_kernel<DT, W_T, 1, 16, false><<<grid(1), 256, 0, s>>>(a);
+  } else {
+    if (small) lora_up_kernel<DT, W_T, 0, 32, true><<<grid(1), 256, 0, s>>>(a);
+    else if (a.rank <= 32) lora_up_kernel<DT, W_T, kTwo, 32, false><<<grid(1), 256, 0, s>>>(a);
+    else if (a.rank <= 64) lora_up_kernel<DT, W_T, 2 * kTwo, 32, false><<<grid(1), 256, 0, s>>>(a);
+    else lora_up_kernel<DT, W_T, 0, 32, false><<<grid(1), 256, 0, s>>>(a);
   }
-  else if (a.rank <= 16) lora_up_kernel<DT, W_T, 1><<<grid, 256, 0, s>>>(a);
-  else if (a.rank <= 32) lora_up_kernel<DT, W_T, 2><<<grid, 256, 0, s>>>(a);
-  else if (a.rank <= 64) lora_up_kernel<DT, W_T, 4><<<grid, 256, 0, s>>>(a);
-  else lora_up_kernel<DT, W_T, 0><<<grid, 256, 0, s>>>(a);
 }
 template <int DT>
 void outer_typed(LoraOuter a, hipStream_t s) {
-  const int nt = a.rank <= 16 ? 1 : 2;
-  int rblocks = (a.rank + 16 * nt - 1) / (16 * nt);
-  a.across = rblocks > 2 ? 4 : rblocks;
-  rblocks = (rblocks + a.across - 1) / a.across;
-  const int64_t cols = 4 / a.across * 16 * kE<DT>;
-  a.units = a.chunks * rblocks;
+  const LoraOuterShape shape = lora_outer_shape(a.tokens, a.rank);
+  const int64_t cols = shape.side_by_side * 16 * kE<DT>;
+  a.across = shape.across, a.split = shape.split;
+  a.units = a.chunks * shape.rblocks;
+  bool small = false;
   for (int i = 0; i < 2; ++i) {
     a.side[i].blocks = a.side[i].d ? (int)((a.side[i].cols + cols - 1) / cols) : 0;
     a.side[i].join_blocks = a.side[i].d ? (a.rank * a.side[i].cols + 1023) / 1024 : 0;
+    small = small || (a.side[i].d && a.side[i].cols < 16 * kE<DT>);
   }
   const int64_t grid = (int64_t)(a.side[0].blocks + a.side[1].blocks) * a.units;
   if (grid > 0) {
-    if (nt == 1) lora_outer_kernel<DT, 1><<<(unsigned)grid, 256, 0, s>>>(a);
-    else lora_outer_kernel<DT, 2><<<(unsigned)grid, 256, 0, s>>>(a);
+    if (a.rank <= 16) {
+      if (small) lora_outer_kernel<DT, 1, true><<<(unsigned)grid, 256, 0, s>>>(a);
+      else lora_outer_kernel<DT, 1, false><<<(unsigned)grid, 256, 0, s>>>(a);
+    } else {
+      if (small) lora_outer_kernel<DT, 2, true><<<(unsigned)grid, 256, 0, s>>>(a);
+      else lora_outer_kernel<DT, 2, false><<<(unsigned)grid, 256, 0, s>>>(a);
+    }
   }
   const int64_t joins = (a.side[0].join_blocks + a.side[1].join_blocks) * a.adapters;
   if (joins > 0) lora_outer_join_kernel<DT><<<grid_of(joins), 256, 0, s>>>(a);
@@ -1099,14 +1206,20 @@ int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 8));
 }
 
-int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank) {
-  const int64_t per_chunk = ((K + 511) / 512 + (N + 511) / 512) * ((rank + 63) / 64);
-  #ifndef OW
-#define OW 512
+#ifndef OW
+#define OW 1024
 #endif
+#ifndef OC
+#define OC 16
+#endif
+int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank) {
+  // a partial sum is written and read in binary32 for every chunk: chunks of at least 16 * rank tokens keep that to a
+  // quarter of the data's bytes; else enough workgroups
+  const LoraOuterShape o = lora_outer_shape(tokens, rank);
+  const int64_t cols = 128 * o.side_by_side, per_chunk = ((K + cols - 1) / cols + (N + cols - 1) / cols) * o.rblocks;
   const int64_t chunks = std::max<int64_t>(1, OW / std::max<int64_t>(1, per_chunk));
-  const int64_t each = ((tokens + chunks - 1) / chunks + 31) / 32 * 32;
-  return (int)std::min<int64_t>(4096, std::max<int64_t>(128, each));
+  const int64_t each = std::max((tokens + chunks - 1) / chunks, (int64_t)OC * std::min(rank, 128));
+  return (int)std::min<int64_t>(4096, std::max<int64_t>(128, (each + 127) / 128 * 128));
 }
 
 hipError_t launch_lora_plan(const void *index, bool wide, int tokens, int adapters, int *plan, hipStream_t stream) {
@@ -1117,9 +1230,9 @@ hipError_t launch_lora_plan(const void *index, bool wide, int tokens, int adapte
 
 hipError_t launch_lora_down(const LoraDown &a, int dtype, bool w_t, hipStream_t stream) {
   if (a.tokens == 0) return hipSuccess;
-  if (dtype == F8LIN_BF16) down_typed<F8LIN_BF16>(a, w_t, stream);
-  else if (dtype == F8LIN_FP16) down_typed<F8LIN_FP16>(a, w_t, stream);
-  else down_typed<F8LIN_FP32>(a, w_t, stream);
+  if (dtype == F8LIN_BF16) w_t ? down_typed<F8LIN_BF16, true>(a, stream) : down_typed<F8LIN_BF16, false>(a, stream);
+  else if (dtype == F8LIN_FP16) w_t ? down_typed<F8LIN_FP16, true>(a, stream) : down_typed<F8LIN_FP16, false>(a, stream);
+  else w_t ? down_typed<F8LIN_FP32, true>(a, stream) : down_typed<F8LIN_FP32, false>(a, stream);
   return hipGetLastError();
 }
 

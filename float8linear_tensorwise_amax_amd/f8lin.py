@@ -1028,7 +1028,7 @@ def lora_backward_workspace_bytes(T: int, K: int, N: int, rank: int, adapters: i
 
 def lora_h_elements(T: int, rank: int) -> int:
     """Float32 elements of the inner products that lora_forward keeps for lora_backward."""
-    return T * (-(-rank // 16) * 16)
+    return T * (16 if rank <= 16 else -(-rank // 32) * 32)
 
 
 def _lora_sizes(x_rows: int, K: int, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan):

@@ -583,8 +583,8 @@ int f8lin_lora_plan(const void *index, int index_bytes, int64_t tokens, int adap
                     void *stream);
 
 /* Forward.  y may be base itself (ldbase = N).  h, if set, receives the inner
- * products times their scale for the backward: T x (rank rounded up to 16)
- * words in a form of its own.  ws: f8lin_lora_forward_workspace_bytes bytes,
+ * products times their scale for the backward: T x (16, or rank rounded
+ * up to 32 where it is more) words in a form of its own.  ws: f8lin_lora_forward_workspace_bytes bytes,
  * 16-byte aligned, no initialisation needed. */
 typedef struct {
   int64_t tokens, K, N;
