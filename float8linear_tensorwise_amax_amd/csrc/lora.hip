@@ -35,9 +35,6 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-#ifndef ROT
-#define ROT 5
-#endif
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- plan
@@ -242,6 +239,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const f32x2_t v = {a, b};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
+// The same of the type DT.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {a, b};
+  if constexpr (DT == F8LIN_BF16) return pack_bf16(a, b);
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
 // What rounding a to the bf16 in `bits` (its low or high half) left over; an
 // infinity leaves nothing.
 __device__ __forceinline__ float left_over(float a, float rounded) {
@@ -267,8 +272,8 @@ __device__ __forceinline__ void split_f16(uint32_t f, uint32_t &hi, uint32_t &lo
 template <int DT>
 __device__ __forceinline__ uint32_t h_word(float v) {
   if constexpr (DT == F8LIN_FP32) return __float_as_uint(v);
-  const uint32_t hi = f32_to_bf16_rne(v);
-  return hi << 16 | f32_to_bf16_rne(left_over(v, __uint_as_float(hi << 16)));
+  const uint32_t hi = pack_bf16(0.0f, v) & 0xFFFF0000u;
+  return hi | pack_bf16(left_over(v, __uint_as_float(hi)), 0.0f);
 }
 // The same for the products over ranks: with fp16 operands two fp16 values of
 // v * 2^-e, e by the largest value of a token's block of 64 ranks (2^-24 of
@@ -349,7 +354,8 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
       for (int h = 0; h < 2; ++h) {
         const int64_t c = c0 + h * E;
 #pragma unroll
-        for (int m = 0; m < M; ++m) s.x[h][m] = SMALL ? load_each<DT, E>(x[m], c, C) : load_whole<DT, E>(x[m] + c);
+        for (int m = 0; m < M; ++m) 
+          s.x[h][m] = SMALL ? load_each<DT, E>(x[m], c, C) : load_whole<DT, E>(x[m] + c);
         if constexpr (!W_T) {
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -405,7 +411,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
     };
     // tiles start at different columns, so that rows a power of two apart do not meet at the same channels
     const int b0 = part * part_blocks, nb = min(blocks, b0 + part_blocks) - b0;
-    const int turn = nb > 0 ? (int)((uint32_t)at * ROT % (uint32_t)nb) : 0;
+    const int turn = nb > 0 ? (int)((uint32_t)at * 5u % (uint32_t)nb) : 0;
     auto block = [&](int b) { return b0 + (b + turn < nb ? b + turn : b + turn - nb); };
     DownStep<DT, NT, W_T, M> s0, s1;
     if (wave < nb) load(block(wave), s0);
@@ -520,7 +526,7 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
 // + j % 2, in binary32 for 16 j + 4 p + q.
 
 // W's fragments for KB ranks from r0 and 64 columns from c0 (SMALL: fewer may
-// be there).  KB = 32: 8 ranks a lane, 16: 4 (binary32: always 16 ranks, 4 a
+// be there; WHOLE: the ranks are whole blocks).  KB = 32: 8 ranks a lane, 16: 4 (binary32: always 16 ranks, 4 a
 // lane).  What lies past the ranks is zero, whatever the memory holds: H is
 // zero there.
 template <int DT, int KB>
@@ -533,7 +539,7 @@ __device__ __forceinline__ v4f up_mma(const UpFrag<DT, KB> &f, const uint32_t *h
   if constexpr (UpFrag<DT, KB>::kWords == 2) return mma16<DT>(u32x2{f.w[0], f.w[1]}, u32x2{h[0], h[1]}, c);
   else return mma<DT>(u32x4{f.w[0], f.w[1], f.w[2], f.w[3]}, u32x4{h[0], h[1], h[2], h[3]}, c);
 }
-template <int DT, bool W_T, bool SMALL, int KB>
+template <int DT, bool W_T, bool SMALL, int KB, bool WHOLE>
 __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, int rank, int64_t C, int64_t c0, int r0,
                                            UpFrag<DT, KB> (&wf)[4]) {
   constexpr bool F32 = DT == F8LIN_FP32;
@@ -548,7 +554,7 @@ __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, i
       row[j] = w + (SMALL ? min(c, C - 1) : c) * rank;
     }
     Few<DT, P> f[4];
-    if (r0 + 4 * P <= rank) {
+    if (WHOLE || r0 + 4 * P <= rank) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] = load_whole<DT, P>(row[j] + rg);
     } else if (rank >= P) {
@@ -568,8 +574,8 @@ __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, i
       const int64_t c = c0 + 16 * j + i;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const uint32_t v = w[(int64_t)min(rg + e, rank - 1) * C + (SMALL ? min(c, C - 1) : c)];
-        wf[j].w[e] = rg + e < rank ? v : 0u;
+        const uint32_t v = w[(int64_t)(WHOLE ? rg + e : min(rg + e, rank - 1)) * C + (SMALL ? min(c, C - 1) : c)];
+        wf[j].w[e] = WHOLE || rg + e < rank ? v : 0u;
       }
     }
   } else {
@@ -579,9 +585,9 @@ __device__ __forceinline__ void up_weights(const typename MxElem<DT>::type *w, i
       const int64_t c = c0 + 32 * jj + 2 * i;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const typename MxElem<DT>::type *const from = w + (int64_t)min(rg + e, rank - 1) * C;
+        const typename MxElem<DT>::type *const from = w + (int64_t)(WHOLE ? rg + e : min(rg + e, rank - 1)) * C;
         rows[e] = SMALL ? load_each<F8LIN_BF16, 2>(from, c, C) : load_whole<F8LIN_BF16, 2>(from + c);
-        rows[e].w[0] = rg + e < rank ? rows[e].w[0] : 0u;
+        rows[e].w[0] = WHOLE || rg + e < rank ? rows[e].w[0] : 0u;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -615,11 +621,11 @@ __device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, const UpCols
 #pragma unroll
   for (int h = 0; h < 16 / E; ++h) {
     const int64_t c = cols.c0 + 4 * E * h + E * g;
-    raw[h] = frag_of<DT>(SMALL ? load_each<DT, E>(base, c, a.cols) : load_whole<DT, E>(base + c));
+        raw[h] = frag_of<DT>(SMALL ? load_each<DT, E>(base, c, a.cols) : load_whole<DT, E>(base + c));
   }
 }
 // One row's pieces of y.
-template <int DT, bool SMALL>
+template <int DT, bool SMALL, bool PAST>
 __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapted, const UpCols &cols,
                                          const u32x4 (&raw)[16 / kE<DT>], const v4f (&acc)[4]) {
   typedef typename MxElem<DT>::type elem;
@@ -630,29 +636,31 @@ __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapte
   for (int h = 0; h < 16 / E; ++h) {
     const int64_t c = cols.c0 + 4 * E * h + E * g;
     elem *const y = reinterpret_cast<elem *>(a.y) + t * a.ldy + c;
-    uint32_t o[8];
+    float f[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const uint32_t bits = F32 ? raw[h][e & 3] : (raw[h][e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
       const float v = F32 ? acc[h & 3][e & 3] : acc[(2 * h + (e & 1)) & 3][e >> 1];
-      // (a token without an adapter keeps base's bits)
-      o[e] = adapted ? f32_to_elem(a.base ? elem_f32<DT>(bits) + v : v, DT) : bits;
+      f[e] = a.base ? elem_f32<DT>(bits) + v : v;
     }
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = F32 ? __float_as_uint(f[e]) : pack2<DT>(f[(2 * e) % E], f[(2 * e + 1) % E]);
+    if (!adapted) v = raw[h];  // (base's bits)
     const bool whole = SMALL ? c + E <= a.cols : c >= cols.own;
     if (whole) {
-      if constexpr (F32) *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0], o[1], o[2], o[3]};
-      else
-        *reinterpret_cast<u32x4_u *>(y) = u32x4{o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16};
+      if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_u *>(y));
+      else *reinterpret_cast<u32x4_u *>(y) = v;
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (SMALL ? c + e < a.cols : c + e >= cols.own) y[e] = (elem)o[e];
+        if (SMALL ? c + e < a.cols : c + e >= cols.own) y[e] = (elem)(F32 ? v[e & 3] : v[e >> 1] >> (16 * (e & 1)));
     }
   }
 }
 // Tiles of 64 rows, H in its final form.  Up to 64 ranks (NB blocks of KB): W
-// stays in registers, the rows pass by in groups of 16, the next group's base
-// and H on their way.  NB = 0: any rank, 64 at a time, all rows' sums kept.
+// stays in registers, the rows pass by in groups of 16, all their base and the
+// next group's H on their way.  NB = 0: any rank, 64 at a time, all rows' sums kept.
 
 // H's fragments of 16 rows and KB ranks: high and low halves (binary32: itself).
 template <int DT, int KB>
@@ -678,7 +686,7 @@ __device__ __forceinline__ void up_products(const UpFrag<DT, KB> (&wf)[4], const
   }
 }
 
-template <int DT, bool W_T, int NB, int KB, bool SMALL>
+template <int DT, bool W_T, int NB, int KB, bool SMALL, bool WHOLE, bool PAST>
 __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, const UpCols cols) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kPieces = 16 / kE<DT>;
@@ -707,36 +715,41 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
       u32x4 raw[kPieces];
       const v4f acc[4] = {zero, zero, zero, zero};
       up_base<DT, SMALL>(a, t, cols, raw);
-      if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t, false, cols, raw, acc);
+      if (16 * m + i < tile.z) up_store<DT, SMALL, PAST>(a, t, false, cols, raw, acc);
     }
     return;
   }
   if constexpr (NB > 0) {
     UpFrag<DT, KB> wf[NB][4];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) up_weights<DT, W_T, SMALL, KB>(w, a.rank, C, cols.c0, kRanks * k, wf[k]);
-    u32x4 raw[2][kPieces];
+    for (int k = 0; k < NB; ++k) up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, cols.c0, kRanks * k, wf[k]);
+    u32x4 raw[4][kPieces];
     UpH<DT, KB> hf[2][NB];
-    int64_t t[2];
-    int exponent[2];
+    int64_t t[4];
+    int exponent[4];
     const int groups = (tile.z + 15) >> 4;
-    auto load = [&](int m, int b) {
-      t[b] = order[position(m)];
-      up_base<DT, SMALL>(a, t[b], cols, raw[b]);
-      if constexpr (DT == F8LIN_FP16) exponent[b] = a.exponents[position(m)];
+    // (rows that are not there: the last one's)
 #pragma unroll
-      for (int k = 0; k < NB; ++k) up_h<DT, KB>(h + m * h_ld, k, hf[b][k]);
+    for (int m = 0; m < 4; ++m) t[m] = order[position(m)];
+    auto load_h = [&](int m) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) up_h<DT, KB>(h + m * h_ld, k, hf[m & 1][k]);
     };
-    load(0, 0);
+    load_h(0);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      up_base<DT, SMALL>(a, t[m], cols, raw[m]);
+      if constexpr (DT == F8LIN_FP16) exponent[m] = a.exponents[position(m)];
+    }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       if (m >= groups) break;
-      if (m + 1 < groups) load(m + 1, (m + 1) & 1);
+      if (m < 3) load_h(m + 1);
       v4f acc[4] = {zero, zero, zero, zero};
 #pragma unroll
       for (int k = 0; k < NB; ++k) up_products<DT, KB>(wf[k], hf[m & 1][k], acc);
-      scale(acc, exponent[m & 1]);
-      if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t[m & 1], true, cols, raw[m & 1], acc);
+      scale(acc, exponent[m]);
+      if (16 * m + i < tile.z) up_store<DT, SMALL, PAST>(a, t[m], true, cols, raw[m], acc);
     }
   } else {
     v4f sum[4][4];
@@ -752,7 +765,7 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
         for (int j = 0; j < 4; ++j) acc[m][j] = zero;
       for (int r = r0; r < min(rp, r0 + 64); r += kRanks) {
         UpFrag<DT, KB> wf[4];
-        up_weights<DT, W_T, SMALL, KB>(w, a.rank, C, cols.c0, r, wf);
+        up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, cols.c0, r, wf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           UpH<DT, KB> hf;
@@ -772,12 +785,12 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
       const int64_t t = order[position(m)];
       u32x4 raw[kPieces];
       up_base<DT, SMALL>(a, t, cols, raw);
-      if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t, true, cols, raw, sum[m]);
+      if (16 * m + i < tile.z) up_store<DT, SMALL, PAST>(a, t, true, cols, raw, sum[m]);
     }
   }
 }
 
-template <int DT, bool W_T, int NB, int KB, bool SMALL>
+template <int DT, bool W_T, int NB, int KB, bool SMALL, bool WHOLE, bool PAST>
 __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
@@ -787,12 +800,12 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
   for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles) break;
-    up_tile<DT, W_T, NB, KB, SMALL>(a, tile, at, order, up_cols(c0, C));
+    up_tile<DT, W_T, NB, KB, SMALL, WHOLE, PAST>(a, tile, at, order, up_cols(c0, C));
   }
 }
 
 // Tiles of 16 rows, H as the sums of its parts.
-template <int DT, bool W_T, int G, int KB, bool SMALL>
+template <int DT, bool W_T, int G, int KB, bool SMALL, bool WHOLE>
 __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, const int *order, int64_t c0) {
   typedef typename MxElem<DT>::type elem;
   constexpr int E = kE<DT>, P = UpFrag<DT, KB>::kPer;
@@ -818,7 +831,7 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
     for (int r0 = 0; r0 < rp; r0 += 4 * P) {
       UpFrag<DT, KB> wf[G][4];
 #pragma unroll
-      for (int k = 0; k < G; ++k) up_weights<DT, W_T, SMALL, KB>(w, a.rank, C, up_cols(c0 + 64 * k, C).c0, r0, wf[k]);
+      for (int k = 0; k < G; ++k) up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, up_cols(c0 + 64 * k, C).c0, r0, wf[k]);
       uint32_t hw[P];
 #pragma unroll
       for (int e = 0; e < P; e += 4) {
@@ -863,11 +876,11 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
   if (i < tile.z) {
 #pragma unroll
     for (int k = 0; k < G; ++k)
-      if (c0 + 64 * k < C) up_store<DT, SMALL>(a, t, adapted, up_cols(c0 + 64 * k, C), raw[k], acc[k]);
+      if (c0 + 64 * k < C) up_store<DT, SMALL, false>(a, t, adapted, up_cols(c0 + 64 * k, C), raw[k], acc[k]);
   }
 }
 
-template <int DT, bool W_T, int G, int KB, bool SMALL>
+template <int DT, bool W_T, int G, int KB, bool SMALL, bool WHOLE>
 __global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
@@ -877,7 +890,7 @@ __global__ __launch_bounds__(256) void lora_up_few_kernel(const LoraUp a) {
   for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles) break;
-    up_few_tile<DT, W_T, G, KB, SMALL>(a, tile, order, c0);
+    up_few_tile<DT, W_T, G, KB, SMALL, WHOLE>(a, tile, order, c0);
   }
 }
 
@@ -947,7 +960,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
 #pragma unroll
       for (int e = 0; e < E; ++e) row[e] = reinterpret_cast<const elem *>(side.x) + (int64_t)order[min(at + e, p1 - 1)] * side.ldx;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s.rows[e] = SMALL ? load_each<DT, E>(row[e], c0, C) : load_whole<DT, E>(row[e] + c0);
+      for (int e = 0; e < E; ++e) 
+          s.rows[e] = SMALL ? load_each<DT, E>(row[e], c0, C) : load_whole<DT, E>(row[e] + c0);
       if (inside) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -1087,6 +1101,7 @@ __global__ __launch_bounds__(256) void lora_outer_join_kernel(const LoraOuter a)
 
 // ---------------------------------------------------------------- launches
 
+constexpr int64_t kCached = (int64_t)256 << 20;
 constexpr int64_t kMaxGrid1 = (int64_t)1 << 22;  // workgroups; the kernels stride over the rest
 unsigned grid_of(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min(n, kMaxGrid1)); }
 
@@ -1097,9 +1112,6 @@ int rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 struct LoraOuterShape {
   int across, split, side_by_side, rblocks;
 };
-#ifndef OS
-#define OS 32768
-#endif
 LoraOuterShape lora_outer_shape(int64_t tokens, int rank) {
   LoraOuterShape o;
   const int blocks = rank <= 16 ? 1 : (rank + 31) / 32;
@@ -1107,7 +1119,7 @@ LoraOuterShape lora_outer_shape(int64_t tokens, int rank) {
   o.rblocks = (blocks + o.across - 1) / o.across;
   // many tokens: waves side by side, so that a workgroup reads 1 KB of a row; else parts of the tokens, so that there
   // are fewer chunks for the same number of waves
-  o.split = tokens >= OS ? 1 : 4 / o.across;
+  o.split = tokens >= 32768 ? 1 : 4 / o.across;
   o.side_by_side = 4 / (o.across * o.split);
   return o;
 }
@@ -1123,48 +1135,57 @@ void down_rows(const LoraDown &a, hipStream_t s) {
   else if (nt == 2) lora_down_kernel<DT, 2, W_T, M, 4, SMALL><<<grid, 256, 0, s>>>(a);
   else lora_down_kernel<DT, 4, W_T, M, 4, SMALL><<<grid, 256, 0, s>>>(a);
 }
-#ifndef DM
-#define DM 512
-#endif
 template <int DT, bool W_T>
 void down_typed(const LoraDown &a, hipStream_t s) {
   // 64 rows a workgroup read W once for four times the rows; fewer where that leaves the chip empty
   const int64_t groups = (int64_t)a.max_tiles * ((a.rank + 63) / 64);
   if (a.cols < 8 * kE<DT>) down_rows<DT, W_T, 1, true>(a, s);
-  else if (lora_tile(a.tokens) == 16 || groups < DM / 4) down_rows<DT, W_T, 1, false>(a, s);
-  else if (groups < DM) down_rows<DT, W_T, 2, false>(a, s);
+  else if (lora_tile(a.tokens) == 16 || groups < 128) down_rows<DT, W_T, 1, false>(a, s);
+  else if (groups < 512) down_rows<DT, W_T, 2, false>(a, s);
   else down_rows<DT, W_T, 4, false>(a, s);
   if (a.parts_out && a.ht) {
     const int64_t grid = (int64_t)((a.tokens + 15) / 16) * (lora_rank_pad(a.rank) / 16);
     lora_sum_kernel<DT><<<(unsigned)grid, 256, 0, s>>>(a);
   }
 }
-#ifndef FG
-#define FG 2
-#endif
+template <int DT, bool W_T, int NB, int KB>
+void up_blocks(const LoraUp &a, const dim3 grid, hipStream_t s) {
+  const bool whole = a.rank % (DT == F8LIN_FP32 ? 16 : KB) == 0;
+  // what is only written goes past the caches where it is more than they hold
+  if constexpr (W_T) {
+    if (whole && !a.base && (int64_t)a.tokens * a.cols * elem_bytes(DT) > kCached)
+      return lora_up_kernel<DT, W_T, NB, KB, false, true, true><<<grid, 256, 0, s>>>(a);
+  }
+  if (whole) lora_up_kernel<DT, W_T, NB, KB, false, true, false><<<grid, 256, 0, s>>>(a);
+  else lora_up_kernel<DT, W_T, NB, KB, false, false, false><<<grid, 256, 0, s>>>(a);
+}
+template <int DT, bool W_T, int KB>
+void up_few_blocks(const LoraUp &a, hipStream_t s) {
+  auto grid = [&](int groups) { return tile_grid((a.cols + 256 * groups - 1) / (256 * groups), a.max_tiles, 1); };
+  const bool whole = a.rank % (DT == F8LIN_FP32 ? 16 : KB) == 0, many = (a.cols + 255) / 256 * a.max_tiles >= 1024;
+  if (a.cols < 64) lora_up_few_kernel<DT, W_T, 1, KB, true, false><<<grid(1), 256, 0, s>>>(a);
+  else if (!whole) lora_up_few_kernel<DT, W_T, 1, KB, false, false><<<grid(1), 256, 0, s>>>(a);
+  else if (many) lora_up_few_kernel<DT, W_T, 2, KB, false, true><<<grid(2), 256, 0, s>>>(a);
+  else lora_up_few_kernel<DT, W_T, 1, KB, false, true><<<grid(1), 256, 0, s>>>(a);
+}
 template <int DT, bool W_T>
 void up_typed(const LoraUp &a, hipStream_t s) {
   constexpr int kTwo = DT == F8LIN_FP32 ? 2 : 1;  // (its blocks have 16 ranks)
-  auto grid = [&](int groups) { return tile_grid((a.cols + 256 * groups - 1) / (256 * groups), a.max_tiles, 1); };
-  const bool small = a.cols < 64;
+  const dim3 grid = tile_grid((a.cols + 255) / 256, a.max_tiles, 1);
   if (a.parts_in) {
-    const bool many = (a.cols + 255) / 256 * a.max_tiles >= 1024;
-    if (a.rank <= 16) {
-      if (small) lora_up_few_kernel<DT, W_T, 1, 16, true><<<grid(1), 256, 0, s>>>(a);
-      else if (many) lora_up_few_kernel<DT, W_T, FG, 16, false><<<grid(FG), 256, 0, s>>>(a);
-      else lora_up_few_kernel<DT, W_T, 1, 16, false><<<grid(1), 256, 0, s>>>(a);
-    } else {
-      if (small) lora_up_few_kernel<DT, W_T, 1, 32, true><<<grid(1), 256, 0, s>>>(a);
-      else lora_up_few_kernel<DT, W_T, 1, 32, false><<<grid(1), 256, 0, s>>>(a);
-    }
+    if (a.rank <= 16) up_few_blocks<DT, W_T, 16>(a, s);
+    else up_few_blocks<DT, W_T, 32>(a, s);
+  } else if (a.cols < 64) {
+    if (a.rank <= 16) lora_up_kernel<DT, W_T, 1, 16, true, false, false><<<grid, 256, 0, s>>>(a);
+    else lora_up_kernel<DT, W_T, 0, 32, true, false, false><<<grid, 256, 0, s>>>(a);
   } else if (a.rank <= 16) {
-    if (small) lora_up_kernel<DT, W_T, 1, 16, true><<<grid(1), 256, 0, s>>>(a);
-    else lora_up_kernel<DT, W_T, 1, 16, false><<<grid(1), 256, 0, s>>>(a);
+    up_blocks<DT, W_T, 1, 16>(a, grid, s);
+  } else if (a.rank <= 32) {
+    up_blocks<DT, W_T, kTwo, 32>(a, grid, s);
+  } else if (a.rank <= 64) {
+    up_blocks<DT, W_T, 2 * kTwo, 32>(a, grid, s);
   } else {
-    if (small) lora_up_kernel<DT, W_T, 0, 32, true><<<grid(1), 256, 0, s>>>(a);
-    else if (a.rank <= 32) lora_up_kernel<DT, W_T, kTwo, 32, false><<<grid(1), 256, 0, s>>>(a);
-    else if (a.rank <= 64) lora_up_kernel<DT, W_T, 2 * kTwo, 32, false><<<grid(1), 256, 0, s>>>(a);
-    else lora_up_kernel<DT, W_T, 0, 32, false><<<grid(1), 256, 0, s>>>(a);
+    up_blocks<DT, W_T, 0, 32>(a, grid, s);
   }
 }
 template <int DT>
@@ -1199,26 +1220,17 @@ int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank) {
   if (!lora_split(tokens)) return 1;
   // enough workgroups for the chip, each with two 64-column blocks a wave at least
   const int64_t groups = std::max<int64_t>(1, lora_max_tiles(tokens, adapters)) * ((rank + 63) / 64);
-  #ifndef PW
-#define PW 256
-#endif
-  const int64_t want = (PW + groups - 1) / groups, most = (cols + 511) / 512;
+    const int64_t want = (256 + groups - 1) / groups, most = (cols + 511) / 512;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 8));
 }
 
-#ifndef OW
-#define OW 1024
-#endif
-#ifndef OC
-#define OC 16
-#endif
 int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank) {
   // a partial sum is written and read in binary32 for every chunk: chunks of at least 16 * rank tokens keep that to a
   // quarter of the data's bytes; else enough workgroups
   const LoraOuterShape o = lora_outer_shape(tokens, rank);
   const int64_t cols = 128 * o.side_by_side, per_chunk = ((K + cols - 1) / cols + (N + cols - 1) / cols) * o.rblocks;
-  const int64_t chunks = std::max<int64_t>(1, OW / std::max<int64_t>(1, per_chunk));
-  const int64_t each = std::max((tokens + chunks - 1) / chunks, (int64_t)OC * std::min(rank, 128));
+  const int64_t chunks = std::max<int64_t>(1, (o.split == 1 ? 512 : 1024) / std::max<int64_t>(1, per_chunk));
+  const int64_t each = std::max((tokens + chunks - 1) / chunks, (int64_t)16 * std::min(rank, 128));
   return (int)std::min<int64_t>(4096, std::max<int64_t>(128, (each + 127) / 128 * 128));
 }
 

@@ -15,8 +15,8 @@ struct Few {
   uint32_t w[kWords];
 };
 
-// V elements at p, all there.
-template <int DT, int V>
+// V elements at p, all there.  PAST: past the caches (16 bytes only).
+template <int DT, int V, bool PAST = false>
 __device__ __forceinline__ Few<DT, V> load_whole(const typename MxElem<DT>::type *p) {
   Few<DT, V> f;
   constexpr int kW = Few<DT, V>::kWords;
@@ -29,7 +29,8 @@ __device__ __forceinline__ Few<DT, V> load_whole(const typename MxElem<DT>::type
     const u32x2 v = *reinterpret_cast<const u32x2_u *>(p);
     f.w[0] = v.x, f.w[1] = v.y;
   } else {
-    const u32x4 v = *reinterpret_cast<const u32x4_u *>(p);
+    const u32x4_u *const q = reinterpret_cast<const u32x4_u *>(p);
+    const u32x4 v = PAST ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.w[i] = v[i];
   }
