@@ -55,19 +55,13 @@ int f8lin_layer_norm_forward(const f8lin_layer_norm_fwd_args *p, void *stream) {
   if (a.weight) F8_TRY(check_dense(a.weight, a.weight_dtype, 1, C, C));
   if (a.bias) F8_TRY(check_dense(a.bias, a.bias_dtype, 1, C, C));
   if (!(a.eps >= 0.0f)) return F8LIN_EINVAL;
-  if (!a.mean != !a.rstd) return F8LIN_EINVAL;
-  if (a.mean) {
-    F8_TRY(check_f32(a.mean, R));
-    F8_TRY(check_f32(a.rstd, R));
-  }
+  if (a.stats) F8_TRY(check_f32(a.stats, R));
   if (a.y_amax && !aligned4(a.y_amax)) return F8LIN_EALIGN;
-  const Range outs[] = {span(a.y, a.y_dtype, R, C, C), {a.mean, a.mean ? 4 * R : 0}, {a.rstd, a.rstd ? 4 * R : 0},
-                        {a.y_amax, a.y_amax ? 4 : 0}};
+  const Range outs[] = {span(a.y, a.y_dtype, R, C, C), {a.stats, a.stats ? 8 * R : 0}, {a.y_amax, a.y_amax ? 4 : 0}};
   const Range ins[] = {span(a.x, a.x_dtype, R, C, ldx), span(a.weight, a.weight_dtype, 1, C, C),
                        span(a.bias, a.bias_dtype, 1, C, C)};
-  if (any_overlap(outs, 4, ins, 3)) return F8LIN_EINVAL;
-  const LayerNormFwd k = {a.x, R, C, ldx, a.weight, a.bias, a.weight_dtype, a.bias_dtype, a.eps, a.y, a.mean, a.rstd,
-                          a.y_amax};
+  if (any_overlap(outs, 3, ins, 3)) return F8LIN_EINVAL;
+  const LayerNormFwd k = {a.x, R, C, ldx, a.weight, a.bias, a.weight_dtype, a.bias_dtype, a.eps, a.y, a.stats, a.y_amax};
   return status_of(launch_layer_norm_forward(k, a.x_dtype, a.y_dtype, (hipStream_t)stream));
 }
 
@@ -85,8 +79,7 @@ int f8lin_layer_norm_backward(const f8lin_layer_norm_bwd_args *p, void *stream) 
   F8_TRY(check_dense(a.x, a.x_dtype, R, C, ldx));
   if (!types_pair(a.x_dtype, a.dy_dtype)) return F8LIN_EINVAL;
   if (a.weight) F8_TRY(check_dense(a.weight, a.weight_dtype, 1, C, C));
-  F8_TRY(check_f32(a.mean, C > 0 ? R : 0));
-  F8_TRY(check_f32(a.rstd, C > 0 ? R : 0));
+  F8_TRY(check_f32(a.stats, C > 0 ? R : 0));
   if (a.dx) F8_TRY(check_dense(a.dx, a.x_dtype, R, C, C));
   if (a.dweight) F8_TRY(check_dense(a.dweight, a.dweight_dtype, 1, C, C));
   if (a.dbias) F8_TRY(check_dense(a.dbias, a.dbias_dtype, 1, C, C));
@@ -100,9 +93,9 @@ int f8lin_layer_norm_backward(const f8lin_layer_norm_bwd_args *p, void *stream) 
   const Range outs[] = {span(a.dx, a.x_dtype, R, C, C), span(a.dweight, a.dweight_dtype, 1, C, C),
                         span(a.dbias, a.dbias_dtype, 1, C, C), {a.ws, (int64_t)need}};
   const Range ins[] = {span(a.dy, a.dy_dtype, R, C, lddy), span(a.x, a.x_dtype, R, C, ldx),
-                       span(a.weight, a.weight_dtype, 1, C, C), {a.mean, 4 * R}, {a.rstd, 4 * R}};
-  if (any_overlap(outs, 4, ins, 5)) return F8LIN_EINVAL;
-  const LayerNormBwd k = {a.dy, a.x, R, C, lddy, ldx, a.weight, a.weight_dtype, a.mean, a.rstd, a.dx,
+                       span(a.weight, a.weight_dtype, 1, C, C), {a.stats, 8 * R}};
+  if (any_overlap(outs, 4, ins, 4)) return F8LIN_EINVAL;
+  const LayerNormBwd k = {a.dy, a.x, R, C, lddy, ldx, a.weight, a.weight_dtype, a.stats, a.dx,
                           need > 0 ? a.ws : nullptr};
   return status_of(launch_layer_norm_backward(k, a.x_dtype, a.dy_dtype, a.dweight, a.dweight_dtype, a.dbias,
                                               a.dbias_dtype, (hipStream_t)stream));

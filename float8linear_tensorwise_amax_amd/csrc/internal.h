@@ -192,7 +192,7 @@ struct LayerNormFwd {
   int weight_dtype, bias_dtype;
   float eps;
   void *y;            // (rows, cols)
-  float *mean, *rstd; // (rows), or both null
+  float *stats;       // (2, rows): mean, rstd; or null
   float *amax;        // max |y| after rounding, or null
 };
 struct LayerNormBwd {
@@ -200,7 +200,7 @@ struct LayerNormBwd {
   int64_t rows, cols, lddy, ldx;
   const void *weight;
   int weight_dtype;
-  const float *mean, *rstd;
+  const float *stats;
   void *dx;     // (rows, cols) of x's type, or null
   float *part;  // ln_parts(rows, cols) x 2 x cols partial sums of dw and db, or null
 };

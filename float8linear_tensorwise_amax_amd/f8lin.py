@@ -10,6 +10,7 @@ are gradients, move the version counters of what they write.
 """
 import array
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -857,19 +858,19 @@ def grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor
 
 class LayerNormFwdArgs(ctypes.Structure):
     _fields_ = [("rows", _i64), ("cols", _i64), ("x", _vp), ("ldx", _i64), ("weight", _vp), ("bias", _vp), ("y", _vp),
-                ("mean", _vp), ("rstd", _vp), ("y_amax", _vp), ("x_dtype", _int), ("weight_dtype", _int),
+                ("stats", _vp), ("y_amax", _vp), ("x_dtype", _int), ("weight_dtype", _int),
                 ("bias_dtype", _int), ("y_dtype", _int), ("eps", ctypes.c_float)]
 
 
 class LayerNormBwdArgs(ctypes.Structure):
     _fields_ = [("rows", _i64), ("cols", _i64), ("dy", _vp), ("x", _vp), ("lddy", _i64), ("ldx", _i64),
-                ("weight", _vp), ("mean", _vp), ("rstd", _vp), ("dx", _vp), ("dweight", _vp), ("dbias", _vp),
+                ("weight", _vp), ("stats", _vp), ("dx", _vp), ("dweight", _vp), ("dbias", _vp),
                 ("dy_dtype", _int), ("x_dtype", _int), ("weight_dtype", _int), ("dweight_dtype", _int),
                 ("dbias_dtype", _int), ("ws", _vp), ("ws_bytes", ctypes.c_size_t)]
 
 
-_LN_FWD = struct.Struct("@10q4if4x")
-_LN_BWD = struct.Struct("@12q5i4x2q")
+_LN_FWD = struct.Struct("@9q4if4x")
+_LN_BWD = struct.Struct("@11q5i4x2q")
 for _fmt, _cls in ((_LN_FWD, LayerNormFwdArgs), (_LN_BWD, LayerNormBwdArgs)):
     assert _fmt.size == ctypes.sizeof(_cls)
 
@@ -885,7 +886,7 @@ def _f32(t: Optional[torch.Tensor], n: int, what: str, device: torch.device) -> 
     """Pointer of a contiguous float32 tensor of n elements on `device` (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != torch.float32 or t.device != device or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.device != device or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"f8lin: {what} must be a contiguous float32 tensor of {n} elements on {device}")
     return t.data_ptr()
 
@@ -904,9 +905,9 @@ def _pair_types(x: torch.Tensor, y: torch.Tensor, what: str):
         raise TypeError(f"f8lin: {what} must be {x.dtype} like x (only a float32 x allows another type), got {y.dtype}")
 
 
-def layer_norm_forward(x, y, weight=None, bias=None, eps: float = 1e-5, mean=None, rstd=None, y_amax=None, stream=None):
-    """y (rows, cols) = the layer norm of each row of x, times weight plus bias (each (cols) or None).  mean and rstd:
-    float32 (rows) each, for the backward, or both None.  y_amax: optional float32 tensor that receives max |y|."""
+def layer_norm_forward(x, y, weight=None, bias=None, eps: float = 1e-5, stats=None, y_amax=None, stream=None):
+    """y (rows, cols) = the layer norm of each row of x, times weight plus bias (each (cols) or None).  stats: optional
+    float32 (2, rows) tensor that receives the rows' mean and rstd for the backward.  y_amax: optional float32 tensor that receives max |y|."""
     if x.dim() != 2 or y.shape != x.shape:
         raise ValueError("layer_norm_forward: x and y must be 2-D tensors of one shape")
     rows, cols = x.shape
@@ -917,16 +918,16 @@ def layer_norm_forward(x, y, weight=None, bias=None, eps: float = 1e-5, mean=Non
         _pair_types(x, y, "y")
     pw, wt = _vector(weight, cols, "weight", dev)
     pb, bt = _vector(bias, cols, "bias", dev)
-    a = _LN_FWD.pack(rows, cols, px, ldx, pw, pb, py, _f32(mean, rows, "mean", dev), _f32(rstd, rows, "rstd", dev),
-                     _f32(y_amax, 1, "y_amax", dev), _DTYPE[x.dtype], wt, bt, _DTYPE[y.dtype], eps)
+    a = _LN_FWD.pack(rows, cols, px, ldx, pw, pb, py, _f32(stats, 2 * rows, "stats", dev), _f32(y_amax, 1, "y_amax", dev), _DTYPE[x.dtype], wt, bt, _DTYPE[y.dtype], eps)
     _call(_lib.f8lin_layer_norm_forward, dev, stream, a)
 
 
+@functools.lru_cache(maxsize=1024)
 def layer_norm_workspace_bytes(rows: int, cols: int) -> int:
     return int(_lib.f8lin_layer_norm_workspace_bytes(rows, cols))
 
 
-def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, ws=None, stream=None):
+def layer_norm_backward(dy, x, weight, stats, dx=None, dweight=None, dbias=None, ws=None, stream=None):
     """dx (rows, cols; x's type), dweight (cols) and dbias (cols) -- each may be None -- from dy, x, weight (or None) and
     the forward's mean and rstd.  ws: layer_norm_workspace_bytes(rows, cols) bytes, for dweight or dbias."""
     if x.dim() != 2 or dy.shape != x.shape or (dx is not None and dx.shape != x.shape):
@@ -943,8 +944,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=
     pdw, dwt = _vector(dweight, cols, "dweight", dev)
     pdb, dbt = _vector(dbias, cols, "dbias", dev)
     _same_device(ws, "ws", dev)
-    a = _LN_BWD.pack(rows, cols, pdy, px, lddy, ldx, pw, _f32(mean, rows, "mean", dev), _f32(rstd, rows, "rstd", dev),
-                     pdx, pdw, pdb, _DTYPE[dy.dtype], _DTYPE[x.dtype], wt, dwt, dbt, _ptr(ws) or 0, _nbytes(ws))
+    a = _LN_BWD.pack(rows, cols, pdy, px, lddy, ldx, pw, _f32(stats, 2 * rows, "stats", dev), pdx, pdw, pdb, _DTYPE[dy.dtype], _DTYPE[x.dtype], wt, dwt, dbt, _ptr(ws) or 0, _nbytes(ws))
     _call(_lib.f8lin_layer_norm_backward, dev, stream, a)
 
 
@@ -1018,10 +1018,12 @@ def lora_plan(index: torch.Tensor, plan: LoraPlan, stream=None):
     torch.autograd.graph.increment_version(plan.buffer)
 
 
+@functools.lru_cache(maxsize=1024)
 def lora_forward_workspace_bytes(T: int, K: int, N: int, rank: int, adapters: int) -> int:
     return int(_lib.f8lin_lora_forward_workspace_bytes(T, K, N, rank, adapters))
 
 
+@functools.lru_cache(maxsize=1024)
 def lora_backward_workspace_bytes(T: int, K: int, N: int, rank: int, adapters: int) -> int:
     return int(_lib.f8lin_lora_backward_workspace_bytes(T, K, N, rank, adapters))
 
@@ -1050,10 +1052,19 @@ def _one_dtype(dtype: torch.dtype, **tensors):
             raise TypeError(f"f8lin: {what} must be {dtype} like x, got {t.dtype}")
 
 
+def _workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+    """Scratch for one call, of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def lora_forward(base, x, a, b, scales, plan: LoraPlan, y, h=None, ws=None, stream=None):
     """y (T, N) = base (T, N; None: 0) + what each token's adapter adds: scales[i] * (x[t] . a[i]^T) . b[i]^T.
     scales: float32 (adapters), or None for 1.  h: optional float32 tensor of lora_h_elements(T, rank) that receives the
-    inner products for lora_backward.  ws: lora_forward_workspace_bytes(T, K, N, rank, adapters) bytes.  y may be base."""
+    inner products for lora_backward.  ws: lora_forward_workspace_bytes(T, K, N, rank, adapters) bytes, or None to
+    allocate them.  y may be base."""
     T, K = x.shape
     rank, N = _lora_sizes(T, K, a, b, plan)
     if tuple(y.shape) != (T, N) or (base is not None and base.shape != y.shape):
@@ -1064,6 +1075,8 @@ def lora_forward(base, x, a, b, scales, plan: LoraPlan, y, h=None, ws=None, stre
     pbase, ldbase = (0, 0) if base is None else _dense_ld(base, "base", dev)
     if plan.device != dev:
         raise ValueError(f"f8lin: the plan is on {plan.device}, expected {dev}")
+    if ws is None:
+        ws = _workspace(lora_forward_workspace_bytes(T, K, N, rank, plan.adapters), dev, stream)
     _same_device(ws, "ws", dev)
     args = _LORA_FWD.pack(T, K, N, px, _dense(a, "a", dev), _dense(b, "b", dev), pbase, ldx, ldbase, _dense(y, "y", dev),
                           _f32(scales, plan.adapters, "scales", dev), plan.buffer.data_ptr(),
@@ -1074,7 +1087,7 @@ def lora_forward(base, x, a, b, scales, plan: LoraPlan, y, h=None, ws=None, stre
 
 def lora_backward(dy, x, a, b, scales, plan: LoraPlan, h, dx=None, da=None, db=None, ws=None, stream=None):
     """dx (T, K), da like a and db like b -- each may be None -- of lora_forward; h as it left it (needed for db).
-    ws: lora_backward_workspace_bytes(T, K, N, rank, adapters) bytes."""
+    ws: lora_backward_workspace_bytes(T, K, N, rank, adapters) bytes, or None to allocate them."""
     T, K = x.shape
     rank, N = _lora_sizes(T, K, a, b, plan)
     if tuple(dy.shape) != (T, N) or (dx is not None and dx.shape != x.shape) or \
@@ -1086,6 +1099,8 @@ def lora_backward(dy, x, a, b, scales, plan: LoraPlan, h, dx=None, da=None, db=N
     pdy, lddy = _dense_ld(dy, "dy", dev)
     if plan.device != dev:
         raise ValueError(f"f8lin: the plan is on {plan.device}, expected {dev}")
+    if ws is None:
+        ws = _workspace(lora_backward_workspace_bytes(T, K, N, rank, plan.adapters), dev, stream)
     _same_device(ws, "ws", dev)
     opt = lambda t, what: 0 if t is None else _dense(t, what, dev)  # noqa: E731
     args = _LORA_BWD.pack(T, K, N, pdy, px, _dense(a, "a", dev), _dense(b, "b", dev), lddy, ldx,

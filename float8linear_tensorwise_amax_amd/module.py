@@ -616,6 +616,15 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
 
 # -------------------------------------------------------------- layer norm
 
+def _needs_graph(*tensors: Optional[torch.Tensor]) -> bool:
+    """Whether a call on these tensors has to pass through autograd."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
 def _vector_of(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     return t if t is None or t.is_contiguous() else t.contiguous()
 
@@ -628,7 +637,7 @@ class _LayerNormFn(torch.autograd.Function):
         weight = _vector_of(weight)
         y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
         stats = torch.empty((2, rows), dtype=torch.float32, device=dev)
-        f8lin.layer_norm_forward(x, y, weight, _vector_of(bias), eps, stats[0], stats[1])
+        f8lin.layer_norm_forward(x, y, weight, _vector_of(bias), eps, stats)
         ctx.save_for_backward(x, weight, stats)
         ctx.b_dtype = None if bias is None else bias.dtype
         return y
@@ -646,7 +655,7 @@ class _LayerNormFn(torch.autograd.Function):
         ws = None
         if need_w or need_b:
             ws = torch.empty(f8lin.layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8, device=dev)
-        f8lin.layer_norm_backward(_rows(dy), x, weight, stats[0], stats[1], dx, dw, db, ws)
+        f8lin.layer_norm_backward(_rows(dy), x, weight, stats, dx, dw, db, ws)
         return dx, dw, db, None, None
 
 
@@ -673,7 +682,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         raise TypeError(f"out_dtype must be {x.dtype} (only a float32 x allows another type), got {dtype}")
     # (an empty last dimension leaves reshape nothing to infer the rows from)
     x2 = _rows(x) if x.numel() else x.reshape(x.shape[:-1].numel(), cols)
-    if torch.is_grad_enabled():
+    if _needs_graph(x, weight, bias):
         y = _LayerNormFn.apply(x2, weight, bias, eps, dtype)
     else:
         _refuse_tangents("layer_norm", x, weight, bias)
@@ -773,13 +782,12 @@ class LoraBatch:
 
 
 def _lora_forward(base, x, a, b, plan, scales, keep):
-    T, K = x.shape
-    rank, N = f8lin._lora_sizes(T, K, a, b, plan)
-    dev = x.device
-    y = torch.empty((T, N), dtype=x.dtype, device=dev)
-    h = torch.empty(f8lin.lora_h_elements(T, rank), dtype=torch.float32, device=dev) if keep else None
-    ws = torch.empty(f8lin.lora_forward_workspace_bytes(T, K, N, rank, plan.adapters), dtype=torch.uint8, device=dev)
-    f8lin.lora_forward(base, x, a, b, scales, plan, y, h, ws)
+    """(y, the inner products if they are to be kept)."""
+    y = torch.empty(base.shape, dtype=x.dtype, device=x.device)
+    h = None
+    if keep:
+        h = torch.empty(f8lin.lora_h_elements(plan.tokens, b.shape[2]), dtype=torch.float32, device=x.device)
+    f8lin.lora_forward(base, x, a, b, scales, plan, y, h)
     return y, h
 
 
@@ -800,13 +808,10 @@ class _LoraAddFn(torch.autograd.Function):
         if need_x or need_a or need_b:
             x, a, b, h, buffer, scales = ctx.saved_tensors
             plan = f8lin.LoraPlan(*ctx.sizes, buffer=buffer)
-            (T, K), (adapters, N, rank) = x.shape, b.shape
-            dx = torch.empty((T, K), dtype=x.dtype, device=x.device) if need_x else None
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
             da = torch.empty_like(a) if need_a else None
             db = torch.empty_like(b) if need_b else None
-            ws = torch.empty(f8lin.lora_backward_workspace_bytes(T, K, N, rank, adapters), dtype=torch.uint8,
-                             device=x.device)
-            f8lin.lora_backward(_rows(dy), x, a, b, scales, plan, h, dx, da, db, ws)
+            f8lin.lora_backward(_rows(dy), x, a, b, scales, plan, h, dx, da, db)
         return dy if need_base else None, dx, da, db, None, None
 
 
@@ -820,15 +825,18 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     adapter that no token uses gets a gradient of zero); forward-mode derivatives are refused (NotImplementedError)."""
     if not x.is_cuda:
         raise RuntimeError("lora_add runs on the GPU only (libf8lin has no CPU path)")
-    if x.dim() < 1 or base.shape[:-1] != x.shape[:-1] or b.dim() != 3 or base.shape[-1] != b.shape[1]:
+    if x.dim() < 1 or base.dim() < 1 or base.shape[:-1] != x.shape[:-1] or b.dim() != 3 or base.shape[-1] != b.shape[1]:
         raise ValueError(f"base must be x's tokens by the adapters' N, got {tuple(base.shape)} beside {tuple(x.shape)} "
                          f"and {tuple(b.shape)}")
     if scales is not None and scales.requires_grad:
         raise ValueError("scales take no part in the graph: detach them")
-    lead = x.shape[:-1]
-    flat = lambda t: _rows(t) if t.numel() else t.reshape(lead.numel(), t.shape[-1])  # noqa: E731
-    base2, x2 = flat(base), flat(x)
-    if torch.is_grad_enabled():
+    if x.dim() == 2:
+        base2, x2 = _rows(base), _rows(x)
+    else:
+        # (an empty last dimension leaves reshape nothing to infer the rows from)
+        tokens = x.shape[:-1].numel()
+        base2, x2 = (_rows(t) if t.numel() else t.reshape(tokens, t.shape[-1]) for t in (base, x))
+    if _needs_graph(base, x, a, b):
         y = _LoraAddFn.apply(base2, x2, a, b, batch.plan, scales)
     else:
         _refuse_tangents("lora_add", base, x, a, b)

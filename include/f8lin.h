@@ -523,8 +523,8 @@ int f8lin_grad_clip(const f8lin_grad *list, int count, int norm_type, float max_
  *   mean = sum(x) / n,  rstd = 1 / sqrt(sum((x - mean)^2) / n + eps)
  *   y = (x - mean) * rstd * weight + bias
  * Any sizes, x with a row stride.  weight and bias may be NULL (1 and 0) and
- * are of any type; y has x's type, or with fp32 x any.  mean and rstd, (rows)
- * each, are what the backward needs (both NULL: not kept).  y_amax, if set,
+ * are of any type; y has x's type, or with fp32 x any.  stats (2, rows), the
+ * rows' mean and then their rstd, are what the backward needs (NULL: not kept).  y_amax, if set,
  * receives max |y| of the rounded values (NaN above all, 0 for no element):
  * for bf16 y what a following f8lin_forward with x_amax_given takes.
  * eps >= 0.  A row with an Inf or NaN is NaN as a whole, and no other row.
@@ -535,7 +535,7 @@ typedef struct {
   int64_t ldx;   /* elements; 0: cols */
   const void *weight, *bias; /* (cols) or NULL */
   void *y;                   /* (rows, cols) */
-  float *mean, *rstd, *y_amax;
+  float *stats, *y_amax;
   int x_dtype, weight_dtype, bias_dtype, y_dtype;
   float eps;
 } f8lin_layer_norm_fwd_args;
@@ -552,7 +552,7 @@ typedef struct {
   const void *dy, *x;
   int64_t lddy, ldx; /* elements; 0: cols */
   const void *weight;
-  const float *mean, *rstd;
+  const float *stats;
   void *dx, *dweight, *dbias;
   int dy_dtype, x_dtype, weight_dtype, dweight_dtype, dbias_dtype;
   float *ws;
