@@ -687,7 +687,8 @@ __device__ __forceinline__ void up_products(const UpFrag<DT, KB> (&wf)[4], const
 }
 
 template <int DT, bool W_T, int NB, int KB, bool SMALL, bool WHOLE, bool PAST>
-__device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, const UpCols cols) {
+__device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, const UpCols cols,
+                                        u32x4 *shared) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kPieces = 16 / kE<DT>;
   constexpr int kRanks = DT == F8LIN_FP32 ? 16 : KB;  // of a block
@@ -698,8 +699,7 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
   const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
   const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
   auto position = [&](int m) { return tile.y + min(16 * m + i, tile.z - 1); };
-  // (what belongs to rows that are not there is whatever the memory holds, and goes to no row that is)
-  const u32x4 *const h = reinterpret_cast<const u32x4 *>(a.h) + (int64_t)at * 4 * (rp / 16) * 64 + (threadIdx.x & 63);
+  const u32x4 *const from = reinterpret_cast<const u32x4 *>(a.h) + (int64_t)at * 4 * (rp / 16) * 64;
   const int h_ld = rp / 16 * 64;
   auto scale = [&](v4f (&acc)[4], int exponent) {
     if constexpr (DT == F8LIN_FP16) {
@@ -724,45 +724,54 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
 #pragma unroll
     for (int k = 0; k < NB; ++k) up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, cols.c0, kRanks * k, wf[k]);
     u32x4 raw[4][kPieces];
-    UpH<DT, KB> hf[2][NB];
     int64_t t[4];
     int exponent[4];
     const int groups = (tile.z + 15) >> 4;
+    // the tile's H, read once by the workgroup (what belongs to rows that are not there is whatever the memory holds,
+    // and goes to no row that is)
+    constexpr int kMine = 4 * NB * kRanks / 16 * 64 / 256;
+    u32x4 mine[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) mine[k] = from[threadIdx.x + 256 * k];
     // (rows that are not there: the last one's)
 #pragma unroll
     for (int m = 0; m < 4; ++m) t[m] = order[position(m)];
-    auto load_h = [&](int m) {
-#pragma unroll
-      for (int k = 0; k < NB; ++k) up_h<DT, KB>(h + m * h_ld, k, hf[m & 1][k]);
-    };
-    load_h(0);
+    const u32x4 *const h = shared + (threadIdx.x & 63);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       up_base<DT, SMALL>(a, t[m], cols, raw[m]);
       if constexpr (DT == F8LIN_FP16) exponent[m] = a.exponents[position(m)];
     }
 #pragma unroll
+    for (int k = 0; k < kMine; ++k) shared[threadIdx.x + 256 * k] = mine[k];
+    __syncthreads();
+#pragma unroll
     for (int m = 0; m < 4; ++m) {
       if (m >= groups) break;
-      if (m < 3) load_h(m + 1);
       v4f acc[4] = {zero, zero, zero, zero};
 #pragma unroll
-      for (int k = 0; k < NB; ++k) up_products<DT, KB>(wf[k], hf[m & 1][k], acc);
+      for (int k = 0; k < NB; ++k) {
+        UpH<DT, KB> hf;
+        up_h<DT, KB>(h + m * h_ld, k, hf);
+        up_products<DT, KB>(wf[k], hf, acc);
+      }
       scale(acc, exponent[m]);
       if (16 * m + i < tile.z) up_store<DT, SMALL, PAST>(a, t[m], true, cols, raw[m], acc);
     }
   } else {
+    const u32x4 *const h = from + (threadIdx.x & 63);
+    constexpr bool kScaled = DT == F8LIN_FP16;  // 64 ranks share an exponent
     v4f sum[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum[m][j] = zero;
     for (int r0 = 0; r0 < rp; r0 += 64) {
-      v4f acc[4][4];
+      v4f part[kScaled ? 4 : 1][4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
+      for (int m = 0; m < (kScaled ? 4 : 1); ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[m][j] = zero;
+        for (int j = 0; j < 4; ++j) part[m][j] = zero;
       for (int r = r0; r < min(rp, r0 + 64); r += kRanks) {
         UpFrag<DT, KB> wf[4];
         up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, cols.c0, r, wf);
@@ -770,14 +779,16 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
         for (int m = 0; m < 4; ++m) {
           UpH<DT, KB> hf;
           up_h<DT, KB>(h + m * h_ld, r / kRanks, hf);
-          up_products<DT, KB>(wf, hf, acc[m]);
+          up_products<DT, KB>(wf, hf, kScaled ? part[m % (kScaled ? 4 : 1)] : sum[m]);
         }
       }
+      if constexpr (kScaled) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if constexpr (DT == F8LIN_FP16) scale(acc[m], a.exponents[(int64_t)(r0 / 64) * a.tokens + position(m)]);
+        for (int m = 0; m < 4; ++m) {
+          scale(part[m], a.exponents[(int64_t)(r0 / 64) * a.tokens + position(m)]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[m][j] += acc[m][j];
+          for (int j = 0; j < 4; ++j) sum[m][j] += part[m][j];
+        }
       }
     }
 #pragma unroll
@@ -792,15 +803,17 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
 
 template <int DT, bool W_T, int NB, int KB, bool SMALL, bool WHOLE, bool PAST>
 __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
+  __shared__ u32x4 shared[NB > 0 ? 4 * NB * (DT == F8LIN_FP32 ? 16 : KB) / 16 * 64 : 1];
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
+  // (a wave past the columns takes the last ones, for the barriers' sake, and stores none of them)
   const int64_t c0 = (int64_t)blockIdx.x * 256 + 64 * (threadIdx.x >> 6);
-  if (c0 >= C) return;
   for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles) break;
-    up_tile<DT, W_T, NB, KB, SMALL, WHOLE, PAST>(a, tile, at, order, up_cols(c0, C));
+    up_tile<DT, W_T, NB, KB, SMALL, WHOLE, PAST>(a, tile, at, order, up_cols(c0, C), shared);
+    if (NB > 0) __syncthreads();  // (of the tile's reads)
   }
 }
 
