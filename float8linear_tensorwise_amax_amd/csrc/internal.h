@@ -194,6 +194,7 @@ struct LayerNormFwd {
   void *y;            // (rows, cols)
   float *stats;       // (2, rows): mean, rstd; or null
   float *amax;        // max |y| after rounding, or null
+  int64_t first = 0;  // row a launch begins with
 };
 struct LayerNormBwd {
   const void *dy, *x;
@@ -203,6 +204,7 @@ struct LayerNormBwd {
   const float *stats;
   void *dx;     // (rows, cols) of x's type, or null
   float *part;  // ln_parts(rows, cols) x 2 x cols partial sums of dw and db, or null
+  int64_t first = 0;
 };
 int ln_parts(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_forward(const LayerNormFwd &a, int x_dtype, int y_dtype, hipStream_t stream);

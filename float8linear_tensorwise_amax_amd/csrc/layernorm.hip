@@ -5,14 +5,20 @@
 //   dw = sum over rows of dy * xhat,  db = sum over rows of dy
 //
 // HBM-bound: the forward reads x and writes y once, the backward reads x and
-// dy and writes dx once.  A row stays in the registers of the wave (or of the
-// workgroup) that normalises it, so that the mean, the centred squares and
-// the output are three passes over registers, not memory; only rows of more
-// than kRowMax values are read again.  Everything is computed in binary32
-// from the values as read, and rounded once.  The backward's workgroups keep
-// dw and db of their rows in registers too and leave one partial sum each,
-// which a second launch adds in a fixed order (no atomics: the same bits on
-// every run).
+// dy and writes dx once (65536 x 4096 bf16: 226 us, 4.8 TB/s, and 298 us, 5.4
+// TB/s; 12288 x 1600: 18 and 32 us).  A row stays in the registers of the wave
+// (or of the workgroup) that normalises it, so that the mean, the centred
+// squares and the output are three passes over registers, not memory; only
+// rows of more than 16384 values are read again.  Everything is computed in
+// binary32 from the values as read, and rounded once.  The backward's
+// workgroups keep dw and db of their rows in registers too and leave one
+// partial sum each, which a second launch adds in a fixed order (no atomics:
+// the same bits on every run).
+//
+// A wave a row up to 2048 values in the forward (12288 x 1600: 18 us, a
+// workgroup a row 22), a workgroup a row above (65536 x 4096: 236 us, a wave a
+// row 257) and from 512 in the backward, whose sums need the registers (12288 x
+// 1600: 37 us in 512 workgroups, a wave a row 41).
 #include <algorithm>
 
 #include "rows.h"
@@ -20,10 +26,14 @@
 namespace f8lin {
 namespace {
 
+// What is read and written goes past the caches where it is more than they
+// hold (65536 x 4096: forward 226 us, through them 231; backward 298 and 318;
+// 8192 x 4096: forward 28.5 past and 25.2 through them).
 constexpr int64_t kPastBytes = (int64_t)256 << 20;
 
 // Sum over the G threads of a row (G = 64: a wave; else the workgroup), the
-// same in all of them.  `slot` keeps consecutive sums apart in the LDS.
+// same in all of them.  Consecutive sums take different `red`: a wave may still
+// read the last one's.
 template <int G, int S>
 __device__ __forceinline__ void row_sum(float (&v)[S], float (*red)[S]) {
 #pragma unroll
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void ln_forward_kernel(const Lay
   __shared__ float red[2][16][1];
   constexpr int kRows = G == 64 ? 4 : 1;  // rows of a workgroup
   const int lane = G == 64 ? (threadIdx.x & 63) : threadIdx.x;
-  const int64_t row = (int64_t)blockIdx.x * kRows + (G == 64 ? threadIdx.x >> 6 : 0);
+  const int64_t row = a.first + (int64_t)blockIdx.x * kRows + (G == 64 ? threadIdx.x >> 6 : 0);
   if (G == 64 && row >= a.rows) return;  // (no barrier below for G = 64)
   const int cols = (int)a.cols;
   Load8<XT, TINY, PAST> raw[C];
@@ -229,7 +239,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void ln_forward_kernel(const Lay
 template <int XT, int YT>
 __global__ __launch_bounds__(1024) void ln_forward_wide_kernel(const LayerNormFwd a) {
   __shared__ float red[2][16][1];
-  const int64_t row = blockIdx.x, at = row * a.ldx, cols = a.cols;
+  const int64_t row = a.first + blockIdx.x, at = row * a.ldx, cols = a.cols;
   float v[8];
   float s[1] = {0.0f}, q[1] = {0.0f};
   for (int64_t col = 8 * (int64_t)threadIdx.x; col < cols; col += 8 * 1024) {
@@ -373,7 +383,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void ln_backward_kernel(const La
 template <int XT, int YT>
 __global__ __launch_bounds__(1024) void ln_backward_wide_kernel(const LayerNormBwd a) {
   __shared__ float red[16][2];
-  const int64_t row = blockIdx.x, cols = a.cols;
+  const int64_t row = a.first + blockIdx.x, cols = a.cols;
   const float mean = a.stats[row], rstd = a.stats[a.rows + row], inv = 1.0f / (float)cols;
   float s[2] = {0.0f, 0.0f}, x[8], d[8], w[8];
 #pragma unroll
@@ -468,9 +478,12 @@ __global__ __launch_bounds__(1024) void ln_join_kernel(const float *part, int pa
   else reinterpret_cast<uint16_t *>(out)[col] = (uint16_t)o;
 }
 
+// Rows of a launch: a grid has fewer than 2^32 threads.
+constexpr int64_t kMaxRows = (int64_t)1 << 21;
+
 template <int XT, int YT, bool PAST>
 void forward_sized(const LayerNormFwd &a, hipStream_t s) {
-  const unsigned rows = (unsigned)a.rows, quads = (unsigned)((a.rows + 3) / 4);
+  const unsigned rows = (unsigned)std::min(a.rows - a.first, kMaxRows), quads = (rows + 3) / 4;
   if (a.cols <= 512) ln_forward_kernel<XT, YT, 64, 1, false, PAST><<<quads, 256, 0, s>>>(a);
   else if (a.cols <= 1024) ln_forward_kernel<XT, YT, 64, 2, false, PAST><<<quads, 256, 0, s>>>(a);
   else if (a.cols <= 2048) ln_forward_kernel<XT, YT, 64, 4, false, PAST><<<quads, 256, 0, s>>>(a);
@@ -481,7 +494,8 @@ void forward_sized(const LayerNormFwd &a, hipStream_t s) {
 }
 template <int XT, int YT>
 void forward_typed(const LayerNormFwd &a, hipStream_t s) {
-  if (a.cols < 8) ln_forward_kernel<XT, YT, 64, 1, true, false><<<(unsigned)((a.rows + 3) / 4), 256, 0, s>>>(a);
+  if (a.cols < 8)
+    ln_forward_kernel<XT, YT, 64, 1, true, false><<<(unsigned)((std::min(a.rows - a.first, kMaxRows) + 3) / 4), 256, 0, s>>>(a);
   else if (a.rows * a.cols * (elem_bytes(XT) + elem_bytes(YT)) > kPastBytes) forward_sized<XT, YT, true>(a, s);
   else forward_sized<XT, YT, false>(a, s);
 }
@@ -494,7 +508,9 @@ void backward_sized(const LayerNormBwd &a, int parts, int64_t each, hipStream_t 
   else if (a.cols <= 8192) ln_backward_kernel<XT, YT, 512, 2, false, PAST><<<parts, 512, 0, s>>>(a, each);
   else if (a.cols <= 16384) ln_backward_kernel<XT, YT, 512, 4, false, PAST><<<parts, 512, 0, s>>>(a, each);
   else {
-    if (a.dx) ln_backward_wide_kernel<XT, YT><<<(unsigned)a.rows, 1024, 0, s>>>(a);
+    LayerNormBwd b = a;
+    for (; a.dx && b.first < a.rows; b.first += kMaxRows)
+      ln_backward_wide_kernel<XT, YT><<<(unsigned)std::min(a.rows - b.first, kMaxRows), 1024, 0, s>>>(b);
     const int blocks = (int)((a.cols + 2047) / 2048);
     if (a.part) ln_param_kernel<XT, YT><<<(unsigned)parts * blocks, 256, 0, s>>>(a, each, blocks);
   }
@@ -540,10 +556,11 @@ int ln_parts(int64_t rows, int64_t cols) {
 hipError_t launch_layer_norm_forward(const LayerNormFwd &a, int x_dtype, int y_dtype, hipStream_t stream) {
   if (!a.amax && (a.rows == 0 || a.cols == 0)) return hipSuccess;
   if (a.amax) ln_clear_kernel<<<1, 1, 0, stream>>>(a.amax);
-  if (a.rows > 0 && a.cols > 0) {
-    if (x_dtype == F8LIN_BF16) forward_by_y<F8LIN_BF16>(a, y_dtype, stream);
-    else if (x_dtype == F8LIN_FP16) forward_by_y<F8LIN_FP16>(a, y_dtype, stream);
-    else forward_by_y<F8LIN_FP32>(a, y_dtype, stream);
+  LayerNormFwd k = a;
+  for (; a.cols > 0 && k.first < a.rows; k.first += kMaxRows) {
+    if (x_dtype == F8LIN_BF16) forward_by_y<F8LIN_BF16>(k, y_dtype, stream);
+    else if (x_dtype == F8LIN_FP16) forward_by_y<F8LIN_FP16>(k, y_dtype, stream);
+    else forward_by_y<F8LIN_FP32>(k, y_dtype, stream);
   }
   return hipGetLastError();
 }
