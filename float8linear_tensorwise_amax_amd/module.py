@@ -870,7 +870,9 @@ class LoraLinear(nn.Module):
         y = self.base(x)
         if self.batch is None:
             return y
-        return lora_add(y, x.to(y.dtype), self.lora_a.to(y.dtype), self.lora_b.to(y.dtype), self.batch, self.lora_scales)
+        # (casting the module casts its scales too)
+        return lora_add(y, x.to(y.dtype), self.lora_a.to(y.dtype), self.lora_b.to(y.dtype), self.batch,
+                        self.lora_scales.float())
 
     def extra_repr(self):
         return f"adapters={self.adapters}, rank={self.rank}"

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_helpers import DTYPES, close, draw, lora_bounds, norm_bounds, np64
+from block_helpers import DTYPES, close, draw, lora_bounds, lora_grad_bounds, norm_bounds, np64
 from test_gpu_lora import check, f8lin, index_of, mod, tensors  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +179,52 @@ def test_overlapping_calls_share_nothing(mod):
     torch.cuda.synchronize()
     for i, outs in got[0] + got[1]:
         assert all(torch.equal(p, q) for p, q in zip(outs, want[i]))
+
+
+def test_subnormal_fp16(mod):
+    """fp16 data in the subnormal range (small gradients) are not taken as zeros, neither in x and dy nor in the weights."""
+    T, K, N, R, L = 1100, 64, 128, 16, 2
+    index = index_of(T, L, 1)
+    base = torch.zeros((T, N), dtype=torch.float16)
+    x = (draw((T, K), torch.float32, 1) * 2.0 ** -18).half()
+    dy = (draw((T, N), torch.float32, 2) * 2.0 ** -20).half()
+    a, b = draw((L, R, K), torch.float32, 3).half() * 64, draw((L, N, R), torch.float32, 4).half() * 64
+    assert float((x.abs() < 2.0 ** -14).float().mean()) > 0.9 and x.any()
+    for small in (False, True):
+        if small:
+            x, a = draw((T, K), torch.float32, 1).half(), (a.float() * 2.0 ** -24).half()
+        for t in (T, 90):
+            i = index[:t]
+            leaves = [q.cuda().requires_grad_() for q in (base[:t], x[:t], a, b)]
+            y = mod.lora_add(*leaves, mod.LoraBatch(torch.from_numpy(i).cuda(), L))
+            dx, da, db = torch.autograd.grad(y, leaves[1:], dy[:t].cuda())
+            args = [np64(q) for q in (base[:t], x[:t], a, b)]
+            ref, h, d_y, d_h = lora_bounds(*args, i, np.ones(L), torch.float16)
+            close(y, ref, d_y, "y")
+            refs, errs = lora_grad_bounds(np64(dy[:t]), *args[1:], i, np.ones(L), h, d_h, torch.float16)
+            for got, r, e in zip((dx, da, db), refs, errs):
+                close(got, r, e, "gradient")
+    rows = (draw((40, 300), torch.float32, 5) * 2.0 ** -20).half()
+    n = norm_bounds(np64(rows), None, None, 0.0, 40, 300)
+    close(mod.layer_norm(rows.cuda(), eps=0.0), n["y"], n["d_y"], "norm")
+
+
+def test_inference_mode_and_cast_modules(mod):
+    """A batch made and used in inference mode; a module cast to bf16 after its conversion keeps working."""
+    lin = torch.nn.Sequential(torch.nn.LayerNorm(48), torch.nn.Linear(48, 80)).cuda()
+    mod.convert_to_lora(mod.convert_layer_norm(lin), 3, 4, scale=1.5)
+    lin.bfloat16()
+    x = draw((20, 48), torch.bfloat16, 1).cuda()
+    index = torch.from_numpy(index_of(20, 3, 2, "single")).cuda()
+    with torch.no_grad():
+        lin[1].lora_b.normal_()
+    with torch.inference_mode():
+        mod.set_lora_batch(lin, mod.LoraBatch(index, 3))
+        y = lin(x)
+        lin[1].batch.update(index)
+        assert torch.equal(lin(x), y)
+    mod.set_lora_batch(lin, mod.LoraBatch(index, 3))
+    z = lin(x)
+    assert torch.equal(z.detach(), y) and z.dtype == torch.bfloat16
+    z.float().sum().backward()
+    assert lin[1].lora_a.grad is not None and lin[0].weight.grad is not None
