@@ -916,9 +916,13 @@ def layer_norm_forward(x, y, weight=None, bias=None, eps: float = 1e-5, stats=No
     py = _dense(y, "y", dev)
     if y.dtype is not x.dtype:
         _pair_types(x, y, "y")
-    pw, wt = _vector(weight, cols, "weight", dev)
-    pb, bt = _vector(bias, cols, "bias", dev)
-    a = _LN_FWD.pack(rows, cols, px, ldx, pw, pb, py, _f32(stats, 2 * rows, "stats", dev), _f32(y_amax, 1, "y_amax", dev), _DTYPE[x.dtype], wt, bt, _DTYPE[y.dtype], eps)
+    pw = wt = pb = bt = 0
+    if weight is not None:
+        pw, wt = _vector(weight, cols, "weight", dev)
+    if bias is not None:
+        pb, bt = _vector(bias, cols, "bias", dev)
+    a = _LN_FWD.pack(rows, cols, px, ldx, pw, pb, py, 0 if stats is None else _f32(stats, 2 * rows, "stats", dev),
+                     0 if y_amax is None else _f32(y_amax, 1, "y_amax", dev), _DTYPE[x.dtype], wt, bt, _DTYPE[y.dtype], eps)
     _call(_lib.f8lin_layer_norm_forward, dev, stream, a)
 
 
@@ -1033,22 +1037,32 @@ def lora_h_elements(T: int, rank: int) -> int:
     return T * (16 if rank <= 16 else -(-rank // 32) * 32)
 
 
-def _lora_sizes(x_rows: int, K: int, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan):
-    """(rank, N) of adapters a (adapters, rank, K), b (adapters, N, rank) beside the plan."""
+def _lora_refuse(x_rows: int, K: int, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan):
+    """Raises for adapters a (adapters, rank, K), b (adapters, N, rank) that do not fit x and the plan."""
     if a.dim() != 3 or b.dim() != 3 or a.shape[0] != plan.adapters or b.shape[0] != plan.adapters or \
             a.shape[2] != K or b.shape[2] != a.shape[1]:
         raise ValueError(f"f8lin: adapters must be ({plan.adapters}, rank, {K}) and ({plan.adapters}, N, rank), got "
                          f"{tuple(a.shape)} and {tuple(b.shape)}")
     if not 1 <= a.shape[1] <= LORA_MAX_RANK:
         raise ValueError(f"f8lin: the rank must be 1 to {LORA_MAX_RANK}, got {a.shape[1]}")
-    if x_rows != plan.tokens:
-        raise ValueError(f"f8lin: the plan is of {plan.tokens} tokens, got {x_rows} rows")
-    return a.shape[1], b.shape[1]
+    raise ValueError(f"f8lin: the plan is of {plan.tokens} tokens, got {x_rows} rows")
 
 
-def _one_dtype(dtype: torch.dtype, **tensors):
-    for what, t in tensors.items():
-        if t is not None and t.dtype != dtype:
+def _lora_sizes(x_rows: int, K: int, a: torch.Tensor, b: torch.Tensor, plan: LoraPlan):
+    """(rank, N) of the adapters beside the plan."""
+    sa, sb = a.shape, b.shape
+    if len(sa) != 3 or len(sb) != 3:
+        _lora_refuse(x_rows, K, a, b, plan)
+    (la, rank, ka), (lb, N, rb) = sa, sb
+    if la != plan.adapters or lb != la or ka != K or rb != rank or x_rows != plan.tokens or not 1 <= rank <= LORA_MAX_RANK:
+        _lora_refuse(x_rows, K, a, b, plan)
+    return rank, N
+
+
+def _one_dtype(dtype: torch.dtype, *named):
+    """Raises unless every (name, tensor or None) has this dtype."""
+    for what, t in named:
+        if t is not None and t.dtype is not dtype:
             raise TypeError(f"f8lin: {what} must be {dtype} like x, got {t.dtype}")
 
 
@@ -1067,21 +1081,26 @@ def lora_forward(base, x, a, b, scales, plan: LoraPlan, y, h=None, ws=None, stre
     allocate them.  y may be base."""
     T, K = x.shape
     rank, N = _lora_sizes(T, K, a, b, plan)
-    if tuple(y.shape) != (T, N) or (base is not None and base.shape != y.shape):
+    if y.shape != (T, N) or (base is not None and base.shape != y.shape):
         raise ValueError("lora_forward: shape mismatch")
     px, ldx = _dense_ld(x, "x")
     dev = x.device
-    _one_dtype(x.dtype, a=a, b=b, base=base, y=y)
+    dt = x.dtype
+    if a.dtype is not dt or b.dtype is not dt or y.dtype is not dt or (base is not None and base.dtype is not dt):
+        _one_dtype(dt, ("a", a), ("b", b), ("base", base), ("y", y))
     pbase, ldbase = (0, 0) if base is None else _dense_ld(base, "base", dev)
     if plan.device != dev:
         raise ValueError(f"f8lin: the plan is on {plan.device}, expected {dev}")
     if ws is None:
-        ws = _workspace(lora_forward_workspace_bytes(T, K, N, rank, plan.adapters), dev, stream)
-    _same_device(ws, "ws", dev)
+        nbytes = lora_forward_workspace_bytes(T, K, N, rank, plan.adapters)
+        pws = (ws := _workspace(nbytes, dev, stream)).data_ptr()
+    else:
+        _same_device(ws, "ws", dev)
+        pws, nbytes = _ptr(ws) or 0, _nbytes(ws)
     args = _LORA_FWD.pack(T, K, N, px, _dense(a, "a", dev), _dense(b, "b", dev), pbase, ldx, ldbase, _dense(y, "y", dev),
                           _f32(scales, plan.adapters, "scales", dev), plan.buffer.data_ptr(),
-                          0 if h is None else _f32(h, lora_h_elements(T, rank), "h", dev), _ptr(ws) or 0, _nbytes(ws),
-                          rank, plan.adapters, _DTYPE[x.dtype])
+                          0 if h is None else _f32(h, lora_h_elements(T, rank), "h", dev), pws, nbytes, rank,
+                          plan.adapters, _DTYPE[dt])
     _call(_lib.f8lin_lora_forward, dev, stream, args)
 
 
@@ -1095,7 +1114,7 @@ def lora_backward(dy, x, a, b, scales, plan: LoraPlan, h, dx=None, da=None, db=N
         raise ValueError("lora_backward: shape mismatch")
     px, ldx = _dense_ld(x, "x")
     dev = x.device
-    _one_dtype(x.dtype, dy=dy, a=a, b=b, dx=dx, da=da, db=db)
+    _one_dtype(x.dtype, ("dy", dy), ("a", a), ("b", b), ("dx", dx), ("da", da), ("db", db))
     pdy, lddy = _dense_ld(dy, "dy", dev)
     if plan.device != dev:
         raise ValueError(f"f8lin: the plan is on {plan.device}, expected {dev}")

@@ -825,23 +825,25 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     adapter that no token uses gets a gradient of zero); forward-mode derivatives are refused (NotImplementedError)."""
     if not x.is_cuda:
         raise RuntimeError("lora_add runs on the GPU only (libf8lin has no CPU path)")
-    if x.dim() < 1 or base.dim() < 1 or base.shape[:-1] != x.shape[:-1] or b.dim() != 3 or base.shape[-1] != b.shape[1]:
-        raise ValueError(f"base must be x's tokens by the adapters' N, got {tuple(base.shape)} beside {tuple(x.shape)} "
-                         f"and {tuple(b.shape)}")
+    sx, sb = x.shape, base.shape
+    if len(sx) < 1 or len(sb) != len(sx) or sb[:-1] != sx[:-1] or b.dim() != 3 or sb[-1] != b.shape[1]:
+        raise ValueError(f"base must be x's tokens by the adapters' N, got {tuple(sb)} beside {tuple(sx)} and "
+                         f"{tuple(b.shape)}")
     if scales is not None and scales.requires_grad:
         raise ValueError("scales take no part in the graph: detach them")
-    if x.dim() == 2:
-        base2, x2 = _rows(base), _rows(x)
-    else:
+    base2, x2 = base, x
+    if len(sx) != 2 and not (x.numel() and base.numel()):
         # (an empty last dimension leaves reshape nothing to infer the rows from)
-        tokens = x.shape[:-1].numel()
-        base2, x2 = (_rows(t) if t.numel() else t.reshape(tokens, t.shape[-1]) for t in (base, x))
+        tokens = sx[:-1].numel()
+        base2, x2 = base.reshape(tokens, sb[-1]), x.reshape(tokens, sx[-1])
+    base2, x2 = _rows(base2), _rows(x2)
     if _needs_graph(base, x, a, b):
         y = _LoraAddFn.apply(base2, x2, a, b, batch.plan, scales)
     else:
         _refuse_tangents("lora_add", base, x, a, b)
-        y = _lora_forward(base2, x2, a.contiguous(), b.contiguous(), batch.plan, scales, False)[0]
-    return y if base.dim() == 2 else y.reshape(base.shape)
+        y = _lora_forward(base2, x2, a if a.is_contiguous() else a.contiguous(),
+                          b if b.is_contiguous() else b.contiguous(), batch.plan, scales, False)[0]
+    return y if len(sx) == 2 else y.reshape(sb)
 
 
 class LoraLinear(nn.Module):
