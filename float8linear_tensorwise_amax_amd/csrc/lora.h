@@ -44,8 +44,9 @@ struct LoraDown {
   // H as the later products take it: in the up product's operand fragments, a
   // tile after the other, max_tiles x 64 x rank_pad (h, with fp16 data beside
   // its exponents, one for 64 ranks of a position: rank / 64 rounded up x
-  // tokens), and by rank, rank_pad x tokens (ht); either may be null.  Only with lora_split: parts_out, the parts' sums in binary32, parts
-  // x tokens x rank_pad, in place of h.
+  // tokens), and by rank, rank_pad x tokens (ht); either may be null.  Only with
+  // lora_split: parts_out, the parts' sums in binary32, parts x tokens x
+  // rank_pad, in place of h.
   uint32_t *h, *ht;
   int *exponents;
   float *parts_out;

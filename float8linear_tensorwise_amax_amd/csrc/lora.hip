@@ -21,13 +21,14 @@
 // adapter's rows, read by every tile, are half of what passes the L2).  64
 // single tokens of 56 adapters, rank 16: 6 and 16 us for 33 MB of adapters,
 // two chains of dependent cold reads.
-// Operands go from memory to registers in the matrix instructions' own layout,
-// with no LDS between: the contraction's order is free, so that a lane's 16
-// bytes are whatever 8 (4 in binary32) values are contiguous, and where the
-// contraction runs across rows a lane takes 8 rows of a block of columns and
-// transposes them in registers.  Loads stand in straight lines, whole blocks
-// ahead of their use: with a bounds check at each load the same kernels took
-// twice as long (down 186 us, outer 379).
+// Rows and weights go from memory to registers in the matrix instructions' own
+// layout, with no LDS between (a tile's H passes through it, once for the four
+// waves): the contraction's order is free, so that a lane's 16 bytes are
+// whatever 8 (4 in binary32) values are contiguous, and where the contraction
+// runs across rows a lane takes 8 rows of a block of columns and transposes
+// them in registers.  Loads stand in straight lines, whole blocks ahead of
+// their use: with a bounds check at each load the same kernels took twice as
+// long (down 186 us, outer 379).
 //
 // H and G are (T, R), summed in binary32.  For the 16-bit types they are handed
 // on as two 16-bit values each, 16 bits of mantissa or more in all, so that the
@@ -366,7 +367,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
       for (int h = 0; h < 2; ++h) {
         const int64_t c = c0 + h * E;
 #pragma unroll
-        for (int m = 0; m < M; ++m) 
+        for (int m = 0; m < M; ++m)
           s.x[h][m] = SMALL ? load_each<DT, E>(x[m], c, C) : load_whole<DT, E>(x[m] + c);
         if constexpr (!W_T) {
 #pragma unroll
@@ -521,8 +522,7 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
     const float *const from = a.parts_out + (int64_t)(p + tp) * rp + r + tr;
     float v = from[0];
     for (int k = 1; k < a.parts; ++k) v += from[k * ld];
-    const uint32_t w = h_word<DT>(v);
-    turn[tp][tr] = w;
+    turn[tp][tr] = h_word<DT>(v);
   }
   __syncthreads();
   if (p + tr < a.tokens) a.ht[(int64_t)(r + tp) * a.tokens + p + tr] = turn[tr][tp];
@@ -987,8 +987,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
 #pragma unroll
       for (int e = 0; e < E; ++e) row[e] = reinterpret_cast<const elem *>(side.x) + (int64_t)order[min(at + e, p1 - 1)] * side.ldx;
 #pragma unroll
-      for (int e = 0; e < E; ++e) 
-          s.rows[e] = SMALL ? load_each<DT, E>(row[e], c0, C) : load_whole<DT, E>(row[e] + c0);
+      for (int e = 0; e < E; ++e)
+        s.rows[e] = SMALL ? load_each<DT, E>(row[e], c0, C) : load_whole<DT, E>(row[e] + c0);
       if (inside) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -1248,7 +1248,7 @@ int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank) {
   // enough workgroups for the chip, each with two 64-column blocks a wave at least (64 single tokens, 4096 columns: four
   // parts 6.0 us, two 7.8; more parts are more to read for the next kernel)
   const int64_t groups = std::max<int64_t>(1, lora_max_tiles(tokens, adapters)) * ((rank + 63) / 64);
-    const int64_t want = (256 + groups - 1) / groups, most = (cols + 511) / 512;
+  const int64_t want = (256 + groups - 1) / groups, most = (cols + 511) / 512;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 8));
 }
 

@@ -907,7 +907,8 @@ def _pair_types(x: torch.Tensor, y: torch.Tensor, what: str):
 
 def layer_norm_forward(x, y, weight=None, bias=None, eps: float = 1e-5, stats=None, y_amax=None, stream=None):
     """y (rows, cols) = the layer norm of each row of x, times weight plus bias (each (cols) or None).  stats: optional
-    float32 (2, rows) tensor that receives the rows' mean and rstd for the backward.  y_amax: optional float32 tensor that receives max |y|."""
+    float32 (2, rows) tensor that receives the rows' mean and rstd for the backward.  y_amax: optional float32 tensor
+    that receives max |y|."""
     if x.dim() != 2 or y.shape != x.shape:
         raise ValueError("layer_norm_forward: x and y must be 2-D tensors of one shape")
     rows, cols = x.shape
@@ -948,7 +949,8 @@ def layer_norm_backward(dy, x, weight, stats, dx=None, dweight=None, dbias=None,
     pdw, dwt = _vector(dweight, cols, "dweight", dev)
     pdb, dbt = _vector(dbias, cols, "dbias", dev)
     _same_device(ws, "ws", dev)
-    a = _LN_BWD.pack(rows, cols, pdy, px, lddy, ldx, pw, _f32(stats, 2 * rows, "stats", dev), pdx, pdw, pdb, _DTYPE[dy.dtype], _DTYPE[x.dtype], wt, dwt, dbt, _ptr(ws) or 0, _nbytes(ws))
+    a = _LN_BWD.pack(rows, cols, pdy, px, lddy, ldx, pw, _f32(stats, 2 * rows, "stats", dev), pdx, pdw, pdb,
+                     _DTYPE[dy.dtype], _DTYPE[x.dtype], wt, dwt, dbt, _ptr(ws) or 0, _nbytes(ws))
     _call(_lib.f8lin_layer_norm_backward, dev, stream, a)
 
 
