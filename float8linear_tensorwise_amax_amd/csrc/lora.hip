@@ -72,9 +72,13 @@ __device__ __forceinline__ int plan_tile_count(const int *p, int tokens, int ada
 }
 
 // A stable counting sort in one workgroup: each wave owns a contiguous part of
-// the tokens and, 64 at a time, finds the lanes that share an adapter; counts
-// and cursors are a wave's own, so that no two waves meet at one.  Bound by the
-// latency of its passes over the index (64 tokens 4 us), once a batch.
+// the tokens and, 64 at a time, finds for each the others of its adapter, one
+// ballot a bit of the adapters' numbers; counts and cursors are a wave's own,
+// so that no two waves meet at one.  Bound by the latency of its passes over
+// the index, and past a few thousand tokens by what one workgroup computes (64
+// tokens 5.5 us, 65536 of 4 adapters 41 in runs and 66 mixed, of 1000 mixed 125;
+// one adapter after the other among 64 tokens 12.9, 108 mixed, 946), once a
+// batch.
 template <int WAVES, int MAXA>
 __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index, int wide, int tokens, int adapters,
                                                                int *plan) {
@@ -94,24 +98,44 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
     const int64_t v = wide ? reinterpret_cast<const int64_t *>(index)[t] : (int64_t) reinterpret_cast<const int *>(index)[t];
     return v >= 0 && v < adapters ? (int)v : adapters;
   };
-  // f(adapter, lanes that have it) for each adapter among 64 tokens
-  auto each_adapter = [&](int a, auto f) {
-    uint64_t left = __ballot(a >= 0);
-    while (left) {
-      const int av = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
-      const uint64_t same = __ballot(a == av);
-      f(av, same);
-      left &= ~same;
+  // f(token, its adapter, the lanes that have the same) for 64 tokens at a time, lanes past the wave's last with none
+  const int bits = 32 - __builtin_clz(adapters);
+  constexpr int kAhead = 4;  // loads on their way
+  auto each_group = [&](auto f) {
+    int next[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) next[k] = adapter_of(begin + 64 * k + lane);
+    for (int t0 = begin; t0 < end; t0 += 64 * kAhead) {
+      int now[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) now[k] = next[k], next[k] = adapter_of(t0 + 64 * (kAhead + k) + lane);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int a = now[k];
+        uint64_t same = __ballot(a >= 0);
+        if (same == 0) break;
+        // (often all 64 are one adapter's; lane 0 is there)
+        if (__ballot(a == __builtin_amdgcn_readfirstlane(a)) != same) {
+          uint32_t lo = (uint32_t)same, hi = (uint32_t)(same >> 32);
+          for (int b = 0; b < bits; ++b) {
+            const uint32_t bit = (uint32_t)(a << (31 - b) >> 31);  // of this lane, 32 times
+            const uint64_t with = __ballot(bit != 0);
+            lo &= ~((uint32_t)with ^ bit), hi &= ~((uint32_t)(with >> 32) ^ bit);
+          }
+          same = (uint64_t)hi << 32 | lo;
+        }
+        if (a >= 0) f(t0 + 64 * k + lane, a, same);
+        // (the next group reads what other lanes have written)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
     }
   };
-  int next = adapter_of(begin + lane);
-  for (int t = begin; t < end; t += 64) {
-    const int a = next;
-    next = adapter_of(t + 64 + lane);
-    each_adapter(a, [&](int av, uint64_t same) {
-      if (lane == 0) count[wave][av] += __builtin_popcountll(same);
-    });
-  }
+  const uint64_t before = (1ull << lane) - 1;
+  // (the first lane of an adapter's counts for all)
+  each_group([&](int, int a, uint64_t same) {
+    if ((same & before) == 0) atomicAdd(&count[wave][a], __builtin_popcountll(same));
+  });
   __syncthreads();
   // exclusive prefix sums over the adapters, of tokens and of tiles
   int tokens_before = 0, tiles_before = 0;
@@ -155,20 +179,12 @@ __global__ __launch_bounds__(64 * WAVES) void lora_plan_kernel(const void *index
   if (tid == 0) starts[groups] = tokens, tile_first[groups] = tiles_before;
   __syncthreads();
   int *const order = plan + lora_order_at(tokens, adapters), *const owner = order + tokens;
-  next = adapter_of(begin + lane);
-  for (int t = begin; t < end; t += 64) {
-    const int a = next;
-    next = adapter_of(t + 64 + lane);
-    each_adapter(a, [&](int av, uint64_t same) {
-      const int at = count[wave][av];
-      if (a == av) {
-        const int p = at + __builtin_popcountll(same & ((1ull << lane) - 1));
-        order[p] = t + lane;
-        owner[p] = av;
-      }
-      if (lane == 0) count[wave][av] = at + __builtin_popcountll(same);
-    });
-  }
+  each_group([&](int t, int a, uint64_t same) {
+    const int p = count[wave][a] + __builtin_popcountll(same & before);
+    order[p] = t;
+    owner[p] = a;
+    if ((same & before) == 0) atomicAdd(&count[wave][a], __builtin_popcountll(same));
+  });
   __syncthreads();  // (order, by other waves)
   for (int a = tid; a <= groups; a += kThreads) plan[4 + a] = starts[a];
   i32x4 *const tiles = reinterpret_cast<i32x4 *>(plan + lora_tiles_at(adapters));
@@ -634,7 +650,7 @@ __device__ __forceinline__ void up_base(const LoraUp &a, int64_t t, const UpCols
 #pragma unroll
   for (int h = 0; h < 16 / E; ++h) {
     const int64_t c = cols.c0 + 4 * E * h + E * g;
-        raw[h] = frag_of<DT>(SMALL ? load_each<DT, E>(base, c, a.cols) : load_whole<DT, E>(base + c));
+    raw[h] = frag_of<DT>(SMALL ? load_each<DT, E>(base, c, a.cols) : load_whole<DT, E>(base + c));
   }
 }
 // One row's pieces of y.
