@@ -222,7 +222,7 @@ int f8lin_lora_forward(const f8lin_lora_fwd_args *p, void *stream) {
   const int tiles = (int)lora_max_tiles(T, a.adapters);
   int *const exps = (int *)((uint8_t *)a.ws + w.exps_at);
   const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, a.x, ldx, K, a.a, a.scales,
-                      split ? nullptr : (uint32_t *)a.ws, (uint32_t *)a.h, exps, split ? (float *)a.ws : nullptr, w.parts};
+                      split ? nullptr : (uint32_t *)a.ws, a.h, exps, split ? (float *)a.ws : nullptr, w.parts};
   F8_TRY(status_of(launch_lora_down(d, a.dtype, false, s)));
   const LoraUp u = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, split ? nullptr : (const uint32_t *)a.ws, exps,
                     split ? (const float *)a.ws : nullptr, w.parts, a.b, a.base, ldb, N, a.y, N};
@@ -265,7 +265,7 @@ int f8lin_lora_backward(const f8lin_lora_bwd_args *p, void *stream) {
   const bool split = w.split;
   const int tiles = (int)lora_max_tiles(T, a.adapters);
   int *const exps = (int *)(ws + w.exps_at);
-  uint32_t *const gt = (uint32_t *)(ws + w.ht_at);
+  float *const gt = (float *)(ws + w.ht_at);
   if (g) {
     const LoraDown d = {(const int *)a.plan, (int)T, a.adapters, a.rank, tiles, a.dy, lddy, N, a.b, a.scales,
                         split ? nullptr : (uint32_t *)ws, a.da ? gt : nullptr, exps, split ? (float *)ws : nullptr, w.parts};
@@ -277,7 +277,7 @@ int f8lin_lora_backward(const f8lin_lora_bwd_args *p, void *stream) {
   if (!a.da && !a.db) return F8LIN_OK;
   LoraOuter o = {(const int *)a.plan, (int)T, a.adapters, a.rank, w.chunk, w.chunks, {}, 0};
   o.side[0] = LoraOuterSide{a.x, ldx, K, gt, a.da, 0, (float *)(ws + w.part_a_at), 0, 0};
-  o.side[1] = LoraOuterSide{a.dy, lddy, N, (const uint32_t *)a.h, a.db, 1, (float *)(ws + w.part_b_at), 0, 0};
+  o.side[1] = LoraOuterSide{a.dy, lddy, N, a.h, a.db, 1, (float *)(ws + w.part_b_at), 0, 0};
   return status_of(launch_lora_outer(o, a.dtype, s));
 }
 

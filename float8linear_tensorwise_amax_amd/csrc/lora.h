@@ -41,13 +41,14 @@ struct LoraDown {
   int64_t ldx, cols;
   const void *w;        // (adapters, rank, cols) or (adapters, cols, rank)
   const float *scales;  // (adapters) or null
-  // H as the later products take it: in the up product's operand fragments, a
-  // tile after the other, max_tiles x 64 x rank_pad (h, with fp16 data beside
-  // its exponents, one for 64 ranks of a position: rank / 64 rounded up x
-  // tokens), and by rank, rank_pad x tokens (ht); either may be null.  Only with
-  // lora_split: parts_out, the parts' sums in binary32, parts x tokens x
-  // rank_pad, in place of h.
-  uint32_t *h, *ht;
+  // H in binary32 where the later products look for it: in the order of the up
+  // product's operand fragments, a tile after the other, max_tiles x 64 x
+  // rank_pad (h; with fp16 data times 2^-e, beside its exponents e, one for 64
+  // ranks of a position: rank / 64 rounded up x tokens), and by rank, rank_pad x
+  // tokens (ht); either may be null.  Only with lora_split: parts_out, the parts'
+  // sums, parts x tokens x rank_pad, in place of h.
+  uint32_t *h;
+  float *ht;
   int *exponents;
   float *parts_out;
   int parts;
@@ -68,7 +69,7 @@ struct LoraUp {
 struct LoraOuterSide {
   const void *x;  // (tokens, cols)
   int64_t ldx, cols;
-  const uint32_t *ht;  // H's final form by rank
+  const float *ht;  // H by rank
   void *d;         // (adapters, rank, cols), or (adapters, cols, rank) where d_t; null: not computed
   int d_t;
   float *part;  // 2 * chunks x rank x cols

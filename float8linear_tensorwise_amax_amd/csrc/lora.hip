@@ -30,13 +30,13 @@
 // their use: with a bounds check at each load the same kernels took twice as
 // long (down 186 us, outer 379).
 //
-// H and G are (T, R), summed in binary32.  For the 16-bit types they are handed
-// on as two 16-bit values each, 16 bits of mantissa or more in all, so that the
-// rounding of the intermediate, 2^-17, stays well below the output's; products
-// over tokens take bf16 pairs (an fp16 operand beside them becomes such a pair
-// too, exactly; the product of both small halves, 2^-18, is left out), products
-// over ranks in fp16 take fp16 pairs scaled by a power of two a token.  Binary32
-// data use the binary32 matrix instruction throughout.
+// H and G are (T, R), summed and handed on in binary32.  Beside 16-bit operands
+// each value becomes a sum of three 16-bit ones, all of its 24 bits, where it
+// meets the matrix instruction: three bf16 (an fp16 operand beside them becomes
+// two, exactly, and all six products are taken), or in the tiled products over
+// ranks in fp16 three fp16 values scaled by a power of two a token.  Two of them
+// (2^-17) showed in the outputs wherever a sum cancels.  Binary32 data use the
+// binary32 matrix instruction throughout.
 #include <algorithm>
 
 #include "lora.h"
@@ -276,8 +276,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (DT == F8LIN_BF16) return pack_bf16(a, b);
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
-// What rounding a to the bf16 in `bits` (its low or high half) left over; an
-// infinity leaves nothing.
+// What rounding a leaves over; an infinity leaves nothing.
 __device__ __forceinline__ float left_over(float a, float rounded) {
   return (__float_as_uint(rounded) & 0x7F800000u) == 0x7F800000u ? 0.0f : a - rounded;
 }
@@ -296,37 +295,45 @@ __device__ __forceinline__ void split_f16(uint32_t f, uint32_t &hi, uint32_t &lo
 
 // ---------------------------------------------------------------- intermediates
 
-// A value of H as the products over tokens take it: for the 16-bit types a
-// bf16 in the high half and what it left over, as another, in the low one.
+// Beside 16-bit operands a value of H is a sum of three values of DT.  bf16: cut
+// off after 8 bits each, which leaves nothing.
+constexpr int kParts = 3;
+// Two values' parts, as packed pairs.
 template <int DT>
-__device__ __forceinline__ uint32_t h_word(float v) {
-  if constexpr (DT == F8LIN_FP32) return __float_as_uint(v);
-  const uint32_t hi = pack_bf16(0.0f, v) & 0xFFFF0000u;
-  return hi | pack_bf16(left_over(v, __uint_as_float(hi)), 0.0f);
+__device__ __forceinline__ void h_parts(float a, float b, uint32_t (&p)[kParts]) {
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) {
+    if constexpr (DT == F8LIN_BF16) {
+      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+      p[k] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+      if (k + 1 == kParts) break;
+      a = left_over(a, __uint_as_float(ua & 0xFFFF0000u)), b = left_over(b, __uint_as_float(ub & 0xFFFF0000u));
+    } else {
+      p[k] = pack2<DT>(a, b);
+      if (k + 1 == kParts) break;
+      a = left_over(a, f16_bits_to_f32(p[k] & 0xFFFFu)), b = left_over(b, f16_bits_to_f32(p[k] >> 16));
+    }
+  }
 }
-// The same for the products over ranks: with fp16 operands two fp16 values of
-// v * 2^-e, e by the largest value of a token's block of 64 ranks (2^-24 of
-// that value is the least that is kept).
-template <int DT>
-__device__ __forceinline__ uint32_t up_word(float v, int e) {
-  if constexpr (DT != F8LIN_FP16) return h_word<DT>(v);
-  v = ldexpf(v, -e);
-  const _Float16 hi = (_Float16)v;
-  const float left = isfinite((float)hi) ? v - (float)hi : 0.0f;
-  return (uint32_t)__builtin_bit_cast(uint16_t, hi) << 16 | __builtin_bit_cast(uint16_t, (_Float16)left);
+// The same of n consecutive values: part k of them in words k * n / 2 ...
+template <int DT, int N>
+__device__ __forceinline__ void h_parts_of(const float (&v)[N], uint32_t *w) {
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    uint32_t p[kParts];
+    h_parts<DT>(v[2 * e], v[2 * e + 1], p);
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) w[k * (N / 2) + e] = p[k];
+  }
 }
-// e for the largest magnitude's bits: it becomes a value of 2^13 to 2^14.
+// With fp16 operands the products over ranks take v * 2^-e, e by the largest
+// value of a token's block of 64 ranks, which becomes one of 2^13 to 2^14: three
+// fp16 values then hold every bit of what is at least 2^-15 of it, and 2^-39 of
+// it is the most that is lost of the rest.
 __device__ __forceinline__ int up_exponent(uint32_t mag) {
   const int field = (int)(mag >> 23);
   return field == 0 || field == 255 ? 0 : field - 127 - 13;
 }
-// The high (or low) halves of eight such words, as a fragment.
-__device__ __forceinline__ u32x4 h_halves(u32x4 a, u32x4 b, bool high) {
-  const uint32_t sel = high ? 0x07060302u : 0x05040100u;
-  return u32x4{__builtin_amdgcn_perm(a.y, a.x, sel), __builtin_amdgcn_perm(a.w, a.z, sel),
-               __builtin_amdgcn_perm(b.y, b.x, sel), __builtin_amdgcn_perm(b.w, b.z, sel)};
-}
-
 // ---------------------------------------------------------------- down
 
 // H[position][r] = scale * sum over columns of X[t][c] * W(r, c), W (R, C) as
@@ -489,38 +496,28 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
 #pragma unroll
           for (int k = 0; k < E; k += 4) *reinterpret_cast<v4f *>(to + k) = v4f{v[k], v[k + 1], v[k + 2], v[k + 3]};
         } else if (a.h) {
-          // its place among the fragments of 16 rows: 1 KB for 16 ranks (of up to 16 a lane's 8 bytes of high halves and
-          // 8 of low ones; else 1 KB of high halves of 32 ranks, then 1 KB of low ones)
+          // its place among the fragments of 16 rows, 1 KB for 16 ranks: 4 ranks a lane (32 ranks in the 16-bit types: 8 a
+          // lane, the first four of them in the first KB, the others in the second)
           const int group = (at * tile_rows + first_row + row) / 16, rr = r0 + r;
           u32x4 *const to = reinterpret_cast<u32x4 *>(a.h) + (int64_t)group * (rp / 16) * 64 + row % 16;
-          uint32_t o[E];
+          u32x4 o[E / 4];
 #pragma unroll
-          for (int k = 0; k < E; ++k) o[k] = up_word<DT>(v[k], e);
-          if constexpr (DT == F8LIN_FP32) {
-            to[rr / 16 * 64 + rr % 16 / 4 * 16] = u32x4{o[0], o[1], o[2], o[3]};
-          } else {
-            const u32x4 first = {o[0], o[1], o[2], o[3]}, second = {o[4 % E], o[5 % E], o[6 % E], o[7 % E]};
-            const u32x4 hi = h_halves(first, second, true), lo = h_halves(first, second, false);
-            if (rp == 16) {
-              to[rr / 4 * 16] = u32x4{hi.x, hi.y, lo.x, lo.y};
-              to[rr / 4 * 16 + 16] = u32x4{hi.z, hi.w, lo.z, lo.w};
-            } else {
-              to[rr / 32 * 128 + rr % 32 / 8 * 16] = hi;
-              to[rr / 32 * 128 + rr % 32 / 8 * 16 + 64] = lo;
-            }
-          }
+          for (int k = 0; k < E; ++k) o[k / 4][k % 4] = __float_as_uint(DT == F8LIN_FP16 ? ldexpf(v[k], -e) : v[k]);
+          u32x4 *const at4 = to + (E == 4 || rp == 16 ? rr / 16 * 64 + rr % 16 / 4 * 16 : rr / 32 * 128 + rr % 32 / 8 * 16);
+          at4[0] = o[0];
+          if constexpr (E == 8) at4[rp == 16 ? 16 : 64] = o[1];
         }
       }
       if (a.ht) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) red[0][row][r + k] = __uint_as_float(h_word<DT>(v[k]));  // (this thread's own)
+        for (int k = 0; k < E; ++k) red[0][row][r + k] = v[k];  // (this thread's own)
       }
     }
     if (!a.parts_out && a.ht) {
       __syncthreads();
       for (int it = threadIdx.x; it < kRows * RB; it += kThreads) {
         const int row = it % kRows, r = it / kRows;
-        if (row < tile.z && r0 + r < rp) a.ht[(int64_t)(r0 + r) * a.tokens + tile.y + row] = __float_as_uint(red[0][row][r]);
+        if (row < tile.z && r0 + r < rp) a.ht[(int64_t)(r0 + r) * a.tokens + tile.y + row] = red[0][row][r];
       }
     }
   }
@@ -528,9 +525,8 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
 
 // Sums the parts that a split down product left, in their order, into H by
 // rank.
-template <int DT>
 __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
-  __shared__ uint32_t turn[16][17];
+  __shared__ float turn[16][17];
   const int rp = lora_rank_pad(a.rank), tr = threadIdx.x & 15, tp = threadIdx.x >> 4;
   const int64_t ld = (int64_t)a.tokens * rp, rblocks = rp / 16;
   const int r = (int)(blockIdx.x % rblocks) * 16, p = (int)(blockIdx.x / rblocks) * 16;
@@ -538,7 +534,7 @@ __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
     const float *const from = a.parts_out + (int64_t)(p + tp) * rp + r + tr;
     float v = from[0];
     for (int k = 1; k < a.parts; ++k) v += from[k * ld];
-    turn[tp][tr] = h_word<DT>(v);
+    turn[tp][tr] = v;
   }
   __syncthreads();
   if (p + tr < a.tokens) a.ht[(int64_t)(r + tp) * a.tokens + p + tr] = turn[tr][tp];
@@ -692,37 +688,79 @@ __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapte
 // 64, 8192 x 4096 to 14336: 131 us, each wave its own reads 140).  NB = 0: any
 // rank, 64 at a time, all rows' sums kept.
 
-// H's fragments of 16 rows and KB ranks: high and low halves (binary32: itself).
+// A lane's ranks of one row of a block of KB, as the memory holds them.
+template <int DT, int KB>
+struct UpRaw {
+  static constexpr int kPieces = DT != F8LIN_FP32 && KB == 32 ? 2 : 1;
+  u32x4 w[kPieces];
+};
+template <int DT, int KB>
+__device__ __forceinline__ UpRaw<DT, KB> up_raw(const u32x4 *h, int block) {
+  UpRaw<DT, KB> r;
+#pragma unroll
+  for (int k = 0; k < UpRaw<DT, KB>::kPieces; ++k) r.w[k] = h[(block * UpRaw<DT, KB>::kPieces + k) * 64];
+  return r;
+}
+// The same as operand fragments: part after part (binary32: itself).
 template <int DT, int KB>
 struct UpH {
-  static constexpr int kWords = DT == F8LIN_FP32 ? 4 : KB / 4;
+  static constexpr int kWords = DT == F8LIN_FP32 ? 4 : kParts * KB / 8;
   uint32_t w[kWords];
 };
 template <int DT, int KB>
-__device__ __forceinline__ void up_h(const u32x4 *h, int block, UpH<DT, KB> &f) {
-  const u32x4 v = h[block * (DT != F8LIN_FP32 && KB == 32 ? 128 : 64)];
-  f.w[0] = v.x, f.w[1] = v.y, f.w[2] = v.z, f.w[3] = v.w;
-  if constexpr (UpH<DT, KB>::kWords == 8) {
-    const u32x4 lo = h[block * 128 + 64];
-    f.w[4] = lo.x, f.w[5] = lo.y, f.w[6] = lo.z, f.w[7] = lo.w;
+__device__ __forceinline__ UpH<DT, KB> up_split(const UpRaw<DT, KB> &r) {
+  UpH<DT, KB> f;
+  if constexpr (DT == F8LIN_FP32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f.w[k] = r.w[0][k];
+  } else {
+    float v[KB / 4];
+#pragma unroll
+    for (int k = 0; k < KB / 4; ++k) v[k] = __uint_as_float(r.w[k / 4][k % 4]);
+    h_parts_of<DT, KB / 4>(v, f.w);
   }
+  return f;
 }
+// Their place in the LDS: 16 bytes a lane at a time, the last of 16 ranks 8.
+template <int DT, int KB>
+struct UpShared {
+  static constexpr int kWhole = UpH<DT, KB>::kWords / 4;
+  u32x4 whole[kWhole][64];
+  u32x2 half[UpH<DT, KB>::kWords % 4 ? 64 : 1];
+  __device__ __forceinline__ void put(int lane, const UpH<DT, KB> &f) {
+#pragma unroll
+    for (int k = 0; k < kWhole; ++k) whole[k][lane] = u32x4{f.w[4 * k], f.w[4 * k + 1], f.w[4 * k + 2], f.w[4 * k + 3]};
+    if constexpr (UpH<DT, KB>::kWords % 4) half[lane] = u32x2{f.w[4 * kWhole], f.w[4 * kWhole + 1]};
+  }
+  __device__ __forceinline__ UpH<DT, KB> get(int lane) const {
+    UpH<DT, KB> f;
+#pragma unroll
+    for (int k = 0; k < 4 * kWhole; ++k) f.w[k] = whole[k / 4][lane][k % 4];
+    if constexpr (UpH<DT, KB>::kWords % 4) f.w[4 * kWhole] = half[lane].x, f.w[4 * kWhole + 1] = half[lane].y;
+    return f;
+  }
+};
 template <int DT, int KB>
 __device__ __forceinline__ void up_products(const UpFrag<DT, KB> (&wf)[4], const UpH<DT, KB> &h, v4f (&acc)[4]) {
+  // (a part after the other: products that follow each other in one sum would wait)
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    acc[j] = up_mma<DT, KB>(wf[j], h.w, acc[j]);
-    if constexpr (DT != F8LIN_FP32) acc[j] = up_mma<DT, KB>(wf[j], h.w + KB / 8, acc[j]);
-  }
+  for (int k = 0; k < (DT == F8LIN_FP32 ? 1 : kParts); ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = up_mma<DT, KB>(wf[j], h.w + k * (KB / 8), acc[j]);
 }
+
+// Blocks of ranks whose H is in the LDS at once.
+template <int DT, int NB>
+constexpr int up_blocks_at_once = NB > 0 ? NB : DT == F8LIN_FP32 ? 4 : 2;
 
 template <int DT, bool W_T, int NB, int KB, bool SMALL, bool WHOLE>
 __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int at, const int *order, const UpCols cols,
-                                        u32x4 *shared) {
+                                        UpShared<DT, KB> (*shared)[up_blocks_at_once<DT, NB>]) {
   typedef typename MxElem<DT>::type elem;
   constexpr int kPieces = 16 / kE<DT>;
   constexpr int kRanks = DT == F8LIN_FP32 ? 16 : KB;  // of a block
-  const int i = threadIdx.x & 15;
+  constexpr int kNB = up_blocks_at_once<DT, NB>;
+  const int lane = threadIdx.x & 63, i = lane & 15, wave = threadIdx.x >> 6;
   const int64_t C = a.cols;
   const int rp = lora_rank_pad(a.rank);
   const bool adapted = tile.x < a.adapters;
@@ -757,23 +795,21 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
     int64_t t[4];
     int exponent[4];
     const int groups = (tile.z + 15) >> 4;
-    // the tile's H, read once by the workgroup (what belongs to rows that are not there is whatever the memory holds,
-    // and goes to no row that is)
-    constexpr int kMine = 4 * NB * kRanks / 16 * 64 / 256;
-    u32x4 mine[kMine];
+    // the tile's H, read once by the workgroup, 16 rows a wave (what belongs to rows that are not there is whatever the
+    // memory holds, and goes to no row that is)
+    UpRaw<DT, KB> mine[NB];
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) mine[k] = from[threadIdx.x + 256 * k];
+    for (int k = 0; k < NB; ++k) mine[k] = up_raw<DT, KB>(from + wave * h_ld + lane, k);
     // (rows that are not there: the last one's)
 #pragma unroll
     for (int m = 0; m < 4; ++m) t[m] = order[position(m)];
-    const u32x4 *const h = shared + (threadIdx.x & 63);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       up_base<DT, SMALL>(a, t[m], cols, raw[m]);
       if constexpr (DT == F8LIN_FP16) exponent[m] = a.exponents[position(m)];
     }
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) shared[threadIdx.x + 256 * k] = mine[k];
+    for (int k = 0; k < NB; ++k) shared[wave][k].put(lane, up_split<DT, KB>(mine[k]));
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -781,22 +817,34 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
       v4f acc[4] = {zero, zero, zero, zero};
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
-        UpH<DT, KB> hf;
-        up_h<DT, KB>(h + m * h_ld, k, hf);
-        up_products<DT, KB>(wf[k], hf, acc);
+        up_products<DT, KB>(wf[k], shared[m][k].get(lane), acc);
       }
       scale(acc, exponent[m]);
       if (16 * m + i < tile.z) up_store<DT, SMALL>(a, t[m], true, cols, raw[m], acc);
     }
   } else {
-    const u32x4 *const h = from + (threadIdx.x & 63);
     constexpr bool kScaled = DT == F8LIN_FP16;  // 64 ranks share an exponent
     v4f sum[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum[m][j] = zero;
+    const u32x4 *const my = from + wave * h_ld + lane;
+    const int blocks = rp / kRanks;
+    UpRaw<DT, KB> mine[kNB];
+    auto load = [&](int b0) {
+#pragma unroll
+      for (int k = 0; k < kNB; ++k)
+        if (b0 + k < blocks) mine[k] = up_raw<DT, KB>(my, b0 + k);
+    };
+    load(0);
     for (int r0 = 0; r0 < rp; r0 += 64) {
+      __syncthreads();  // (of the last ranks' reads)
+#pragma unroll
+      for (int k = 0; k < kNB; ++k)
+        if (r0 / kRanks + k < blocks) shared[wave][k].put(lane, up_split<DT, KB>(mine[k]));
+      load(r0 / kRanks + kNB);
+      __syncthreads();
       v4f part[kScaled ? 4 : 1][4];
 #pragma unroll
       for (int m = 0; m < (kScaled ? 4 : 1); ++m)
@@ -806,11 +854,8 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
         UpFrag<DT, KB> wf[4];
         up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, cols.c0, r, wf);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          UpH<DT, KB> hf;
-          up_h<DT, KB>(h + m * h_ld, r / kRanks, hf);
-          up_products<DT, KB>(wf, hf, kScaled ? part[m % (kScaled ? 4 : 1)] : sum[m]);
-        }
+        for (int m = 0; m < 4; ++m)
+          up_products<DT, KB>(wf, shared[m][(r - r0) / kRanks].get(lane), kScaled ? part[m % (kScaled ? 4 : 1)] : sum[m]);
       }
       if constexpr (kScaled) {
 #pragma unroll
@@ -833,7 +878,7 @@ __device__ __forceinline__ void up_tile(const LoraUp &a, const i32x4 tile, int a
 
 template <int DT, bool W_T, int NB, int KB, bool SMALL, bool WHOLE>
 __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
-  __shared__ u32x4 shared[NB > 0 ? 4 * NB * (DT == F8LIN_FP32 ? 16 : KB) / 16 * 64 : 1];
+  __shared__ UpShared<DT, KB> shared[4][up_blocks_at_once<DT, NB>];
   const int tiles = plan_tile_count(a.plan, a.tokens, a.adapters);
   const int64_t C = a.cols;
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
@@ -843,7 +888,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraUp a) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
     if (at >= tiles) break;
     up_tile<DT, W_T, NB, KB, SMALL, WHOLE>(a, tile, at, order, up_cols(c0, C), shared);
-    if (NB > 0) __syncthreads();  // (of the tile's reads)
+    __syncthreads();  // (of the tile's reads)
   }
 }
 
@@ -875,7 +920,7 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
       UpFrag<DT, KB> wf[G][4];
 #pragma unroll
       for (int k = 0; k < G; ++k) up_weights<DT, W_T, SMALL, KB, WHOLE>(w, a.rank, C, up_cols(c0 + 64 * k, C).c0, r0, wf[k]);
-      uint32_t hw[P];
+      float hv[P];
 #pragma unroll
       for (int e = 0; e < P; e += 4) {
         const float *const from = a.parts_in + (int64_t)p * rp + r0 + P * g + e;
@@ -883,22 +928,22 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
 #pragma unroll 4
         for (int k = 1; k < a.parts; ++k) s += *reinterpret_cast<const v4f *>(from + k * part_ld);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) hw[e + k] = h_word<DT>(s[k]);
+        for (int k = 0; k < 4; ++k) hv[e + k] = s[k];
       }
       if constexpr (F32) {
+        uint32_t hw[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) hw[e] = __float_as_uint(hv[e]);
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[k][j] = up_mma<DT, KB>(wf[k][j], hw, acc[k][j]);
       } else {
-        uint32_t hi[P / 2], lo[P / 2], finite[P / 2];
+        uint32_t hw[kParts * P / 2], finite[P / 2];
+        h_parts_of<F8LIN_BF16, P>(hv, hw);
+        // (an infinite H meets an fp16 operand's main part only: the other is often zero)
 #pragma unroll
-        for (int e = 0; e < P / 2; ++e) {
-          hi[e] = __builtin_amdgcn_perm(hw[2 * e + 1], hw[2 * e], 0x07060302u);
-          lo[e] = __builtin_amdgcn_perm(hw[2 * e + 1], hw[2 * e], 0x05040100u);
-          // (an infinite H meets an fp16 operand's main half only: the other is often zero)
-          finite[e] = no_inf(hi[e]);
-        }
+        for (int e = 0; e < P / 2; ++e) finite[e] = no_inf(hw[e]);
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
@@ -909,9 +954,12 @@ __device__ __forceinline__ void up_few_tile(const LoraUp &a, const i32x4 tile, c
               f.w[e] = wf[k][j].w[e];
               if constexpr (DT == F8LIN_FP16) split_f16(wf[k][j].w[e], f.w[e], left.w[e]);
             }
-            acc[k][j] = up_mma<F8LIN_BF16, KB>(f, hi, acc[k][j]);
-            acc[k][j] = up_mma<F8LIN_BF16, KB>(f, lo, acc[k][j]);
-            if constexpr (DT == F8LIN_FP16) acc[k][j] = up_mma<F8LIN_BF16, KB>(left, finite, acc[k][j]);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+              acc[k][j] = up_mma<F8LIN_BF16, KB>(f, hw + part * (P / 2), acc[k][j]);
+              if constexpr (DT == F8LIN_FP16)
+                acc[k][j] = up_mma<F8LIN_BF16, KB>(left, part == 0 ? finite : hw + part * (P / 2), acc[k][j]);
+            }
           }
       }
     }
@@ -985,7 +1033,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
   if (split == 1 && own >= C) return;
   const int64_t first = (int64_t)chunk * a.chunk;
   const int end = (int)min((int64_t)adapted, first + a.chunk);
-  const uint32_t *ht[NT];
+  const float *ht[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) ht[j] = side.ht + (int64_t)min(r0 + 16 * j + i, rp - 1) * a.tokens;  // (past the ranks: not stored)
   for (int p0 = (int)min((int64_t)adapted, first); p0 < end;) {
@@ -1015,8 +1063,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const uint32_t v = ht[j][min(at + e, p1 - 1)];
-            s.h[j][e >> 2][e & 3] = at + e < p1 ? v : 0u;
+            const float v = ht[j][min(at + e, p1 - 1)];
+            s.h[j][e >> 2][e & 3] = at + e < p1 ? __float_as_uint(v) : 0u;
           }
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -1024,6 +1072,16 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
       }
     };
     auto multiply = [&](const OuterStep<DT, NT> &s) {
+      u32x4 hp[NT][kParts];
+      if constexpr (DT != F8LIN_FP32) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float v[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = __uint_as_float(s.h[j][e >> 2][e & 3]);
+          h_parts_of<F8LIN_BF16, E>(v, reinterpret_cast<uint32_t *>(hp[j]));
+        }
+      }
 #pragma unroll
       for (int c = 0; c < E; ++c) {
         u32x4 xf = pick<DT, E>(s.rows, c);
@@ -1041,12 +1099,12 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void lora_outer_kernel(const 
             }
           }
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const u32x4 hi = h_halves(s.h[j][0], s.h[j][E / 4 - 1], true), lo = h_halves(s.h[j][0], s.h[j][E / 4 - 1], false);
-            acc[c][j] = mma<F8LIN_BF16>(xf, hi, acc[c][j]);
-            acc[c][j] = mma<F8LIN_BF16>(xf, lo, acc[c][j]);
-            if constexpr (DT == F8LIN_FP16) acc[c][j] = mma<F8LIN_BF16>(xl, hi, acc[c][j]);
-          }
+          for (int k = 0; k < kParts; ++k)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              acc[c][j] = mma<F8LIN_BF16>(xf, hp[j][k], acc[c][j]);
+              if constexpr (DT == F8LIN_FP16) acc[c][j] = mma<F8LIN_BF16>(xl, hp[j][k], acc[c][j]);
+            }
         }
       }
     };
@@ -1190,7 +1248,7 @@ void down_typed(const LoraDown &a, hipStream_t s) {
   else down_rows<DT, W_T, 4, false>(a, s);
   if (a.parts_out && a.ht) {
     const int64_t grid = (int64_t)((a.tokens + 15) / 16) * (lora_rank_pad(a.rank) / 16);
-    lora_sum_kernel<DT><<<(unsigned)grid, 256, 0, s>>>(a);
+    lora_sum_kernel<<<(unsigned)grid, 256, 0, s>>>(a);
   }
 }
 template <int DT, bool W_T, int NB, int KB>
