@@ -11,6 +11,7 @@ are gradients, move the version counters of what they write.
 import array
 import ctypes
 import functools
+import itertools
 import math
 import os
 import struct
@@ -990,10 +991,14 @@ for _name in ("f8lin_lora_plan", "f8lin_lora_forward", "f8lin_lora_backward"):
     getattr(_lib, _name).restype = _int
 
 
-class LoraPlan:
-    """The buffer of a plan (lora_plan writes it) for a batch of `tokens` tokens over `adapters` adapters."""
+_lora_serials = itertools.count(1)
 
-    __slots__ = ("tokens", "adapters", "device", "buffer")
+
+class LoraPlan:
+    """The buffer of a plan (lora_plan writes it) for a batch of `tokens` tokens over `adapters` adapters.  `serial` is
+    another number each time that any plan is written, 0 before; `writes` counts this one's."""
+
+    __slots__ = ("tokens", "adapters", "device", "buffer", "serial", "writes", "_mark")
 
     def __init__(self, tokens: int, adapters: int, device="cuda", buffer: Optional[torch.Tensor] = None):
         """buffer: an int32 tensor to use instead of a new one."""
@@ -1007,6 +1012,16 @@ class LoraPlan:
         elif buffer.dtype != torch.int32 or not buffer.is_contiguous() or buffer.numel() < need // 4 or not buffer.is_cuda:
             raise ValueError(f"f8lin: this plan needs a contiguous int32 GPU buffer of {need // 4} elements")
         self.tokens, self.adapters, self.device, self.buffer = tokens, adapters, buffer.device, buffer
+        self.serial, self.writes, self._mark = 0, 0, None
+
+    def written(self) -> None:
+        self.serial, self.writes, self._mark = next(_lora_serials), self.writes + 1, None
+
+    def mark(self) -> torch.Tensor:
+        """The serial as a tensor in host memory, to be saved beside the tensors of a graph."""
+        if self._mark is None:
+            self._mark = torch.tensor(self.serial, device="cpu")
+        return self._mark
 
 
 def lora_plan(index: torch.Tensor, plan: LoraPlan, stream=None):
@@ -1022,6 +1037,7 @@ def lora_plan(index: torch.Tensor, plan: LoraPlan, stream=None):
     _call(_lib.f8lin_lora_plan, plan.device, stream, p, index.element_size(), plan.tokens, plan.adapters,
           plan.buffer.data_ptr(), 4 * plan.buffer.numel())
     torch.autograd.graph.increment_version(plan.buffer)
+    plan.written()
 
 
 @functools.lru_cache(maxsize=1024)

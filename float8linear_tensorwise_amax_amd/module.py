@@ -796,23 +796,59 @@ class _LoraAddFn(torch.autograd.Function):
     def forward(ctx, base, x, a, b, plan, scales):
         a, b = a.contiguous(), b.contiguous()
         y, h = _lora_forward(base, x, a, b, plan, scales, ctx.needs_input_grad[3])
-        ctx.save_for_backward(x, a, b, h, plan.buffer, scales)
-        ctx.sizes = plan.tokens, plan.adapters
+        # (the plan first: activation checkpointing compares what a forward and its recomputation save, one after the
+        # other, and no other layer saves the like)
+        ctx.save_for_backward(plan.buffer, plan.mark(), x, a, b, h, scales)
+        ctx.sizes, ctx.serial = (plan.tokens, plan.adapters), plan.serial
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         need_base, need_x, need_a, need_b = ctx.needs_input_grad[:4]
+        buffer, mark, x, a, b, h, scales = ctx.saved_tensors
+        # Under checkpointing these tensors are the recomputation's, the node is the forward's.
+        if int(mark) != ctx.serial:
+            raise RuntimeError("low-rank adapters were recomputed for the backward with another batch than their forward "
+                               "had (set or updated in between): pass the batch in the call")
         dx = da = db = None
         if need_x or need_a or need_b:
-            x, a, b, h, buffer, scales = ctx.saved_tensors
             plan = f8lin.LoraPlan(*ctx.sizes, buffer=buffer)
             dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
             da = torch.empty_like(a) if need_a else None
             db = torch.empty_like(b) if need_b else None
             f8lin.lora_backward(_rows(dy), x, a, b, scales, plan, h, dx, da, db)
         return dy if need_base else None, dx, da, db, None, None
+
+
+class _InsideBackward(torch.autograd.Function):
+    """Identity.  Its backward only runs where the forward that a backward made (a recomputation) is itself
+    differentiated: no node of the first forward is there then to compare its batch with."""
+
+    @staticmethod
+    def forward(ctx, y):
+        return y.view_as(y)
+
+    @staticmethod
+    def backward(ctx, dy):
+        _refuse_unclear()
+
+
+def _refuse_unclear():
+    raise RuntimeError("low-rank adapters were recomputed inside a backward with a batch that need not be their forward's: "
+                       "use checkpoint(..., use_reentrant=False), or pass a LoraBatch in the call that is not updated")
+
+
+def _inside_backward() -> bool:
+    """Whether this is a forward under autograd inside a backward pass: a recomputation."""
+    return torch._C._current_graph_task_id() != -1 and torch.is_grad_enabled()
+
+
+def _unclear(y: torch.Tensor) -> torch.Tensor:
+    """y of a recomputation whose batch is not known to be the forward's; refused where no node can find out."""
+    if not y.requires_grad:
+        _refuse_unclear()
+    return _InsideBackward.apply(y)
 
 
 def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, batch: LoraBatch,
@@ -843,12 +879,20 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
         _refuse_tangents("lora_add", base, x, a, b)
         y = _lora_forward(base2, x2, a if a.is_contiguous() else a.contiguous(),
                           b if b.is_contiguous() else b.contiguous(), batch.plan, scales, False)[0]
+    if batch.plan.writes > 1 and _inside_backward():
+        y = _unclear(y)
     return y if len(sx) == 2 else y.reshape(sb)
 
 
+_SET = object()  # the batch that is set on the layer
+
+
 class LoraLinear(nn.Module):
-    """A linear layer with low-rank adapters beside it: base(x), then lora_add for the batch set in `batch` (a
-    LoraBatch; None: the base alone).  base: nn.Linear, Float8Linear or MXFP4Linear (also a frozen one, for serving).
+    """A linear layer with low-rank adapters beside it: base(x), then lora_add for the batch in the call, or else the one
+    set in `batch` (a LoraBatch; None: the base alone).  A batch in the call belongs to that call: threads that serve one
+    model at once, and what is recomputed in a backward after another batch was set, need it there.  Under activation
+    checkpointing a layer whose set batch is another one by then raises RuntimeError (with use_reentrant=True, which
+    leaves nothing to compare, any set batch does).  base: nn.Linear, Float8Linear or MXFP4Linear (also a frozen one, for serving).
     lora_a starts random and lora_b at zero, so that a new adapter adds nothing.  They are kept in `dtype` (default: the
     weight's, bfloat16 beside a frozen one) and used in the base output's."""
 
@@ -866,15 +910,29 @@ class LoraLinear(nn.Module):
         self.lora_a = nn.Parameter(a.normal_(std=self.in_features ** -0.5))
         self.lora_b = nn.Parameter(torch.zeros((adapters, self.out_features, rank), dtype=dtype, device=weight.device))
         self.register_buffer("lora_scales", torch.full((adapters,), scale, dtype=torch.float32, device=weight.device))
-        self.batch: Optional[LoraBatch] = None
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    _batch: Optional[LoraBatch] = None
+    _had_batch = False
+
+    @property
+    def batch(self) -> Optional[LoraBatch]:
+        return self._batch
+
+    @batch.setter
+    def batch(self, batch: Optional[LoraBatch]) -> None:
+        self._batch = batch
+        self._had_batch = self._had_batch or batch is not None
+
+    def forward(self, x: torch.Tensor, batch=_SET) -> torch.Tensor:
+        unclear = batch is _SET and self._had_batch and _inside_backward()
+        if batch is _SET:
+            batch = self._batch
         y = self.base(x)
-        if self.batch is None:
-            return y
-        # (casting the module casts its scales too)
-        return lora_add(y, x.to(y.dtype), self.lora_a.to(y.dtype), self.lora_b.to(y.dtype), self.batch,
-                        self.lora_scales.float())
+        if batch is not None:
+            # (casting the module casts its scales too)
+            y = lora_add(y, x.to(y.dtype), self.lora_a.to(y.dtype), self.lora_b.to(y.dtype), batch,
+                         self.lora_scales.float())
+        return _unclear(y) if unclear else y
 
     def extra_repr(self):
         return f"adapters={self.adapters}, rank={self.rank}"
@@ -892,7 +950,7 @@ def convert_to_lora(module: nn.Module, adapters: int, rank: int, scale: float = 
 
 
 def set_lora_batch(module: nn.Module, batch: Optional[LoraBatch]) -> None:
-    """The batch that every LoraLinear of the module serves next (None: the bases alone)."""
+    """The batch that every LoraLinear of the module serves next, where the call brings none (None: the bases alone)."""
     for m in module.modules():
         if isinstance(m, LoraLinear):
             m.batch = batch
