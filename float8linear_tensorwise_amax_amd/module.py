@@ -876,7 +876,7 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     if _needs_graph(base, x, a, b):
         y = _LoraAddFn.apply(base2, x2, a, b, batch.plan, scales)
     else:
-        _refuse_tangents("lora_add", base, x, a, b)
+        _refuse_tangents("lora_add", base, x, a, b, scales)
         y = _lora_forward(base2, x2, a if a.is_contiguous() else a.contiguous(),
                           b if b.is_contiguous() else b.contiguous(), batch.plan, scales, False)[0]
     if batch.plan.writes > 1 and _inside_backward():
