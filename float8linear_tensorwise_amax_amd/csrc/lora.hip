@@ -71,7 +71,8 @@ __device__ __forceinline__ const int *plan_order(const int *p, int tokens, int a
 __device__ __forceinline__ const int *plan_owner(const int *p, int tokens, int adapters) {
   return p + lora_order_at(tokens, adapters) + tokens;
 }
-// Tiles of the plan, or -1 where the buffer is no plan of this batch size.
+// Tiles of the plan, or -1 where the buffer is no plan of this batch size; it may
+// then be shorter than such a plan, and nothing more of it is read.
 __device__ __forceinline__ int plan_tile_count(const int *p, int tokens, int adapters) {
   const i32x4 h = *reinterpret_cast<const i32x4 *>(p);
   return h.x == kLoraMagic && h.y == tokens && h.z == adapters ? h.w : -1;
@@ -386,10 +387,9 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
   const int blocks = (int)((C + kBlock - 1) / kBlock), part_blocks = (blocks + a.parts - 1) / a.parts;
   const int rp = lora_rank_pad(a.rank), tile_rows = lora_tile(a.tokens);
   const bool whole_ranks = !W_T || a.rank % NT == 0;
-  // (the tile's words are read beside the count: there is room for as many as the grid has)
-  for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
+  for (int at = blockIdx.y; at < tiles; at += gridDim.y) {
     i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
-    if (at >= tiles || tile.x >= a.adapters) break;  // (tokens without an adapter come last)
+    if (tile.x >= a.adapters) break;  // (tokens without an adapter come last)
     tile.y += first_row, tile.z -= first_row;
     if (tile.z <= 0) continue;
     const elem *const w = reinterpret_cast<const elem *>(a.w) + (int64_t)tile.x * a.rank * C;
@@ -547,6 +547,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
 // rank.
 __global__ __launch_bounds__(256) void lora_sum_kernel(const LoraDown a) {
   __shared__ float turn[16][17];
+  if (plan_tile_count(a.plan, a.tokens, a.adapters) < 0) return;
   const int rp = lora_rank_pad(a.rank), tr = threadIdx.x & 15, tp = threadIdx.x >> 4;
   const int64_t ld = (int64_t)a.tokens * rp, rblocks = rp / 16;
   const int r = (int)(blockIdx.x % rblocks) * 16, p = (int)(blockIdx.x / rblocks) * 16;
@@ -940,9 +941,8 @@ __global__ __launch_bounds__(256, (up_waves<DT, W_T, NB, KB, SMALL, WHOLE>)) voi
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   // (a wave past the columns takes the last ones, for the barriers' sake, and stores none of them)
   const int64_t c0 = (int64_t)blockIdx.x * 256 + 64 * (threadIdx.x >> 6);
-  for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
+  for (int at = blockIdx.y; at < tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
-    if (at >= tiles) break;
     up_tile<DT, W_T, NB, KB, SMALL, WHOLE>(a, tile, at, order, up_cols(c0, C), shared);
     __syncthreads();  // (of the tile's reads)
   }
@@ -1054,9 +1054,8 @@ __global__ __launch_bounds__(256, DT != F8LIN_FP32 && !SMALL && G == 1 && (WHOLE
   const int *const order = plan_order(a.plan, a.tokens, a.adapters);
   const int64_t c0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 64 * G;
   if (c0 >= C) return;
-  for (int at = blockIdx.y; at < a.max_tiles; at += gridDim.y) {
+  for (int at = blockIdx.y; at < tiles; at += gridDim.y) {
     const i32x4 tile = plan_tiles(a.plan, a.adapters)[at];
-    if (at >= tiles) break;
     up_few_tile<DT, W_T, G, KB, SMALL, WHOLE>(a, tile, order, c0);
   }
 }

@@ -576,7 +576,8 @@ size_t f8lin_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
  * outside 0 .. adapters - 1 is no adapter -- it serves every projection of a
  * model, and tokens may come in any order.  Buffer: f8lin_lora_plan_bytes
  * (tokens, adapters) bytes, 16-byte aligned.  A call whose tokens or adapters
- * are not the plan's writes nothing.
+ * are not the plan's writes nothing, h and ws included, and reads no more of the
+ * buffer than its first 16 bytes.
  * Errors: EINVAL, ESHAPE, EALIGN, EWORKSPACE, before anything is launched. */
 size_t f8lin_lora_plan_bytes(int64_t tokens, int adapters); /* 0: refused sizes */
 int f8lin_lora_plan(const void *index, int index_bytes, int64_t tokens, int adapters, void *plan, size_t plan_bytes,
