@@ -11,6 +11,8 @@ namespace {
 
 bool bad_size(int64_t d) { return d < 0 || d > kMaxDim; }
 bool bad_matrix(int64_t r, int64_t c) { return bad_size(r) || bad_size(c) || r * c > kMaxElems; }
+// Of a layer norm: its rows are only counted.
+bool bad_rows(int64_t r, int64_t c) { return r < 0 || r > kMaxElems || bad_size(c) || (c > 0 && r > kMaxElems / c); }
 int es_of(int dt) { return dt == F8LIN_FP32 ? 4 : 2; }
 int check_dtype(int dt) { return dt >= F8LIN_BF16 && dt <= F8LIN_FP32 ? F8LIN_OK : F8LIN_EINVAL; }
 bool aligned_to(const void *p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -47,7 +49,7 @@ extern "C" {
 int f8lin_layer_norm_forward(const f8lin_layer_norm_fwd_args *p, void *stream) {
   if (!p) return F8LIN_EINVAL;
   const f8lin_layer_norm_fwd_args &a = *p;
-  if (bad_matrix(a.rows, a.cols)) return F8LIN_ESHAPE;
+  if (bad_rows(a.rows, a.cols)) return F8LIN_ESHAPE;
   const int64_t R = a.rows, C = a.cols, ldx = a.ldx ? a.ldx : C;
   F8_TRY(check_dense(a.x, a.x_dtype, R, C, ldx));
   F8_TRY(check_dense(a.y, a.y_dtype, R, C, C));
@@ -66,14 +68,14 @@ int f8lin_layer_norm_forward(const f8lin_layer_norm_fwd_args *p, void *stream) {
 }
 
 size_t f8lin_layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
-  if (bad_matrix(rows, cols) || rows == 0) return 0;
+  if (bad_rows(rows, cols) || rows == 0) return 0;
   return (size_t)ln_parts(rows, cols) * 2 * (size_t)cols * sizeof(float);
 }
 
 int f8lin_layer_norm_backward(const f8lin_layer_norm_bwd_args *p, void *stream) {
   if (!p) return F8LIN_EINVAL;
   const f8lin_layer_norm_bwd_args &a = *p;
-  if (bad_matrix(a.rows, a.cols)) return F8LIN_ESHAPE;
+  if (bad_rows(a.rows, a.cols)) return F8LIN_ESHAPE;
   const int64_t R = a.rows, C = a.cols, ldx = a.ldx ? a.ldx : C, lddy = a.lddy ? a.lddy : C;
   F8_TRY(check_dense(a.dy, a.dy_dtype, R, C, lddy));
   F8_TRY(check_dense(a.x, a.x_dtype, R, C, ldx));

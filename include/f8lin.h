@@ -39,7 +39,7 @@
  *    enqueues work on it: nothing synchronises, nothing is read back to the
  *    host, nothing is allocated, and no pointer is kept after the call.
  *  - Matrix dimensions (rows, cols, M, N, K) must be >= 0, at most 2^22
- *    and multiples of 16 (every row is then a whole number of 16-byte
+ *    (a layer norm's rows excepted) and multiples of 16 (every row is then a whole number of 16-byte
  *    vectors in both the row-major and the transposed layout).  A zero dimension is allowed and
  *    computes the degenerate result (e.g. dW = 0 when M = 0).
  *  - A transposed fp8 copy (qt of a (rows, cols) tensor; x8t (K, M), w8t
@@ -522,7 +522,8 @@ int f8lin_grad_clip(const f8lin_grad *list, int count, int norm_type, float max_
  * rounded once:
  *   mean = sum(x) / n,  rstd = 1 / sqrt(sum((x - mean)^2) / n + eps)
  *   y = (x - mean) * rstd * weight + bias
- * Any sizes, x with a row stride.  weight and bias may be NULL (1 and 0) and
+ * Any number of rows, up to 2^22 columns and 2^40 elements; x with a row
+ * stride.  weight and bias may be NULL (1 and 0) and
  * are of any type; y has x's type, or with fp32 x any.  stats (2, rows), the
  * rows' mean and then their rstd, are what the backward needs (NULL: not kept).  y_amax, if set,
  * receives max |y| of the rounded values (NaN above all, 0 for no element):
