@@ -617,12 +617,13 @@ def clip_grad_norm_(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max
 # -------------------------------------------------------------- layer norm
 
 def _needs_graph(*tensors: Optional[torch.Tensor]) -> bool:
-    """Whether a call on these tensors has to pass through autograd."""
+    """Whether a call on these tensors has to pass through autograd.  (torch.jit.trace too sees a Function, and of the
+    library's own call nothing but the empty output.)"""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
-    return False
+    return torch._C._get_tracing_state() is not None
 
 
 def _vector_of(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
