@@ -443,9 +443,13 @@ def mxfp4_linear(x: torch.Tensor, weight: Union[torch.Tensor, f8lin.MXFP4Tensor]
     lead = x.shape[:-1]
     # (an empty last dimension leaves reshape nothing to infer the rows from)
     x2 = _rows(x) if x.numel() else x.reshape(lead.numel(), K)
-    if not packed and torch.is_grad_enabled():
+    # (torch.jit.trace sees a Function, and of the library's own call nothing but the empty output)
+    traced = torch._C._get_tracing_state() is not None
+    if not packed and (traced or torch.is_grad_enabled()):
         return _MXFP4LinearFn.apply(x2, weight, bias, rule).reshape(*lead, N)
     _refuse_tangents("mxfp4_linear", x, bias, None if packed else weight)
+    if traced:
+        raise RuntimeError("mxfp4_linear: a call with a quantised weight cannot be traced")
     if not packed:
         return _mxfp4_forward(x2, weight, bias, rule, False, False)[0].reshape(*lead, N)
     if torch.is_grad_enabled() and (x.requires_grad or (bias is not None and bias.requires_grad)):

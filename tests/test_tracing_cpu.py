@@ -1,4 +1,4 @@
-"""torch.jit.trace of the layer norm and the adapters outside autograd, with the kernels replaced by their formulas on the
+"""torch.jit.trace of the layer norm, the adapters and the MXFP4 linear outside autograd, with the kernels replaced by their formulas on the
 CPU: the traced call computes, and does not hand out memory that nothing was written to."""
 import pytest
 import torch
@@ -47,3 +47,18 @@ def test_adapters():
     a, b = torch.randn(1, 3, 8), torch.randn(1, 12, 3)
     got, want = traced(lambda base, x: m.lora_add(base, x, a, b, batch), torch.randn(5, 12), torch.randn(5, 8))
     assert torch.equal(got, want)
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_mxfp4_linear(monkeypatch):
+    def mxfp4_forward(x, w, y, *args, **kw):
+        y.detach().numpy()[...] = (x @ w.t()).numpy()
+
+    monkeypatch.setattr(f8lin, "mxfp4_forward", mxfp4_forward)
+    monkeypatch.setattr(f8lin, "new_mxfp4s", lambda shapes, dev, *args: (None, [None] * len(shapes)))
+    w = torch.randn(12, 8)
+    got, want = traced(lambda x: m.mxfp4_linear(x, w), torch.randn(5, 8))
+    assert torch.equal(got, want)
+    packed = f8lin.MXFP4Tensor(torch.zeros((12, 16), dtype=torch.uint8), torch.zeros((12, 16), dtype=torch.uint8), 12, 8)
+    with pytest.raises(RuntimeError, match="traced"), torch.no_grad():
+        torch.jit.trace(lambda x: m.mxfp4_linear(x, packed), (torch.randn(5, 8),), check_trace=False)
