@@ -5,8 +5,9 @@
 //   dw = sum over rows of dy * xhat,  db = sum over rows of dy
 //
 // HBM-bound: the forward reads x and writes y once, the backward reads x and
-// dy and writes dx once (65536 x 4096 bf16: 226 us, 4.8 TB/s, and 298 us, 5.4
-// TB/s; 12288 x 1600: 18 and 32 us).  A row stays in the registers of the wave
+// dy and writes dx once (65536 x 4096 bf16, in a loop over two inputs and
+// outputs: 235 us, 4.6 TB/s, and 297 us, 5.4 TB/s; with one output, as a program
+// calls it again, forward 200; 12288 x 1600: 19 and 32 us).  A row stays in the registers of the wave
 // (or of the workgroup) that normalises it, so that the mean, the centred
 // squares and the output are three passes over registers, not memory; only
 // rows of more than 16384 values are read again.  Everything is computed in
@@ -15,10 +16,14 @@
 // partial sum each, which a second launch adds in a fixed order (no atomics:
 // the same bits on every run).
 //
-// A wave a row up to 2048 values in the forward (12288 x 1600: 18 us, a
-// workgroup a row 22), a workgroup a row above (65536 x 4096: 236 us, a wave a
-// row 257) and from 512 in the backward, whose sums need the registers (12288 x
-// 1600: 37 us in 512 workgroups, a wave a row 41).
+// A wave a row up to 2048 values in the forward (12288 x 1600: 19 us, a
+// workgroup a row 22), a workgroup a row above (8192 x 4096: 25 us, a wave a row
+// 32; 1021 x 2055 fp32 6.9 and 8.9; but 65536 x 4096 235 and 218) and from 512 in the backward, whose sums need the registers (12288 x
+// 1600: 32 us, a wave a row 46).  From 8193 to 16384 values the backward keeps
+// more than its registers hold (17 spilled in the 16-bit types, 345 in binary32:
+// 4096 x 16384 110 us, 3.7 TB/s, and 370 us, 2.2 TB/s).  Longer rows are read
+// three times forward and back (4096 x 20000 bf16: 99 and 211 us; 1024 x 70000:
+// 101 and 250).
 #include <algorithm>
 
 #include "rows.h"
@@ -27,8 +32,9 @@ namespace f8lin {
 namespace {
 
 // What is read and written goes past the caches where it is more than they
-// hold (65536 x 4096: forward 226 us, through them 231; backward 298 and 318;
-// 8192 x 4096: forward 28.5 past and 25.2 through them).
+// hold (65536 x 4096 bf16: forward 235 us, through them 248; backward 297 and
+// 321; 8192 x 4096: forward 32 past and 25 through them; the backward of 4096 x
+// 16384 in binary32, which spills, the other way: 370 and 361).
 constexpr int64_t kPastBytes = (int64_t)256 << 20;
 
 // Sum over the G threads of a row (G = 64: a wave; else the workgroup), the
@@ -545,8 +551,8 @@ void backward_by_y(const LayerNormBwd &a, int dy_dtype, hipStream_t s) {
 
 // Partial sums of dw and db, one a workgroup: enough workgroups to fill the
 // chip, but at least two rows each up to 256 of them and eight beyond, since a
-// partial sum is written and read again (1805 x 1601 fp16 into 903: 18.5 us,
-// into 256: 16.1; 12288 x 1600 bf16 into 512: 37.2 us, into 1024: 31.7).
+// partial sum is written and read again (1021 x 2055 fp32 into 511: 16.2 us,
+// into 256: 14.8; 12288 x 1600 bf16 into 512: 39 us, into 1024: 32).
 int ln_parts(int64_t rows, int64_t cols) {
   const int64_t most = std::max(std::min<int64_t>((rows + 1) / 2, 256), rows / 8);
   const int64_t fill = cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256;

@@ -16,8 +16,8 @@ constexpr int kLoraMagic = 0x4C6F5241;
 __host__ __device__ inline int lora_rank_pad(int rank) { return rank <= 16 ? 16 : (rank + 31) / 32 * 32; }
 // Rows of a tile: few tokens are mostly single ones of many adapters, or need
 // more workgroups than 64-row tiles give (1024 tokens of 4 adapters, 4096 x
-// 4096, rank 16: down and up 15.5 us in 16-row tiles, 20.3 in 64-row ones; 2048
-// tokens 20.4 and 21.8; 4096 of rank 32 40.5 and 31.8).
+// 4096, rank 16: forward 14.0 us in 16-row tiles, 18.4 in 64-row ones; 2048
+// tokens 21.1 and 21.6; 4096 of rank 32 42 and 32).
 __host__ __device__ inline int lora_tile(int64_t tokens) { return tokens <= 1024 ? 16 : 64; }
 __host__ __device__ inline int64_t lora_max_tiles(int64_t tokens, int64_t adapters) {
   const int64_t groups = tokens < adapters + 1 ? tokens : adapters + 1, rows = lora_tile(tokens);

@@ -15,20 +15,20 @@
 //
 // All of it is bound by memory up to ranks of about 64 (R flops a byte of x):
 // down reads x, up reads base and writes y, outer reads x and dy once more.
-// 65536 bf16 tokens, 4096 x 4096, rank 16: down 92 us (5.0 TB/s), up 230 us
-// (4.7), down from dy 95, dx 131 (4.1, all of it written), outer 200 (4.7).
-// 8192 tokens from 4096 to 14336 at rank 64: 27 and 130 us (3.6 TB/s: the
-// adapter's rows, read by every tile, are half of what passes the L2).  64
-// single tokens of 56 adapters, rank 16: 6 and 16 us for 33 MB of adapters,
-// two chains of dependent cold reads.
+// 65535 bf16 tokens, 4096 x 4096, rank 16, in a training step: down 93 us (5.8
+// TB/s), up 210 (5.1), down from dy 122, dx 138 (3.9, all of it written), outer
+// 228 (4.7).  8192 tokens from 4096 to 14336 at rank 64: 29 and 127 us (3.7
+// TB/s: the adapter's rows, read by every tile, are half of what passes the L2).
+// 64 single tokens of as many adapters, rank 16: 6 and 14.5 us for 37 MB, two
+// chains of dependent cold reads.
 // Rows and weights go from memory to registers in the matrix instructions' own
 // layout, with no LDS between (a tile's H passes through it, once for the four
 // waves): the contraction's order is free, so that a lane's 16 bytes are
 // whatever 8 (4 in binary32) values are contiguous, and where the contraction
 // runs across rows a lane takes 8 rows of a block of columns and transposes
 // them in registers.  Loads stand in straight lines, whole blocks ahead of
-// their use: with a bounds check at each load the same kernels took twice as
-// long (down 186 us, outer 379).
+// their use: with a bounds check at each load down took 186 us and outer 379
+// where they took 92 and 200 without.
 //
 // H and G are (T, R), summed and handed on in binary32.  Beside 16-bit operands
 // each value becomes a sum of three 16-bit ones, all of its 24 bits, where it
@@ -41,7 +41,8 @@
 // An infinity times a value's parts is NaN where one of them is zero, although
 // the product is infinite.  Sums that come out as NaN are therefore taken once
 // more, an infinite value with the other side's main part alone (which is zero
-// only where the value is); products of ordinary data pay a comparison.
+// only where the value is, or in bf16 below 2^-133); products of ordinary data
+// pay a comparison.
 #include <algorithm>
 #include <type_traits>
 
@@ -465,8 +466,8 @@ __global__ __launch_bounds__(64 * WAVES) void lora_down_kernel(const LoraDown a)
           for (int m = 0; m < M; ++m) acc[m][j] = mma<DT>(wf, frag_of<DT>(s.x[h][m]), acc[m][j]);
         }
     };
-    // tiles start at different columns, so that rows a power of two apart do not meet at the same channels (65536 x
-    // 4096: 117 us, all from the first column 129)
+    // tiles start at different columns, so that rows a power of two apart do not meet at the same channels (65535 x
+    // 4096, rank 16: forward 337 us, all from the first column 342; but dx of 8192 x 14336, rank 64, 174 and 163)
     const int b0 = part * part_blocks, nb = min(blocks, b0 + part_blocks) - b0;
     const int turn = nb > 0 ? (int)((uint32_t)at * 5u % (uint32_t)nb) : 0;
     auto block = [&](int b) { return b0 + (b + turn < nb ? b + turn : b + turn - nb); };
@@ -705,9 +706,10 @@ __device__ __forceinline__ void up_store(const LoraUp &a, int64_t t, bool adapte
 }
 // Tiles of 64 rows, H in its final form.  Up to 64 ranks (NB blocks of KB): W
 // stays in registers, the rows pass by in groups of 16, all their base on its
-// way ahead; the tile's H comes through the LDS, once for the four waves (rank
-// 64, 8192 x 4096 to 14336: 131 us, each wave its own reads 140).  NB = 0: any
-// rank, 64 at a time, all rows' sums kept.
+// way ahead; the tile's H comes through the LDS, once for the four waves, and
+// becomes parts on that way.  NB = 0: any rank, 64 at a time, all rows' sums kept
+// (8192 x 4096 to 14336, rank 128: forward 277 us, of two parts only and each
+// wave with its own reads of H 286).
 
 // A lane's ranks of one row of a block of KB, as the memory holds them.
 template <int DT, int KB>
@@ -1323,9 +1325,9 @@ LoraOuterShape lora_outer_shape(int64_t tokens, int rank) {
   const int blocks = rank <= 16 ? 1 : (rank + 31) / 32;
   o.across = blocks > 2 ? 4 : blocks;
   o.rblocks = (blocks + o.across - 1) / o.across;
-  // many tokens: waves side by side, so that a workgroup reads 1 KB of a row (65536 x 4096, rank 16: 200 us, split
-  // over the tokens 240); else parts of the tokens, so that there are fewer chunks for the same number of waves (4096
-  // tokens of rank 32: 29 us, side by side 50)
+  // many tokens: waves side by side, so that a workgroup reads 1 KB of a row (65535 x 4096, rank 16: dA and dB with
+  // their G 318 us, split over the tokens 341); else parts of the tokens, so that there are fewer chunks for the same
+  // number of waves (4096 tokens of rank 32: 44 us, side by side 58)
   o.split = tokens >= 32768 ? 1 : 4 / o.across;
   o.side_by_side = 4 / (o.across * o.split);
   return o;
@@ -1367,8 +1369,8 @@ template <int DT, bool W_T, int KB>
 void up_few_blocks(const LoraUp &a, hipStream_t s) {
   auto grid = [&](int groups) { return tile_grid((a.cols + 256 * groups - 1) / (256 * groups), a.max_tiles, 1); };
   const bool whole = a.rank % (DT == F8LIN_FP32 ? 16 : KB) == 0;
-  // two blocks of columns a wave where there are workgroups enough for either (64 tokens of as many adapters to 14336:
-  // one 17.5 us, two 16.4, four 17.8; one token to 4096: one 3.9, four 8)
+  // two blocks of columns a wave where there are workgroups enough for either (64 tokens of as many adapters, 4096 to
+  // 14336: forward with one 21.6 us, with two 21.2; dx 15.6 and 16.7)
   const bool many = (a.cols + 255) / 256 * a.max_tiles >= 1024;
   if (a.cols < 64) lora_up_few_kernel<DT, W_T, 1, KB, true, false><<<grid(1), 256, 0, s>>>(a);
   else if (!whole) lora_up_few_kernel<DT, W_T, 1, KB, false, false><<<grid(1), 256, 0, s>>>(a);
@@ -1433,9 +1435,11 @@ int lora_parts(int64_t tokens, int adapters, int64_t cols, int rank) {
 }
 
 int lora_chunk(int64_t tokens, int64_t K, int64_t N, int rank) {
-  // a partial sum is written and read in binary32 for every chunk: chunks of at least 16 * rank tokens keep that to a
-  // quarter of the data's bytes; else workgroups for the chip (65536 tokens of rank 16 in 512 workgroups 200 us, in 1024
-  // 243; 8192 of rank 64 from 4096 to 14336, split over the tokens, in 1024 137, in 2048 150)
+  // a partial sum is written and read in binary32 for every chunk: chunks of at least 16 * rank tokens (2048 at most)
+  // keep that to a quarter of the data's bytes, at the price of workgroups where there are few features (4096 tokens,
+  // 1024 x 1024, rank 128: 32 of them); else workgroups for the chip (dA and dB with their G, 65535 tokens of rank 16 in
+  // 512 workgroups 318 us, in 1024 365; 8192 of rank 64 from 4096 to 14336, split over the tokens, in 1024 314, in 2048
+  // 324)
   const LoraOuterShape o = lora_outer_shape(tokens, rank);
   const int64_t cols = 128 * o.side_by_side, per_chunk = ((K + cols - 1) / cols + (N + cols - 1) / cols) * o.rblocks;
   const int64_t chunks = std::max<int64_t>(1, (o.split == 1 ? 512 : 1024) / std::max<int64_t>(1, per_chunk));

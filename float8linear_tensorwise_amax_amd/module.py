@@ -863,7 +863,9 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
 
     base (..., N) and x (..., K) with batch.tokens tokens; a (adapters, rank, K), b (adapters, N, rank); all of one
     dtype.  scales: float32 (adapters) or None (1), outside the graph.  Differentiable once in base, x, a and b (an
-    adapter that no token uses gets a gradient of zero); forward-mode derivatives are refused (NotImplementedError)."""
+    adapter that no token uses gets a gradient of zero); forward-mode derivatives are refused (NotImplementedError).
+    The order of a token's sums depends on the batch it comes in, within their rounding; the same batch gives the same
+    bits."""
     if not x.is_cuda:
         raise RuntimeError("lora_add runs on the GPU only (libf8lin has no CPU path)")
     sx, sb = x.shape, base.shape

@@ -569,7 +569,8 @@ size_t f8lin_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
  *   y[t] = base[t] + scales[i] * (x[t] . A_i^T) . B_i^T
  * A (adapters, rank, K), B (adapters, N, rank), contiguous, of x's type, as
  * are base and y; scales fp32 or NULL (1).  The inner product of a token is
- * kept in fp32.  A token without an adapter gets base[t] and nothing is read
+ * kept in fp32.  The order of a token's sums depends on the batch that it comes
+ * in (within their rounding); the same batch gives the same bits.  A token without an adapter gets base[t] and nothing is read
  * of its x; base NULL: 0.
  *
  * The plan says which tokens an adapter has.  Made once per batch from
