@@ -899,9 +899,11 @@ class LoraLinear(nn.Module):
     set in `batch` (a LoraBatch; None: the base alone).  A batch in the call belongs to that call: threads that serve one
     model at once, and what is recomputed in a backward after another batch was set, need it there.  Under activation
     checkpointing a layer whose set batch is another one by then raises RuntimeError (with use_reentrant=True, which
-    leaves nothing to compare, any set batch does).  base: nn.Linear, Float8Linear or MXFP4Linear (also a frozen one, for serving).
-    lora_a starts random and lora_b at zero, so that a new adapter adds nothing.  They are kept in `dtype` (default: the
-    weight's, bfloat16 beside a frozen one) and used in the base output's."""
+    leaves nothing to compare, any set batch does).
+
+    base: nn.Linear, Float8Linear or MXFP4Linear (also a frozen one, for serving).  lora_a starts random and lora_b at
+    zero, so that a new adapter adds nothing.  They are kept in `dtype` (default: the weight's, bfloat16 beside a frozen
+    one) and used in the base output's."""
 
     def __init__(self, base: nn.Module, adapters: int, rank: int, scale: float = 1.0, dtype: Optional[torch.dtype] = None):
         super().__init__()

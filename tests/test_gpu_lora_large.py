@@ -65,6 +65,12 @@ def test_outer_products(mod, dtype, T, R, K, N):
     check(mod, T, K, N, R, 2, DTYPES[dtype], index_of(T, 2, T + R), (0.05, 0.2, 0.3, 0.02))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_most_tokens(mod, dtype):
+    """As many tokens as a plan holds: more tiles than a grid's second dimension."""
+    check(mod, 1 << 22, 64, 70, 16, 3, DTYPES[dtype], index_of(1 << 22, 3, 5), (0.5, 0.2, 0.3, 0.0005))
+
+
 @pytest.mark.parametrize("T", [900, 5000, 33000])
 def test_one_gradient_at_a_time(f8lin, mod, T):
     K, N, R, L, dt = 200, 333, 24, 3, torch.bfloat16
